@@ -72,7 +72,8 @@ typedef enum {
     SSM_ERR_UNSUPPORTED = 3, /* N > SSM_MAX_N, unknown dtype, or an option value not accepted */
     SSM_ERR_HIP = 4,         /* a HIP runtime call or a launch failed                          */
     SSM_ERR_ALIAS = 5,       /* an output overlaps an input or another output                 */
-    SSM_ERR_SCRATCH = 6,     /* ssm_scan_fwd_noalloc: the plan needs more than its fixed scratch */
+    SSM_ERR_SCRATCH = 6,     /* ssm_scan_fwd_noalloc: the plan needs more than its fixed scratch;
+                                a caller's workspace is smaller than the call needs            */
     SSM_STATUS_MAX_ENUM = 0x7fffffff
 } ssm_status_t;
 
@@ -275,6 +276,106 @@ SSM_API ssm_status_t ssm_ssd_fwd(const void *x, const void *delta, const float *
                                  const float *D, const void *z, const float *initial_state, void *y,
                                  float *final_state, int64_t b, int64_t H, int64_t P, int64_t L, int64_t N,
                                  ssm_dtype_t dtype, hipStream_t stream);
+
+/*
+ * Linear attention with a decay for each head: the scalar-decay recurrence of ssm_ssd_fwd on queries, keys and
+ * values of any head width, token by token in memory as projections write them (page "State Space Models（SSM）と
+ * Mamba" §4.6 relates the two; in the notation of ssm_ssd_fwd the queries are C, the keys B, the values β·x and
+ * e^g the decay e^{a·Δ}). Per batch row and head h, with the queries and keys of group h·G/H (integer division):
+ *     S_t = e^{g_t} · S_{t−1} + v_t k_tᵀ          [P][N], fp32, S_{−1} = initial_state or 0
+ *     o_t = scale · S_t q_t
+ * ssm_linattn_fwd evaluates it in chunks of 64 steps as matrix products (prompts), ssm_linattn_step advances a
+ * stored state by one token, ssm_linattn_bwd gives the gradients of ssm_linattn_fwd.
+ *   q, k              [b][L][G][N] dtype (step: [b][G][N])
+ *   v, o              [b][L][H][P] dtype (step: [b][H][P])
+ *   g                 log-decay, fp32: [b][L][H] (step: [b][H]) when g_per_step is 1, [H] (the same at every
+ *                     step) when it is 0. Any value; −inf, and everything below −1e4, is a decay of exactly 0
+ *                     (the state restarts at that step). Positive values let the state grow.
+ *   states            [b][H][P][N] fp32, as ssm_ssd_fwd's
+ *   lengths           [b] int32 on the device or NULL (every row has L steps): row i has lengths[i] steps (taken
+ *                     as 0 below 0 and as L above L). Nothing past them is read; outputs past them (o, dq, dk, dv,
+ *                     dg) are 0. The final state is the one after the row's last step.
+ *   strides           NULL: q, k, v, do_ dense as above. Otherwise the distance in elements between batch rows
+ *                     (b), steps (t) and heads or groups (h) of q, k, v and do_, each >= 0; the last axis is
+ *                     dense. Inputs may so be slices of one packed projection, or broadcast (distance 0).
+ *                     Outputs are always dense.
+ *   workspace         device memory of at least the bytes ssm_linattn_workspace gives, 16-byte aligned, or NULL:
+ *                     scratch is then taken stream-ordered as by the other entry points, which a capturing stream
+ *                     may refuse. A call writes what it reads there, and keeps nothing in it; calls that
+ *                     may overlap (other streams, captured graphs replayed at once) need one each.
+ * Products are exact bf16 products summed in fp32 (bf16; fp32 operands, that is the state and the decayed scores,
+ * enter as two or three bf16 parts) or fp32 products (f32). All sums, decays and states are fp32, the running sum
+ * of g in a chunk fp64. Results are deterministic. A NaN or Inf at one step reaches outputs and gradients as the
+ * formulas say, except that gradients (dq, dk, dv, dg) may become NaN at every step of the 64-step chunk it is in.
+ * b, H, G, N, P >= 1; G divides H; N <= SSM_LINATTN_MAX_N, P <= SSM_LINATTN_MAX_P (SSM_ERR_UNSUPPORTED above);
+ * L >= 0. With L = 0 the forward call copies the initial state (or zeros) to final_state, the gradient call
+ * d_final_state (or zeros) to d_initial_state and zeros to a g_per_step = 0 dg. No output may overlap an input,
+ * the workspace or another output. Errors as for ssm_scan_fwd; SSM_ERR_SCRATCH: workspace_bytes is too small.
+ */
+#define SSM_LINATTN_MAX_N 128
+#define SSM_LINATTN_MAX_P 1024
+typedef struct {
+    int64_t q_b, q_t, q_h, k_b, k_t, k_h, v_b, v_t, v_h, do_b, do_t, do_h;
+} ssm_linattn_strides_t;
+
+/* Workspace bytes of ssm_linattn_fwd (gradient = 0) or ssm_linattn_bwd (gradient = 1) for this shape (host
+ * only, may be 0). Returns SSM_OK or the validation error. */
+SSM_API ssm_status_t ssm_linattn_workspace(int32_t gradient, int64_t b, int64_t L, int64_t H, int64_t G, int64_t N,
+                                           int64_t P, ssm_dtype_t dtype, int32_t g_per_step, int64_t *bytes);
+
+/* o required (unless L = 0); initial_state, final_state, lengths, strides, workspace may be NULL. */
+SSM_API ssm_status_t ssm_linattn_fwd(const void *q, const void *k, const void *v, const float *g, int32_t g_per_step,
+                                     float scale, const float *initial_state, const int32_t *lengths, void *o,
+                                     float *final_state, int64_t b, int64_t L, int64_t H, int64_t G, int64_t N,
+                                     int64_t P, ssm_dtype_t dtype, const ssm_linattn_strides_t *strides,
+                                     void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* One token: state is read and written in place (it may not overlap any other argument). The strides' t members
+ * and do_ are not used. */
+SSM_API ssm_status_t ssm_linattn_step(float *state, const void *q, const void *k, const void *v, const float *g,
+                                      int32_t g_per_step, float scale, void *o, int64_t b, int64_t H, int64_t G,
+                                      int64_t N, int64_t P, ssm_dtype_t dtype, const ssm_linattn_strides_t *strides,
+                                      hipStream_t stream);
+
+/* Gradients for an upstream gradient do_ [b][L][H][P] dtype on o and, optionally, d_final_state [b][H][P][N] fp32.
+ *   dq, dk            [b][L][G][N] dtype, required (summed over the heads of the group in fp32)
+ *   dv                [b][L][H][P] dtype, required
+ *   dg                fp32, required: [b][L][H], or [H] (summed over rows and steps) when g_per_step is 0
+ *   d_initial_state   [b][H][P][N] fp32 or NULL */
+SSM_API ssm_status_t ssm_linattn_bwd(const void *q, const void *k, const void *v, const float *g, int32_t g_per_step,
+                                     float scale, const float *initial_state, const int32_t *lengths,
+                                     const void *do_, const float *d_final_state, void *dq, void *dk, void *dv,
+                                     float *dg, float *d_initial_state, int64_t b, int64_t L, int64_t H, int64_t G,
+                                     int64_t N, int64_t P, ssm_dtype_t dtype, const ssm_linattn_strides_t *strides,
+                                     void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Layer norm: the norm the Mamba block starts with (page "Mambaとは？Transformer以外の系列モデル", section Mamba
+ * blockのarchitecture), or, with a weight row per head, the norm on each head's output of ssm_linattn_fwd. Per row
+ * of d values, with mean μ and biased variance σ² over the row and r = 1/sqrt(σ² + eps):
+ *     y = w ⊙ (x − μ)·r + bias
+ *   x, y              [rows][d] dtype; x rows x_stride elements apart (>= d, or 0 for dense)
+ *   w, bias           [w_rows][d] fp32 or NULL (1 and 0): row i uses row i mod w_rows; w_rows divides rows
+ *   mean, rstd        [rows] fp32 outputs μ and r, or NULL
+ *   eps               >= 0 and finite (SSM_ERR_UNSUPPORTED otherwise)
+ * ssm_layernorm_bwd: with x̂ = (x − μ)·r, from the forward call's mean and rstd,
+ *     dx = r·(w ⊙ dy − avg(w ⊙ dy) − x̂·avg(w ⊙ dy ⊙ x̂)),  dw = Σ_rows dy ⊙ x̂,  dbias = Σ_rows dy
+ *   dy                [rows][d] dtype, rows dy_stride elements apart (>= d, or 0 for dense)
+ *   dx                [rows][d] dtype, required; dw, dbias [w_rows][d] fp32 or NULL, summed in a fixed order
+ *   workspace         as for ssm_linattn_fwd, of the bytes ssm_layernorm_bwd_workspace gives (0 without dw and dbias)
+ * All sums are fp32 or wider. rows >= 0 (0: only dw and dbias are written, with zeros), d, w_rows >= 1,
+ * d <= SSM_LAYERNORM_MAX_D (SSM_ERR_UNSUPPORTED above), rows·d <= 2^40. y may be x itself (x dense), dx may be dy or x itself (dense); other overlaps are refused. Errors
+ * as for ssm_scan_fwd and ssm_linattn_fwd.
+ */
+#define SSM_LAYERNORM_MAX_D 16384
+SSM_API ssm_status_t ssm_layernorm_fwd(const void *x, const float *w, const float *bias, void *y, float *mean,
+                                       float *rstd, int64_t rows, int64_t d, int64_t w_rows, int64_t x_stride,
+                                       float eps, ssm_dtype_t dtype, hipStream_t stream);
+SSM_API ssm_status_t ssm_layernorm_bwd_workspace(int64_t rows, int64_t d, int64_t w_rows, int64_t *bytes);
+SSM_API ssm_status_t ssm_layernorm_bwd(const void *x, const float *w, const void *dy, const float *mean,
+                                       const float *rstd, void *dx, float *dw, float *dbias, int64_t rows, int64_t d,
+                                       int64_t w_rows, int64_t x_stride, int64_t dy_stride, ssm_dtype_t dtype,
+                                       void *workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /*
  * Options of ssm_scan_fwd_ex. Zero-initialise, then set what you need; zero means "choose".

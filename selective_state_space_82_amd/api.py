@@ -44,6 +44,11 @@ class FwdPlan(ctypes.Structure):
                 ("scratch_bytes", ctypes.c_int64)]
 
 
+class LinAttnStrides(ctypes.Structure):
+    """ssm_linattn_strides_t: elements between batch rows, steps and heads of each input."""
+    _fields_ = [(f"{t}_{a}", ctypes.c_int64) for t in ("q", "k", "v", "do") for a in ("b", "t", "h")]
+
+
 _lib = None
 
 
@@ -90,6 +95,22 @@ def lib() -> ctypes.CDLL:
     L.ssm_lti_fwd.restype = i32
     L.ssm_ssd_fwd.argtypes = [vp] * 10 + [i64, i64, i64, i64, i64, i32, vp]
     L.ssm_ssd_fwd.restype = i32
+    f32 = ctypes.c_float
+    strides = ctypes.POINTER(LinAttnStrides)
+    L.ssm_linattn_workspace.argtypes = [i32] + [i64] * 6 + [i32, i32, ctypes.POINTER(i64)]
+    L.ssm_linattn_workspace.restype = i32
+    L.ssm_linattn_fwd.argtypes = [vp] * 4 + [i32, f32] + [vp] * 4 + [i64] * 6 + [i32, strides, vp, i64, vp]
+    L.ssm_linattn_fwd.restype = i32
+    L.ssm_linattn_step.argtypes = [vp] * 5 + [i32, f32, vp] + [i64] * 5 + [i32, strides, vp]
+    L.ssm_linattn_step.restype = i32
+    L.ssm_linattn_bwd.argtypes = [vp] * 4 + [i32, f32] + [vp] * 9 + [i64] * 6 + [i32, strides, vp, i64, vp]
+    L.ssm_linattn_bwd.restype = i32
+    L.ssm_layernorm_fwd.argtypes = [vp] * 6 + [i64] * 4 + [f32, i32, vp]
+    L.ssm_layernorm_fwd.restype = i32
+    L.ssm_layernorm_bwd_workspace.argtypes = [i64] * 3 + [ctypes.POINTER(i64)]
+    L.ssm_layernorm_bwd_workspace.restype = i32
+    L.ssm_layernorm_bwd.argtypes = [vp] * 8 + [i64] * 5 + [i32, vp, i64, vp]
+    L.ssm_layernorm_bwd.restype = i32
     L.ssm_status_string.argtypes = [i32]
     L.ssm_status_string.restype = ctypes.c_char_p
     L.ssm_abi_version.argtypes = []
@@ -471,3 +492,231 @@ def ssm_scan_fwd_plan(b, d, L, N, dtype=torch.float32, seg_len=0, lanes_per_chan
     status = lib().ssm_scan_fwd_plan(b, d, L, N, _dtype_code(dtype), ctypes.byref(o), ctypes.byref(p))
     _raise(status, "ssm_scan_fwd_plan")
     return {k: getattr(p, k) for k, _ in FwdPlan._fields_}
+
+
+def _check_rows(name, t, shape, dtype, device):
+    """As _check, but only the last axis has to be dense (a slice of a packed projection, a broadcast view)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+
+
+def _linattn_inputs(q, k, v, g, lead):
+    """Checks the inputs that the prompt, step and gradient calls share; lead: (b, L) or (b,).
+    Returns (H, G, N, P, storage dtype code, whether g is per step)."""
+    G, N = q.shape[-2:]
+    H, P = v.shape[-2:]
+    dev, st = v.device, v.dtype
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on a ROCm GPU")
+    code = _dtype_code(st)
+    _check_rows("q", q, (*lead, G, N), st, dev)
+    _check_rows("k", k, (*lead, G, N), st, dev)
+    _check_rows("v", v, (*lead, H, P), st, dev)
+    if not isinstance(g, torch.Tensor):
+        raise TypeError("g must be a torch.Tensor")
+    per_step = g.dim() != 1
+    _check("g", g, (*lead, H) if per_step else (H,), torch.float32, dev)
+    return H, G, N, P, code, per_step
+
+
+def _linattn_strides(q, k, v, do=None):
+    """The strides of [b, L, heads, width] (or [b, heads, width]) inputs, or None when all are dense."""
+    if all(t is None or t.is_contiguous() for t in (q, k, v, do)):
+        return None
+    s = LinAttnStrides()
+    for name, t in (("q", q), ("k", k), ("v", v), ("do", do)):
+        if t is not None:
+            st = t.stride()
+            setattr(s, f"{name}_b", st[0])
+            setattr(s, f"{name}_t", st[1] if len(st) == 4 else 0)
+            setattr(s, f"{name}_h", st[-2])
+    return ctypes.byref(s)
+
+
+def _workspace(bytes_, device):
+    """Scratch of a call from torch's allocator on the current stream, so that a call captured into a graph keeps it
+    for the graph's life."""
+    return torch.empty(bytes_, dtype=torch.uint8, device=device) if bytes_ else None
+
+
+def _on_device(device):
+    """Makes `device` current for the launches of a call (a no-op where it is)."""
+    return torch.cuda.device(device)
+
+
+def ssm_linattn_workspace(b, L, H, G, N, P, dtype=torch.float32, *, gradient=False, g_per_step=True) -> int:
+    """Workspace bytes of ssm_linattn_fwd (or ssm_linattn_bwd) for this shape (host only)."""
+    n = ctypes.c_int64()
+    status = lib().ssm_linattn_workspace(int(bool(gradient)), b, L, H, G, N, P, _dtype_code(dtype),
+                                         int(bool(g_per_step)), ctypes.byref(n))
+    _raise(status, "ssm_linattn_workspace")
+    return n.value
+
+
+def ssm_linattn_fwd(q, k, v, g, *, scale=1.0, initial_state=None, lengths=None, o=None, final_state=None,
+                    return_final_state=True):
+    """Linear attention with a per-head decay over a prompt: S_t = e^{g_t} S_{t-1} + v_t k_tᵀ, o_t = scale·S_t q_t.
+    q, k: [b, L, G, N] and v: [b, L, H, P] (float32 or bfloat16, G divides H, N <= 128; views whose last axis is
+    contiguous, such as slices of a packed projection, are read in place); g: log-decay, float32, [b, L, H], or
+    [H] for the same decay at every step; initial_state: [b, H, P, N] float32; lengths: [b] int32 on the GPU, the
+    steps of each row of a padded batch (o is 0 past them). Returns (o [b, L, H, P], final_state [b, H, P, N] or
+    None)."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and k must be [b, L, G, N] and v [b, L, H, P]")
+    b, L = v.shape[:2]
+    H, G, N, P, code, per_step = _linattn_inputs(q, k, v, g, (b, L))
+    dev = v.device
+    _check("initial_state", initial_state, (b, H, P, N), torch.float32, dev)
+    _check("lengths", lengths, (b,), torch.int32, dev)
+    with _on_device(dev):
+        if o is None:
+            o = torch.empty((b, L, H, P), dtype=v.dtype, device=dev)
+        _check("o", o, (b, L, H, P), v.dtype, dev)
+        if final_state is None and return_final_state:
+            final_state = torch.empty((b, H, P, N), dtype=torch.float32, device=dev)
+        _check("final_state", final_state, (b, H, P, N), torch.float32, dev)
+        need = ctypes.c_int64()
+        _raise(lib().ssm_linattn_workspace(0, b, L, H, G, N, P, code, per_step, ctypes.byref(need)), "ssm_linattn_fwd")
+        ws = _workspace(need.value, dev)
+        status = lib().ssm_linattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), per_step, float(scale), _ptr(initial_state),
+                                       _ptr(lengths), _ptr(o), _ptr(final_state), b, L, H, G, N, P, code,
+                                       _linattn_strides(q, k, v), _ptr(ws), need.value, _stream(dev))
+    _raise(status, "ssm_linattn_fwd")
+    return o, final_state
+
+
+def ssm_linattn_step(state, q, k, v, g, *, scale=1.0, o=None):
+    """One token of ssm_linattn_fwd's recurrence: state [b, H, P, N] float32 (updated in place); q, k: [b, G, N];
+    v: [b, H, P]; g: [b, H] or [H] float32. Returns o [b, H, P]."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and k must be [b, G, N] and v [b, H, P]")
+    b = v.shape[0]
+    H, G, N, P, code, per_step = _linattn_inputs(q, k, v, g, (b,))
+    dev = v.device
+    if state is None:
+        raise TypeError("state must be a torch.Tensor")
+    _check("state", state, (b, H, P, N), torch.float32, dev)
+    with _on_device(dev):
+        if o is None:
+            o = torch.empty((b, H, P), dtype=v.dtype, device=dev)
+        _check("o", o, (b, H, P), v.dtype, dev)
+        status = lib().ssm_linattn_step(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_step, float(scale), _ptr(o),
+                                        b, H, G, N, P, code, _linattn_strides(q, k, v), _stream(dev))
+    _raise(status, "ssm_linattn_step")
+    return o
+
+
+def ssm_linattn_bwd(q, k, v, g, *, do, scale=1.0, initial_state=None, d_final_state=None, lengths=None,
+                    want_d_initial_state=True) -> dict:
+    """Gradients of ssm_linattn_fwd for an upstream gradient do [b, L, H, P] (and optionally d_final_state
+    [b, H, P, N]). Returns a dict: dq, dk [b, L, G, N], dv [b, L, H, P] (storage dtype), dg (g's shape, float32),
+    d_initial_state [b, H, P, N] float32 (None unless want_d_initial_state)."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and k must be [b, L, G, N] and v [b, L, H, P]")
+    b, L = v.shape[:2]
+    H, G, N, P, code, per_step = _linattn_inputs(q, k, v, g, (b, L))
+    dev, st, f32 = v.device, v.dtype, torch.float32
+    _check_rows("do", do, (b, L, H, P), st, dev)
+    _check("initial_state", initial_state, (b, H, P, N), f32, dev)
+    _check("d_final_state", d_final_state, (b, H, P, N), f32, dev)
+    _check("lengths", lengths, (b,), torch.int32, dev)
+    with _on_device(dev):
+        out = {"dq": torch.empty((b, L, G, N), dtype=st, device=dev), "dk": torch.empty((b, L, G, N), dtype=st, device=dev),
+               "dv": torch.empty((b, L, H, P), dtype=st, device=dev), "dg": torch.empty(g.shape, dtype=f32, device=dev),
+               "d_initial_state": torch.empty((b, H, P, N), dtype=f32, device=dev) if want_d_initial_state else None}
+        need = ctypes.c_int64()
+        _raise(lib().ssm_linattn_workspace(1, b, L, H, G, N, P, code, per_step, ctypes.byref(need)), "ssm_linattn_bwd")
+        ws = _workspace(need.value, dev)
+        status = lib().ssm_linattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), per_step, float(scale), _ptr(initial_state),
+                                       _ptr(lengths), _ptr(do), _ptr(d_final_state), _ptr(out["dq"]), _ptr(out["dk"]),
+                                       _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["d_initial_state"]), b, L, H, G, N, P,
+                                       code, _linattn_strides(q, k, v, do), _ptr(ws), need.value, _stream(dev))
+    _raise(status, "ssm_linattn_bwd")
+    return out
+
+
+def _norm_rows(name, x):
+    """(rows, elements between them) of a tensor [..., d] whose rows are evenly spaced."""
+    if x.is_contiguous():
+        return x.numel() // x.shape[-1], x.shape[-1]
+    if x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= x.shape[1]:
+        return x.shape[0], x.stride(0)
+    raise ValueError(f"{name} must be contiguous, or [rows, d] with contiguous rows")
+
+
+def _norm_weight_rows(x, *weights):
+    """Weight rows of a norm over x [..., K, d]: K for weights [K, d], 1 for weights [d]; all weights alike."""
+    d = x.shape[-1]
+    given = [w for w in weights if w is not None]
+    k = x.shape[-2] if given and given[0].dim() == 2 and x.dim() > 1 else 1
+    for w in given:
+        _check("weight or bias", w, (k, d) if given[0].dim() == 2 else (d,), torch.float32, x.device)
+    return k
+
+
+def ssm_layernorm_fwd(x, w=None, bias=None, *, eps=1e-5, y=None, return_stats=False):
+    """Layer norm over the last axis: x [..., d] (float32 or bfloat16, d <= 16384); w, bias: [d] float32, or
+    [K, d] with a row per head for x [..., K, d]. Returns y, or (y, mean, rstd) with mean and rstd float32 of x's
+    shape without its last axis when return_stats is set. y may be x itself."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., d] with d >= 1")
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on a ROCm GPU")
+    code = _dtype_code(x.dtype)
+    rows, stride = _norm_rows("x", x)
+    k = _norm_weight_rows(x, w, bias)
+    with _on_device(dev):
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        _check("y", y, x.shape, x.dtype, dev)
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if return_stats else None
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if return_stats else None
+        status = lib().ssm_layernorm_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), rows,
+                                         x.shape[-1], k, stride, float(eps), code, _stream(dev))
+    _raise(status, "ssm_layernorm_fwd")
+    return (y, mean, rstd) if return_stats else y
+
+
+def ssm_layernorm_bwd(x, w=None, *, dy, mean, rstd, want_dw=True, want_dbias=True, w_rows=None) -> dict:
+    """Gradients of ssm_layernorm_fwd for an upstream gradient dy, from the forward call's mean and rstd. Returns a
+    dict: dx (x's shape and dtype), dw, dbias (float32; w's shape, or without w [d], or [w_rows, d] for w_rows;
+    None unless wanted)."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., d] with d >= 1")
+    dev, d = x.device, x.shape[-1]
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on a ROCm GPU")
+    code = _dtype_code(x.dtype)
+    rows, stride = _norm_rows("x", x)
+    _check_rows("dy", dy, x.shape, x.dtype, dev)
+    dy_stride = _norm_rows("dy", dy)[1]
+    k = _norm_weight_rows(x, w)
+    shape = tuple(w.shape) if w is not None else (d,)
+    if w is None and w_rows is not None:
+        if x.dim() < 2 or x.shape[-2] != w_rows:
+            raise ValueError("w_rows must be the length of x's axis before the last")
+        k, shape = w_rows, (w_rows, d)
+    _check("mean", mean, x.shape[:-1], torch.float32, dev)
+    _check("rstd", rstd, x.shape[:-1], torch.float32, dev)
+    with _on_device(dev):
+        out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
+               "dw": torch.empty(shape, dtype=torch.float32, device=dev) if want_dw else None,
+               "dbias": torch.empty(shape, dtype=torch.float32, device=dev) if want_dbias else None}
+        need = ctypes.c_int64()
+        if want_dw or want_dbias:
+            _raise(lib().ssm_layernorm_bwd_workspace(rows, d, k, ctypes.byref(need)), "ssm_layernorm_bwd")
+        ws = _workspace(need.value, dev)
+        status = lib().ssm_layernorm_bwd(_ptr(x), _ptr(w), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(out["dx"]),
+                                         _ptr(out["dw"]), _ptr(out["dbias"]), rows, d, k, stride, dy_stride, code,
+                                         _ptr(ws), need.value, _stream(dev))
+    _raise(status, "ssm_layernorm_bwd")
+    return out

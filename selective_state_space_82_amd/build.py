@@ -13,7 +13,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libssmscan.so")
 SOURCES = ["scan_fwd.hip", "scan_small.hip", "agg_rev.hip", "scan_bwd.hip", "scan_step.hip", "conv1d.hip", "lti.hip", "ssd.hip",
-           "ssd_scan.hip", "noalloc.hip", "abi.cpp"]
+           "ssd_scan.hip", "linattn_fwd.hip", "linattn_bwd.hip", "linattn_step.hip", "layernorm.hip", "noalloc.hip",
+           "abi.cpp", "abi_attn.cpp"]
 ARCH = "gfx950"
 
 # Packed fp32 VALU forms are kept out of the generated code.
@@ -34,6 +35,9 @@ PROFILE_SOURCES = {
     "conv1d": ("abi.cpp", "device_common.h", "launch.h", "conv1d.hip", "tile_common.h"),
     "frontend": ("abi.cpp", "conv1d.hip", "device_common.h", "launch.h", "scan_fwd.hip", "tile_common.h"),
     "lti": ("abi.cpp", "device_common.h", "launch.h", "lti.hip", "tile_common.h"),
+    "linattn": ("abi_attn.cpp", "device_common.h", "host_util.h", "launch.h", "linattn_bwd.hip", "linattn_common.h",
+                "linattn_fwd.hip", "linattn_step.hip"),
+    "layernorm": ("abi_attn.cpp", "device_common.h", "host_util.h", "launch.h", "layernorm.hip"),
     "ssd": ("abi.cpp", "device_common.h", "launch.h", "ssd.hip", "ssd_common.h", "ssd_scan.hip"),
 }
 

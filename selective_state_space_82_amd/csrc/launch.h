@@ -221,4 +221,52 @@ inline int64_t bwd_scratch_floats(int64_t n_seg, int64_t grad_n_seg, int64_t b, 
     return scratch_floats(n_seg, b, d, N) + b * d * ((L + ck - 1) / ck) * N + 2 * (grad_n_seg - 1) * b * d * N;
 }
 
+// Linear attention with a per-head decay (validated by the ABI layer). The steps are cut into n_seg segments of
+// seg_chunks chunks of 64; S and E are the segments' states and adjoints, [b·H][n_seg][⌈P/64⌉·64][NT] floats with
+// NT = linattn_nt(N), first the segments' own, then those entering (S) and leaving (E) them.
+struct LinAttnLaunch {
+    const void *q, *k, *v, *dout;
+    const float *g;
+    bool g_per_step;
+    float scale;
+    const float *initial_state, *d_final_state;
+    const int32_t *lengths;
+    void *o, *dq, *dk, *dv;
+    float *dg, *final_state, *d_initial_state;
+    int64_t b, L;
+    int H, G, N, P;
+    bool bf16;
+    int64_t q_b, q_t, q_h, k_b, k_t, k_h, v_b, v_t, v_h, do_b, do_t, do_h;  // elements
+    int64_t seg_chunks, n_seg;
+    float *S, *E;
+    double *gsum;          // [b·H][n_seg] sums of g
+    float *dg_steps;       // [b][L][H] when g_per_step is false
+    float *dq_part, *dk_part;  // [b][L][H][N] when G < H
+    bool vec_q, vec_k, vec_v, vec_do;      // 16-byte loads allowed
+    bool vec_n, vec_p;                     // 4-element stores allowed on rows of N, P
+};
+inline int linattn_nt(int64_t N) { return N <= 32 ? 32 : N <= 64 ? 64 : 128; }
+hipError_t launch_linattn_fwd(const LinAttnLaunch &p, hipStream_t stream);
+hipError_t launch_linattn_bwd(const LinAttnLaunch &p, hipStream_t stream);
+hipError_t launch_linattn_step(float *state, const LinAttnLaunch &p, hipStream_t stream);
+// The segments' states from their own (launch_linattn_states) to the entering (leaving) ones.
+hipError_t launch_linattn_states(const LinAttnLaunch &p, bool adjoint, int64_t first_seg, int64_t n, hipStream_t stream);
+hipError_t launch_linattn_carry(const LinAttnLaunch &p, bool adjoint, hipStream_t stream);
+
+// Layer norm (validated by the ABI layer).
+struct NormLaunch {
+    const void *x, *dy;
+    const float *w, *bias, *mean_in, *rstd_in;
+    void *y;                 // dx in the gradient
+    float *mean, *rstd, *dw, *dbias;
+    int64_t rows, d, w_rows, x_stride, dy_stride;
+    float eps;
+    bool bf16;
+    float *part;             // gradient: partial sums of dw, dbias
+    bool vec;                // 16-byte accesses allowed on every row
+};
+hipError_t launch_layernorm_fwd(const NormLaunch &p, hipStream_t stream);
+hipError_t launch_layernorm_bwd(const NormLaunch &p, hipStream_t stream);
+int64_t layernorm_part_floats(int64_t rows, int64_t d, int64_t w_rows);
+
 }  // namespace ssm

@@ -1,0 +1,373 @@
+// linattn_bwd.hip — gradients of linear attention with a per-head decay.
+//
+// By the chain rule on o_t = scale·S_t q_t, S_t = e^{g_t} S_{t−1} + v_t k_tᵀ (page "Mambaとは？Transformer以外の系列
+// モデル", section 状態空間モデルを一つの式から理解する): with E_t = scale·do_t q_tᵀ + e^{g_{t+1}} E_{t+1} the adjoint
+// of S_t,
+//     dq_t = scale·S_tᵀ do_t,  dk_t = E_tᵀ v_t,  dv_t = E_t k_t,  dg_t = e^{g_t}·<S_{t−1}, E_t>.
+// In a chunk with running sums c, the state S entering it and the adjoint E leaving it (of the state after its last
+// step), A1_ts = scale·e^{c_t − c_s} q_t·k_s and A2_ts = scale·e^{c_t − c_s} do_t·v_s for s <= t:
+//     dq_t = Σ_s A2_ts k_s + scale·e^{c_t} Sᵀdo_t,      dk_s = Σ_t A2_ts q_t + e^{c_end − c_s} Eᵀv_s,
+//     dv_s = Σ_t A1_ts do_t + e^{c_end − c_s} E k_s,
+//     dg_t = Σ_{u>=t} (Σ_{s<u} W_us − Σ_{s>u} W_su + X_u) + Σ_{s<t} Y_s + e^{c_end}<S, E>
+// with W_us = A1_us·(do_u·v_s), X_u = q_u·(scale·e^{c_u} Sᵀdo_u), Y_s = v_s·(e^{c_end − c_s} E k_s): the paths from a
+// step before t to one at or after it, by whether either end lies outside the chunk. The W terms come from the same
+// fp32 products in the sum over rows and the one over columns, so the pairs that do not span t cancel in them, and
+// no sum runs past the chunk.
+#include "linattn_common.h"
+
+namespace ssm {
+namespace la {
+namespace {
+
+// Sum over the four 16-lane groups of a wavefront (same column), for every lane.
+__device__ __forceinline__ float sum_groups(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+// Sum over the 16 lanes of a group.
+__device__ __forceinline__ float sum_cols(float v) {
+    v += __shfl_xor(v, 1);
+    v += __shfl_xor(v, 2);
+    v += __shfl_xor(v, 4);
+    return v + __shfl_xor(v, 8);
+}
+
+// ---- one workgroup per (row, head, chunk), all value columns -----------------------------------------------------
+//
+// The four wavefronts share the lower-triangular tiles of both score matrices through LDS; then wavefront w takes
+// the value columns 16w .. of dv, and 16-column jobs of dq and dk.
+template <typename T, int NT>
+__global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
+    constexpr int SN = NT + kPad<T>, SP = kC + kPad<T>, SV = kPB + kPad<T>;
+    constexpr int PARTS = sizeof(T) == 2 ? 2 : 1;
+    constexpr int TILES = NT / 16, JOBS = 2 * TILES / 4;
+    __shared__ __align__(16) T s_q[kC * SN];
+    __shared__ __align__(16) T s_k[kC * SN];
+    __shared__ __align__(16) T s_v[kC * SV];
+    __shared__ __align__(16) T s_d[kC * SV];
+    __shared__ __align__(16) T s_a1[PARTS][kC * SP];  // [t][s]
+    __shared__ __align__(16) T s_a2[PARTS][kC * SP];
+    __shared__ Sums s_c;
+    __shared__ float s_in[kC], s_out[kC];
+    __shared__ float s_row[4][kC], s_col[4][kC], s_x[TILES][kC], s_y[4][kC], s_z[4];
+    __shared__ float s_end;
+
+    int64_t id = work_index(blockIdx.x, gridDim.x);
+    const int h = (int)(id % a.H);
+    id /= a.H;
+    const int64_t ch = id % a.n_seg, ib = id / a.n_seg;
+    const int ratio = a.H / a.G, grp = h / ratio;
+    const int64_t bh = ib * a.H + h;
+    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, col = l & 15, g4 = 4 * (l >> 4);
+    const int64_t len = row_length(a.lengths, ib, a.L);
+    const int64_t t0 = ch * kC;
+    const int64_t rows = a.L - t0 < kC ? a.L - t0 : kC;
+    const int npb = (a.P + kPB - 1) / kPB;
+
+    float *dgp = (a.g_per_step ? a.dg : a.dg_steps) + (ib * a.L + t0) * a.H + h;
+    T *dvp = static_cast<T *>(a.dv) + ((ib * a.L + t0) * a.H + h) * a.P;
+    const int64_t dv_t = (int64_t)a.H * a.P;
+    // dq and dk: straight to the outputs, or this head's share in fp32
+    const bool part = ratio > 1;
+    const int64_t n_t = (int64_t)(part ? a.H : a.G) * a.N, n_off = (ib * a.L + t0) * n_t + (int64_t)(part ? h : grp) * a.N;
+
+    if (t0 >= len) {
+        for (int64_t i = tid; i < rows * a.P; i += kThreads) dvp[i / a.P * dv_t + i % a.P] = (T)0;
+        for (int64_t i = tid; i < rows * a.N; i += kThreads) {
+            const int64_t at = n_off + i / a.N * n_t + i % a.N;
+            if (part) {
+                a.dq_part[at] = 0.0f;
+                a.dk_part[at] = 0.0f;
+            } else {
+                static_cast<T *>(a.dq)[at] = (T)0;
+                static_cast<T *>(a.dk)[at] = (T)0;
+            }
+        }
+        for (int64_t i = tid; i < rows; i += kThreads) dgp[i * a.H] = 0.0f;
+        return;
+    }
+
+    const int64_t g_stride = a.g_per_step ? a.H : 0;
+    const float *gp = a.g_per_step ? a.g + ib * a.L * a.H + h : a.g + h;
+    const T *qp = static_cast<const T *>(a.q) + ib * a.q_b + grp * a.q_h;
+    const T *kp = static_cast<const T *>(a.k) + ib * a.k_b + grp * a.k_h;
+    const T *vp = static_cast<const T *>(a.v) + ib * a.v_b + h * a.v_h;
+    const T *dp = static_cast<const T *>(a.dout) + ib * a.do_b + h * a.do_h;
+
+    stage<T, NT>(s_q, qp, a.q_t, t0, len, 0, a.N, a.vec_q);
+    stage<T, NT>(s_k, kp, a.k_t, t0, len, 0, a.N, a.vec_k);
+    if (w == 0) {
+        const double c = wave_running_sum(log_decay(gp, g_stride, t0 + l, len));
+        const double end = __shfl(c, 63);
+        s_c.set(l, c);
+        s_in[l] = a.scale * exp_of((float)c);
+        s_out[l] = exp_of((float)(end - c));
+        if (l == 63) s_end = exp_of((float)c);
+    }
+    // the tiles right of the diagonal that a 32-step contraction touches
+    for (int i = tid; i < 2 * 16 * 16; i += kThreads) {
+        const int t = 32 * (i >> 8) + ((i >> 4) & 15), s = 32 * (i >> 8) + 16 + (i & 15);
+#pragma unroll
+        for (int e = 0; e < PARTS; ++e) {
+            s_a1[e][t * SP + s] = (T)0;
+            s_a2[e][t * SP + s] = (T)0;
+        }
+    }
+
+    // scores: tile (tb, sb) holds D[s][t] of q·k and do·v
+    f4 aq[3], ad[3];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) aq[j] = ad[j] = f4{0, 0, 0, 0};
+    for (int pb = 0; pb < npb; ++pb) {
+        if (pb) __syncthreads();
+        stage<T, kPB>(s_v, vp, a.v_t, t0, len, pb * kPB, a.P, a.vec_v);
+        stage<T, kPB>(s_d, dp, a.do_t, t0, len, pb * kPB, a.P, a.vec_do);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            const int i = w + 4 * j;
+            if (i < 10) {
+                const int tb = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3, sb = i - tb * (tb + 1) / 2;
+                if (pb == 0)
+#pragma unroll
+                    for (int n = 0; n < NT; n += 32) mma(aq[j], row_frag(s_k, SN, 16 * sb, n), row_frag(s_q, SN, 16 * tb, n));
+#pragma unroll
+                for (int n = 0; n < kPB; n += 32) mma(ad[j], row_frag(s_v, SV, 16 * sb, n), row_frag(s_d, SV, 16 * tb, n));
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        const int i = w + 4 * j;
+        if (i < 10) {
+            const int tb = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3, sb = i - tb * (tb + 1) / 2;
+            const int t = 16 * tb + col, s = 16 * sb + g4;
+            const float th = s_c.hi[t], tl = s_c.lo[t];
+            f4 a1, a2;
+            float row = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float d = a.scale * exp_of((th - s_c.hi[s + r]) + (tl - s_c.lo[s + r]));
+                a1[r] = s + r <= t ? aq[j][r] * d : 0.0f;
+                a2[r] = s + r <= t ? ad[j][r] * d : 0.0f;
+                const float wv = s + r < t ? a1[r] * ad[j][r] : 0.0f;
+                row += wv;
+                const float cs = sum_cols(wv);
+                if (col == 0) s_col[tb][s + r] = cs;
+            }
+            row = sum_groups(row);
+            if (l < 16) s_row[sb][t] = row;
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int e = 0; e < PARTS; ++e) {
+                    const bf4 u = __builtin_convertvector(a1, bf4), v = __builtin_convertvector(a2, bf4);
+                    *reinterpret_cast<bf4 *>(&s_a1[e][t * SP + s]) = u;
+                    *reinterpret_cast<bf4 *>(&s_a2[e][t * SP + s]) = v;
+                    a1 -= __builtin_convertvector(u, f4);
+                    a2 -= __builtin_convertvector(v, f4);
+                }
+            } else {
+                *reinterpret_cast<f4 *>(&s_a1[0][t * SP + s]) = a1;
+                *reinterpret_cast<f4 *>(&s_a2[0][t * SP + s]) = a2;
+            }
+        }
+    }
+
+    const int64_t Pp = (int64_t)npb * kPB;
+    const float *Sp = a.S + (bh * a.n_seg + ch) * Pp * NT;
+    const float *Ep = a.E + (bh * a.n_seg + ch) * Pp * NT;
+    f4 acc[JOBS][4];
+#pragma unroll
+    for (int j = 0; j < JOBS; ++j)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) acc[j][b] = f4{0, 0, 0, 0};
+    float y[4] = {0, 0, 0, 0}, z = 0.0f;
+    for (int pb = 0; pb < npb; ++pb) {
+        __syncthreads();
+        if (npb > 1) {
+            stage<T, kPB>(s_v, vp, a.v_t, t0, len, pb * kPB, a.P, a.vec_v);
+            stage<T, kPB>(s_d, dp, a.do_t, t0, len, pb * kPB, a.P, a.vec_do);
+            __syncthreads();
+        }
+        // dv: value columns 16w ..
+        {
+            const int64_t p = pb * kPB + 16 * w + col;
+            f4 e[NT / 16];
+#pragma unroll
+            for (int i = 0; i < NT / 16; ++i) {
+                e[i] = *reinterpret_cast<const f4 *>(Ep + p * NT + 16 * i + g4);
+                const f4 s = *reinterpret_cast<const f4 *>(Sp + p * NT + 16 * i + g4);
+                z += (e[i][0] * s[0] + e[i][1] * s[1]) + (e[i][2] * s[2] + e[i][3] * s[3]);
+            }
+            f4 dv[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) dv[b] = f4{0, 0, 0, 0};
+#pragma unroll
+            for (int n = 0; n < NT / 32; ++n) {
+                const Split<T, 3> es(join(e[2 * n], e[2 * n + 1]));
+#pragma unroll
+                for (int b = 0; b < 4; ++b) mma(dv[b], es, row_frag(s_k, SN, 16 * b, 32 * n));
+            }
+            const Frag<T> d0 = col_frag(s_d, SV, 0, 16 * w), d1 = col_frag(s_d, SV, 32, 16 * w);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int s = 16 * b + col;
+                dv[b] *= s_out[s];
+                const T *vr = &s_v[s * SV + 16 * w + g4];
+                y[b] += (dv[b][0] * widen(vr[0]) + dv[b][1] * widen(vr[1])) + (dv[b][2] * widen(vr[2]) + dv[b][3] * widen(vr[3]));
+#pragma unroll
+                for (int part_i = 0; part_i < PARTS; ++part_i) {
+                    if (b < 2) mma(dv[b], d0, col_frag(s_a1[part_i], SP, 0, 16 * b));
+                    mma(dv[b], d1, col_frag(s_a1[part_i], SP, 32, 16 * b));
+                }
+                if (s < rows) {
+                    if (t0 + s >= len) dv[b] = f4{0, 0, 0, 0};
+                    store4<T>(dvp + s * dv_t, pb * kPB + 16 * w + g4, a.P, a.vec_p, dv[b]);
+                }
+            }
+        }
+        // dq, dk: the parts through the entering state and the leaving adjoint
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j) {
+            const int job = w + 4 * j;
+            const bool is_q = job < TILES;
+            const int n0 = 16 * (is_q ? job : job - TILES);
+            const float *src = (is_q ? Sp : Ep) + (pb * kPB + g4) * NT + n0 + col;
+            const T *tile = is_q ? s_d : s_v;
+#pragma unroll
+            for (int pp = 0; pp < 2; ++pp) {
+                f8 x;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    x[r] = src[(32 * pp + r) * NT];
+                    x[4 + r] = src[(32 * pp + 16 + r) * NT];
+                }
+                const Split<T, 3> xs(x);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) mma(acc[j][b], xs, row_frag(tile, SV, 16 * b, 32 * pp));
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < JOBS; ++j) {
+        const int job = w + 4 * j;
+        const bool is_q = job < TILES;
+        const int n0 = 16 * (is_q ? job : job - TILES);
+        const T *tile = is_q ? s_k : s_q;
+        const Frag<T> f0 = col_frag(tile, SN, 0, n0), f1 = col_frag(tile, SN, 32, n0);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int t = 16 * b + col;
+            f4 &v = acc[j][b];
+            v *= is_q ? s_in[t] : s_out[t];
+            if (is_q) {
+                const T *qr = &s_q[t * SN + n0 + g4];
+                const float x = sum_groups((v[0] * widen(qr[0]) + v[1] * widen(qr[1])) + (v[2] * widen(qr[2]) + v[3] * widen(qr[3])));
+                if (l < 16) s_x[job][t] = x;
+#pragma unroll
+                for (int e = 0; e < PARTS; ++e) {
+                    mma(v, f0, row_frag(s_a2[e], SP, 16 * b, 0));
+                    if (b >= 2) mma(v, f1, row_frag(s_a2[e], SP, 16 * b, 32));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < PARTS; ++e) {
+                    if (b < 2) mma(v, f0, col_frag(s_a2[e], SP, 0, 16 * b));
+                    mma(v, f1, col_frag(s_a2[e], SP, 32, 16 * b));
+                }
+            }
+            if (t < rows) {
+                if (t0 + t >= len) v = f4{0, 0, 0, 0};
+                if (part) store4<float>((is_q ? a.dq_part : a.dk_part) + n_off + t * n_t, n0 + g4, a.N, a.vec_n, v);
+                else store4<T>(static_cast<T *>(is_q ? a.dq : a.dk) + n_off + t * n_t, n0 + g4, a.N, a.vec_n, v);
+            }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const float v = sum_groups(y[b]);
+        if (l < 16) s_y[w][16 * b + l] = v;
+    }
+    z = sum_groups(sum_cols(z));
+    if (l == 0) s_z[w] = z;
+    __syncthreads();
+    if (w == 0) {
+        const int b = l >> 4;
+        double after = 0.0;
+        for (int i = 0; i <= b; ++i) after += s_row[i][l];
+        for (int i = b; i < 4; ++i) after -= s_col[i][l];
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) after += s_x[i][l];
+        const double ys = ((double)s_y[0][l] + s_y[1][l]) + ((double)s_y[2][l] + s_y[3][l]);
+        const double upto = wave_running_sum(after), yto = wave_running_sum(ys);
+        const double zs = (((double)s_z[0] + s_z[1]) + ((double)s_z[2] + s_z[3])) * s_end;
+        const double v = (__shfl(upto, 63) - upto + after) + (yto - ys) + zs;
+        if (l < rows) dgp[(int64_t)l * a.H] = t0 + l < len ? (float)v : 0.0f;
+    }
+}
+
+// dq and dk of a group: the sum over its heads, in order.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void la_group_sum_kernel(const float *dq_part, const float *dk_part, T *dq, T *dk,
+                                                                int64_t n, int N, int ratio) {
+    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t src = i / N * ratio * N + i % N;  // [b][L][G][ratio][N]
+        float q = 0.0f, k = 0.0f;
+        for (int r = 0; r < ratio; ++r) {
+            q += dq_part[src + (int64_t)r * N];
+            k += dk_part[src + (int64_t)r * N];
+        }
+        dq[i] = narrow<T>(q);
+        dk[i] = narrow<T>(k);
+    }
+}
+
+// dg of a decay that is the same at every step: the sum over rows and steps, one workgroup per head.
+__global__ __launch_bounds__(kThreads) void la_dg_sum_kernel(const float *dg_steps, float *dg, int64_t n, int H) {
+    __shared__ double s[kThreads];
+    double v = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) v += dg_steps[i * H + blockIdx.x];
+    s[threadIdx.x] = v;
+    for (int d = kThreads / 2; d > 0; d >>= 1) {
+        __syncthreads();
+        if ((int)threadIdx.x < d) s[threadIdx.x] += s[threadIdx.x + d];
+    }
+    if (threadIdx.x == 0) dg[blockIdx.x] = (float)s[0];
+}
+
+template <typename T>
+hipError_t grads(const LinAttnLaunch &p, hipStream_t stream) {
+    const int nt = linattn_nt(p.N);
+    const dim3 grid((unsigned)(p.b * p.H * p.n_seg));
+    if (nt == 32) la_grad_kernel<T, 32><<<grid, kThreads, 0, stream>>>(p);
+    else if (nt == 64) la_grad_kernel<T, 64><<<grid, kThreads, 0, stream>>>(p);
+    else la_grad_kernel<T, 128><<<grid, kThreads, 0, stream>>>(p);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && p.G < p.H) {
+        const int64_t n = p.b * p.L * p.G * p.N, blocks = (n + kThreads - 1) / kThreads;
+        la_group_sum_kernel<T><<<dim3((unsigned)(blocks < 16384 ? blocks : 16384)), kThreads, 0, stream>>>(
+            p.dq_part, p.dk_part, static_cast<T *>(p.dq), static_cast<T *>(p.dk), n, p.N, p.H / p.G);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && !p.g_per_step) {
+        la_dg_sum_kernel<<<dim3((unsigned)p.H), kThreads, 0, stream>>>(p.dg_steps, p.dg, p.b * p.L, p.H);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+}  // namespace
+}  // namespace la
+
+hipError_t launch_linattn_bwd(const LinAttnLaunch &p, hipStream_t stream) {
+    hipError_t e = hipSuccess;
+    const int64_t first = p.d_initial_state ? 0 : 1;  // the first segment's own adjoint only feeds d_initial_state
+    if (p.n_seg > 1) e = launch_linattn_states(p, false, 0, p.n_seg - 1, stream);
+    if (e == hipSuccess && p.n_seg > first) e = launch_linattn_states(p, true, first, p.n_seg - first, stream);
+    if (e == hipSuccess) e = launch_linattn_carry(p, false, stream);
+    if (e == hipSuccess) e = launch_linattn_carry(p, true, stream);
+    if (e == hipSuccess) e = p.bf16 ? la::grads<uint16_t>(p, stream) : la::grads<float>(p, stream);
+    return e;
+}
+
+}  // namespace ssm

@@ -1,0 +1,437 @@
+"""Linear attention with a per-head decay on the GPU (ssm_linattn_fwd, _step, _bwd) against the recurrence in 64 bits
+(linattn_ref.py, which derives the bounds)."""
+import math
+
+import pytest
+import torch
+
+import linattn_ref as R
+from selective_state_space_82_amd import api
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm GPU visible")
+    api.lib()
+
+
+def make(b, L, H, G, N, P, dtype=F32, decay="token", rate=0.5, seed=0, first=False, lengths=None):
+    """Inputs on the CPU; every value is exact in `dtype`."""
+    r = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(s, generator=r).to(dtype)  # noqa: E731
+    x = {"q": n(b, L, G, N), "k": n(b, L, G, N), "v": n(b, L, H, P), "do": n(b, L, H, P)}
+    shape = (b, L, H) if decay == "token" else (H,)
+    x["g"] = -rate * torch.rand(shape, generator=r)
+    x["first"] = torch.randn((b, H, P, N), generator=r) if first else None
+    x["d_final"] = torch.randn((b, H, P, N), generator=r) if first else None
+    x["lengths"] = None if lengths is None else torch.tensor(lengths, dtype=torch.int32)
+    x["scale"] = 1 / math.sqrt(N)
+    return x
+
+
+def gpu(x):
+    return {k: t.cuda() if isinstance(t, torch.Tensor) else t for k, t in x.items()}
+
+
+def wide(x, absolute=False):
+    f = lambda t: t.double().abs() if absolute else t.double()  # noqa: E731
+    return {k: (t if t is None or k == "lengths" else f(t)) if k != "scale" else t for k, t in x.items()}
+
+
+def reference(x, absolute=False):
+    w = wide(x, absolute)
+    g = x["g"].double()  # decays are positive either way
+    return R.recur(w["q"], w["k"], w["v"], g, w["scale"], w["first"], w["lengths"])
+
+
+def check_fwd(x, what=""):
+    t = gpu(x)
+    o, S = api.ssm_linattn_fwd(t["q"], t["k"], t["v"], t["g"], scale=t["scale"], initial_state=t["first"],
+                               lengths=t["lengths"])
+    torch.cuda.synchronize()
+    (ro, rS), (mo, mS) = reference(x), reference(x, True)
+    dt, L, N, P = x["v"].dtype, x["v"].shape[1], x["q"].shape[3], x["v"].shape[3]
+    R.assert_within(o, ro, R.bound(ro, mo, dt, L, N, P), what + " o")
+    R.assert_within(S, rS, R.bound(rS, mS, dt, L, N, P, F32), what + " state")
+    return o, S
+
+
+def grad_bounds(x, ref):
+    dt, L, N, P = x["v"].dtype, x["v"].shape[1], x["q"].shape[3], x["v"].shape[3]
+    H, G = x["v"].shape[2], x["q"].shape[2]
+    w, g = wide(x, True), x["g"].double()
+    m = R.grads(w["q"], w["k"], w["v"], g, w["scale"], w["do"], w["first"], w["d_final"], w["lengths"])
+    tol = {n: R.bound(ref[n], m[n], dt, L, N, P, ratio=H // G) for n in ("dq", "dk", "dv")}
+    tol["d_initial_state"] = R.bound(ref["d_initial_state"], m["d_initial_state"], dt, L, N, P, F32)
+    # dg sums, over the 64 steps of a chunk, products that cancel where they do not span the step: per head, their
+    # magnitudes are those of q·dq (pairs with earlier steps and the entering state) and v·dv
+    b = x["v"].shape[0]
+    rep = lambda t: t.repeat_interleave(H // G, 2)  # noqa: E731
+    one = R.grads(rep(w["q"]), rep(w["k"]), w["v"], g, w["scale"], w["do"], w["first"], w["d_final"], w["lengths"])
+    size = (rep(w["q"]) * one["dq"]).sum(-1) + (w["v"] * one["dv"]).sum(-1)  # [b, L, H]
+    nc = -(-L // 64)
+    chunk = torch.nn.functional.pad(size, (0, 0, 0, nc * 64 - L)).view(b, nc, 64, H).sum(2, keepdim=True)
+    chunk = chunk.expand(b, nc, 64, H).reshape(b, nc * 64, H)[:, :L]
+    n = R.paths(L, N, P) + 2 * 64
+    if x["g"].dim() == 1:
+        chunk = chunk.sum((0, 1))
+    tol["dg"] = n * R.U * (chunk + m["dg"]) + R.U * ref["dg"].abs() + 2.0 ** -110
+    return tol
+
+
+def check_bwd(x, what=""):
+    t = gpu(x)
+    got = api.ssm_linattn_bwd(t["q"], t["k"], t["v"], t["g"], do=t["do"], scale=t["scale"], initial_state=t["first"],
+                              d_final_state=t["d_final"], lengths=t["lengths"])
+    torch.cuda.synchronize()
+    w = wide(x)
+    ref = R.grads(w["q"], w["k"], w["v"], w["g"], w["scale"], w["do"], w["first"], w["d_final"], w["lengths"])
+    tol = grad_bounds(x, ref)
+    for n in ref:
+        R.assert_within(got[n], ref[n], tol[n], f"{what} {n}")
+    return got
+
+
+SHAPES = [
+    # b, L, H, G, N, P
+    (1, 1, 1, 1, 1, 1),
+    (2, 1, 3, 3, 16, 16),
+    (1, 2, 2, 1, 5, 3),
+    (1, 63, 2, 2, 32, 64),
+    (2, 64, 4, 2, 33, 65),
+    (1, 65, 3, 1, 64, 31),
+    (1, 129, 2, 2, 72, 40),
+    (2, 200, 6, 2, 128, 96),
+    (1, 333, 2, 1, 100, 130),
+    (3, 97, 4, 4, 20, 200),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "b%d_L%d_H%d_G%d_N%d_P%d" % s)
+def test_forward(shape, dtype):
+    check_fwd(make(*shape, dtype=dtype, seed=sum(shape)), str(shape))
+    check_fwd(make(*shape, dtype=dtype, decay="head", first=True, seed=sum(shape) + 1), str(shape) + " initial")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "b%d_L%d_H%d_G%d_N%d_P%d" % s)
+def test_gradient(shape, dtype):
+    check_bwd(make(*shape, dtype=dtype, seed=sum(shape)), str(shape))
+    check_bwd(make(*shape, dtype=dtype, decay="head", first=True, seed=sum(shape) + 1), str(shape) + " states")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_segments(dtype):
+    """Long rows of few heads: the steps run in segments joined by the carry."""
+    assert api.ssm_linattn_workspace(1, 1500, 1, 1, 32, 16, dtype) > 0
+    x = make(1, 1500, 1, 1, 32, 16, dtype=dtype, rate=0.02, first=True, seed=5)
+    check_fwd(x, "segments")
+    check_bwd(x, "segments")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_padded_batch(dtype):
+    """Rows of other lengths (none, one, a chunk's end, all, beyond): nothing past them is read, and outputs there
+    are 0."""
+    L, lens = 150, [0, 1, 64, 100, 150, 400, -3]
+    x = make(len(lens), L, 4, 2, 24, 40, dtype=dtype, lengths=lens, first=True, seed=3)
+    for i, n in enumerate(lens):
+        n = min(max(n, 0), L)
+        for name in ("q", "k", "v", "do", "g"):
+            x[name][i, n:] = float("nan")
+    clean = dict(x, **{name: torch.nan_to_num(x[name], nan=0.0) for name in ("q", "k", "v", "do", "g")})
+    t = gpu(x)
+    o, S = api.ssm_linattn_fwd(t["q"], t["k"], t["v"], t["g"], scale=t["scale"], initial_state=t["first"],
+                               lengths=t["lengths"])
+    co, cS = check_fwd(clean, "padded")
+    assert torch.equal(o, co) and torch.equal(S, cS)
+    got = api.ssm_linattn_bwd(t["q"], t["k"], t["v"], t["g"], do=t["do"], scale=t["scale"], initial_state=t["first"],
+                              d_final_state=t["d_final"], lengths=t["lengths"])
+    want = check_bwd(clean, "padded")
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    for i, n in enumerate(lens):
+        n = min(max(n, 0), L)
+        assert not o[i, n:].any() and not got["dv"][i, n:].any() and not got["dg"][i, n:].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_packed_and_broadcast_inputs(dtype):
+    """Slices of one projection, a head-major layout, and a key shared by the whole batch give the dense result's bits;
+    the gradients are those of the dense tensors."""
+    b, L, H, G, N, P = 2, 70, 4, 2, 24, 40
+    x = gpu(make(b, L, H, G, N, P, dtype=dtype, seed=11))
+    buf = torch.cat([x["q"].flatten(2), x["k"].flatten(2), x["v"].flatten(2)], -1)
+    q, k, v = buf[..., :G * N].unflatten(-1, (G, N)), buf[..., G * N:2 * G * N].unflatten(-1, (G, N)), \
+        buf[..., 2 * G * N:].unflatten(-1, (H, P))
+    assert not q.is_contiguous()
+    o, S = api.ssm_linattn_fwd(x["q"], x["k"], x["v"], x["g"], scale=0.2)
+    o2, S2 = api.ssm_linattn_fwd(q, k, v, x["g"], scale=0.2)
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    head_major = lambda t: t.transpose(1, 2).contiguous().transpose(1, 2)  # noqa: E731
+    do = head_major(x["do"])
+    a = api.ssm_linattn_bwd(x["q"], x["k"], x["v"], x["g"], do=x["do"])
+    c = api.ssm_linattn_bwd(q, k, head_major(x["v"]), x["g"], do=do)
+    for n in a:
+        assert torch.equal(a[n], c[n]), n
+    kb = x["k"][:1].expand(b, L, G, N)
+    o, S = api.ssm_linattn_fwd(x["q"], kb, x["v"], x["g"])
+    o2, S2 = api.ssm_linattn_fwd(x["q"], kb.contiguous(), x["v"], x["g"])
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    # odd offset: rows that take no 16-byte loads
+    odd = torch.empty(b, L, H, P + 1, dtype=dtype, device="cuda")[..., 1:]
+    odd.copy_(x["v"])
+    o3, S3 = api.ssm_linattn_fwd(x["q"], kb, odd, x["g"])
+    assert torch.equal(o, o3) and torch.equal(S, S3)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_resets_and_strong_decays(dtype):
+    """A decay of 0 (−inf, the type's lowest value) restarts the state: what follows does not depend on what was
+    before, and no NaN appears."""
+    x = make(1, 140, 2, 2, 16, 20, dtype=dtype, first=True, seed=2)
+    x["g"][:, 70] = -math.inf
+    x["g"][:, 100, 0] = torch.finfo(F32).min
+    x["g"][:, 20:40] = -30.0
+    x["g"][:, 128:] = -math.inf
+    y = {k: (t.clone() if isinstance(t, torch.Tensor) else t) for k, t in x.items()}
+    y["g"] = y["g"].clamp(min=-1e4)
+    t = gpu(x)
+    o, S = api.ssm_linattn_fwd(t["q"], t["k"], t["v"], t["g"], scale=t["scale"], initial_state=t["first"])
+    co, cS = check_fwd(y, "resets")
+    assert torch.equal(o, co) and torch.equal(S, cS)
+    got = api.ssm_linattn_bwd(t["q"], t["k"], t["v"], t["g"], do=t["do"], scale=t["scale"], initial_state=t["first"],
+                              d_final_state=t["d_final"])
+    want = check_bwd(y, "resets")
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    t["v"][:, :70], t["k"][:, :70] = 3.0, -2.0
+    o2, _ = api.ssm_linattn_fwd(t["q"], t["k"], t["v"], t["g"], scale=t["scale"], initial_state=t["first"])
+    assert torch.equal(o2[:, 70:], o[:, 70:])
+
+
+def test_growth_and_zero_decay_logs():
+    """g = 0 (plain causal linear attention) and g > 0 (a growing state)."""
+    x = make(1, 130, 2, 1, 16, 16, seed=4)
+    x["g"].zero_()
+    check_fwd(x, "g = 0")
+    check_bwd(x, "g = 0")
+    x["g"].fill_(0.05)
+    check_fwd(x, "g > 0")
+    check_bwd(x, "g > 0")
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_nan_reaches_no_earlier_step(dtype, bad):
+    x = gpu(make(1, 130, 2, 2, 16, 40, dtype=dtype, seed=6))
+    o, _ = api.ssm_linattn_fwd(x["q"], x["k"], x["v"], x["g"])
+    for name in ("q", "k", "v"):
+        y = dict(x)
+        y[name] = x[name].clone()
+        y[name][0, 37, 1, 3] = bad
+        p, S = api.ssm_linattn_fwd(y["q"], y["k"], y["v"], y["g"])
+        assert torch.equal(p[:, :, 0], o[:, :, 0]), name
+        # bf16 rounds the same sums in another order only where V itself holds the value
+        tol = 2.0 ** -7 if dtype == BF16 else 1e-5
+        assert (p[0, :37, 1].double() - o[0, :37, 1].double()).abs().max() <= tol * o.double().abs().max(), name
+        assert not torch.isfinite(p[0, 37, 1]).all(), name
+        if name != "q":
+            assert not torch.isfinite(S[0, 1]).all(), name
+        else:
+            assert torch.isfinite(p[0, 38:, 1]).all() and torch.isfinite(S).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 1, 1, 1, 1), (3, 4, 2, 16, 20), (2, 6, 3, 30, 64), (2, 3, 1, 64, 100),
+                                   (5, 2, 2, 100, 33), (2, 4, 4, 128, 130)], ids=str)
+def test_step(shape, dtype):
+    b, H, G, N, P = shape
+    for decay in ("token", "head"):
+        x = make(b, 1, H, G, N, P, dtype=dtype, decay=decay, first=True, seed=N)
+        t = gpu(x)
+        state = t["first"].clone()
+        g = t["g"][:, 0].contiguous() if decay == "token" else t["g"]
+        o = api.ssm_linattn_step(state, t["q"][:, 0], t["k"][:, 0], t["v"][:, 0], g, scale=t["scale"])
+        (ro, rS), (mo, mS) = reference(x), reference(x, True)
+        R.assert_within(o[:, None], ro, R.bound(ro, mo, dtype, 1, N, P), "o")
+        R.assert_within(state, rS, R.bound(rS, mS, dtype, 1, N, P, F32), "state")
+
+
+def test_step_resets_at_minus_infinity():
+    x = gpu(make(2, 1, 2, 2, 8, 8, first=True, seed=1))
+    g = torch.tensor([[-math.inf, -0.1], [-0.2, -math.inf]], device="cuda")
+    state = x["first"].clone()
+    api.ssm_linattn_step(state, x["q"][:, 0], x["k"][:, 0], x["v"][:, 0], g)
+    kv = x["v"][:, 0][..., :, None] * x["k"][:, 0][..., None, :]
+    assert torch.equal(state[0, 0], kv[0, 0]) and torch.equal(state[1, 1], kv[1, 1])
+    assert torch.isfinite(state).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_prompt_then_tokens(dtype):
+    """A prompt, then single tokens on its state, then another prompt on theirs: the whole sequence's outputs."""
+    b, L, H, G, N, P = 2, 150, 4, 2, 32, 48
+    x = make(b, L, H, G, N, P, dtype=dtype, seed=8)
+    t = gpu(x)
+    cut = lambda a, z: {n: t[n][:, a:z].contiguous() for n in ("q", "k", "v", "g")}  # noqa: E731
+    p = cut(0, 70)
+    o1, S = api.ssm_linattn_fwd(p["q"], p["k"], p["v"], p["g"], scale=t["scale"])
+    mid = []
+    for i in range(70, 75):
+        p = cut(i, i + 1)
+        mid.append(api.ssm_linattn_step(S, p["q"][:, 0], p["k"][:, 0], p["v"][:, 0], p["g"][:, 0].contiguous(),
+                                        scale=t["scale"]))
+    p = cut(75, L)
+    o2, S = api.ssm_linattn_fwd(p["q"], p["k"], p["v"], p["g"], scale=t["scale"], initial_state=S)
+    (ro, rS), (mo, mS) = reference(x), reference(x, True)
+    R.assert_within(torch.cat([o1, torch.stack(mid, 1), o2], 1), ro, R.bound(ro, mo, dtype, L + 64 * 5, N, P), "o")
+    R.assert_within(S, rS, R.bound(rS, mS, dtype, L + 64 * 5, N, P, F32), "state")
+
+
+def test_empty_sequence():
+    x = gpu(make(2, 0, 2, 1, 8, 8, first=True))
+    o, S = api.ssm_linattn_fwd(x["q"], x["k"], x["v"], x["g"], initial_state=x["first"])
+    assert o.shape == (2, 0, 2, 8) and torch.equal(S, x["first"])
+    _, S = api.ssm_linattn_fwd(x["q"], x["k"], x["v"], x["g"])
+    assert not S.any()
+    r = api.ssm_linattn_bwd(x["q"], x["k"], x["v"], torch.zeros(2, device="cuda"), do=x["do"], d_final_state=x["d_final"])
+    assert torch.equal(r["d_initial_state"], x["d_final"]) and not r["dg"].any()
+
+
+def test_gradient_against_differences():
+    """Central differences of the forward call's own results, summed in 64 bits, along a random direction of each
+    input. o and the state are linear in q, k, v and the initial state, so there the step is 1 and only rounding is
+    left; for g the truncation is what the same difference of the 64-bit reference has."""
+    b, L, H, G, N, P = 1, 80, 2, 1, 12, 16
+    x = make(b, L, H, G, N, P, first=True, seed=21)
+    t, w = gpu(x), wide(x)
+    got = api.ssm_linattn_bwd(t["q"], t["k"], t["v"], t["g"], do=t["do"], scale=t["scale"], initial_state=t["first"],
+                              d_final_state=t["d_final"])
+    r = torch.Generator().manual_seed(22)
+    refs = R.grads(w["q"], w["k"], w["v"], w["g"], w["scale"], w["do"], w["first"], w["d_final"])
+    tols = grad_bounds(x, refs)
+    names = {"q": "dq", "k": "dk", "v": "dv", "g": "dg", "first": "d_initial_state"}
+
+    def loss(z):
+        o, S = api.ssm_linattn_fwd(z["q"], z["k"], z["v"], z["g"], scale=z["scale"], initial_state=z["first"])
+        return float((o.cpu().double() * w["do"]).sum() + (S.cpu().double() * w["d_final"]).sum())
+
+    def loss64(z):
+        o, S = R.recur(z["q"], z["k"], z["v"], z["g"], z["scale"], z["first"])
+        return float((o * w["do"]).sum() + (S * w["d_final"]).sum())
+
+    for name, grad in names.items():
+        d = (torch.randn(x[name].shape, generator=r) * 64).round() / 64  # exact steps
+        eps = 2.0 ** -6 if name == "g" else 1.0
+        base = x[name]
+        up, down = base + eps * d, base - eps * d
+        num = (loss(dict(t, **{name: up.cuda()})) - loss(dict(t, **{name: down.cuda()}))) / (2 * eps)
+        num64 = (loss64(dict(w, **{name: up.double()})) - loss64(dict(w, **{name: down.double()}))) / (2 * eps)
+        trunc = abs(num64 - float((refs[grad] * d.double()).sum()))
+        # rounding of the two losses: the forward bound on every output, weighted
+        far = 0.0
+        for z in (up, down):
+            m = wide(dict(x, **{name: z}), True)
+            gg = z.double() if name == "g" else w["g"]
+            mo, mS = R.recur(m["q"], m["k"], m["v"], gg, m["scale"], m["first"])
+            far += float((R.bound(mo, mo, F32, L, N, P) * m["do"]).sum() + (R.bound(mS, mS, F32, L, N, P) * m["d_final"]).sum())
+        mine = float((got[grad].cpu().double() * d.double()).sum())
+        tol = tols[grad]
+        assert abs(mine - num) <= far / (2 * eps) + trunc + float((tol * d.abs().double()).sum()), (name, mine, num)
+
+
+def test_groups_share_keys():
+    """Heads of a group read the same queries and keys: the result of repeating them, and gradients that are the sum."""
+    b, L, H, G, N, P = 2, 90, 6, 2, 16, 24
+    x = gpu(make(b, L, H, G, N, P, seed=31))
+    rep = lambda n: x[n].repeat_interleave(H // G, 2)  # noqa: E731
+    o, S = api.ssm_linattn_fwd(x["q"], x["k"], x["v"], x["g"])
+    o2, S2 = api.ssm_linattn_fwd(rep("q"), rep("k"), x["v"], x["g"])
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    a = api.ssm_linattn_bwd(x["q"], x["k"], x["v"], x["g"], do=x["do"])
+    c = api.ssm_linattn_bwd(rep("q"), rep("k"), x["v"], x["g"], do=x["do"])
+    assert torch.equal(a["dv"], c["dv"]) and torch.equal(a["dg"], c["dg"])
+    for n in ("dq", "dk"):
+        want = c[n].double().view(b, L, G, H // G, N).sum(3)
+        mag = c[n].double().abs().view(b, L, G, H // G, N).sum(3)
+        assert ((a[n].double() - want).abs() <= 4 * (H // G) * R.U * mag).all(), n
+
+
+def test_matches_the_state_space_duality_form():
+    """With keys shared by all heads, P = 64, and the ZOH coefficient folded into the values, the call is ssm_ssd_fwd."""
+    from selective_state_space_82_amd import inputs as I
+    b, H, L, N, P = 2, 2, 130, 32, 64
+    inp = I.random_ssd(b, H, L, N, dtype="f32", seed=3)
+    c = lambda n: torch.from_numpy(inp[n]).cuda()  # noqa: E731
+    y, hT = api.ssm_ssd_fwd(c("x"), c("delta"), c("A"), c("B"), c("C"))
+    A, dl = inp["A"], inp["delta"]
+    a64 = torch.from_numpy(A).double()[None, :, None]
+    d64 = torch.from_numpy(dl).double()
+    beta = torch.where(a64 == 0, d64, torch.expm1(a64 * d64) / torch.where(a64 == 0, torch.ones_like(a64), a64))
+    v = (torch.from_numpy(inp["x"]).double().view(b, H, P, L) * beta[:, :, None]).permute(0, 3, 1, 2).float().cuda()
+    g = (a64 * d64).permute(0, 2, 1).float().contiguous().cuda()
+    o, S = api.ssm_linattn_fwd(c("C")[:, :, None], c("B")[:, :, None], v.contiguous(), g)
+    torch.cuda.synchronize()
+    o = o.permute(0, 2, 3, 1).reshape(b, H * P, L)
+    for got, want in ((o, y), (S.reshape(b, H * P, N), hT)):
+        assert ((got - want).abs() <= 1e-4 * (1 + want.abs())).all()
+
+
+def test_calls_on_streams_and_in_graphs():
+    """The calls run on the current stream; captured once and replayed on new inputs between eager calls, each replay
+    gives the eager result's bits."""
+    b, L, H, G, N, P = 1, 1500, 2, 1, 32, 32  # segments: a workspace is used
+    x = gpu(make(b, L, H, G, N, P, first=True, seed=41))
+    run = lambda: (*api.ssm_linattn_fwd(x["q"], x["k"], x["v"], x["g"], initial_state=x["first"]),  # noqa: E731
+                   *api.ssm_linattn_bwd(x["q"], x["k"], x["v"], x["g"], do=x["do"], initial_state=x["first"],
+                                        d_final_state=x["d_final"]).values())
+    want = run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = run()
+    side.synchronize()
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+    graphs, outs = [], []
+    for _ in range(2):  # two graphs with their own workspaces
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(run())
+        graphs.append(gr)
+    for i in range(4):
+        x["v"].copy_(torch.randn_like(x["v"]))
+        want = run()
+        torch.cuda.synchronize()
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            assert all(torch.equal(a, c) for a, c in zip(o, want)), i
+
+
+def test_repeated_calls_give_the_same_bits():
+    x = gpu(make(2, 300, 4, 2, 64, 64, dtype=BF16, seed=51))
+    first = api.ssm_linattn_bwd(x["q"], x["k"], x["v"], x["g"], do=x["do"])
+    for _ in range(3):
+        again = api.ssm_linattn_bwd(x["q"], x["k"], x["v"], x["g"], do=x["do"])
+        assert all(torch.equal(first[n], again[n]) for n in first)
+
+
+def test_no_workspace_takes_the_librarys_scratch():
+    import ctypes
+    x = gpu(make(1, 1500, 1, 1, 32, 16, seed=61))
+    o, S = api.ssm_linattn_fwd(x["q"], x["k"], x["v"], x["g"])
+    o2, S2 = torch.empty_like(o), torch.empty_like(S)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    st = api.lib().ssm_linattn_fwd(p(x["q"]), p(x["k"]), p(x["v"]), p(x["g"]), 1, 1.0, None, None, p(o2), p(S2), 1, 1500, 1,
+                                   1, 32, 16, 0, None, None, 0, api._stream(x["q"].device))
+    assert st == 0
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(S, S2)
