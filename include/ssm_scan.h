@@ -296,8 +296,8 @@ SSM_API ssm_status_t ssm_ssd_fwd(const void *x, const void *delta, const float *
  *                     as 0 below 0 and as L above L). Nothing past them is read; outputs past them (o, dq, dk, dv,
  *                     dg) are 0. The final state is the one after the row's last step.
  *   strides           NULL: q, k, v, do_ dense as above. Otherwise the distance in elements between batch rows
- *                     (b), steps (t) and heads or groups (h) of q, k, v and do_, each >= 0; the last axis is
- *                     dense. Inputs may so be slices of one packed projection, or broadcast (distance 0).
+ *                     (b), steps (t) and heads or groups (h) of q, k, v and do_, each >= 0, t at most 2^24;
+ *                     the last axis is dense. Inputs may so be slices of one packed projection, or broadcast (distance 0).
  *                     Outputs are always dense.
  *   workspace         device memory of at least the bytes ssm_linattn_workspace gives, 16-byte aligned, or NULL:
  *                     scratch is then taken stream-ordered as by the other entry points, which a capturing stream
@@ -307,7 +307,7 @@ SSM_API ssm_status_t ssm_ssd_fwd(const void *x, const void *delta, const float *
  * enter as two or three bf16 parts) or fp32 products (f32). All sums, decays and states are fp32, the running sum
  * of g in a chunk fp64. Results are deterministic. A NaN or Inf at one step reaches outputs and gradients as the
  * formulas say, except that gradients (dq, dk, dv, dg) may become NaN at every step of the 64-step chunk it is in.
- * b, H, G, N, P >= 1; G divides H; N <= SSM_LINATTN_MAX_N, P <= SSM_LINATTN_MAX_P (SSM_ERR_UNSUPPORTED above);
+ * b, H, G, N, P >= 1; G divides H; H times the larger of 128 and P (rounded up to 64) is at most 2^24; N <= SSM_LINATTN_MAX_N, P <= SSM_LINATTN_MAX_P (SSM_ERR_UNSUPPORTED above);
  * L >= 0. With L = 0 the forward call copies the initial state (or zeros) to final_state, the gradient call
  * d_final_state (or zeros) to d_initial_state and zeros to a g_per_step = 0 dg. No output may overlap an input,
  * the workspace or another output. Errors as for ssm_scan_fwd; SSM_ERR_SCRATCH: workspace_bytes is too small.

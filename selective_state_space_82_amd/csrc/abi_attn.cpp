@@ -21,6 +21,8 @@ using ssm::scratch_alloc;
 using ssm::valid_dtype;
 
 constexpr int64_t kMost = INT64_C(1) << 40;  // elements of any tensor, and reach of any stride
+// A chunk's rows are addressed with 32-bit byte offsets: 64 rows of 2^24 fp32 elements.
+constexpr int64_t kMostStep = INT64_C(1) << 24;
 constexpr int64_t kChunk = 64, kBlockP = 64;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -75,25 +77,27 @@ ssm_status_t check_sizes(const AttnSizes &z, ssm_dtype_t dtype) {
     if (z.N > SSM_LINATTN_MAX_N || z.P > SSM_LINATTN_MAX_P) return SSM_ERR_UNSUPPORTED;
     int64_t bl = 0, bh = 0, n = 0;
     const int64_t L = z.L > 0 ? z.L : 1;
-    if (!mul_ok(z.b, L, &bl) || !mul_ok(z.b, z.H, &bh) || bl > kMost || bh > kMost || z.H > kMost) return SSM_ERR_SHAPE;
+    if (!mul_ok(z.b, L, &bl) || !mul_ok(z.b, z.H, &bh) || bl > kMost || bh > kMost) return SSM_ERR_SHAPE;
     // the padded widths bound every tensor, the states of all chunks and every grid (one workgroup per 64 value
     // columns of a chunk)
     const int64_t width = ceil_div(z.P, kBlockP) * kBlockP;
+    if (z.H > kMostStep / (width > 128 ? width : 128)) return SSM_ERR_SHAPE;
     if (!mul_ok(bl, z.H * (width > 128 ? width : 128), &n) || n > kMost) return SSM_ERR_SHAPE;
     if (!mul_ok(bh, ceil_div(L, kChunk) * (width / kBlockP) * 32, &n) || n >= (INT64_C(1) << 31)) return SSM_ERR_SHAPE;
     return SSM_OK;
 }
 
 // How the steps are cut into segments. One workgroup walks a segment's chunks in order. The forward call uses one
-// segment where rows, heads and value blocks alone give the device two workgroups per compute unit, and otherwise
-// as many as give it four, of at least four chunks each. The gradient's chunks run independently of each other.
+// segment where rows, heads and value columns alone give the device two wavefronts per SIMD (512 times four of them,
+// for 64 value columns each), and otherwise as many as give it four, of at least four chunks each. The gradient's
+// chunks run independently of each other.
 void plan(const AttnSizes &z, bool gradient, LinAttnLaunch *p) {
     const int64_t chunks = ceil_div(z.L, kChunk);
     p->seg_chunks = chunks;
     if (gradient) {
         p->seg_chunks = 1;
     } else {
-        const int64_t groups = z.b * z.H * ceil_div(z.P, kBlockP);
+        const int64_t groups = z.b * z.H * ceil_div(z.P, ssm::linattn_cols(z.P)) * (ssm::linattn_cols(z.P) / 64);
         if (groups < 512) {
             int64_t s = ceil_div(1024, groups);
             if (s > chunks / 4) s = chunks / 4;
@@ -135,6 +139,7 @@ bool set_strides(const AttnSizes &z, const ssm_linattn_strides_t *st, bool step,
         const int64_t count = i % 3 < 2 ? n[i % 3] : (i < 6 ? z.G : z.H);
         int64_t reach = 0;
         if (all[i] < 0 || !mul_ok(all[i], count, &reach) || reach > kMost) return false;
+        if (i % 3 == 1 && count > 1 && all[i] > kMostStep) return false;
         use[i] = count > 1 ? all[i] : 0;
     }
     p->q_b = use[0]; p->q_t = use[1]; p->q_h = use[2];
@@ -160,10 +165,11 @@ void set_common(const AttnSizes &z, ssm_dtype_t dtype, LinAttnLaunch *p) {
     p->H = (int)z.H; p->G = (int)z.G; p->N = (int)z.N; p->P = (int)z.P;
     p->bf16 = dtype == SSM_BF16;
     const int64_t es = p->bf16 ? 2 : 4;
-    p->vec_q = loads16(p->q, z.N, p->q_b, p->q_t, p->q_h, es);
-    p->vec_k = loads16(p->k, z.N, p->k_b, p->k_t, p->k_h, es);
-    p->vec_v = loads16(p->v, z.P, p->v_b, p->v_t, p->v_h, es);
-    p->vec_do = p->dout && loads16(p->dout, z.P, p->do_b, p->do_t, p->do_h, es);
+    const int64_t v = 16 / es;
+    p->vec = z.N % v == 0 && z.P % v == 0 && loads16(p->q, z.N, p->q_b, p->q_t, p->q_h, es) &&
+             loads16(p->k, z.N, p->k_b, p->k_t, p->k_h, es) && loads16(p->v, z.P, p->v_b, p->v_t, p->v_h, es) &&
+             (!p->dout || loads16(p->dout, z.P, p->do_b, p->do_t, p->do_h, es)) && aligned(p->o, 16) &&
+             aligned(p->dq, 16) && aligned(p->dk, 16) && aligned(p->dv, 16);
 }
 
 ssm_status_t fill_state(const float *src, float *dst, int64_t n, hipStream_t stream) {
@@ -230,7 +236,6 @@ ssm_status_t ssm_linattn_fwd(const void *q, const void *k, const void *v, const 
     p.scale = scale;
     p.initial_state = initial_state; p.lengths = lengths; p.o = o; p.final_state = final_state;
     set_common(z, dtype, &p);
-    p.vec_p = P % 4 == 0 && aligned(o, 4 * es);
     return scratch.done(ssm::launch_linattn_fwd(p, stream));
 }
 
@@ -299,9 +304,6 @@ ssm_status_t ssm_linattn_bwd(const void *q, const void *k, const void *v, const 
     p.initial_state = initial_state; p.d_final_state = d_final_state; p.lengths = lengths;
     p.dq = dq; p.dk = dk; p.dv = dv; p.dg = dg; p.d_initial_state = d_initial_state;
     set_common(z, dtype, &p);
-    p.vec_p = P % 4 == 0 && aligned(dv, 4 * es);
-    // a group's heads are summed from fp32 shares, whose rows are 16-byte aligned where N is a multiple of 4
-    p.vec_n = N % 4 == 0 && (G < H || (aligned(dq, 4 * es) && aligned(dk, 4 * es)));
     return scratch.done(ssm::launch_linattn_bwd(p, stream));
 }
 

@@ -242,9 +242,10 @@ struct LinAttnLaunch {
     double *gsum;          // [b·H][n_seg] sums of g
     float *dg_steps;       // [b][L][H] when g_per_step is false
     float *dq_part, *dk_part;  // [b][L][H][N] when G < H
-    bool vec_q, vec_k, vec_v, vec_do;      // 16-byte loads allowed
-    bool vec_n, vec_p;                     // 4-element stores allowed on rows of N, P
+    bool vec;              // every input and output row takes 16-byte accesses at multiples of 16 bytes
 };
+// Value columns per workgroup of the walks over chunks.
+inline int64_t linattn_cols(int64_t P) { return P > 64 ? 128 : 64; }
 inline int linattn_nt(int64_t N) { return N <= 32 ? 32 : N <= 64 ? 64 : 128; }
 hipError_t launch_linattn_fwd(const LinAttnLaunch &p, hipStream_t stream);
 hipError_t launch_linattn_bwd(const LinAttnLaunch &p, hipStream_t stream);

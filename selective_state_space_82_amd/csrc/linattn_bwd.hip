@@ -36,7 +36,7 @@ __device__ __forceinline__ float sum_cols(float v) {
 //
 // The four wavefronts share the lower-triangular tiles of both score matrices through LDS; then wavefront w takes
 // the value columns 16w .. of dv, and 16-column jobs of dq and dk.
-template <typename T, int NT>
+template <typename T, int NT, bool VEC>
 __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
     constexpr int SN = NT + kPad<T>, SP = kC + kPad<T>, SV = kPB + kPad<T>;
     constexpr int PARTS = sizeof(T) == 2 ? 2 : 1;
@@ -47,10 +47,8 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
     __shared__ __align__(16) T s_d[kC * SV];
     __shared__ __align__(16) T s_a1[PARTS][kC * SP];  // [t][s]
     __shared__ __align__(16) T s_a2[PARTS][kC * SP];
-    __shared__ Sums s_c;
-    __shared__ float s_in[kC], s_out[kC];
+    __shared__ Decays s_g;
     __shared__ float s_row[4][kC], s_col[4][kC], s_x[TILES][kC], s_y[4][kC], s_z[4];
-    __shared__ float s_end;
 
     int64_t id = work_index(blockIdx.x, gridDim.x);
     const int h = (int)(id % a.H);
@@ -87,6 +85,11 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
         return;
     }
 
+    const Buffer dv_buf = rows_buffer(dvp, (uint32_t)dv_t, (int)rows, a.P);
+    const Buffer dq_buf = part ? rows_buffer(a.dq_part + n_off, (uint32_t)n_t, (int)rows, a.N)
+                               : rows_buffer(static_cast<T *>(a.dq) + n_off, (uint32_t)n_t, (int)rows, a.N);
+    const Buffer dk_buf = part ? rows_buffer(a.dk_part + n_off, (uint32_t)n_t, (int)rows, a.N)
+                               : rows_buffer(static_cast<T *>(a.dk) + n_off, (uint32_t)n_t, (int)rows, a.N);
     const int64_t g_stride = a.g_per_step ? a.H : 0;
     const float *gp = a.g_per_step ? a.g + ib * a.L * a.H + h : a.g + h;
     const T *qp = static_cast<const T *>(a.q) + ib * a.q_b + grp * a.q_h;
@@ -94,15 +97,13 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
     const T *vp = static_cast<const T *>(a.v) + ib * a.v_b + h * a.v_h;
     const T *dp = static_cast<const T *>(a.dout) + ib * a.do_b + h * a.do_h;
 
-    stage<T, NT>(s_q, qp, a.q_t, t0, len, 0, a.N, a.vec_q);
-    stage<T, NT>(s_k, kp, a.k_t, t0, len, 0, a.N, a.vec_k);
-    if (w == 0) {
-        const double c = wave_running_sum(log_decay(gp, g_stride, t0 + l, len));
-        const double end = __shfl(c, 63);
-        s_c.set(l, c);
-        s_in[l] = a.scale * exp_of((float)c);
-        s_out[l] = exp_of((float)(end - c));
-        if (l == 63) s_end = exp_of((float)c);
+    {
+        Stage<T, NT, kThreads, VEC> q, k;
+        q.load(qp + t0 * a.q_t, (uint32_t)a.q_t, rows_of(t0, len), 0, a.N);
+        k.load(kp + t0 * a.k_t, (uint32_t)a.k_t, rows_of(t0, len), 0, a.N);
+        if (w == 0) s_g.set(log_decay(load_g(gp + t0 * g_stride, (uint32_t)g_stride, rows_of(t0, len))), a.scale);
+        q.store(s_q);
+        k.store(s_k);
     }
     // the tiles right of the diagonal that a 32-step contraction touches
     for (int i = tid; i < 2 * 16 * 16; i += kThreads) {
@@ -119,10 +120,13 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
 #pragma unroll
     for (int j = 0; j < 3; ++j) aq[j] = ad[j] = f4{0, 0, 0, 0};
     for (int pb = 0; pb < npb; ++pb) {
-        if (pb) __syncthreads();
-        stage<T, kPB>(s_v, vp, a.v_t, t0, len, pb * kPB, a.P, a.vec_v);
-        stage<T, kPB>(s_d, dp, a.do_t, t0, len, pb * kPB, a.P, a.vec_do);
-        __syncthreads();
+        if (pb) lds_barrier();
+        Stage<T, kPB, kThreads, VEC> v, d;
+        v.load(vp + t0 * a.v_t, (uint32_t)a.v_t, rows_of(t0, len), pb * kPB, a.P);
+        d.load(dp + t0 * a.do_t, (uint32_t)a.do_t, rows_of(t0, len), pb * kPB, a.P);
+        v.store(s_v);
+        d.store(s_d);
+        lds_barrier();
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
             const int i = w + 4 * j;
@@ -142,12 +146,12 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
         if (i < 10) {
             const int tb = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3, sb = i - tb * (tb + 1) / 2;
             const int t = 16 * tb + col, s = 16 * sb + g4;
-            const float th = s_c.hi[t], tl = s_c.lo[t];
+            const float th = s_g.c.hi[t], tl = s_g.c.lo[t];
             f4 a1, a2;
             float row = 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float d = a.scale * exp_of((th - s_c.hi[s + r]) + (tl - s_c.lo[s + r]));
+                const float d = a.scale * exp2_fast((th - s_g.c.hi[s + r]) + (tl - s_g.c.lo[s + r]));
                 a1[r] = s + r <= t ? aq[j][r] * d : 0.0f;
                 a2[r] = s + r <= t ? ad[j][r] * d : 0.0f;
                 const float wv = s + r < t ? a1[r] * ad[j][r] : 0.0f;
@@ -183,11 +187,14 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
         for (int b = 0; b < 4; ++b) acc[j][b] = f4{0, 0, 0, 0};
     float y[4] = {0, 0, 0, 0}, z = 0.0f;
     for (int pb = 0; pb < npb; ++pb) {
-        __syncthreads();
+        lds_barrier();
         if (npb > 1) {
-            stage<T, kPB>(s_v, vp, a.v_t, t0, len, pb * kPB, a.P, a.vec_v);
-            stage<T, kPB>(s_d, dp, a.do_t, t0, len, pb * kPB, a.P, a.vec_do);
-            __syncthreads();
+            Stage<T, kPB, kThreads, VEC> v, d;
+            v.load(vp + t0 * a.v_t, (uint32_t)a.v_t, rows_of(t0, len), pb * kPB, a.P);
+            d.load(dp + t0 * a.do_t, (uint32_t)a.do_t, rows_of(t0, len), pb * kPB, a.P);
+            v.store(s_v);
+            d.store(s_d);
+            lds_barrier();
         }
         // dv: value columns 16w ..
         {
@@ -212,7 +219,7 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const int s = 16 * b + col;
-                dv[b] *= s_out[s];
+                dv[b] *= s_g.out[s];
                 const T *vr = &s_v[s * SV + 16 * w + g4];
                 y[b] += (dv[b][0] * widen(vr[0]) + dv[b][1] * widen(vr[1])) + (dv[b][2] * widen(vr[2]) + dv[b][3] * widen(vr[3]));
 #pragma unroll
@@ -220,10 +227,8 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
                     if (b < 2) mma(dv[b], d0, col_frag(s_a1[part_i], SP, 0, 16 * b));
                     mma(dv[b], d1, col_frag(s_a1[part_i], SP, 32, 16 * b));
                 }
-                if (s < rows) {
-                    if (t0 + s >= len) dv[b] = f4{0, 0, 0, 0};
-                    store4<T>(dvp + s * dv_t, pb * kPB + 16 * w + g4, a.P, a.vec_p, dv[b]);
-                }
+                if (t0 + s >= len) dv[b] = f4{0, 0, 0, 0};
+                store4<T, VEC>(dv_buf, (uint32_t)dv_t, s, pb * kPB + 16 * w + g4, a.P, dv[b]);
             }
         }
         // dq, dk: the parts through the entering state and the leaving adjoint
@@ -259,7 +264,7 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
         for (int b = 0; b < 4; ++b) {
             const int t = 16 * b + col;
             f4 &v = acc[j][b];
-            v *= is_q ? s_in[t] : s_out[t];
+            v *= is_q ? s_g.in[t] : s_g.out[t];
             if (is_q) {
                 const T *qr = &s_q[t * SN + n0 + g4];
                 const float x = sum_groups((v[0] * widen(qr[0]) + v[1] * widen(qr[1])) + (v[2] * widen(qr[2]) + v[3] * widen(qr[3])));
@@ -276,11 +281,10 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
                     mma(v, f1, col_frag(s_a2[e], SP, 32, 16 * b));
                 }
             }
-            if (t < rows) {
-                if (t0 + t >= len) v = f4{0, 0, 0, 0};
-                if (part) store4<float>((is_q ? a.dq_part : a.dk_part) + n_off + t * n_t, n0 + g4, a.N, a.vec_n, v);
-                else store4<T>(static_cast<T *>(is_q ? a.dq : a.dk) + n_off + t * n_t, n0 + g4, a.N, a.vec_n, v);
-            }
+            if (t0 + t >= len) v = f4{0, 0, 0, 0};
+            const Buffer &buf = is_q ? dq_buf : dk_buf;
+            if (part) store4<float, VEC>(buf, (uint32_t)n_t, t, n0 + g4, a.N, v);
+            else store4<T, VEC>(buf, (uint32_t)n_t, t, n0 + g4, a.N, v);
         }
     }
 #pragma unroll
@@ -290,7 +294,7 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
     }
     z = sum_groups(sum_cols(z));
     if (l == 0) s_z[w] = z;
-    __syncthreads();
+    lds_barrier();
     if (w == 0) {
         const int b = l >> 4;
         double after = 0.0;
@@ -300,7 +304,7 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
         for (int i = 0; i < TILES; ++i) after += s_x[i][l];
         const double ys = ((double)s_y[0][l] + s_y[1][l]) + ((double)s_y[2][l] + s_y[3][l]);
         const double upto = wave_running_sum(after), yto = wave_running_sum(ys);
-        const double zs = (((double)s_z[0] + s_z[1]) + ((double)s_z[2] + s_z[3])) * s_end;
+        const double zs = (((double)s_z[0] + s_z[1]) + ((double)s_z[2] + s_z[3])) * s_g.end;
         const double v = (__shfl(upto, 63) - upto + after) + (yto - ys) + zs;
         if (l < rows) dgp[(int64_t)l * a.H] = t0 + l < len ? (float)v : 0.0f;
     }
@@ -339,9 +343,15 @@ template <typename T>
 hipError_t grads(const LinAttnLaunch &p, hipStream_t stream) {
     const int nt = linattn_nt(p.N);
     const dim3 grid((unsigned)(p.b * p.H * p.n_seg));
-    if (nt == 32) la_grad_kernel<T, 32><<<grid, kThreads, 0, stream>>>(p);
-    else if (nt == 64) la_grad_kernel<T, 64><<<grid, kThreads, 0, stream>>>(p);
-    else la_grad_kernel<T, 128><<<grid, kThreads, 0, stream>>>(p);
+    if (p.vec) {
+        if (nt == 32) la_grad_kernel<T, 32, true><<<grid, kThreads, 0, stream>>>(p);
+        else if (nt == 64) la_grad_kernel<T, 64, true><<<grid, kThreads, 0, stream>>>(p);
+        else la_grad_kernel<T, 128, true><<<grid, kThreads, 0, stream>>>(p);
+    } else {
+        if (nt == 32) la_grad_kernel<T, 32, false><<<grid, kThreads, 0, stream>>>(p);
+        else if (nt == 64) la_grad_kernel<T, 64, false><<<grid, kThreads, 0, stream>>>(p);
+        else la_grad_kernel<T, 128, false><<<grid, kThreads, 0, stream>>>(p);
+    }
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.G < p.H) {
         const int64_t n = p.b * p.L * p.G * p.N, blocks = (n + kThreads - 1) / kThreads;

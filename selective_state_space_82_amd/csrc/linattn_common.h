@@ -18,7 +18,7 @@ namespace ssm {
 namespace la {
 
 constexpr int kC = 64;        // steps per chunk
-constexpr int kPB = 64;       // value columns per workgroup (16 per wavefront)
+constexpr int kPB = 64;       // value columns per four wavefronts (16 each); P is padded to it in scratch
 constexpr int kThreads = 256; // four wavefronts
 // Log-decays below this count as this: e^-1e4 is 0 in fp32, and so is every product with it, while running sums
 // stay finite (−inf would turn differences of sums into NaN).
@@ -42,6 +42,13 @@ __device__ __forceinline__ void mma(f4 &acc, const bf8 &a, const bf8 &b) {
 __device__ __forceinline__ void mma(f4 &acc, const f8 &a, const f8 &b) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], acc, 0, 0, 0);
+}
+
+// Workgroup barrier that orders LDS only: the next chunk's loads and the outputs' stores stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Operand fragment of tile row `row0 + col`, contraction values n0 .. n0+31 along the row.
@@ -117,76 +124,149 @@ __device__ __forceinline__ void mma(f4 &acc, const f8 &a, const Whole &b) { mma(
 // e^v for a difference of running sums.
 __device__ __forceinline__ float exp_of(float v) { return exp2_fast(kLog2e * v); }
 
-// Inclusive running sum over the 64 lanes of a wavefront, fp64.
+// Inclusive running sum over the 64 lanes of a wavefront, fp64: data-parallel moves inside each row of 16 lanes (lanes
+// shifted in from outside add 0), then the totals of the rows before.
+template <int CTRL> __device__ __forceinline__ double row_shift(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ double wave_running_sum(double v) {
-    const int l = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double u = __shfl_up(v, d);
-        if (l >= d) v += u;
-    }
-    return v;
+    v += row_shift<0x111>(v);
+    v += row_shift<0x112>(v);
+    v += row_shift<0x114>(v);
+    v += row_shift<0x118>(v);
+    const double r0 = lane_value(v, 15), r1 = lane_value(v, 31), r2 = lane_value(v, 47);
+    const int row = (threadIdx.x & 63) >> 4;
+    return v + (row == 0 ? 0.0 : row == 1 ? r0 : row == 2 ? r0 + r1 : (r0 + r1) + r2);
 }
 
-// The lane's clamped log-decay of step t (0 past `len`).
-__device__ __forceinline__ double log_decay(const float *g, int64_t stride, int64_t t, int64_t len) {
-    if (t >= len) return 0.0;
-    const float v = g[t * stride];
-    return v < kMinG ? (double)kMinG : (double)v;
-}
+// The clamped log-decay.
+__device__ __forceinline__ double log_decay(float v) { return v < kMinG ? (double)kMinG : (double)v; }
 
-// Running sums of g in a chunk as fp32 hi + lo, so that their differences keep fp32's accuracy however large the
-// sums are.
+// Running sums of g in a chunk, in units of log 2, as fp32 hi + lo, so that their differences keep fp32's accuracy
+// however large the sums are; decay(t, s) = e^{c_t − c_s}.
 struct Sums {
     float hi[kC], lo[kC];
     __device__ __forceinline__ void set(int t, double c) {
-        hi[t] = (float)c;
-        lo[t] = (float)(c - (double)hi[t]);
+        const double e = c * 1.4426950408889634074;
+        const float h = (float)e;
+        hi[t] = h;
+        lo[t] = (float)(e - (double)h);
     }
 };
 
-// Rows [t0, t0 + 64) × columns [c0, c0 + W) of a strided array into an LDS tile, zeros past `len` rows and `cols`
-// columns; `vec` says that 16-byte accesses at multiples of kVec elements are allowed and that cols − c0 ends on one.
-template <typename T, int W>
-__device__ __forceinline__ void stage(T *tile, const T *src, int64_t stride, int64_t t0, int64_t len, int c0, int cols,
-                                      bool vec) {
-    constexpr int V = kVec<T>, PER = W / V, S = W + kPad<T>;
+// What a chunk's decays are needed for: pairs of steps, from the chunk's start (times a factor), to its end, across.
+struct Decays {
+    Sums c;
+    __attribute__((aligned(16))) float in[kC], out[kC];
+    float end;
+    // By one wavefront, lane t for step t; returns the chunk's sum.
+    __device__ __forceinline__ double set(double g, float factor) {
+        const int l = threadIdx.x & 63;
+        const double sum = wave_running_sum(g), total = lane_value(sum, 63);
+        c.set(l, sum);
+        in[l] = factor * exp_of((float)sum);
+        out[l] = exp_of((float)(total - sum));
+        if (l == 63) end = exp_of((float)total);
+        return total;
+    }
+};
+
+// A buffer descriptor of `bytes` from `first` on (the same in every lane): loads outside give 0, stores outside are
+// dropped, so a chunk's edge needs no branch (which would make every load wait for the one before).
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer buffer_of(const void *first, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(first), 0, (int)bytes, 0x00027000);
+}
+constexpr uint32_t kOutside = 0xfffffff0u;  // past every buffer: 64 rows of 2^24 fp32 elements end below it
+
+// `rows` rows (0 .. 64) of `cols` elements, `stride` elements apart.
+template <typename T> __device__ __forceinline__ Buffer rows_buffer(const T *first, uint32_t stride, int rows, int cols) {
+    return buffer_of(first, rows > 0 ? (uint32_t)((rows - 1) * stride + cols) * (uint32_t)sizeof(T) : 0u);
+}
+
+// The log-decay of the lane's step in a chunk of `rows` rows (0 past them), not yet clamped; first: that of row 0.
+__device__ __forceinline__ float load_g(const float *first, uint32_t stride, int rows) {
+    const int l = threadIdx.x & 63;
+    const Buffer buf = rows_buffer(first, stride, rows, 1);
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buf, l < rows ? l * stride * 4u : kOutside, 0, 0));
+}
+
+// Rows of a chunk × columns [c0, c0 + W) of a strided array on their way into an LDS tile, zeros past the rows and
+// columns there are. VEC: 16-byte accesses at multiples of kVec elements are allowed and `cols` is one of them;
+// otherwise element by element. A thread holds its pieces between load and store, so that a chunk is fetched
+// while the one before is computed.
+template <typename T, int W, int THREADS, bool VEC> struct Stage {
+    static constexpr int V = kVec<T>, PER = W / V, S = W + kPad<T>, PIECES = kC * PER,
+                         N = (PIECES + THREADS - 1) / THREADS;
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    u4 w[N];
+    // first: row 0 of the chunk, column 0, the same in every lane
+    __device__ __forceinline__ void load(const T *first, uint32_t stride, int rows, int c0, int cols) {
+        const Buffer buf = rows_buffer(first, stride, rows, cols);
 #pragma unroll
-    for (int i = threadIdx.x; i < kC * PER; i += kThreads) {
-        const int r = i / PER, c = (i % PER) * V;
-        const int64_t t = t0 + r;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (t < len) {
-            const T *p = src + t * stride + c0 + c;
-            if (vec) {
-                if (c0 + c < cols) w = *reinterpret_cast<const uint4 *>(p);
+        for (int j = 0; j < N; ++j) {
+            const int i = threadIdx.x + j * THREADS, r = i / PER, c = c0 + (i % PER) * V;
+            const uint32_t at = (r * stride + c) * (uint32_t)sizeof(T);
+            // by row as well: a distance of 0 between steps never leaves the buffer
+            const bool mine = r < rows && (PIECES % THREADS == 0 || i < PIECES);
+            if constexpr (VEC) {
+                w[j] = __builtin_amdgcn_raw_buffer_load_b128(buf, mine && c < cols ? at : kOutside, 0, 0);
             } else {
                 T e[V];
 #pragma unroll
-                for (int j = 0; j < V; ++j) e[j] = c0 + c + j < cols ? p[j] : (T)0;
-                __builtin_memcpy(&w, e, sizeof(w));
+                for (int k = 0; k < V; ++k) {
+                    const uint32_t off = mine && c + k < cols ? at + k * (uint32_t)sizeof(T) : kOutside;
+                    if constexpr (sizeof(T) == 2) e[k] = (T)__builtin_amdgcn_raw_buffer_load_b16(buf, off, 0, 0);
+                    else e[k] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(buf, off, 0, 0));
+                }
+                __builtin_memcpy(&w[j], e, sizeof(w[j]));
             }
         }
-        *reinterpret_cast<uint4 *>(tile + r * S + c) = w;
+    }
+    __device__ __forceinline__ void store(T *tile) const {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int i = threadIdx.x + j * THREADS;
+            if (PIECES % THREADS == 0 || i < PIECES) *reinterpret_cast<u4 *>(tile + i / PER * S + (i % PER) * V) = w[j];
+        }
+    }
+};
+
+// Four consecutive results (row r, columns c .. c+3) of dense rows in `buf` (rows_buffer), `stride` elements apart.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store4(const Buffer &buf, uint32_t stride, int r, int c, int cols, const f4 &v) {
+    const uint32_t at = (r * stride + c) * (uint32_t)sizeof(T);
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    if constexpr (VEC) {
+        const uint32_t off = c < cols ? at : kOutside;
+        if constexpr (sizeof(T) == 2)
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, __builtin_convertvector(v, bf4)), buf, off, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), buf, off, 0, 0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t off = c + j < cols ? at + j * (uint32_t)sizeof(T) : kOutside;
+            if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(narrow<T>(v[j]), buf, off, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[j]), buf, off, 0, 0);
+        }
     }
 }
 
-// Four consecutive results row[c .. c+3] of a dense row of `cols`.
-template <typename T>
-__device__ __forceinline__ void store4(T *row, int c, int cols, bool vec, const f4 &v) {
-    if (vec) {
-        if (c < cols) {
-            if constexpr (sizeof(T) == 2) {
-                *reinterpret_cast<bf4 *>(row + c) = __builtin_convertvector(v, bf4);
-            } else {
-                *reinterpret_cast<f4 *>(row + c) = v;
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (c + j < cols) row[c + j] = narrow<T>(v[j]);
+// Rows of a chunk that starts at step t0, of a row of `len` steps.
+__device__ __forceinline__ int rows_of(int64_t t0, int64_t len) {
+    const int64_t n = len - t0;
+    return n > kC ? kC : n < 0 ? 0 : (int)n;
 }
 
 // Steps of batch row i.

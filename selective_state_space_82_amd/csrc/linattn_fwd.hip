@@ -13,13 +13,13 @@ namespace {
 
 struct Work {
     int64_t ib, seg, bh;
-    int h, grp, pb;
+    int h, grp, p0;  // p0: first value column
 };
-__device__ __forceinline__ Work work_of(const LinAttnLaunch &a, int64_t n_seg) {
+template <int NW> __device__ __forceinline__ Work work_of(const LinAttnLaunch &a, int64_t n_seg) {
     int64_t id = work_index(blockIdx.x, gridDim.x);
-    const int npb = (a.P + kPB - 1) / kPB;
+    const int npb = (a.P + 16 * NW - 1) / (16 * NW);
     Work w;
-    w.pb = (int)(id % npb);
+    w.p0 = 16 * NW * (int)(id % npb);
     id /= npb;
     w.h = (int)(id % a.H);
     id /= a.H;
@@ -48,25 +48,25 @@ __device__ __forceinline__ void load_state(f4 (&S)[NT / 16], const float *src, i
         }
 }
 
-// ---- outputs: one workgroup walks the chunks of (row, head, 64 value columns, segment) in order ----------------
+// ---- outputs: one workgroup walks the chunks of (row, head, 16·NW value columns, segment) in order ---------------
 //
-// Wavefront w keeps the state's value columns 16w .. 16w+15 (all N of them) in its result tiles. Per chunk the four
-// share the 10 lower-triangular 16×16 tiles of the decayed scores through LDS; the rest (outputs of its own
+// Wavefront w keeps the state's value columns 16w .. 16w+15 (all N of them) in its result tiles. Per chunk the NW of
+// them share the 10 lower-triangular 16×16 tiles of the decayed scores through LDS; the rest (outputs of its own
 // columns, the state's update) each wavefront does from its own state and its own columns of V, which are scaled
-// and cut into bf16 parts once and used for every tile of N.
-template <typename T, int NT>
-__global__ __launch_bounds__(kThreads) void la_out_kernel(LinAttnLaunch a) {
-    constexpr int SN = NT + kPad<T>, SP = kC + kPad<T>, SV = kPB + kPad<T>;
+// and cut into bf16 parts once and used for every tile of N. The next chunk's rows are fetched into registers, and its
+// decays formed by the last wavefront (which has the fewest tiles), while this one is computed.
+template <typename T, int NT, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void la_out_kernel(LinAttnLaunch a) {
+    constexpr int THREADS = 64 * NW, PB = 16 * NW;
+    constexpr int SN = NT + kPad<T>, SP = kC + kPad<T>, SV = PB + kPad<T>;
     constexpr int PARTS = sizeof(T) == 2 ? 2 : 1;
     __shared__ __align__(16) T s_q[kC * SN];
     __shared__ __align__(16) T s_k[kC * SN];
     __shared__ __align__(16) T s_v[kC * SV];
     __shared__ __align__(16) T s_p[PARTS][kC * SP];  // decayed scores [t][s]
-    __shared__ Sums s_c;
-    __shared__ __align__(16) float s_in[kC], s_out[kC];  // scale·e^{c_t}, e^{c_end − c_s}
-    __shared__ float s_end;
+    __shared__ Decays s_g[2];
 
-    const Work wk = work_of(a, a.n_seg);
+    const Work wk = work_of<NW>(a, a.n_seg);
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, col = l & 15, g4 = 4 * (l >> 4);
     const int64_t len = row_length(a.lengths, wk.ib, a.L);
     int64_t g_stride;
@@ -75,17 +75,16 @@ __global__ __launch_bounds__(kThreads) void la_out_kernel(LinAttnLaunch a) {
     const T *kp = static_cast<const T *>(a.k) + wk.ib * a.k_b + wk.grp * a.k_h;
     const T *vp = static_cast<const T *>(a.v) + wk.ib * a.v_b + wk.h * a.v_h;
     T *op = static_cast<T *>(a.o) + (wk.ib * a.L * a.H + wk.h) * a.P;
-    const int64_t o_t = (int64_t)a.H * a.P;
-    const int p0 = kPB * wk.pb;
+    const uint32_t o_t = (uint32_t)a.H * a.P;  // elements between steps of o
+    const int p0 = wk.p0, p_wave = p0 + 16 * w;
 
     f4 S[NT / 16];
-    const int64_t p_lane = p0 + 16 * w + col;
-    if (a.n_seg > 1) {
-        const int64_t Pp = (a.P + kPB - 1) / kPB * kPB;
+    const int64_t p_lane = p_wave + col, Pp = (a.P + kPB - 1) / kPB * kPB;
+    if (a.n_seg > 1 && p_lane < Pp) {
         const float *src = a.S + ((wk.bh * a.n_seg + wk.seg) * Pp + p_lane) * NT + g4;
 #pragma unroll
         for (int i = 0; i < NT / 16; ++i) S[i] = *reinterpret_cast<const f4 *>(src + 16 * i);
-    } else if (a.initial_state) {
+    } else if (a.n_seg == 1 && a.initial_state) {
         load_state<NT>(S, a.initial_state + wk.bh * a.P * a.N, p_lane, a.P, a.N);
     } else {
 #pragma unroll
@@ -93,50 +92,58 @@ __global__ __launch_bounds__(kThreads) void la_out_kernel(LinAttnLaunch a) {
     }
 
     // the tiles right of the diagonal that a 32-step contraction touches stay zero
-    for (int i = tid; i < 2 * 16 * 16; i += kThreads) {
+    for (int i = tid; i < 2 * 16 * 16; i += THREADS) {
         const int t = 32 * (i >> 8) + ((i >> 4) & 15), s = 32 * (i >> 8) + 16 + (i & 15);
 #pragma unroll
         for (int e = 0; e < PARTS; ++e) s_p[e][t * SP + s] = (T)0;
     }
 
-    const int64_t n_chunks = (a.L + kC - 1) / kC;
+    const int64_t n_chunks = (a.L + kC - 1) / kC, live = (len + kC - 1) / kC;
     const int64_t ch0 = wk.seg * a.seg_chunks, ch1 = ch0 + a.seg_chunks < n_chunks ? ch0 + a.seg_chunks : n_chunks;
-    for (int64_t ch = ch0; ch < ch1; ++ch) {
+    const int64_t chl = ch1 < live ? ch1 : live;  // chunks with any step of the row
+    Stage<T, NT, THREADS, VEC> rq, rk;
+    Stage<T, PB, THREADS, VEC> rv;
+    float g_next = 0.0f;
+    auto fetch = [&](int64_t t0) {
+        const int rows = rows_of(t0, len);
+        rq.load(qp + t0 * a.q_t, (uint32_t)a.q_t, rows, 0, a.N);
+        rk.load(kp + t0 * a.k_t, (uint32_t)a.k_t, rows, 0, a.N);
+        rv.load(vp + t0 * a.v_t, (uint32_t)a.v_t, rows, p0, a.P);
+    };
+    auto fetch_g = [&](int64_t t0) { return load_g(gp + t0 * g_stride, (uint32_t)g_stride, rows_of(t0, len)); };
+    if (ch0 < chl) {
+        if (VEC) fetch(ch0 * kC);
+        if (w == NW - 1) {
+            s_g[0].set(log_decay(fetch_g(ch0 * kC)), a.scale);
+            g_next = fetch_g((ch0 + 1) * kC);
+        }
+    }
+    for (int64_t ch = ch0; ch < chl; ++ch) {
         const int64_t t0 = ch * kC;
-        if (t0 >= len) {  // past the row's end: outputs are zero, the state stays
-#pragma unroll
-            for (int tb = 0; tb < 4; ++tb) {
-                const int64_t t = t0 + 16 * tb + col;
-                if (t < a.L) store4<T>(op + t * o_t, p0 + 16 * w + g4, a.P, a.vec_p, f4{0, 0, 0, 0});
-            }
-            continue;
-        }
-        stage<T, NT>(s_q, qp, a.q_t, t0, len, 0, a.N, a.vec_q);
-        stage<T, NT>(s_k, kp, a.k_t, t0, len, 0, a.N, a.vec_k);
-        stage<T, kPB>(s_v, vp, a.v_t, t0, len, p0, a.P, a.vec_v);
-        if (w == 0) {
-            const double c = wave_running_sum(log_decay(gp, g_stride, t0 + l, len));
-            const double end = __shfl(c, 63);
-            s_c.set(l, c);
-            s_in[l] = a.scale * exp_of((float)c);
-            s_out[l] = exp_of((float)(end - c));
-            if (l == 63) s_end = exp_of((float)c);
-        }
-        __syncthreads();
+        const Decays &dec = s_g[(ch - ch0) & 1];
+        const int all = rows_of(t0, a.L), some = rows_of(t0, len);
+        const Buffer out = rows_buffer(op + t0 * o_t, o_t, all, a.P);
+        if (!VEC) fetch(t0);
+        rq.store(s_q);
+        rk.store(s_k);
+        rv.store(s_v);
+        lds_barrier();
+        if (VEC) fetch(t0 + kC);  // past the last chunk: nothing
 
         // decayed scores, tile (tb, sb): D[s][t] = k_s·q_t
-        for (int i = w; i < 10; i += 4) {
+        for (int i = w; i < 10; i += NW) {
             const int tb = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3;
             const int sb = i - tb * (tb + 1) / 2;
             f4 acc = {0, 0, 0, 0};
 #pragma unroll
             for (int n = 0; n < NT; n += 32) mma(acc, row_frag(s_k, SN, 16 * sb, n), row_frag(s_q, SN, 16 * tb, n));
             const int t = 16 * tb + col, s = 16 * sb + g4;
-            const float th = s_c.hi[t], tl = s_c.lo[t];
+            const float th = dec.c.hi[t], tl = dec.c.lo[t];
+            const f4 sh = *reinterpret_cast<const f4 *>(&dec.c.hi[s]), sl = *reinterpret_cast<const f4 *>(&dec.c.lo[s]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float d = (th - s_c.hi[s + r]) + (tl - s_c.lo[s + r]);
-                acc[r] = s + r <= t ? acc[r] * (a.scale * exp_of(d)) : 0.0f;
+                const float d = a.scale * exp2_fast((th - sh[r]) + (tl - sl[r]));
+                acc[r] = s + r <= t ? acc[r] * d : 0.0f;
             }
             if constexpr (sizeof(T) == 2) {
 #pragma unroll
@@ -149,7 +156,11 @@ __global__ __launch_bounds__(kThreads) void la_out_kernel(LinAttnLaunch a) {
                 *reinterpret_cast<f4 *>(&s_p[0][t * SP + s]) = acc;
             }
         }
-        __syncthreads();
+        if (w == NW - 1) {
+            s_g[(ch + 1 - ch0) & 1].set(log_decay(g_next), a.scale);
+            g_next = fetch_g(t0 + 2 * kC);
+        }
+        lds_barrier();
 
         Frag<T> vf[2];
         f8 vw[2];
@@ -175,7 +186,7 @@ __global__ __launch_bounds__(kThreads) void la_out_kernel(LinAttnLaunch a) {
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
             const int tl = 16 * tb + col;
-            acc[tb] *= s_in[tl];
+            acc[tb] *= dec.in[tl];
             if (finite) {
 #pragma unroll
                 for (int sp = 0; sp <= tb / 2; ++sp)
@@ -191,26 +202,30 @@ __global__ __launch_bounds__(kThreads) void la_out_kernel(LinAttnLaunch a) {
                         acc[tb][r] = __builtin_fmaf(pr, widen(s_v[s * SV + 16 * w + g4 + r]), acc[tb][r]);
                 }
             }
-            const int64_t t = t0 + tl;
-            if (t < a.L) {
-                if (t >= len) acc[tb] = f4{0, 0, 0, 0};
-                store4<T>(op + t * o_t, p0 + 16 * w + g4, a.P, a.vec_p, acc[tb]);
-            }
+            if (tl >= some) acc[tb] = f4{0, 0, 0, 0};
+            store4<T, VEC>(out, o_t, tl, p_wave + g4, a.P, acc[tb]);
         }
 
         // the state's update: V's columns scaled, three parts (the state is an fp32 result)
-        const float end = s_end;
+        const float end = dec.end;
 #pragma unroll
         for (int i = 0; i < NT / 16; ++i) S[i] *= end;
 #pragma unroll
         for (int sp = 0; sp < 2; ++sp) {
-            const f4 u = *reinterpret_cast<const f4 *>(&s_out[32 * sp + g4]);
-            const f4 v = *reinterpret_cast<const f4 *>(&s_out[32 * sp + 16 + g4]);
+            const f4 u = *reinterpret_cast<const f4 *>(&dec.out[32 * sp + g4]);
+            const f4 v = *reinterpret_cast<const f4 *>(&dec.out[32 * sp + 16 + g4]);
             const Split<T, 3> vs(vw[sp] * join(u, v));
 #pragma unroll
             for (int i = 0; i < NT / 16; ++i) mma(S[i], col_frag(s_k, SN, 32 * sp, 16 * i), vs);
         }
-        __syncthreads();
+        lds_barrier();
+    }
+
+    // past the row's end: outputs are zero, the state stays
+    for (int64_t ch = chl > ch0 ? chl : ch0; ch < ch1; ++ch) {
+        const Buffer out = rows_buffer(op + ch * kC * o_t, o_t, rows_of(ch * kC, a.L), a.P);
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) store4<T, VEC>(out, o_t, 16 * tb + col, p_wave + g4, a.P, f4{0, 0, 0, 0});
     }
 
     if (a.final_state && wk.seg == a.n_seg - 1 && p_lane < a.P) {
@@ -225,18 +240,21 @@ __global__ __launch_bounds__(kThreads) void la_out_kernel(LinAttnLaunch a) {
 
 // ---- a segment's own state, or its own adjoint -------------------------------------------------------------------
 //
-// Forward: S = Σ_s e^{c_end − c_s} v_s k_sᵀ over the segment. Adjoint (REV, chunks in reverse order): the gradient
-// reaching the state that enters the segment from its own outputs, E = Σ_u scale·e^{c_u} do_u q_uᵀ. Workgroup (row,
-// head, 64 value columns, segment) as above.
-template <typename T, int NT, bool REV>
-__global__ __launch_bounds__(kThreads) void la_states_kernel(LinAttnLaunch a, int64_t first_seg, int64_t n_own) {
-    constexpr int SN = NT + kPad<T>, SV = kPB + kPad<T>;
+// Forward: S = Σ_s e^{c_end − c_s} v_s k_sᵀ over the segment. Adjoint (REV): the gradient reaching the state that
+// enters the segment from its own outputs, E = Σ_u scale·e^{c_u} do_u q_uᵀ. Workgroup (row, head, 16·NW value columns,
+// segment) as above. Both walk the chunks from the far end of the decay to the near one, S from the last chunk back
+// and E from the first on, so that each chunk's weights carry the decay of all chunks walked before it. The walk ends
+// where that decay is below e^-200: what the rest would add is it times a state (adjoint) of the recurrence, which as
+// an fp32 number is at most e^88.8, and the product is 0 in fp32 (smallest positive value e^-103.3).
+template <typename T, int NT, int NW, bool VEC, bool REV>
+__global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int64_t first_seg, int64_t n_own) {
+    constexpr int THREADS = 64 * NW, PB = 16 * NW;
+    constexpr int SN = NT + kPad<T>, SV = PB + kPad<T>;
     __shared__ __align__(16) T s_k[kC * SN];
     __shared__ __align__(16) T s_v[kC * SV];
-    __shared__ __align__(16) float s_w[kC];
-    __shared__ float s_end;
+    __shared__ Decays s_g;
 
-    Work wk = work_of(a, n_own);
+    Work wk = work_of<NW>(a, n_own);
     wk.seg += first_seg;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, col = l & 15, g4 = 4 * (l >> 4);
     const int64_t len = row_length(a.lengths, wk.ib, a.L);
@@ -247,48 +265,61 @@ __global__ __launch_bounds__(kThreads) void la_states_kernel(LinAttnLaunch a, in
                       : static_cast<const T *>(a.k) + wk.ib * a.k_b + wk.grp * a.k_h;
     const T *vp = REV ? static_cast<const T *>(a.dout) + wk.ib * a.do_b + wk.h * a.do_h
                       : static_cast<const T *>(a.v) + wk.ib * a.v_b + wk.h * a.v_h;
-    const bool vec_k = REV ? a.vec_q : a.vec_k, vec_v = REV ? a.vec_do : a.vec_v;
-    const int p0 = kPB * wk.pb;
+    const int p0 = wk.p0;
 
     f4 S[NT / 16];
 #pragma unroll
     for (int i = 0; i < NT / 16; ++i) S[i] = f4{0, 0, 0, 0};
-    const int64_t n_chunks = (a.L + kC - 1) / kC;
-    const int64_t ch0 = wk.seg * a.seg_chunks;
-    const int64_t ch1 = ch0 + a.seg_chunks < n_chunks ? ch0 + a.seg_chunks : n_chunks;
-    double total = 0.0;
-    for (int64_t j = ch0; j < ch1; ++j) {
-        const int64_t ch = REV ? ch1 - 1 - (j - ch0) : j;
-        const int64_t t0 = ch * kC;
-        if (t0 >= len) continue;
-        stage<T, NT>(s_k, kp, kt, t0, len, 0, a.N, vec_k);
-        stage<T, kPB>(s_v, vp, vt, t0, len, p0, a.P, vec_v);
-        if (w == 0) {
-            const double c = wave_running_sum(log_decay(gp, g_stride, t0 + l, len));
-            const double end = __shfl(c, 63);
-            s_w[l] = REV ? a.scale * exp_of((float)c) : exp_of((float)(end - c));
-            if (l == 63) s_end = exp_of((float)c);
-            total += end;
+    const int64_t n_chunks = (a.L + kC - 1) / kC, live = (len + kC - 1) / kC;
+    const int64_t ch0 = wk.seg * a.seg_chunks, ch1 = ch0 + a.seg_chunks < n_chunks ? ch0 + a.seg_chunks : n_chunks;
+    const int64_t chl = ch1 < live ? ch1 : live;
+    Stage<T, NT, THREADS, VEC> rk;
+    Stage<T, PB, THREADS, VEC> rv;
+    double passed = 0.0;  // in every wavefront: the sum of g over the chunks walked
+    float g_next = 0.0f;
+    const int64_t n = chl - ch0;
+    auto start = [&](int64_t j) { return (REV ? ch0 + j : chl - 1 - j) * kC; };
+    auto fetch = [&](int64_t t0) {
+        const int rows = rows_of(t0, len);
+        rk.load(kp + t0 * kt, (uint32_t)kt, rows, 0, a.N);
+        rv.load(vp + t0 * vt, (uint32_t)vt, rows, p0, a.P);
+    };
+    auto fetch_g = [&](int64_t t0) { return load_g(gp + t0 * g_stride, (uint32_t)g_stride, rows_of(t0, len)); };
+    if (n > 0) {
+        if (VEC) fetch(start(0));
+        g_next = fetch_g(start(0));
+    }
+    for (int64_t j = 0; j < n && !(passed <= -200.0); ++j) {
+        if (!VEC) fetch(start(j));
+        rk.store(s_k);
+        rv.store(s_v);
+        const double sum = wave_running_sum(log_decay(g_next)), total = lane_value(sum, 63);
+        // the weight of the lane's step, from all chunks walked and from this one
+        const float wt = (REV ? a.scale : 1.0f) * exp_of((float)(passed + (REV ? sum : total - sum)));
+        if (w == 0) s_g.out[l] = wt;
+        passed += total;
+        lds_barrier();
+        if (j + 1 < n) {
+            if (VEC) fetch(start(j + 1));
+            g_next = fetch_g(start(j + 1));
         }
-        __syncthreads();
-        const float end = s_end;
-#pragma unroll
-        for (int i = 0; i < NT / 16; ++i) S[i] *= end;
 #pragma unroll
         for (int sp = 0; sp < 2; ++sp) {
-            const f4 u = *reinterpret_cast<const f4 *>(&s_w[32 * sp + g4]);
-            const f4 v = *reinterpret_cast<const f4 *>(&s_w[32 * sp + 16 + g4]);
+            const f4 u = *reinterpret_cast<const f4 *>(&s_g.out[32 * sp + g4]);
+            const f4 v = *reinterpret_cast<const f4 *>(&s_g.out[32 * sp + 16 + g4]);
             const Split<T, 3> vs(wide(col_frag(s_v, SV, 32 * sp, 16 * w)) * join(u, v));
 #pragma unroll
             for (int i = 0; i < NT / 16; ++i) mma(S[i], col_frag(s_k, SN, 32 * sp, 16 * i), vs);
         }
-        __syncthreads();
+        lds_barrier();
     }
-    const int64_t Pp = (a.P + kPB - 1) / kPB * kPB, at = wk.bh * a.n_seg + wk.seg;
-    float *dst = (REV ? a.E : a.S) + (at * Pp + p0 + 16 * w + col) * NT + g4;
+    const int64_t Pp = (a.P + kPB - 1) / kPB * kPB, at = wk.bh * a.n_seg + wk.seg, p = p0 + 16 * w + col;
+    if (p < Pp) {
+        float *dst = (REV ? a.E : a.S) + (at * Pp + p) * NT + g4;
 #pragma unroll
-    for (int i = 0; i < NT / 16; ++i) *reinterpret_cast<f4 *>(dst + 16 * i) = S[i];
-    if (tid == 0 && wk.pb == 0) a.gsum[at] = total;
+        for (int i = 0; i < NT / 16; ++i) *reinterpret_cast<f4 *>(dst + 16 * i) = S[i];
+    }
+    if (tid == 0 && p0 == 0) a.gsum[at] = passed;
 }
 
 // ---- from the segments' own states to those entering them (adjoints: leaving them), in place ---------------------
@@ -336,31 +367,46 @@ __global__ __launch_bounds__(kThreads) void la_carry_kernel(LinAttnLaunch a, int
             if (n + r < a.N) a.d_initial_state[(bh * a.P + p) * a.N + n + r] = carry[r];
 }
 
+// f(NT, NW, VEC): the padded width of N, wavefronts per workgroup, and whether all rows take 16-byte accesses. Eight
+// wavefronts share the scores, queries and keys of 128 value columns where P is that wide.
+template <typename F> hipError_t by_width(const LinAttnLaunch &p, F f) {
+    const int nt = linattn_nt(p.N);
+    auto with = [&](auto nw, auto vec) {
+        return nt == 32 ? f(std::integral_constant<int, 32>{}, nw, vec)
+               : nt == 64 ? f(std::integral_constant<int, 64>{}, nw, vec)
+                          : f(std::integral_constant<int, 128>{}, nw, vec);
+    };
+    const std::integral_constant<int, 4> four;
+    const std::integral_constant<int, 8> eight;
+    if (linattn_cols(p.P) == 64) return p.vec ? with(four, std::true_type{}) : with(four, std::false_type{});
+    return p.vec ? with(eight, std::true_type{}) : with(eight, std::false_type{});
+}
+unsigned value_blocks(const LinAttnLaunch &p) {
+    const int cols = (int)linattn_cols(p.P);
+    return (unsigned)((p.P + cols - 1) / cols);
+}
+
 template <typename T>
 hipError_t states(const LinAttnLaunch &p, bool adjoint, int64_t first, int64_t n, hipStream_t stream) {
-    const int nt = linattn_nt(p.N);
-    const dim3 grid((unsigned)(p.b * p.H * n * ((p.P + kPB - 1) / kPB)));
-    if (nt == 32) {
-        if (adjoint) la_states_kernel<T, 32, true><<<grid, kThreads, 0, stream>>>(p, first, n);
-        else la_states_kernel<T, 32, false><<<grid, kThreads, 0, stream>>>(p, first, n);
-    } else if (nt == 64) {
-        if (adjoint) la_states_kernel<T, 64, true><<<grid, kThreads, 0, stream>>>(p, first, n);
-        else la_states_kernel<T, 64, false><<<grid, kThreads, 0, stream>>>(p, first, n);
-    } else {
-        if (adjoint) la_states_kernel<T, 128, true><<<grid, kThreads, 0, stream>>>(p, first, n);
-        else la_states_kernel<T, 128, false><<<grid, kThreads, 0, stream>>>(p, first, n);
-    }
-    return hipGetLastError();
+    const dim3 grid((unsigned)(p.b * p.H * n) * value_blocks(p));
+    return by_width(p, [&](auto nt, auto nw, auto vec) {
+        constexpr int NT = decltype(nt)::value, NW = decltype(nw)::value;
+        constexpr bool VEC = decltype(vec)::value;
+        if (adjoint) la_states_kernel<T, NT, NW, VEC, true><<<grid, 64 * NW, 0, stream>>>(p, first, n);
+        else la_states_kernel<T, NT, NW, VEC, false><<<grid, 64 * NW, 0, stream>>>(p, first, n);
+        return hipGetLastError();
+    });
 }
 
 template <typename T>
 hipError_t outputs(const LinAttnLaunch &p, hipStream_t stream) {
-    const int nt = linattn_nt(p.N);
-    const dim3 grid((unsigned)(p.b * p.H * p.n_seg * ((p.P + kPB - 1) / kPB)));
-    if (nt == 32) la_out_kernel<T, 32><<<grid, kThreads, 0, stream>>>(p);
-    else if (nt == 64) la_out_kernel<T, 64><<<grid, kThreads, 0, stream>>>(p);
-    else la_out_kernel<T, 128><<<grid, kThreads, 0, stream>>>(p);
-    return hipGetLastError();
+    const dim3 grid((unsigned)(p.b * p.H * p.n_seg) * value_blocks(p));
+    return by_width(p, [&](auto nt, auto nw, auto vec) {
+        constexpr int NT = decltype(nt)::value, NW = decltype(nw)::value;
+        constexpr bool VEC = decltype(vec)::value;
+        la_out_kernel<T, NT, NW, VEC><<<grid, 64 * NW, 0, stream>>>(p);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace
