@@ -88,16 +88,16 @@ ssm_status_t check_sizes(const AttnSizes &z, ssm_dtype_t dtype) {
 }
 
 // How the steps are cut into segments. One workgroup walks a segment's chunks in order. The forward call uses one
-// segment where rows, heads and value columns alone give the device two wavefronts per SIMD (512 times four of them,
-// for 64 value columns each), and otherwise as many as give it four, of at least four chunks each. The gradient's
-// chunks run independently of each other.
+// segment where rows, heads and blocks of 64 value columns alone give the device two workgroups per compute unit, and
+// otherwise as many as give it four, of at least four chunks each. The gradient's chunks run independently of each
+// other.
 void plan(const AttnSizes &z, bool gradient, LinAttnLaunch *p) {
     const int64_t chunks = ceil_div(z.L, kChunk);
     p->seg_chunks = chunks;
     if (gradient) {
         p->seg_chunks = 1;
     } else {
-        const int64_t groups = z.b * z.H * ceil_div(z.P, ssm::linattn_cols(z.P)) * (ssm::linattn_cols(z.P) / 64);
+        const int64_t groups = z.b * z.H * ceil_div(z.P, kBlockP);
         if (groups < 512) {
             int64_t s = ceil_div(1024, groups);
             if (s > chunks / 4) s = chunks / 4;
@@ -133,14 +133,16 @@ bool set_strides(const AttnSizes &z, const ssm_linattn_strides_t *st, bool step,
     const ssm_linattn_strides_t &s = st ? *st : dense;
     const int64_t all[12] = {s.q_b, s.q_t, s.q_h, s.k_b, s.k_t, s.k_h, s.v_b, s.v_t, s.v_h, s.do_b, s.do_t, s.do_h};
     const int64_t n[3] = {z.b, L > 0 ? L : 1, 0};
-    int64_t use[12] = {0};  // an axis of one element has no stride
+    // an axis of one element has no stride of its own; one step's is the row's width, as if more rows followed
+    const int64_t width[4] = {z.N, z.N, z.P, z.P};
+    int64_t use[12] = {0};
     for (int i = 0; i < 12; ++i) {
         if (step && (i % 3 == 1 || i >= 9)) continue;
         const int64_t count = i % 3 < 2 ? n[i % 3] : (i < 6 ? z.G : z.H);
         int64_t reach = 0;
         if (all[i] < 0 || !mul_ok(all[i], count, &reach) || reach > kMost) return false;
         if (i % 3 == 1 && count > 1 && all[i] > kMostStep) return false;
-        use[i] = count > 1 ? all[i] : 0;
+        use[i] = count > 1 ? all[i] : i % 3 == 1 ? width[i / 3] : 0;
     }
     p->q_b = use[0]; p->q_t = use[1]; p->q_h = use[2];
     p->k_b = use[3]; p->k_t = use[4]; p->k_h = use[5];
@@ -154,10 +156,10 @@ int64_t extent(int64_t b, int64_t t, int64_t h, int64_t width, int64_t sb, int64
     return ((b - 1) * sb + (t - 1) * st + (h - 1) * sh + width) * es;
 }
 
-// Whether rows of `width` elements at these strides take 16-byte loads.
+// Whether rows of `width` elements at these strides take 16-byte loads, and steps lie at least a row apart.
 bool loads16(const void *p, int64_t width, int64_t sb, int64_t st, int64_t sh, int64_t es) {
     const int64_t v = 16 / es;
-    return aligned(p, 16) && width % v == 0 && sb % v == 0 && st % v == 0 && sh % v == 0;
+    return aligned(p, 16) && width % v == 0 && st >= width && sb % v == 0 && st % v == 0 && sh % v == 0;
 }
 
 void set_common(const AttnSizes &z, ssm_dtype_t dtype, LinAttnLaunch *p) {

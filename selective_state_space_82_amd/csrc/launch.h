@@ -244,7 +244,7 @@ struct LinAttnLaunch {
     float *dq_part, *dk_part;  // [b][L][H][N] when G < H
     bool vec;              // every input and output row takes 16-byte accesses at multiples of 16 bytes
 };
-// Value columns per workgroup of the walks over chunks.
+// Value columns per workgroup of the segment states' walk.
 inline int64_t linattn_cols(int64_t P) { return P > 64 ? 128 : 64; }
 inline int linattn_nt(int64_t N) { return N <= 32 ? 32 : N <= 64 ? 64 : 128; }
 hipError_t launch_linattn_fwd(const LinAttnLaunch &p, hipStream_t stream);

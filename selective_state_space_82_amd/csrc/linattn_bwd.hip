@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
     const int64_t ch = id % a.n_seg, ib = id / a.n_seg;
     const int ratio = a.H / a.G, grp = h / ratio;
     const int64_t bh = ib * a.H + h;
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, col = l & 15, g4 = 4 * (l >> 4);
+    const int tid = threadIdx.x, w = wave_id(), l = tid & 63, col = l & 15, g4 = 4 * (l >> 4);
     const int64_t len = row_length(a.lengths, ib, a.L);
     const int64_t t0 = ch * kC;
     const int64_t rows = a.L - t0 < kC ? a.L - t0 : kC;
@@ -98,10 +98,10 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
     const T *dp = static_cast<const T *>(a.dout) + ib * a.do_b + h * a.do_h;
 
     {
-        Stage<T, NT, kThreads, VEC> q, k;
-        q.load(qp + t0 * a.q_t, (uint32_t)a.q_t, rows_of(t0, len), 0, a.N);
-        k.load(kp + t0 * a.k_t, (uint32_t)a.k_t, rows_of(t0, len), 0, a.N);
-        if (w == 0) s_g.set(log_decay(load_g(gp + t0 * g_stride, (uint32_t)g_stride, rows_of(t0, len))), a.scale);
+        Stage<T, NT, kThreads, VEC> q((uint32_t)a.q_t, 0, a.N), k((uint32_t)a.k_t, 0, a.N);
+        q.load(qp + t0 * a.q_t, rows_of(t0, len));
+        k.load(kp + t0 * a.k_t, rows_of(t0, len));
+        if (w == 0) s_g.set<false>(log_decay(load_g(gp + t0 * g_stride, (uint32_t)g_stride, rows_of(t0, len))), a.scale);
         q.store(s_q);
         k.store(s_k);
     }
@@ -121,9 +121,9 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
     for (int j = 0; j < 3; ++j) aq[j] = ad[j] = f4{0, 0, 0, 0};
     for (int pb = 0; pb < npb; ++pb) {
         if (pb) lds_barrier();
-        Stage<T, kPB, kThreads, VEC> v, d;
-        v.load(vp + t0 * a.v_t, (uint32_t)a.v_t, rows_of(t0, len), pb * kPB, a.P);
-        d.load(dp + t0 * a.do_t, (uint32_t)a.do_t, rows_of(t0, len), pb * kPB, a.P);
+        Stage<T, kPB, kThreads, VEC> v((uint32_t)a.v_t, pb * kPB, a.P), d((uint32_t)a.do_t, pb * kPB, a.P);
+        v.load(vp + t0 * a.v_t, rows_of(t0, len));
+        d.load(dp + t0 * a.do_t, rows_of(t0, len));
         v.store(s_v);
         d.store(s_d);
         lds_barrier();
@@ -189,9 +189,9 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
     for (int pb = 0; pb < npb; ++pb) {
         lds_barrier();
         if (npb > 1) {
-            Stage<T, kPB, kThreads, VEC> v, d;
-            v.load(vp + t0 * a.v_t, (uint32_t)a.v_t, rows_of(t0, len), pb * kPB, a.P);
-            d.load(dp + t0 * a.do_t, (uint32_t)a.do_t, rows_of(t0, len), pb * kPB, a.P);
+            Stage<T, kPB, kThreads, VEC> v((uint32_t)a.v_t, pb * kPB, a.P), d((uint32_t)a.do_t, pb * kPB, a.P);
+            v.load(vp + t0 * a.v_t, rows_of(t0, len));
+            d.load(dp + t0 * a.do_t, rows_of(t0, len));
             v.store(s_v);
             d.store(s_d);
             lds_barrier();
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
             for (int n = 0; n < NT / 32; ++n) {
                 const Split<T, 3> es(join(e[2 * n], e[2 * n + 1]));
 #pragma unroll
-                for (int b = 0; b < 4; ++b) mma(dv[b], es, row_frag(s_k, SN, 16 * b, 32 * n));
+                for (int b = 0; b < 4; ++b) mma(dv[b], es, half_frag(s_k, SN, 16 * b, 32 * n));
             }
             const Frag<T> d0 = col_frag(s_d, SV, 0, 16 * w), d1 = col_frag(s_d, SV, 32, 16 * w);
 #pragma unroll
@@ -237,16 +237,13 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
             const int job = w + 4 * j;
             const bool is_q = job < TILES;
             const int n0 = 16 * (is_q ? job : job - TILES);
-            const float *src = (is_q ? Sp : Ep) + (pb * kPB + g4) * NT + n0 + col;
+            const float *src = (is_q ? Sp : Ep) + (pb * kPB + 2 * g4) * NT + n0 + col;
             const T *tile = is_q ? s_d : s_v;
 #pragma unroll
             for (int pp = 0; pp < 2; ++pp) {
                 f8 x;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    x[r] = src[(32 * pp + r) * NT];
-                    x[4 + r] = src[(32 * pp + 16 + r) * NT];
-                }
+                for (int r = 0; r < 8; ++r) x[r] = src[(32 * pp + r) * NT];
                 const Split<T, 3> xs(x);
 #pragma unroll
                 for (int b = 0; b < 4; ++b) mma(acc[j][b], xs, row_frag(tile, SV, 16 * b, 32 * pp));

@@ -2,11 +2,15 @@
 // chunk geometry, tile staging, and matrix products on fragments of 16×16×32 steps.
 //
 // Every product is a sum of 16×16 tiles D = A·Bᵀ over a contraction axis taken 32 at a time. Lane l = 16·grp + col
-// of a wavefront supplies, for row `col` of A (and of B), the 8 contraction values 4·grp + j and 16 + 4·grp + j
-// (j < 4) of the 32, and receives D[4·grp + r][col], r < 4. The order of a contraction axis is free as long as
-// both operands use the same, and this one makes a result tile an operand without moving it: D's lane holds, for
-// row (as an operand) `col`, four consecutive values 4·grp + r of a 16-block, so two neighbouring result tiles are
-// the lane's 8 values of one contraction step. The state, kept as result tiles, is thus read as an operand in place.
+// of a wavefront supplies, for row `col` of A (and of B), 8 of the 32 contraction values, and receives
+// D[4·grp + r][col], r < 4. The order of a contraction axis is free as long as both operands use the same:
+//   plain    values 8·grp .. 8·grp + 7: one 16-byte LDS read along a row (bf16);
+//   halves   4·grp + j and 16 + 4·grp + j, j < 4: what two neighbouring result tiles hold in each lane, so that the
+//            state, kept as result tiles, is an operand without being moved;
+//   spread   8·(grp % 2) + grp / 2 + 2j, and the same + 16: rows two apart, which lie 8 LDS banks apart at the row
+//            distances used here, so that the 32 lanes of a transposing read down 16 columns touch 64 different
+//            banks (with neighbouring rows they meet in half of them, which the counters showed as the largest
+//            part of all LDS conflicts).
 #pragma once
 
 #include <type_traits>
@@ -24,8 +28,10 @@ constexpr int kThreads = 256; // four wavefronts
 // stay finite (−inf would turn differences of sums into NaN).
 constexpr float kMinG = -1e4f;
 
+typedef float f2 __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef float f8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
@@ -44,6 +50,9 @@ __device__ __forceinline__ void mma(f4 &acc, const f8 &a, const f8 &b) {
     for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], acc, 0, 0, 0);
 }
 
+// The wavefront's number in its workgroup, as a scalar.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
+
 // Workgroup barrier that orders LDS only: the next chunk's loads and the outputs' stores stay in flight across it.
 __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -54,39 +63,54 @@ __device__ __forceinline__ void lds_barrier() {
 // Operand fragment of tile row `row0 + col`, contraction values n0 .. n0+31 along the row.
 __device__ __forceinline__ bf8 row_frag(const uint16_t *tile, int stride, int row0, int n0) {
     const int l = threadIdx.x & 63;
+    return *reinterpret_cast<const bf8 *>(tile + (row0 + (l & 15)) * stride + n0 + 8 * (l >> 4));
+}
+__device__ __forceinline__ f8 row_frag(const float *tile, int stride, int row0, int n0) {
+    const int l = threadIdx.x & 63;
+    const float *p = tile + (row0 + (l & 15)) * stride + n0 + 8 * (l >> 4);
+    const f4 u = *reinterpret_cast<const f4 *>(p), v = *reinterpret_cast<const f4 *>(p + 4);
+    return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// The same in the order `halves`.
+__device__ __forceinline__ bf8 half_frag(const uint16_t *tile, int stride, int row0, int n0) {
+    const int l = threadIdx.x & 63;
     const uint16_t *p = tile + (row0 + (l & 15)) * stride + n0 + 4 * (l >> 4);
     const bf4 u = *reinterpret_cast<const bf4 *>(p), v = *reinterpret_cast<const bf4 *>(p + 16);
     return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-__device__ __forceinline__ f8 row_frag(const float *tile, int stride, int row0, int n0) {
+__device__ __forceinline__ f8 half_frag(const float *tile, int stride, int row0, int n0) {
     const int l = threadIdx.x & 63;
     const float *p = tile + (row0 + (l & 15)) * stride + n0 + 4 * (l >> 4);
     const f4 u = *reinterpret_cast<const f4 *>(p), v = *reinterpret_cast<const f4 *>(p + 16);
     return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Operand fragment of tile column n0 + col, contraction values s0 .. s0+31 down the column. bf16: the transposing
-// LDS read, which gives lane `col` of 16 lanes column `col` of the 4×16 block whose quarter rows they address.
-__device__ __forceinline__ bf8 col_frag(const uint16_t *tile, int stride, int s0, int n0) {
+// Operand fragment of tile column n0 + col, contraction values s0 .. s0+31 down the column, in the order plain or
+// spread. bf16: the transposing LDS read, which gives lane `col` of 16 lanes column `col` of the 4×16 block whose
+// quarter rows they address.
+template <bool SPREAD = false> __device__ __forceinline__ bf8 col_frag(const uint16_t *tile, int stride, int s0, int n0) {
     typedef __attribute__((address_space(3))) s4 lds_s4;
-    const int l = threadIdx.x & 63, c = l & 15;
-    const uint16_t *p = tile + (s0 + 4 * (l >> 4) + (c >> 2)) * stride + n0 + 4 * (c & 3);
+    const int l = threadIdx.x & 63, c = l & 15, g = l >> 4;
+    const int row = SPREAD ? 8 * (g & 1) + (g >> 1) + 2 * (c >> 2) : 8 * g + (c >> 2);
+    const uint16_t *p = tile + (s0 + row) * stride + n0 + 4 * (c & 3);
     const s4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)p);
-    const s4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p + 16 * stride));
+    const s4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p + (SPREAD ? 16 : 4) * stride));
     typedef short s8 __attribute__((ext_vector_type(8)));
     const s8 w = __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(bf8, w);
 }
-__device__ __forceinline__ f8 col_frag(const float *tile, int stride, int s0, int n0) {
-    const int l = threadIdx.x & 63;
-    const float *p = tile + (s0 + 4 * (l >> 4)) * stride + n0 + (l & 15);
+template <bool SPREAD = false> __device__ __forceinline__ f8 col_frag(const float *tile, int stride, int s0, int n0) {
+    const int l = threadIdx.x & 63, g = l >> 4;
+    const float *p = tile + (s0 + (SPREAD ? 8 * (g & 1) + (g >> 1) : 8 * g)) * stride + n0 + (l & 15);
     f8 r;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        r[j] = p[j * stride];
-        r[4 + j] = p[(16 + j) * stride];
-    }
+    for (int j = 0; j < 8; ++j) r[j] = p[(SPREAD ? 2 * (j & 3) + 16 * (j >> 2) : j) * stride];
     return r;
+}
+// Where step s of a chunk stands in the order spread (8·grp + j of its 32).
+__device__ __forceinline__ int spread_of(int s) {
+    return (s & 32) + 8 * ((s >> 3 & 1) + 2 * (s & 1)) + 4 * (s >> 4 & 1) + (s >> 1 & 3);
 }
 
 __device__ __forceinline__ f8 wide(const bf8 &v) { return __builtin_convertvector(v, f8); }
@@ -97,6 +121,7 @@ __device__ __forceinline__ f8 join(const f4 &u, const f4 &v) { return __builtin_
 // remainder of those before (relative error at most 2^-8, 2^-16, 2^-24 for 1, 2, 3 parts); for f32 it is one part.
 template <int PARTS> struct Parts {
     bf8 p[PARTS];
+    Parts() = default;
     __device__ __forceinline__ explicit Parts(f8 v) {
 #pragma unroll
         for (int i = 0; i < PARTS; ++i) {
@@ -107,6 +132,7 @@ template <int PARTS> struct Parts {
 };
 struct Whole {
     f8 v;
+    Whole() = default;
     __device__ __forceinline__ explicit Whole(f8 x) : v(x) {}
 };
 template <typename T, int PARTS> using Split = typename std::conditional<sizeof(T) == 2, Parts<PARTS>, Whole>::type;
@@ -168,15 +194,14 @@ struct Decays {
     Sums c;
     __attribute__((aligned(16))) float in[kC], out[kC];
     float end;
-    // By one wavefront, lane t for step t; returns the chunk's sum.
-    __device__ __forceinline__ double set(double g, float factor) {
+    // By one wavefront, lane t for step t; `out` in the order spread or as the steps are.
+    template <bool SPREAD> __device__ __forceinline__ void set(double g, float factor) {
         const int l = threadIdx.x & 63;
         const double sum = wave_running_sum(g), total = lane_value(sum, 63);
         c.set(l, sum);
         in[l] = factor * exp_of((float)sum);
-        out[l] = exp_of((float)(total - sum));
+        out[SPREAD ? spread_of(l) : l] = exp_of((float)(total - sum));
         if (l == 63) end = exp_of((float)total);
-        return total;
     }
 };
 
@@ -194,37 +219,45 @@ template <typename T> __device__ __forceinline__ Buffer rows_buffer(const T *fir
 }
 
 // The log-decay of the lane's step in a chunk of `rows` rows (0 past them), not yet clamped; first: that of row 0.
-__device__ __forceinline__ float load_g(const float *first, uint32_t stride, int rows) {
+__device__ __forceinline__ float load_g(const Buffer &buf, uint32_t stride, int rows) {
     const int l = threadIdx.x & 63;
-    const Buffer buf = rows_buffer(first, stride, rows, 1);
     return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buf, l < rows ? l * stride * 4u : kOutside, 0, 0));
+}
+__device__ __forceinline__ float load_g(const float *first, uint32_t stride, int rows) {
+    return load_g(rows_buffer(first, stride, rows, 1), stride, rows);
 }
 
 // Rows of a chunk × columns [c0, c0 + W) of a strided array on their way into an LDS tile, zeros past the rows and
-// columns there are. VEC: 16-byte accesses at multiples of kVec elements are allowed and `cols` is one of them;
-// otherwise element by element. A thread holds its pieces between load and store, so that a chunk is fetched
-// while the one before is computed.
+// columns there are. VEC: 16-byte accesses at multiples of kVec elements are allowed, `cols` is one of them, and
+// rows are at least `cols` apart, so that the buffer's end alone cuts off the rows; otherwise element by element. A
+// thread holds its pieces between load and store, so that a chunk is fetched while the one before is computed.
 template <typename T, int W, int THREADS, bool VEC> struct Stage {
     static constexpr int V = kVec<T>, PER = W / V, S = W + kPad<T>, PIECES = kC * PER,
-                         N = (PIECES + THREADS - 1) / THREADS;
+                         N = (PIECES + THREADS - 1) / THREADS, STEP = THREADS / PER;  // rows between a thread's pieces
+    static_assert(THREADS % PER == 0, "a thread's pieces are in one column");
     typedef uint32_t u4 __attribute__((ext_vector_type(4)));
     u4 w[N];
+    uint32_t at;  // of the first piece, in bytes from row 0
+    int c0, cols;
+    uint32_t stride;
+    __device__ __forceinline__ Stage(uint32_t stride_, int c0_, int cols_) : c0(c0_), cols(cols_), stride(stride_) {
+        const int c = c0 + (int)(threadIdx.x % PER) * V;
+        at = c < cols && (int)threadIdx.x < PIECES ? (threadIdx.x / PER * stride + c) * (uint32_t)sizeof(T) : kOutside;
+    }
     // first: row 0 of the chunk, column 0, the same in every lane
-    __device__ __forceinline__ void load(const T *first, uint32_t stride, int rows, int c0, int cols) {
-        const Buffer buf = rows_buffer(first, stride, rows, cols);
+    __device__ __forceinline__ void load(const T *first, int rows) { load(rows_buffer(first, stride, rows, cols), rows); }
+    __device__ __forceinline__ void load(const Buffer &buf, int rows) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int i = threadIdx.x + j * THREADS, r = i / PER, c = c0 + (i % PER) * V;
-            const uint32_t at = (r * stride + c) * (uint32_t)sizeof(T);
-            // by row as well: a distance of 0 between steps never leaves the buffer
-            const bool mine = r < rows && (PIECES % THREADS == 0 || i < PIECES);
             if constexpr (VEC) {
-                w[j] = __builtin_amdgcn_raw_buffer_load_b128(buf, mine && c < cols ? at : kOutside, 0, 0);
+                w[j] = __builtin_amdgcn_raw_buffer_load_b128(buf, at, j * STEP * stride * (uint32_t)sizeof(T), 0);
             } else {
+                const int r = threadIdx.x / PER + j * STEP, c = c0 + (int)(threadIdx.x % PER) * V;
                 T e[V];
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
-                    const uint32_t off = mine && c + k < cols ? at + k * (uint32_t)sizeof(T) : kOutside;
+                    const bool mine = r < rows && (int)threadIdx.x < PIECES && c + k < cols;
+                    const uint32_t off = mine ? (r * stride + c + k) * (uint32_t)sizeof(T) : kOutside;
                     if constexpr (sizeof(T) == 2) e[k] = (T)__builtin_amdgcn_raw_buffer_load_b16(buf, off, 0, 0);
                     else e[k] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(buf, off, 0, 0));
                 }
@@ -235,8 +268,8 @@ template <typename T, int W, int THREADS, bool VEC> struct Stage {
     __device__ __forceinline__ void store(T *tile) const {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int i = threadIdx.x + j * THREADS;
-            if (PIECES % THREADS == 0 || i < PIECES) *reinterpret_cast<u4 *>(tile + i / PER * S + (i % PER) * V) = w[j];
+            if (PIECES % THREADS == 0 || (int)threadIdx.x < PIECES)
+                *reinterpret_cast<u4 *>(tile + (threadIdx.x / PER + j * STEP) * S + threadIdx.x % PER * V) = w[j];
         }
     }
 };
@@ -244,7 +277,7 @@ template <typename T, int W, int THREADS, bool VEC> struct Stage {
 // Four consecutive results (row r, columns c .. c+3) of dense rows in `buf` (rows_buffer), `stride` elements apart.
 template <typename T, bool VEC>
 __device__ __forceinline__ void store4(const Buffer &buf, uint32_t stride, int r, int c, int cols, const f4 &v) {
-    const uint32_t at = (r * stride + c) * (uint32_t)sizeof(T);
+    const uint32_t at = (r * stride + c) * (uint32_t)sizeof(T);  // r is a lane's own
     typedef uint32_t u2 __attribute__((ext_vector_type(2)));
     typedef uint32_t u4 __attribute__((ext_vector_type(4)));
     if constexpr (VEC) {
@@ -268,6 +301,32 @@ __device__ __forceinline__ int rows_of(int64_t t0, int64_t len) {
     const int64_t n = len - t0;
     return n > kC ? kC : n < 0 ? 0 : (int)n;
 }
+
+// The chunks of a strided array in order, without products on the way: the place and byte count of the next one's rows,
+// of `left` rows in all.
+struct Cursor {
+    const char *at;
+    int64_t step;      // bytes from one chunk to the next
+    uint32_t full, row;// bytes of a whole chunk, and between rows
+    template <typename T> __device__ __forceinline__ Cursor(const T *first, int64_t stride, int cols)
+        : at(reinterpret_cast<const char *>(first)), step(stride * kC * (int64_t)sizeof(T)),
+          full((uint32_t)((kC - 1) * stride + cols) * (uint32_t)sizeof(T)), row((uint32_t)stride * (uint32_t)sizeof(T)) {}
+    // the chunk's buffer, rows: 0 .. 64 of them; then on to the next
+    __device__ __forceinline__ Buffer next(int rows) {
+        const Buffer b = buffer_of(at, rows > 0 ? full - (kC - rows) * row : 0u);
+        at += step;
+        return b;
+    }
+};
+// Rows still to come, counted down by chunks: the next chunk's.
+struct RowsLeft {
+    int64_t left;
+    __device__ __forceinline__ int next() {
+        const int n = left > kC ? kC : left < 0 ? 0 : (int)left;
+        left -= kC;
+        return n;
+    }
+};
 
 // Steps of batch row i.
 __device__ __forceinline__ int64_t row_length(const int32_t *lengths, int64_t i, int64_t L) {

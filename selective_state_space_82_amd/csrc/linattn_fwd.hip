@@ -11,6 +11,8 @@ namespace ssm {
 namespace la {
 namespace {
 
+constexpr int kOutThreads = 512;
+
 struct Work {
     int64_t ib, seg, bh;
     int h, grp, p0;  // p0: first value column
@@ -35,39 +37,30 @@ __device__ __forceinline__ const float *decays_of(const LinAttnLaunch &a, const 
     return a.g_per_step ? a.g + w.ib * a.L * a.H + w.h : a.g + w.h;
 }
 
-// A lane's part of the state, four values of N at row p, as result tiles; zeros outside [P][N].
-template <int NT>
-__device__ __forceinline__ void load_state(f4 (&S)[NT / 16], const float *src, int64_t p, int P, int N) {
-    const int g4 = 4 * ((threadIdx.x & 63) >> 4);
-#pragma unroll
-    for (int i = 0; i < NT / 16; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int n = 16 * i + g4 + r;
-            S[i][r] = p < P && n < N ? src[p * N + n] : 0.0f;
-        }
-}
-
-// ---- outputs: one workgroup walks the chunks of (row, head, 16·NW value columns, segment) in order ---------------
+// ---- outputs: one workgroup walks the chunks of (row, head, 64 value columns, segment) in order ------------------
 //
-// Wavefront w keeps the state's value columns 16w .. 16w+15 (all N of them) in its result tiles. Per chunk the NW of
-// them share the 10 lower-triangular 16×16 tiles of the decayed scores through LDS; the rest (outputs of its own
-// columns, the state's update) each wavefront does from its own state and its own columns of V, which are scaled
-// and cut into bf16 parts once and used for every tile of N. The next chunk's rows are fetched into registers, and its
-// decays formed by the last wavefront (which has the fewest tiles), while this one is computed.
-template <typename T, int NT, int NW, bool VEC>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void la_out_kernel(LinAttnLaunch a) {
-    constexpr int THREADS = 64 * NW, PB = 16 * NW;
-    constexpr int SN = NT + kPad<T>, SP = kC + kPad<T>, SV = PB + kPad<T>;
-    constexpr int PARTS = sizeof(T) == 2 ? 2 : 1;
+// Eight wavefronts: w % 4 names 16 value columns, w / 4 a half of the chunk's steps for the outputs and a half of N for
+// the state. A wavefront keeps its columns and its half of N of the state in result tiles and updates them; the outputs
+// of its columns and steps need all of N, so the state's bf16 parts pass through LDS (a sixteenth of what is read
+// there). The decayed scores, 10 lower-triangular 16×16 tiles, are shared through LDS too. The next chunk's rows are
+// fetched into registers, and its decays formed by a wavefront without score tiles, while this chunk is computed.
+// Four wavefronts of twice the work each took as long on arithmetic alone as on everything: two per SIMD left 40 % of the
+// issue slots empty.
+template <typename T, int NT, bool VEC>
+__global__ __launch_bounds__(kOutThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && VEC ? 4 : 2))) void la_out_kernel(LinAttnLaunch a) {
+    constexpr int SN = NT + kPad<T>, SP = kC + kPad<T>, SV = kPB + kPad<T>;
+    constexpr int PARTS = sizeof(T) == 2 ? 2 : 1, NF = NT / 32;
+    typedef typename std::conditional<sizeof(T) == 2, bf4, f4>::type Half;  // a lane's part of one result tile
     __shared__ __align__(16) T s_q[kC * SN];
     __shared__ __align__(16) T s_k[kC * SN];
     __shared__ __align__(16) T s_v[kC * SV];
-    __shared__ __align__(16) T s_p[PARTS][kC * SP];  // decayed scores [t][s]
+    __shared__ __align__(16) T s_p[PARTS][kC * SP];  // decayed scores [t][s], s in the order spread
+    __shared__ __align__(16) Half s_s[4][NF][64][2]; // the state's operand fragments
     __shared__ Decays s_g[2];
 
-    const Work wk = work_of<NW>(a, a.n_seg);
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, col = l & 15, g4 = 4 * (l >> 4);
+    const Work wk = work_of<4>(a, a.n_seg);
+    const int tid = threadIdx.x, w = wave_id(), l = tid & 63, col = l & 15, g4 = 4 * (l >> 4);
+    const int pw = w & 3, tw = w >> 2;
     const int64_t len = row_length(a.lengths, wk.ib, a.L);
     int64_t g_stride;
     const float *gp = decays_of(a, wk, &g_stride);
@@ -76,165 +69,214 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
     const T *vp = static_cast<const T *>(a.v) + wk.ib * a.v_b + wk.h * a.v_h;
     T *op = static_cast<T *>(a.o) + (wk.ib * a.L * a.H + wk.h) * a.P;
     const uint32_t o_t = (uint32_t)a.H * a.P;  // elements between steps of o
-    const int p0 = wk.p0, p_wave = p0 + 16 * w;
+    const int p0 = wk.p0, p_wave = p0 + 16 * pw;
 
-    f4 S[NT / 16];
-    const int64_t p_lane = p_wave + col, Pp = (a.P + kPB - 1) / kPB * kPB;
-    if (a.n_seg > 1 && p_lane < Pp) {
-        const float *src = a.S + ((wk.bh * a.n_seg + wk.seg) * Pp + p_lane) * NT + g4;
+    // result tiles of the state: rows n0 + 16i + 4·grp + r, column p_lane
+    const int n0 = tw * (NT / 2);
+    const int64_t p_lane = p_wave + col;
+    f4 S[NF];
+    if (a.n_seg > 1) {
+        const int64_t Pp = (a.P + kPB - 1) / kPB * kPB;
+        const float *src = a.S + ((wk.bh * a.n_seg + wk.seg) * Pp + p_lane) * NT + n0 + g4;
 #pragma unroll
-        for (int i = 0; i < NT / 16; ++i) S[i] = *reinterpret_cast<const f4 *>(src + 16 * i);
-    } else if (a.n_seg == 1 && a.initial_state) {
-        load_state<NT>(S, a.initial_state + wk.bh * a.P * a.N, p_lane, a.P, a.N);
+        for (int i = 0; i < NF; ++i) S[i] = *reinterpret_cast<const f4 *>(src + 16 * i);
     } else {
 #pragma unroll
-        for (int i = 0; i < NT / 16; ++i) S[i] = f4{0, 0, 0, 0};
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int n = n0 + 16 * i + g4 + r;
+                S[i][r] = a.initial_state && p_lane < a.P && n < a.N
+                              ? a.initial_state[(wk.bh * a.P + p_lane) * a.N + n] : 0.0f;
+            }
     }
+    // the state enters the outputs as one bf16 part: half a step of bf16 on each product's size, as their own rounding
+    auto put_state = [&]() {
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+            // four values of N of column col, 16·(tile % 2) + 4·grp into their 32, where the plain order has them
+            const int tile = tw * NF + i;
+            s_s[pw][tile >> 1][16 * (2 * (tile & 1) + (g4 >> 3)) + col][g4 >> 2 & 1] = __builtin_convertvector(S[i], Half);
+        }
+    };
+    put_state();
 
     // the tiles right of the diagonal that a 32-step contraction touches stay zero
-    for (int i = tid; i < 2 * 16 * 16; i += THREADS) {
+    for (int i = tid; i < 2 * 16 * 16; i += kOutThreads) {
         const int t = 32 * (i >> 8) + ((i >> 4) & 15), s = 32 * (i >> 8) + 16 + (i & 15);
 #pragma unroll
-        for (int e = 0; e < PARTS; ++e) s_p[e][t * SP + s] = (T)0;
+        for (int e = 0; e < PARTS; ++e) s_p[e][t * SP + spread_of(s)] = (T)0;
     }
 
     const int64_t n_chunks = (a.L + kC - 1) / kC, live = (len + kC - 1) / kC;
     const int64_t ch0 = wk.seg * a.seg_chunks, ch1 = ch0 + a.seg_chunks < n_chunks ? ch0 + a.seg_chunks : n_chunks;
     const int64_t chl = ch1 < live ? ch1 : live;  // chunks with any step of the row
-    Stage<T, NT, THREADS, VEC> rq, rk;
-    Stage<T, PB, THREADS, VEC> rv;
+    Stage<T, NT, kOutThreads, VEC> rq((uint32_t)a.q_t, 0, a.N), rk((uint32_t)a.k_t, 0, a.N);
+    Stage<T, kPB, kOutThreads, VEC> rv((uint32_t)a.v_t, p0, a.P);
+    // Loads and stores share one in-order counter, and a wait in a loop is for what both ways into it have outstanding.
+    // So the order is kept: a chunk's outputs are stored just before the loads of the chunk after next are issued, and
+    // the decays' load goes with the others, one chunk further ahead (its scan comes while this one is computed).
     float g_next = 0.0f;
-    auto fetch = [&](int64_t t0) {
-        const int rows = rows_of(t0, len);
-        rq.load(qp + t0 * a.q_t, (uint32_t)a.q_t, rows, 0, a.N);
-        rk.load(kp + t0 * a.k_t, (uint32_t)a.k_t, rows, 0, a.N);
-        rv.load(vp + t0 * a.v_t, (uint32_t)a.v_t, rows, p0, a.P);
+    f4 res[2] = {f4{0, 0, 0, 0}, f4{0, 0, 0, 0}};
+    Buffer out = buffer_of(op, 0);  // nothing to store before the first chunk
+    auto store_res = [&]() {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) store4<T, VEC>(out, o_t, 16 * (2 * tw + b) + col, p_wave + g4, a.P, res[b]);
     };
-    auto fetch_g = [&](int64_t t0) { return load_g(gp + t0 * g_stride, (uint32_t)g_stride, rows_of(t0, len)); };
+    const int64_t t_first = ch0 * kC;
+    Cursor cq(qp + t_first * a.q_t, a.q_t, a.N), ck(kp + t_first * a.k_t, a.k_t, a.N), cv(vp + t_first * a.v_t, a.v_t, a.P);
+    Cursor cg(gp + t_first * g_stride, g_stride, 1), co(op + t_first * (int64_t)o_t, o_t, a.P);
+    RowsLeft in{len - t_first}, ing{len - t_first}, outs{a.L - t_first};
+    auto fetch = [&]() {
+        const int rows = in.next();
+        rq.load(cq.next(rows), rows);
+        rk.load(ck.next(rows), rows);
+        rv.load(cv.next(rows), rows);
+    };
+    auto fetch_g = [&]() {
+        const int rows = ing.next();
+        return load_g(cg.next(rows), (uint32_t)g_stride, rows);
+    };
     if (ch0 < chl) {
-        if (VEC) fetch(ch0 * kC);
-        if (w == NW - 1) {
-            s_g[0].set(log_decay(fetch_g(ch0 * kC)), a.scale);
-            g_next = fetch_g((ch0 + 1) * kC);
-        }
+        const float g0 = fetch_g();
+        g_next = fetch_g();
+        if (VEC) fetch();
+        if (w == 3) s_g[0].set<true>(log_decay(g0), a.scale);
     }
     for (int64_t ch = ch0; ch < chl; ++ch) {
-        const int64_t t0 = ch * kC;
         const Decays &dec = s_g[(ch - ch0) & 1];
-        const int all = rows_of(t0, a.L), some = rows_of(t0, len);
-        const Buffer out = rows_buffer(op + t0 * o_t, o_t, all, a.P);
-        if (!VEC) fetch(t0);
+        const int all = outs.next(), some = ch + 1 == live ? (int)(len - ch * kC) : kC;
+        if (!VEC) fetch();
         rq.store(s_q);
         rk.store(s_k);
         rv.store(s_v);
+        float g_now = g_next;
+        asm volatile("" : "+v"(g_now));  // it has arrived with the rest: no wait for it behind the next loads
         lds_barrier();
-        if (VEC) fetch(t0 + kC);  // past the last chunk: nothing
+        store_res();
+        out = co.next(all);
+        g_next = fetch_g();
+        if (VEC) fetch();  // past the last chunk: nothing
 
-        // decayed scores, tile (tb, sb): D[s][t] = k_s·q_t
-        for (int i = w; i < 10; i += NW) {
-            const int tb = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3;
-            const int sb = i - tb * (tb + 1) / 2;
-            f4 acc = {0, 0, 0, 0};
+        // Through the state, and the decayed scores: a query fragment serves both. Score tile (tb, sb) holds
+        // D[s][t] = k_s·q_t; a wavefront takes those of its two blocks of t and of s block pw, in two bf16 parts.
+        f4 acc[2];
+        Frag<T> sf[NF];
 #pragma unroll
-            for (int n = 0; n < NT; n += 32) mma(acc, row_frag(s_k, SN, 16 * sb, n), row_frag(s_q, SN, 16 * tb, n));
-            const int t = 16 * tb + col, s = 16 * sb + g4;
-            const float th = dec.c.hi[t], tl = dec.c.lo[t];
-            const f4 sh = *reinterpret_cast<const f4 *>(&dec.c.hi[s]), sl = *reinterpret_cast<const f4 *>(&dec.c.lo[s]);
+        for (int n = 0; n < NF; ++n) sf[n] = *reinterpret_cast<const Frag<T> *>(&s_s[pw][n][l][0]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float d = a.scale * exp2_fast((th - sh[r]) + (tl - sl[r]));
-                acc[r] = s + r <= t ? acc[r] * d : 0.0f;
-            }
-            if constexpr (sizeof(T) == 2) {
+        for (int b = 0; b < 2; ++b) {
+            const int tb = 2 * tw + b;
+            Frag<T> qf[NF];
 #pragma unroll
-                for (int e = 0; e < PARTS; ++e) {
-                    const bf4 v = __builtin_convertvector(acc, bf4);
-                    *reinterpret_cast<bf4 *>(&s_p[e][t * SP + s]) = v;
-                    acc -= __builtin_convertvector(v, f4);
+            for (int n = 0; n < NF; ++n) qf[n] = row_frag(s_q, SN, 16 * tb, 32 * n);
+            acc[b] = f4{0, 0, 0, 0};
+#pragma unroll
+            for (int n = 0; n < NF; ++n) mma(acc[b], sf[n], qf[n]);
+            acc[b] *= dec.in[16 * tb + col];
+            if (tb >= pw) {
+                f4 sc = {0, 0, 0, 0};
+#pragma unroll
+                for (int n = 0; n < NF; ++n) mma(sc, row_frag(s_k, SN, 16 * pw, 32 * n), qf[n]);
+                const int t = 16 * tb + col, s = 16 * pw + g4;
+                const float th = dec.c.hi[t], tl = dec.c.lo[t];
+                const f4 sh = *reinterpret_cast<const f4 *>(&dec.c.hi[s]), sl = *reinterpret_cast<const f4 *>(&dec.c.lo[s]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sc[r] *= a.scale * exp2_fast((th - sh[r]) + (tl - sl[r]));
+                if (pw == tb)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sc[r] = s + r <= t ? sc[r] : 0.0f;
+                // steps s, s + 2 and s + 1, s + 3 are neighbours in the order spread
+                const int at = t * SP + 32 * (pw >> 1) + 8 * (g4 >> 3) + 4 * (pw & 1) + (g4 >> 1 & 3);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    f2 v = {sc[r], sc[r + 2]};
+                    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                        for (int e = 0; e < PARTS; ++e) {
+                            const bf2 u = __builtin_convertvector(v, bf2);
+                            *reinterpret_cast<bf2 *>(&s_p[e][at + 16 * r]) = u;
+                            v -= __builtin_convertvector(u, f2);
+                        }
+                    } else {
+                        *reinterpret_cast<f2 *>(&s_p[0][at + 16 * r]) = v;
+                    }
                 }
-            } else {
-                *reinterpret_cast<f4 *>(&s_p[0][t * SP + s]) = acc;
             }
         }
-        if (w == NW - 1) {
-            s_g[(ch + 1 - ch0) & 1].set(log_decay(g_next), a.scale);
-            g_next = fetch_g(t0 + 2 * kC);
-        }
+        if (w == 3) s_g[(ch + 1 - ch0) & 1].set<true>(log_decay(g_now), a.scale);
         lds_barrier();
 
         Frag<T> vf[2];
-        f8 vw[2];
-        float probe = 0.0f;
 #pragma unroll
-        for (int sp = 0; sp < 2; ++sp) {
-            vf[sp] = col_frag(s_v, SV, 32 * sp, 16 * w);
-            vw[sp] = wide(vf[sp]);
+        for (int sp = 0; sp < 2; ++sp) vf[sp] = col_frag<true>(s_v, SV, 32 * sp, 16 * pw);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) probe = __builtin_fmaf(vw[sp][j], 0.0f, probe);
-        }
-        // A NaN or Inf in V would reach earlier steps through the zero scores of the later ones.
-        const bool finite = !__any(probe != 0.0f);
-        f4 acc[4];
+        for (int sp = 0; sp < 2; ++sp)
+            if (sp <= tw)
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) acc[tb] = f4{0, 0, 0, 0};
+                for (int e = 0; e < PARTS; ++e)
 #pragma unroll
-        for (int n = 0; n < NT / 32; ++n) {
-            const Split<T, 2> sv(join(S[2 * n], S[2 * n + 1]));
+                    for (int b = 0; b < 2; ++b) mma(acc[b], vf[sp], row_frag(s_p[e], SP, 16 * (2 * tw + b), 32 * sp));
+        // A NaN or Inf in V reaches earlier steps through the zero scores of the later ones; it also reaches each of the
+        // wavefront's last 16 steps, so these tell. Then the sums are taken again over the steps up to each step's own.
+        const float probe = (acc[1][0] * 0.0f + acc[1][1] * 0.0f) + (acc[1][2] * 0.0f + acc[1][3] * 0.0f);
+        if (__any(probe != 0.0f)) {
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                const int tl = 16 * (2 * tw + b) + col;
+                Frag<T> qf[NF];
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) mma(acc[tb], sv, row_frag(s_q, SN, 16 * tb, 32 * n));
-        }
+                for (int n = 0; n < NF; ++n) qf[n] = row_frag(s_q, SN, 16 * (2 * tw + b), 32 * n);
+                f4 v = {0, 0, 0, 0};
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-            const int tl = 16 * tb + col;
-            acc[tb] *= dec.in[tl];
-            if (finite) {
-#pragma unroll
-                for (int sp = 0; sp <= tb / 2; ++sp)
-#pragma unroll
-                    for (int e = 0; e < PARTS; ++e) mma(acc[tb], vf[sp], row_frag(s_p[e], SP, 16 * tb, 32 * sp));
-            } else {
+                for (int n = 0; n < NF; ++n) mma(v, *reinterpret_cast<const Frag<T> *>(&s_s[pw][n][l][0]), qf[n]);
+                v *= dec.in[tl];
                 for (int s = 0; s <= tl; ++s) {
                     float pr = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < PARTS; ++e) pr += widen(s_p[e][tl * SP + s]);
+                    for (int e = 0; e < PARTS; ++e) pr += widen(s_p[e][tl * SP + spread_of(s)]);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[tb][r] = __builtin_fmaf(pr, widen(s_v[s * SV + 16 * w + g4 + r]), acc[tb][r]);
+                    for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(pr, widen(s_v[s * SV + 16 * pw + g4 + r]), v[r]);
                 }
+                if (b == 0) acc[0] = v;
+                else acc[1] = v;
             }
-            if (tl >= some) acc[tb] = f4{0, 0, 0, 0};
-            store4<T, VEC>(out, o_t, tl, p_wave + g4, a.P, acc[tb]);
         }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) res[b] = some < kC && 16 * (2 * tw + b) + col >= some ? f4{0, 0, 0, 0} : acc[b];
 
-        // the state's update: V's columns scaled, three parts (the state is an fp32 result)
+        // the state's update: V's columns scaled, in three parts (the state is an fp32 result)
         const float end = dec.end;
 #pragma unroll
-        for (int i = 0; i < NT / 16; ++i) S[i] *= end;
+        for (int i = 0; i < NF; ++i) S[i] *= end;
 #pragma unroll
         for (int sp = 0; sp < 2; ++sp) {
-            const f4 u = *reinterpret_cast<const f4 *>(&dec.out[32 * sp + g4]);
-            const f4 v = *reinterpret_cast<const f4 *>(&dec.out[32 * sp + 16 + g4]);
-            const Split<T, 3> vs(vw[sp] * join(u, v));
+            const f4 u = *reinterpret_cast<const f4 *>(&dec.out[32 * sp + 2 * g4]);
+            const f4 v = *reinterpret_cast<const f4 *>(&dec.out[32 * sp + 2 * g4 + 4]);
+            const Split<T, 3> vs(wide(vf[sp]) * join(u, v));
 #pragma unroll
-            for (int i = 0; i < NT / 16; ++i) mma(S[i], col_frag(s_k, SN, 32 * sp, 16 * i), vs);
+            for (int i = 0; i < NF; ++i) mma(S[i], col_frag<true>(s_k, SN, 32 * sp, n0 + 16 * i), vs);
         }
+        put_state();  // its readers passed the last barrier
         lds_barrier();
     }
+    store_res();
 
     // past the row's end: outputs are zero, the state stays
     for (int64_t ch = chl > ch0 ? chl : ch0; ch < ch1; ++ch) {
-        const Buffer out = rows_buffer(op + ch * kC * o_t, o_t, rows_of(ch * kC, a.L), a.P);
+        const Buffer rest = rows_buffer(op + ch * kC * o_t, o_t, rows_of(ch * kC, a.L), a.P);
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) store4<T, VEC>(out, o_t, 16 * tb + col, p_wave + g4, a.P, f4{0, 0, 0, 0});
+        for (int b = 0; b < 2; ++b)
+            store4<T, VEC>(rest, o_t, 16 * (2 * tw + b) + col, p_wave + g4, a.P, f4{0, 0, 0, 0});
     }
 
     if (a.final_state && wk.seg == a.n_seg - 1 && p_lane < a.P) {
         float *dst = a.final_state + (wk.bh * a.P + p_lane) * a.N;
 #pragma unroll
-        for (int i = 0; i < NT / 16; ++i)
+        for (int i = 0; i < NF; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                if (16 * i + g4 + r < a.N) dst[16 * i + g4 + r] = S[i][r];
+                if (n0 + 16 * i + g4 + r < a.N) dst[n0 + 16 * i + g4 + r] = S[i][r];
     }
 }
 
@@ -256,7 +298,7 @@ __global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int
 
     Work wk = work_of<NW>(a, n_own);
     wk.seg += first_seg;
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, col = l & 15, g4 = 4 * (l >> 4);
+    const int tid = threadIdx.x, w = wave_id(), l = tid & 63, col = l & 15, g4 = 4 * (l >> 4);
     const int64_t len = row_length(a.lengths, wk.ib, a.L);
     int64_t g_stride;
     const float *gp = decays_of(a, wk, &g_stride);
@@ -273,16 +315,16 @@ __global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int
     const int64_t n_chunks = (a.L + kC - 1) / kC, live = (len + kC - 1) / kC;
     const int64_t ch0 = wk.seg * a.seg_chunks, ch1 = ch0 + a.seg_chunks < n_chunks ? ch0 + a.seg_chunks : n_chunks;
     const int64_t chl = ch1 < live ? ch1 : live;
-    Stage<T, NT, THREADS, VEC> rk;
-    Stage<T, PB, THREADS, VEC> rv;
+    Stage<T, NT, THREADS, VEC> rk((uint32_t)kt, 0, a.N);
+    Stage<T, PB, THREADS, VEC> rv((uint32_t)vt, p0, a.P);
     double passed = 0.0;  // in every wavefront: the sum of g over the chunks walked
     float g_next = 0.0f;
     const int64_t n = chl - ch0;
     auto start = [&](int64_t j) { return (REV ? ch0 + j : chl - 1 - j) * kC; };
     auto fetch = [&](int64_t t0) {
         const int rows = rows_of(t0, len);
-        rk.load(kp + t0 * kt, (uint32_t)kt, rows, 0, a.N);
-        rv.load(vp + t0 * vt, (uint32_t)vt, rows, p0, a.P);
+        rk.load(kp + t0 * kt, rows);
+        rv.load(vp + t0 * vt, rows);
     };
     auto fetch_g = [&](int64_t t0) { return load_g(gp + t0 * g_stride, (uint32_t)g_stride, rows_of(t0, len)); };
     if (n > 0) {
@@ -293,10 +335,10 @@ __global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int
         if (!VEC) fetch(start(j));
         rk.store(s_k);
         rv.store(s_v);
-        const double sum = wave_running_sum(log_decay(g_next)), total = lane_value(sum, 63);
+        const double sum = wave_running_sum(log_decay(g_next)), total = lane_value(sum, 63);  // before the next loads
         // the weight of the lane's step, from all chunks walked and from this one
         const float wt = (REV ? a.scale : 1.0f) * exp_of((float)(passed + (REV ? sum : total - sum)));
-        if (w == 0) s_g.out[l] = wt;
+        if (w == 0) s_g.out[spread_of(l)] = wt;
         passed += total;
         lds_barrier();
         if (j + 1 < n) {
@@ -305,19 +347,19 @@ __global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int
         }
 #pragma unroll
         for (int sp = 0; sp < 2; ++sp) {
-            const f4 u = *reinterpret_cast<const f4 *>(&s_g.out[32 * sp + g4]);
-            const f4 v = *reinterpret_cast<const f4 *>(&s_g.out[32 * sp + 16 + g4]);
-            const Split<T, 3> vs(wide(col_frag(s_v, SV, 32 * sp, 16 * w)) * join(u, v));
+            const f4 u = *reinterpret_cast<const f4 *>(&s_g.out[32 * sp + 2 * g4]);
+            const f4 v = *reinterpret_cast<const f4 *>(&s_g.out[32 * sp + 2 * g4 + 4]);
+            const Split<T, 3> vs(wide(col_frag<true>(s_v, SV, 32 * sp, 16 * w)) * join(u, v));
 #pragma unroll
-            for (int i = 0; i < NT / 16; ++i) mma(S[i], col_frag(s_k, SN, 32 * sp, 16 * i), vs);
+            for (int i = 0; i < NT / 16; ++i) mma(S[i], col_frag<true>(s_k, SN, 32 * sp, 16 * i), vs);
         }
         lds_barrier();
     }
     const int64_t Pp = (a.P + kPB - 1) / kPB * kPB, at = wk.bh * a.n_seg + wk.seg, p = p0 + 16 * w + col;
     if (p < Pp) {
-        float *dst = (REV ? a.E : a.S) + (at * Pp + p) * NT + g4;
+        float *dst = (REV ? a.E : a.S) + (at * Pp + p) * NT;
 #pragma unroll
-        for (int i = 0; i < NT / 16; ++i) *reinterpret_cast<f4 *>(dst + 16 * i) = S[i];
+        for (int i = 0; i < NT / 16; ++i) *reinterpret_cast<f4 *>(dst + 16 * i + g4) = S[i];
     }
     if (tid == 0 && p0 == 0) a.gsum[at] = passed;
 }
@@ -400,11 +442,9 @@ hipError_t states(const LinAttnLaunch &p, bool adjoint, int64_t first, int64_t n
 
 template <typename T>
 hipError_t outputs(const LinAttnLaunch &p, hipStream_t stream) {
-    const dim3 grid((unsigned)(p.b * p.H * p.n_seg) * value_blocks(p));
-    return by_width(p, [&](auto nt, auto nw, auto vec) {
-        constexpr int NT = decltype(nt)::value, NW = decltype(nw)::value;
-        constexpr bool VEC = decltype(vec)::value;
-        la_out_kernel<T, NT, NW, VEC><<<grid, 64 * NW, 0, stream>>>(p);
+    const dim3 grid((unsigned)(p.b * p.H * p.n_seg) * (unsigned)((p.P + kPB - 1) / kPB));
+    return by_width(p, [&](auto nt, auto, auto vec) {
+        la_out_kernel<T, decltype(nt)::value, decltype(vec)::value><<<grid, kOutThreads, 0, stream>>>(p);
         return hipGetLastError();
     });
 }

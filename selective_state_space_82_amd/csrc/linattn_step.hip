@@ -21,7 +21,7 @@ __global__ __launch_bounds__(kThreads) void la_step_kernel(float *state, LinAttn
     id /= npb;
     const int h = (int)(id % a.H), grp = h / (a.H / a.G);
     const int64_t ib = id / a.H;
-    const int w = threadIdx.x >> 6, l = threadIdx.x & 63, lr = l % LR;
+    const int w = wave_id(), l = threadIdx.x & 63, lr = l % LR;
     const int p0 = pb * kRows + 16 * w + l / LR;
 
     float *sp = state + (ib * a.H + h) * (int64_t)a.P * a.N;

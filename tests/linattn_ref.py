@@ -8,8 +8,9 @@ exact, is off by at most n·u·M. n counts, for every path from an input to the 
 (N + P), the steps of a chunk (64), and per chunk passed the state's scaling and adding (4); and the decays: e^d is
 taken of a difference of sums rounded to fp32 and multiplied by log2 e, so it is off by (2|d| + 2)·u, summed over the
 path 2·104 + 2 per chunk at most (past |d| = 104 e^d is below fp32's range, and the product is 0, an absolute error
-below 2^-125 times the operands). bf16 adds the operands cut into two parts (2^-16 each, at most three on a path) and
-the rounding of the result (2^-8 of it).
+below 2^-125 times the operands). bf16 adds, for results in bf16, the one rounding of the state or adjoint on a path
+through it (2^-8 of the product), the scores cut into two parts (2^-16, at most two on a path), and the rounding of the
+result (2^-8 of it); fp32 results take their fp32 operands in three parts (2^-24).
 """
 import math
 
@@ -58,7 +59,7 @@ def paths(L, N, P, ratio=1):
 def bound(ref, mag, dtype, L, N, P, out_dtype=None, ratio=1):
     """How far a result may be from `ref`, element by element; dtype: of the inputs, out_dtype: of the result."""
     out_dtype = out_dtype or dtype
-    parts = 3 * 2.0 ** -16 if dtype == torch.bfloat16 and out_dtype == torch.bfloat16 else 0.0
+    parts = 2.0 ** -8 + 2 * 2.0 ** -16 if dtype == torch.bfloat16 and out_dtype == torch.bfloat16 else 0.0
     n = paths(L, N, P, ratio)
     return HALF[out_dtype] * ref.abs() + (parts + (n + 8) * U) * mag + 2.0 ** -110
 
