@@ -6,6 +6,7 @@ or the tensors are not on a ROCm GPU, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -502,7 +503,7 @@ def _check_rows(name, t, shape, dtype, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
@@ -548,8 +549,20 @@ def _workspace(bytes_, device):
 
 
 def _on_device(device):
-    """Makes `device` current for the launches of a call (a no-op where it is)."""
-    return torch.cuda.device(device)
+    """Makes `device` current for the launches of a call (nothing to do where it is)."""
+    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _raw_stream(device) -> int:
+    """The current stream's handle, without a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def ssm_linattn_workspace(b, L, H, G, N, P, dtype=torch.float32, *, gradient=False, g_per_step=True) -> int:
@@ -586,9 +599,9 @@ def ssm_linattn_fwd(q, k, v, g, *, scale=1.0, initial_state=None, lengths=None, 
         need = ctypes.c_int64()
         _raise(lib().ssm_linattn_workspace(0, b, L, H, G, N, P, code, per_step, ctypes.byref(need)), "ssm_linattn_fwd")
         ws = _workspace(need.value, dev)
-        status = lib().ssm_linattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), per_step, float(scale), _ptr(initial_state),
-                                       _ptr(lengths), _ptr(o), _ptr(final_state), b, L, H, G, N, P, code,
-                                       _linattn_strides(q, k, v), _ptr(ws), need.value, _stream(dev))
+        status = lib().ssm_linattn_fwd(_at(q), _at(k), _at(v), _at(g), per_step, float(scale), _at(initial_state),
+                                       _at(lengths), _at(o), _at(final_state), b, L, H, G, N, P, code,
+                                       _linattn_strides(q, k, v), _at(ws), need.value, _raw_stream(dev))
     _raise(status, "ssm_linattn_fwd")
     return o, final_state
 
@@ -608,8 +621,8 @@ def ssm_linattn_step(state, q, k, v, g, *, scale=1.0, o=None):
         if o is None:
             o = torch.empty((b, H, P), dtype=v.dtype, device=dev)
         _check("o", o, (b, H, P), v.dtype, dev)
-        status = lib().ssm_linattn_step(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_step, float(scale), _ptr(o),
-                                        b, H, G, N, P, code, _linattn_strides(q, k, v), _stream(dev))
+        status = lib().ssm_linattn_step(_at(state), _at(q), _at(k), _at(v), _at(g), per_step, float(scale), _at(o),
+                                        b, H, G, N, P, code, _linattn_strides(q, k, v), _raw_stream(dev))
     _raise(status, "ssm_linattn_step")
     return o
 
@@ -635,10 +648,10 @@ def ssm_linattn_bwd(q, k, v, g, *, do, scale=1.0, initial_state=None, d_final_st
         need = ctypes.c_int64()
         _raise(lib().ssm_linattn_workspace(1, b, L, H, G, N, P, code, per_step, ctypes.byref(need)), "ssm_linattn_bwd")
         ws = _workspace(need.value, dev)
-        status = lib().ssm_linattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), per_step, float(scale), _ptr(initial_state),
-                                       _ptr(lengths), _ptr(do), _ptr(d_final_state), _ptr(out["dq"]), _ptr(out["dk"]),
-                                       _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["d_initial_state"]), b, L, H, G, N, P,
-                                       code, _linattn_strides(q, k, v, do), _ptr(ws), need.value, _stream(dev))
+        status = lib().ssm_linattn_bwd(_at(q), _at(k), _at(v), _at(g), per_step, float(scale), _at(initial_state),
+                                       _at(lengths), _at(do), _at(d_final_state), _at(out["dq"]), _at(out["dk"]),
+                                       _at(out["dv"]), _at(out["dg"]), _at(out["d_initial_state"]), b, L, H, G, N, P,
+                                       code, _linattn_strides(q, k, v, do), _at(ws), need.value, _raw_stream(dev))
     _raise(status, "ssm_linattn_bwd")
     return out
 
@@ -680,8 +693,8 @@ def ssm_layernorm_fwd(x, w=None, bias=None, *, eps=1e-5, y=None, return_stats=Fa
         _check("y", y, x.shape, x.dtype, dev)
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if return_stats else None
         rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if return_stats else None
-        status = lib().ssm_layernorm_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), rows,
-                                         x.shape[-1], k, stride, float(eps), code, _stream(dev))
+        status = lib().ssm_layernorm_fwd(_at(x), _at(w), _at(bias), _at(y), _at(mean), _at(rstd), rows,
+                                         x.shape[-1], k, stride, float(eps), code, _raw_stream(dev))
     _raise(status, "ssm_layernorm_fwd")
     return (y, mean, rstd) if return_stats else y
 
@@ -715,8 +728,8 @@ def ssm_layernorm_bwd(x, w=None, *, dy, mean, rstd, want_dw=True, want_dbias=Tru
         if want_dw or want_dbias:
             _raise(lib().ssm_layernorm_bwd_workspace(rows, d, k, ctypes.byref(need)), "ssm_layernorm_bwd")
         ws = _workspace(need.value, dev)
-        status = lib().ssm_layernorm_bwd(_ptr(x), _ptr(w), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(out["dx"]),
-                                         _ptr(out["dw"]), _ptr(out["dbias"]), rows, d, k, stride, dy_stride, code,
-                                         _ptr(ws), need.value, _stream(dev))
+        status = lib().ssm_layernorm_bwd(_at(x), _at(w), _at(dy), _at(mean), _at(rstd), _at(out["dx"]),
+                                         _at(out["dw"]), _at(out["dbias"]), rows, d, k, stride, dy_stride, code,
+                                         _at(ws), need.value, _raw_stream(dev))
     _raise(status, "ssm_layernorm_bwd")
     return out

@@ -22,10 +22,10 @@ typedef float f8 __attribute__((ext_vector_type(8)));
 template <typename T> constexpr int kV = 16 / sizeof(T);
 
 // A 16-byte piece of a row as fp32, zeros past d.
-template <typename T>
-__device__ __forceinline__ uint4 load_piece(const T *row, int c, int d, bool vec) {
+template <typename T, bool VEC>
+__device__ __forceinline__ uint4 load_piece(const T *row, int c, int d) {
     uint4 w = make_uint4(0, 0, 0, 0);
-    if (vec) {
+    if constexpr (VEC) {
         if (c < d) w = *reinterpret_cast<const uint4 *>(row + c);
     } else {
         T e[kV<T>];
@@ -43,9 +43,9 @@ template <> __device__ __forceinline__ void spread<uint16_t>(const uint4 &w, flo
     f[0] = bf16_lo(w.x); f[1] = bf16_hi(w.x); f[2] = bf16_lo(w.y); f[3] = bf16_hi(w.y);
     f[4] = bf16_lo(w.z); f[5] = bf16_hi(w.z); f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
 }
-template <typename T>
-__device__ __forceinline__ void store_piece(T *row, int c, int d, bool vec, const float *f) {
-    if (vec) {
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_piece(T *row, int c, int d, const float *f) {
+    if constexpr (VEC) {
         if (c < d) {
             if constexpr (sizeof(T) == 4) {
                 *reinterpret_cast<f4 *>(row + c) = f4{f[0], f[1], f[2], f[3]};
@@ -102,7 +102,7 @@ struct Rows {
     }
 };
 
-template <typename T, int LR, int K>
+template <typename T, int LR, int K, bool VEC>
 __global__ __launch_bounds__((Lay<T, LR, K>::THREADS)) void norm_fwd_kernel(NormLaunch a) {
     typedef Lay<T, LR, K> Y;
     __shared__ float2 s_buf[2][16];
@@ -119,19 +119,24 @@ __global__ __launch_bounds__((Lay<T, LR, K>::THREADS)) void norm_fwd_kernel(Norm
             w[i * Y::V + j] = a.w && c < d ? a.w[rows.wr * d + c] : 1.0f;
             bias[i * Y::V + j] = a.bias && c < d ? a.bias[rows.wr * d + c] : 0.0f;
         }
+    uint4 ahead[K];  // the next row's pieces, fetched while this one is computed
+    auto fetch = [&](int64_t m) {
+        const T *x = static_cast<const T *>(a.x) + (m * a.w_rows + rows.wr) * a.x_stride;
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            ahead[i] = m < rows.count ? load_piece<T, VEC>(x, Y::col(i), d) : make_uint4(0, 0, 0, 0);
+    };
+    fetch(rows.first);
     // all lanes of a workgroup take as many turns as its first row, so that its barriers meet
     for (int64_t m0 = rows.first - threadIdx.x / LR; m0 < rows.count; m0 += rows.step) {
         const int64_t m = m0 + threadIdx.x / LR;
         const bool live = m < rows.count;
         const int64_t row = m * a.w_rows + rows.wr;
-        const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
         float f[Y::E];
         float sum = 0.0f, none = 0.0f;
 #pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const uint4 p = live ? load_piece<T>(x, Y::col(i), d, a.vec) : make_uint4(0, 0, 0, 0);
-            spread<T>(p, f + i * Y::V);
-        }
+        for (int i = 0; i < K; ++i) spread<T>(ahead[i], f + i * Y::V);
+        fetch(m + rows.step);
 #pragma unroll
         for (int e = 0; e < Y::E; ++e) sum += f[e];
         row_sums<LR>(sum, none, s_buf, turn);
@@ -161,12 +166,12 @@ __global__ __launch_bounds__((Lay<T, LR, K>::THREADS)) void norm_fwd_kernel(Norm
                 const int e = i * Y::V + j;
                 o[j] = __builtin_fmaf(f[e] * rstd, w[e], bias[e]);
             }
-            store_piece<T>(y, Y::col(i), d, a.vec, o);
+            store_piece<T, VEC>(y, Y::col(i), d, o);
         }
     }
 }
 
-template <typename T, int LR, int K>
+template <typename T, int LR, int K, bool VEC>
 __global__ __launch_bounds__((Lay<T, LR, K>::THREADS)) void norm_bwd_kernel(NormLaunch a) {
     typedef Lay<T, LR, K> Y;
     __shared__ float2 s_buf[2][16];
@@ -184,25 +189,37 @@ __global__ __launch_bounds__((Lay<T, LR, K>::THREADS)) void norm_bwd_kernel(Norm
             w[e] = a.w && c < d ? a.w[rows.wr * d + c] : 1.0f;
             dw[e] = db[e] = 0.0f;
         }
+    uint4 px[K], pd[K];  // the next row's pieces, fetched while this one is computed
+    float next_mean, next_rstd;
+    auto fetch = [&](int64_t m) {
+        const int64_t row = m * a.w_rows + rows.wr;
+        const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
+        const T *dy = static_cast<const T *>(a.dy) + row * a.dy_stride;
+        const bool live = m < rows.count;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            px[i] = live ? load_piece<T, VEC>(x, Y::col(i), d) : make_uint4(0, 0, 0, 0);
+            pd[i] = live ? load_piece<T, VEC>(dy, Y::col(i), d) : make_uint4(0, 0, 0, 0);
+        }
+        next_mean = live ? a.mean_in[row] : 0.0f;
+        next_rstd = live ? a.rstd_in[row] : 0.0f;
+    };
+    fetch(rows.first);
     for (int64_t m0 = rows.first - slot; m0 < rows.count; m0 += rows.step) {
         const int64_t m = m0 + slot;
         const bool live = m < rows.count;
         const int64_t row = m * a.w_rows + rows.wr;
-        const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
-        const T *dy = static_cast<const T *>(a.dy) + row * a.dy_stride;
-        uint4 px[K], pd[K];
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            px[i] = live ? load_piece<T>(x, Y::col(i), d, a.vec) : make_uint4(0, 0, 0, 0);
-            pd[i] = live ? load_piece<T>(dy, Y::col(i), d, a.vec) : make_uint4(0, 0, 0, 0);
-        }
-        const float mean = live ? a.mean_in[row] : 0.0f, rstd = live ? a.rstd_in[row] : 0.0f;
+        const float mean = next_mean, rstd = next_rstd;
         float xh[Y::E], g[Y::E];
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < K; ++i) {
             spread<T>(px[i], xh + i * Y::V);
             spread<T>(pd[i], g + i * Y::V);
+        }
+        fetch(m + rows.step);
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
 #pragma unroll
             for (int j = 0; j < Y::V; ++j) {
                 const int e = i * Y::V + j;
@@ -227,7 +244,7 @@ __global__ __launch_bounds__((Lay<T, LR, K>::THREADS)) void norm_bwd_kernel(Norm
                 const int e = i * Y::V + j;
                 o[j] = rstd * (g[e] - s1 - xh[e] * s2);
             }
-            store_piece<T>(dx, Y::col(i), d, a.vec, o);
+            store_piece<T, VEC>(dx, Y::col(i), d, o);
         }
     }
     if (!a.part) return;
@@ -259,27 +276,36 @@ __global__ __launch_bounds__((Lay<T, LR, K>::THREADS)) void norm_bwd_kernel(Norm
     }
 }
 
-// dw and dbias from the workgroups' partial sums: 64 columns of one weight row per workgroup, 4 interleaved runs of
-// partial sums each, joined in order.
-__global__ __launch_bounds__(256) void norm_part_sum_kernel(const float *part, float *dw, float *dbias, int64_t d,
-                                                            int64_t w_rows, int64_t per) {
-    __shared__ float s[2][4][64];
-    const int64_t blocks = (d + 63) / 64, wr = blockIdx.x / blocks, c = blockIdx.x % blocks * 64 + (threadIdx.x & 63);
-    const int run = threadIdx.x >> 6;
+// dw and dbias from the workgroups' partial sums: 16 columns of one weight row per workgroup (64-byte pieces of the
+// partial rows), 64 interleaved runs of partial sums each, joined in order. With 64 columns and 4 runs, 12 workgroups of
+// 256 dependent loads each took 78 us for 768 columns and 1024 partial rows.
+__global__ __launch_bounds__(1024) void norm_part_sum_kernel(const float *part, float *dw, float *dbias, int64_t d,
+                                                             int64_t w_rows, int64_t per) {
+    __shared__ float s[2][64][17];
+    const int64_t blocks = (d + 15) / 16, wr = blockIdx.x / blocks;
+    const int col = threadIdx.x & 15, run = threadIdx.x >> 4;
+    const int64_t c = blockIdx.x % blocks * 16 + col;
     float u = 0.0f, v = 0.0f;
-    if (c < d)
-        for (int64_t i = run; i < per; i += 4) {
+    if (c < d) {
+#pragma unroll 4
+        for (int64_t i = run; i < per; i += 64) {
             const float *p = part + 2 * (i * w_rows + wr) * d + c;
             u += p[0];
             v += p[d];
         }
-    s[0][run][threadIdx.x & 63] = u;
-    s[1][run][threadIdx.x & 63] = v;
-    __syncthreads();
-    if (run < 2 && c < d) {
-        const float *t = s[run][0] + (threadIdx.x & 63);
-        float *out = run ? dbias : dw;
-        if (out) out[wr * d + c] = (t[0] + t[64]) + (t[128] + t[192]);
+    }
+    s[0][run][col] = u;
+    s[1][run][col] = v;
+    for (int h = 32; h > 0; h >>= 1) {
+        __syncthreads();
+        if (run < h) {
+            s[0][run][col] += s[0][run + h][col];
+            s[1][run][col] += s[1][run + h][col];
+        }
+    }
+    if (run == 0 && c < d) {
+        if (dw) dw[wr * d + c] = s[0][0][col];
+        if (dbias) dbias[wr * d + c] = s[1][0][col];
     }
 }
 
@@ -298,7 +324,8 @@ int64_t groups(int64_t rows, int64_t w_rows, int slots, int64_t most) {
 }
 constexpr int64_t kFwdGroups = 2048, kBwdGroups = 1024;
 
-// f(LR, K) for the fewest lanes that hold a row of d in at most 4 pieces each.
+// f(LR, K): the lanes of a row and their pieces; at most 16 elements of a row to a lane, so that the gradient's row,
+// its weight and its two partial sums stay in registers with the next row on its way.
 template <typename T, typename F> hipError_t by_width(int64_t d, F f) {
     const int64_t n = (d + kV<T> - 1) / kV<T>;
 #define SSM_LN(LR, K) if (n <= (LR) * (K)) return f(std::integral_constant<int, LR>{}, std::integral_constant<int, K>{})
@@ -306,9 +333,11 @@ template <typename T, typename F> hipError_t by_width(int64_t d, F f) {
     SSM_LN(16, 2);
     SSM_LN(64, 1);
     SSM_LN(64, 2);
-    SSM_LN(64, 4);
+    if constexpr (sizeof(T) == 4) SSM_LN(64, 4);
+    SSM_LN(256, 1);
     SSM_LN(256, 2);
-    SSM_LN(256, 4);
+    if constexpr (sizeof(T) == 4) SSM_LN(256, 4);
+    SSM_LN(1024, 1);
     SSM_LN(1024, 2);
     if constexpr (sizeof(T) == 4) SSM_LN(1024, 4);
 #undef SSM_LN
@@ -320,7 +349,8 @@ template <typename T> hipError_t fwd(const NormLaunch &p, hipStream_t stream) {
         constexpr int LR = decltype(lr)::value, K = decltype(k)::value;
         typedef Lay<T, LR, K> Y;
         const int64_t n = groups(p.rows, p.w_rows, Y::SLOTS, kFwdGroups) * p.w_rows;
-        norm_fwd_kernel<T, LR, K><<<dim3((unsigned)n), Y::THREADS, 0, stream>>>(p);
+        if (p.vec) norm_fwd_kernel<T, LR, K, true><<<dim3((unsigned)n), Y::THREADS, 0, stream>>>(p);
+        else norm_fwd_kernel<T, LR, K, false><<<dim3((unsigned)n), Y::THREADS, 0, stream>>>(p);
         return hipGetLastError();
     });
 }
@@ -330,10 +360,12 @@ template <typename T> hipError_t bwd(const NormLaunch &p, hipStream_t stream) {
         constexpr int LR = decltype(lr)::value, K = decltype(k)::value;
         typedef Lay<T, LR, K> Y;
         const int64_t per = groups(p.rows, p.w_rows, Y::SLOTS, kBwdGroups);
-        norm_bwd_kernel<T, LR, K><<<dim3((unsigned)(per * p.w_rows)), Y::THREADS, 0, stream>>>(p);
+        const dim3 grid((unsigned)(per * p.w_rows));
+        if (p.vec) norm_bwd_kernel<T, LR, K, true><<<grid, Y::THREADS, 0, stream>>>(p);
+        else norm_bwd_kernel<T, LR, K, false><<<grid, Y::THREADS, 0, stream>>>(p);
         hipError_t e = hipGetLastError();
         if (e == hipSuccess && p.part) {
-            norm_part_sum_kernel<<<dim3((unsigned)(p.w_rows * ((p.d + 63) / 64))), 256, 0, stream>>>(
+            norm_part_sum_kernel<<<dim3((unsigned)(p.w_rows * ((p.d + 15) / 16))), 1024, 0, stream>>>(
                 p.part, p.dw, p.dbias, p.d, p.w_rows, per);
             e = hipGetLastError();
         }
