@@ -250,8 +250,9 @@ inline int linattn_nt(int64_t N) { return N <= 32 ? 32 : N <= 64 ? 64 : 128; }
 hipError_t launch_linattn_fwd(const LinAttnLaunch &p, hipStream_t stream);
 hipError_t launch_linattn_bwd(const LinAttnLaunch &p, hipStream_t stream);
 hipError_t launch_linattn_step(float *state, const LinAttnLaunch &p, hipStream_t stream);
-// The segments' states from their own (launch_linattn_states) to the entering (leaving) ones.
-hipError_t launch_linattn_states(const LinAttnLaunch &p, bool adjoint, int64_t first_seg, int64_t n, hipStream_t stream);
+// The own states of the first n_states segments and the own adjoints of those from first_adjoint on, in one launch.
+hipError_t launch_linattn_states(const LinAttnLaunch &p, int64_t n_states, int64_t first_adjoint, hipStream_t stream);
+// From own states (and, if `adjoint`, own adjoints) to those entering (leaving) the segments, in place, in one launch.
 hipError_t launch_linattn_carry(const LinAttnLaunch &p, bool adjoint, hipStream_t stream);
 
 // Layer norm (validated by the ABI layer).

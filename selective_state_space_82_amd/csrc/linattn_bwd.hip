@@ -19,17 +19,22 @@ namespace ssm {
 namespace la {
 namespace {
 
-// Sum over the four 16-lane groups of a wavefront (same column), for every lane.
+// Sum over the four 16-lane groups of a wavefront (same column), for every lane: the rows of 16 lanes swapped pairwise.
 __device__ __forceinline__ float sum_groups(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
-// Sum over the 16 lanes of a group.
+// Sum over the 16 lanes of a group, for every lane: rotations within the row.
+template <int N> __device__ __forceinline__ float row_rotate(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x120 + N, 0xf, 0xf, false));
+}
 __device__ __forceinline__ float sum_cols(float v) {
-    v += __shfl_xor(v, 1);
-    v += __shfl_xor(v, 2);
-    v += __shfl_xor(v, 4);
-    return v + __shfl_xor(v, 8);
+    v += row_rotate<8>(v);
+    v += row_rotate<4>(v);
+    v += row_rotate<2>(v);
+    return v + row_rotate<1>(v);
 }
 
 // ---- one workgroup per (row, head, chunk), all value columns -----------------------------------------------------
@@ -39,14 +44,16 @@ __device__ __forceinline__ float sum_cols(float v) {
 template <typename T, int NT, bool VEC>
 __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
     constexpr int SN = NT + kPad<T>, SP = kC + kPad<T>, SV = kPB + kPad<T>;
-    constexpr int PARTS = sizeof(T) == 2 ? 2 : 1;
     constexpr int TILES = NT / 16, JOBS = 2 * TILES / 4;
+    constexpr bool AHEAD = NT < 128;  // at 128 they take 96 registers
     __shared__ __align__(16) T s_q[kC * SN];
     __shared__ __align__(16) T s_k[kC * SN];
     __shared__ __align__(16) T s_v[kC * SV];
     __shared__ __align__(16) T s_d[kC * SV];
-    __shared__ __align__(16) T s_a1[PARTS][kC * SP];  // [t][s]
-    __shared__ __align__(16) T s_a2[PARTS][kC * SP];
+    // [t][s]; bf16: one part, half a step of bf16 on each product's size, as the results' own rounding (the terms of dg
+    // are taken before it)
+    __shared__ __align__(16) T s_a1[kC * SP];
+    __shared__ __align__(16) T s_a2[kC * SP];
     __shared__ Decays s_g;
     __shared__ float s_row[4][kC], s_col[4][kC], s_x[TILES][kC], s_y[4][kC], s_z[4];
 
@@ -108,12 +115,33 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
     // the tiles right of the diagonal that a 32-step contraction touches
     for (int i = tid; i < 2 * 16 * 16; i += kThreads) {
         const int t = 32 * (i >> 8) + ((i >> 4) & 15), s = 32 * (i >> 8) + 16 + (i & 15);
-#pragma unroll
-        for (int e = 0; e < PARTS; ++e) {
-            s_a1[e][t * SP + s] = (T)0;
-            s_a2[e][t * SP + s] = (T)0;
-        }
+        s_a1[t * SP + s] = (T)0;
+        s_a2[t * SP + s] = (T)0;
     }
+
+    // The wavefront's parts of the entering state and the leaving adjoint, for the first 64 value columns fetched before
+    // the scores are formed: E with a lane's four values along N (for dv), S and E with eight along P (for dq, dk).
+    const int64_t Pp = (int64_t)npb * kPB;
+    const float *Sp = a.S + (bh * a.n_seg + ch) * Pp * NT;
+    const float *Ep = a.E + (bh * a.n_seg + ch) * Pp * NT;
+    f4 e[NT / 16];
+    f8 x[JOBS][2];
+    auto fetch_states = [&](int pb) {
+        const int64_t p = pb * kPB + 16 * w + col;
+#pragma unroll
+        for (int i = 0; i < NT / 16; ++i) e[i] = *reinterpret_cast<const f4 *>(Ep + p * NT + 16 * i + g4);
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j) {
+            const int job = w + 4 * j;
+            const bool is_q = job < TILES;
+            const float *src = (is_q ? Sp : Ep) + (pb * kPB + 2 * g4) * NT + 16 * (is_q ? job : job - TILES) + col;
+#pragma unroll
+            for (int pp = 0; pp < 2; ++pp)
+#pragma unroll
+                for (int r = 0; r < 8; ++r) x[j][pp][r] = src[(32 * pp + r) * NT];
+        }
+    };
+    if (AHEAD) fetch_states(0);
 
     // scores: tile (tb, sb) holds D[s][t] of q·k and do·v
     f4 aq[3], ad[3];
@@ -162,24 +190,15 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
             row = sum_groups(row);
             if (l < 16) s_row[sb][t] = row;
             if constexpr (sizeof(T) == 2) {
-#pragma unroll
-                for (int e = 0; e < PARTS; ++e) {
-                    const bf4 u = __builtin_convertvector(a1, bf4), v = __builtin_convertvector(a2, bf4);
-                    *reinterpret_cast<bf4 *>(&s_a1[e][t * SP + s]) = u;
-                    *reinterpret_cast<bf4 *>(&s_a2[e][t * SP + s]) = v;
-                    a1 -= __builtin_convertvector(u, f4);
-                    a2 -= __builtin_convertvector(v, f4);
-                }
+                *reinterpret_cast<bf4 *>(&s_a1[t * SP + s]) = __builtin_convertvector(a1, bf4);
+                *reinterpret_cast<bf4 *>(&s_a2[t * SP + s]) = __builtin_convertvector(a2, bf4);
             } else {
-                *reinterpret_cast<f4 *>(&s_a1[0][t * SP + s]) = a1;
-                *reinterpret_cast<f4 *>(&s_a2[0][t * SP + s]) = a2;
+                *reinterpret_cast<f4 *>(&s_a1[t * SP + s]) = a1;
+                *reinterpret_cast<f4 *>(&s_a2[t * SP + s]) = a2;
             }
         }
     }
 
-    const int64_t Pp = (int64_t)npb * kPB;
-    const float *Sp = a.S + (bh * a.n_seg + ch) * Pp * NT;
-    const float *Ep = a.E + (bh * a.n_seg + ch) * Pp * NT;
     f4 acc[JOBS][4];
 #pragma unroll
     for (int j = 0; j < JOBS; ++j)
@@ -188,6 +207,7 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
     float y[4] = {0, 0, 0, 0}, z = 0.0f;
     for (int pb = 0; pb < npb; ++pb) {
         lds_barrier();
+        if (!AHEAD || pb) fetch_states(pb);
         if (npb > 1) {
             Stage<T, kPB, kThreads, VEC> v((uint32_t)a.v_t, pb * kPB, a.P), d((uint32_t)a.do_t, pb * kPB, a.P);
             v.load(vp + t0 * a.v_t, rows_of(t0, len));
@@ -198,13 +218,20 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
         }
         // dv: value columns 16w ..
         {
-            const int64_t p = pb * kPB + 16 * w + col;
-            f4 e[NT / 16];
+            if (JOBS == 1) {  // a wavefront has dq's state or dk's adjoint, not both
+                const int64_t p = pb * kPB + 16 * w + col;
 #pragma unroll
-            for (int i = 0; i < NT / 16; ++i) {
-                e[i] = *reinterpret_cast<const f4 *>(Ep + p * NT + 16 * i + g4);
-                const f4 s = *reinterpret_cast<const f4 *>(Sp + p * NT + 16 * i + g4);
-                z += (e[i][0] * s[0] + e[i][1] * s[1]) + (e[i][2] * s[2] + e[i][3] * s[3]);
+                for (int i = 0; i < NT / 16; ++i) {
+                    const f4 s = *reinterpret_cast<const f4 *>(Sp + p * NT + 16 * i + g4);
+                    z += (e[i][0] * s[0] + e[i][1] * s[1]) + (e[i][2] * s[2] + e[i][3] * s[3]);
+                }
+            } else {  // the same columns of N in its job of dq and in that of dk
+#pragma unroll
+                for (int j = 0; j < JOBS / 2; ++j)
+#pragma unroll
+                    for (int pp = 0; pp < 2; ++pp)
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) z = __builtin_fmaf(x[j][pp][r], x[j + JOBS / 2][pp][r], z);
             }
             f4 dv[4];
 #pragma unroll
@@ -222,11 +249,8 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
                 dv[b] *= s_g.out[s];
                 const T *vr = &s_v[s * SV + 16 * w + g4];
                 y[b] += (dv[b][0] * widen(vr[0]) + dv[b][1] * widen(vr[1])) + (dv[b][2] * widen(vr[2]) + dv[b][3] * widen(vr[3]));
-#pragma unroll
-                for (int part_i = 0; part_i < PARTS; ++part_i) {
-                    if (b < 2) mma(dv[b], d0, col_frag(s_a1[part_i], SP, 0, 16 * b));
-                    mma(dv[b], d1, col_frag(s_a1[part_i], SP, 32, 16 * b));
-                }
+                if (b < 2) mma(dv[b], d0, col_frag(s_a1, SP, 0, 16 * b));
+                mma(dv[b], d1, col_frag(s_a1, SP, 32, 16 * b));
                 if (t0 + s >= len) dv[b] = f4{0, 0, 0, 0};
                 store4<T, VEC>(dv_buf, (uint32_t)dv_t, s, pb * kPB + 16 * w + g4, a.P, dv[b]);
             }
@@ -236,15 +260,10 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
         for (int j = 0; j < JOBS; ++j) {
             const int job = w + 4 * j;
             const bool is_q = job < TILES;
-            const int n0 = 16 * (is_q ? job : job - TILES);
-            const float *src = (is_q ? Sp : Ep) + (pb * kPB + 2 * g4) * NT + n0 + col;
             const T *tile = is_q ? s_d : s_v;
 #pragma unroll
             for (int pp = 0; pp < 2; ++pp) {
-                f8 x;
-#pragma unroll
-                for (int r = 0; r < 8; ++r) x[r] = src[(32 * pp + r) * NT];
-                const Split<T, 3> xs(x);
+                const Split<T, 3> xs(x[j][pp]);
 #pragma unroll
                 for (int b = 0; b < 4; ++b) mma(acc[j][b], xs, row_frag(tile, SV, 16 * b, 32 * pp));
             }
@@ -266,17 +285,11 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
                 const T *qr = &s_q[t * SN + n0 + g4];
                 const float x = sum_groups((v[0] * widen(qr[0]) + v[1] * widen(qr[1])) + (v[2] * widen(qr[2]) + v[3] * widen(qr[3])));
                 if (l < 16) s_x[job][t] = x;
-#pragma unroll
-                for (int e = 0; e < PARTS; ++e) {
-                    mma(v, f0, row_frag(s_a2[e], SP, 16 * b, 0));
-                    if (b >= 2) mma(v, f1, row_frag(s_a2[e], SP, 16 * b, 32));
-                }
+                mma(v, f0, row_frag(s_a2, SP, 16 * b, 0));
+                if (b >= 2) mma(v, f1, row_frag(s_a2, SP, 16 * b, 32));
             } else {
-#pragma unroll
-                for (int e = 0; e < PARTS; ++e) {
-                    if (b < 2) mma(v, f0, col_frag(s_a2[e], SP, 0, 16 * b));
-                    mma(v, f1, col_frag(s_a2[e], SP, 32, 16 * b));
-                }
+                if (b < 2) mma(v, f0, col_frag(s_a2, SP, 0, 16 * b));
+                mma(v, f1, col_frag(s_a2, SP, 32, 16 * b));
             }
             if (t0 + t >= len) v = f4{0, 0, 0, 0};
             const Buffer &buf = is_q ? dq_buf : dk_buf;
@@ -367,11 +380,8 @@ hipError_t grads(const LinAttnLaunch &p, hipStream_t stream) {
 }  // namespace la
 
 hipError_t launch_linattn_bwd(const LinAttnLaunch &p, hipStream_t stream) {
-    hipError_t e = hipSuccess;
-    const int64_t first = p.d_initial_state ? 0 : 1;  // the first segment's own adjoint only feeds d_initial_state
-    if (p.n_seg > 1) e = launch_linattn_states(p, false, 0, p.n_seg - 1, stream);
-    if (e == hipSuccess && p.n_seg > first) e = launch_linattn_states(p, true, first, p.n_seg - first, stream);
-    if (e == hipSuccess) e = launch_linattn_carry(p, false, stream);
+    // the last segment's own state is not needed, the first's own adjoint only for d_initial_state
+    hipError_t e = launch_linattn_states(p, p.n_seg - 1, p.d_initial_state ? 0 : 1, stream);
     if (e == hipSuccess) e = launch_linattn_carry(p, true, stream);
     if (e == hipSuccess) e = p.bf16 ? la::grads<uint16_t>(p, stream) : la::grads<float>(p, stream);
     return e;

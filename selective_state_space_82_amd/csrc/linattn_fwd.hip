@@ -17,8 +17,8 @@ struct Work {
     int64_t ib, seg, bh;
     int h, grp, p0;  // p0: first value column
 };
-template <int NW> __device__ __forceinline__ Work work_of(const LinAttnLaunch &a, int64_t n_seg) {
-    int64_t id = work_index(blockIdx.x, gridDim.x);
+// id: of a piece of work; n_seg: segments that are worked on.
+template <int NW> __device__ __forceinline__ Work work_of(const LinAttnLaunch &a, int64_t id, int64_t n_seg) {
     const int npb = (a.P + 16 * NW - 1) / (16 * NW);
     Work w;
     w.p0 = 16 * NW * (int)(id % npb);
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(kOutThreads) __attribute__((amdgpu_waves_per_eu(siz
     __shared__ __align__(16) Half s_s[4][NF][64][2]; // the state's operand fragments
     __shared__ Decays s_g[2];
 
-    const Work wk = work_of<4>(a, a.n_seg);
+    const Work wk = work_of<4>(a, work_index(blockIdx.x, gridDim.x), a.n_seg);
     const int tid = threadIdx.x, w = wave_id(), l = tid & 63, col = l & 15, g4 = 4 * (l >> 4);
     const int pw = w & 3, tw = w >> 2;
     const int64_t len = row_length(a.lengths, wk.ib, a.L);
@@ -282,30 +282,34 @@ __global__ __launch_bounds__(kOutThreads) __attribute__((amdgpu_waves_per_eu(siz
 
 // ---- a segment's own state, or its own adjoint -------------------------------------------------------------------
 //
-// Forward: S = Σ_s e^{c_end − c_s} v_s k_sᵀ over the segment. Adjoint (REV): the gradient reaching the state that
+// State: S = Σ_s e^{c_end − c_s} v_s k_sᵀ over the segment. Adjoint: the gradient reaching the state that
 // enters the segment from its own outputs, E = Σ_u scale·e^{c_u} do_u q_uᵀ. Workgroup (row, head, 16·NW value columns,
 // segment) as above. Both walk the chunks from the far end of the decay to the near one, S from the last chunk back
 // and E from the first on, so that each chunk's weights carry the decay of all chunks walked before it. The walk ends
 // where that decay is below e^-200: what the rest would add is it times a state (adjoint) of the recurrence, which as
 // an fp32 number is at most e^88.8, and the product is 0 in fp32 (smallest positive value e^-103.3).
-template <typename T, int NT, int NW, bool VEC, bool REV>
-__global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int64_t first_seg, int64_t n_own) {
+template <typename T, int NT, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int64_t n_states, int64_t first_adjoint) {
     constexpr int THREADS = 64 * NW, PB = 16 * NW;
     constexpr int SN = NT + kPad<T>, SV = PB + kPad<T>;
     __shared__ __align__(16) T s_k[kC * SN];
     __shared__ __align__(16) T s_v[kC * SV];
     __shared__ Decays s_g;
 
-    Work wk = work_of<NW>(a, n_own);
-    wk.seg += first_seg;
+    // the states of the first n_states segments, then the adjoints of those from first_adjoint on
+    const int64_t blocks = a.b * a.H * ((a.P + PB - 1) / PB), n_fwd = blocks * n_states;
+    const bool rev = (int64_t)blockIdx.x >= n_fwd;
+    Work wk = rev ? work_of<NW>(a, work_index(blockIdx.x - n_fwd, gridDim.x - n_fwd), a.n_seg - first_adjoint)
+                  : work_of<NW>(a, work_index(blockIdx.x, n_fwd), n_states);
+    if (rev) wk.seg += first_adjoint;
     const int tid = threadIdx.x, w = wave_id(), l = tid & 63, col = l & 15, g4 = 4 * (l >> 4);
     const int64_t len = row_length(a.lengths, wk.ib, a.L);
     int64_t g_stride;
     const float *gp = decays_of(a, wk, &g_stride);
-    const int64_t kt = REV ? a.q_t : a.k_t, vt = REV ? a.do_t : a.v_t;
-    const T *kp = REV ? static_cast<const T *>(a.q) + wk.ib * a.q_b + wk.grp * a.q_h
+    const int64_t kt = rev ? a.q_t : a.k_t, vt = rev ? a.do_t : a.v_t;
+    const T *kp = rev ? static_cast<const T *>(a.q) + wk.ib * a.q_b + wk.grp * a.q_h
                       : static_cast<const T *>(a.k) + wk.ib * a.k_b + wk.grp * a.k_h;
-    const T *vp = REV ? static_cast<const T *>(a.dout) + wk.ib * a.do_b + wk.h * a.do_h
+    const T *vp = rev ? static_cast<const T *>(a.dout) + wk.ib * a.do_b + wk.h * a.do_h
                       : static_cast<const T *>(a.v) + wk.ib * a.v_b + wk.h * a.v_h;
     const int p0 = wk.p0;
 
@@ -320,7 +324,7 @@ __global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int
     double passed = 0.0;  // in every wavefront: the sum of g over the chunks walked
     float g_next = 0.0f;
     const int64_t n = chl - ch0;
-    auto start = [&](int64_t j) { return (REV ? ch0 + j : chl - 1 - j) * kC; };
+    auto start = [&](int64_t j) { return (rev ? ch0 + j : chl - 1 - j) * kC; };
     auto fetch = [&](int64_t t0) {
         const int rows = rows_of(t0, len);
         rk.load(kp + t0 * kt, rows);
@@ -337,7 +341,7 @@ __global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int
         rv.store(s_v);
         const double sum = wave_running_sum(log_decay(g_next)), total = lane_value(sum, 63);  // before the next loads
         // the weight of the lane's step, from all chunks walked and from this one
-        const float wt = (REV ? a.scale : 1.0f) * exp_of((float)(passed + (REV ? sum : total - sum)));
+        const float wt = (rev ? a.scale : 1.0f) * exp_of((float)(passed + (rev ? sum : total - sum)));
         if (w == 0) s_g.out[spread_of(l)] = wt;
         passed += total;
         lds_barrier();
@@ -357,7 +361,7 @@ __global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int
     }
     const int64_t Pp = (a.P + kPB - 1) / kPB * kPB, at = wk.bh * a.n_seg + wk.seg, p = p0 + 16 * w + col;
     if (p < Pp) {
-        float *dst = (REV ? a.E : a.S) + (at * Pp + p) * NT;
+        float *dst = (rev ? a.E : a.S) + (at * Pp + p) * NT;
 #pragma unroll
         for (int i = 0; i < NT / 16; ++i) *reinterpret_cast<f4 *>(dst + 16 * i + g4) = S[i];
     }
@@ -367,16 +371,18 @@ __global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int
 // ---- from the segments' own states to those entering them (adjoints: leaving them), in place ---------------------
 //
 // One thread per four state elements steps over the segments; four loads are kept in flight.
-template <bool REV>
 __global__ __launch_bounds__(kThreads) void la_carry_kernel(LinAttnLaunch a, int NT) {
     const int64_t Pp = (a.P + kPB - 1) / kPB * kPB;
     const int64_t per = Pp * NT / 4;                       // four-element groups of one state: a multiple of 256
-    const int64_t bh = blockIdx.x / (per / kThreads);
-    const int64_t e = blockIdx.x % (per / kThreads) * kThreads + threadIdx.x;
+    const int64_t blocks = per / kThreads * a.b * a.H;     // the states', then (in the gradient) the adjoints'
+    const bool rev = blockIdx.x >= blocks;
+    const int64_t block = rev ? blockIdx.x - blocks : blockIdx.x;
+    const int64_t bh = block / (per / kThreads);
+    const int64_t e = block % (per / kThreads) * kThreads + threadIdx.x;
     const int64_t p = 4 * e / NT, n = 4 * e % NT;
-    f4 *base = reinterpret_cast<f4 *>(REV ? a.E : a.S) + bh * a.n_seg * per + e;
+    f4 *base = reinterpret_cast<f4 *>(rev ? a.E : a.S) + bh * a.n_seg * per + e;
     const double *gs = a.gsum + bh * a.n_seg;
-    const float *first = REV ? a.d_final_state : a.initial_state;
+    const float *first = rev ? a.d_final_state : a.initial_state;
     f4 carry = {0, 0, 0, 0};
     if (first && p < a.P)
 #pragma unroll
@@ -389,21 +395,21 @@ __global__ __launch_bounds__(kThreads) void la_carry_kernel(LinAttnLaunch a, int
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             // the last own state (adjoint: the first, unless asked for) is not needed and may not be there
-            const int64_t j = j0 + u, s = REV ? a.n_seg - 1 - j : j;
-            const bool need = j < a.n_seg && (j + 1 < a.n_seg || (REV && a.d_initial_state));
+            const int64_t j = j0 + u, s = rev ? a.n_seg - 1 - j : j;
+            const bool need = j < a.n_seg && (j + 1 < a.n_seg || (rev && a.d_initial_state));
             own[u] = need ? base[s * per] : f4{0, 0, 0, 0};
             d[u] = need ? exp_of((float)gs[s]) : 0.0f;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t j = j0 + u, s = REV ? a.n_seg - 1 - j : j;
+            const int64_t j = j0 + u, s = rev ? a.n_seg - 1 - j : j;
             if (j < a.n_seg) {
                 base[s * per] = carry;
                 carry = carry * d[u] + own[u];
             }
         }
     }
-    if (REV && a.d_initial_state && p < a.P)
+    if (rev && a.d_initial_state && p < a.P)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             if (n + r < a.N) a.d_initial_state[(bh * a.P + p) * a.N + n + r] = carry[r];
@@ -429,13 +435,12 @@ unsigned value_blocks(const LinAttnLaunch &p) {
 }
 
 template <typename T>
-hipError_t states(const LinAttnLaunch &p, bool adjoint, int64_t first, int64_t n, hipStream_t stream) {
-    const dim3 grid((unsigned)(p.b * p.H * n) * value_blocks(p));
+hipError_t states(const LinAttnLaunch &p, int64_t n_states, int64_t first_adjoint, hipStream_t stream) {
+    const dim3 grid((unsigned)(p.b * p.H * (n_states + p.n_seg - first_adjoint)) * value_blocks(p));
     return by_width(p, [&](auto nt, auto nw, auto vec) {
         constexpr int NT = decltype(nt)::value, NW = decltype(nw)::value;
         constexpr bool VEC = decltype(vec)::value;
-        if (adjoint) la_states_kernel<T, NT, NW, VEC, true><<<grid, 64 * NW, 0, stream>>>(p, first, n);
-        else la_states_kernel<T, NT, NW, VEC, false><<<grid, 64 * NW, 0, stream>>>(p, first, n);
+        la_states_kernel<T, NT, NW, VEC><<<grid, 64 * NW, 0, stream>>>(p, n_states, first_adjoint);
         return hipGetLastError();
     });
 }
@@ -452,22 +457,22 @@ hipError_t outputs(const LinAttnLaunch &p, hipStream_t stream) {
 }  // namespace
 }  // namespace la
 
-hipError_t launch_linattn_states(const LinAttnLaunch &p, bool adjoint, int64_t first, int64_t n, hipStream_t stream) {
-    return p.bf16 ? la::states<uint16_t>(p, adjoint, first, n, stream) : la::states<float>(p, adjoint, first, n, stream);
+hipError_t launch_linattn_states(const LinAttnLaunch &p, int64_t n_states, int64_t first_adjoint, hipStream_t stream) {
+    if (n_states == 0 && first_adjoint == p.n_seg) return hipSuccess;
+    return p.bf16 ? la::states<uint16_t>(p, n_states, first_adjoint, stream)
+                  : la::states<float>(p, n_states, first_adjoint, stream);
 }
 
 hipError_t launch_linattn_carry(const LinAttnLaunch &p, bool adjoint, hipStream_t stream) {
     const int nt = linattn_nt(p.N);
     const int64_t per = (p.P + la::kPB - 1) / la::kPB * la::kPB * nt / 4 / la::kThreads;
-    const dim3 grid((unsigned)(p.b * p.H * per));
-    if (adjoint) la::la_carry_kernel<true><<<grid, la::kThreads, 0, stream>>>(p, nt);
-    else la::la_carry_kernel<false><<<grid, la::kThreads, 0, stream>>>(p, nt);
+    la::la_carry_kernel<<<dim3((unsigned)(p.b * p.H * per * (adjoint ? 2 : 1))), la::kThreads, 0, stream>>>(p, nt);
     return hipGetLastError();
 }
 
 hipError_t launch_linattn_fwd(const LinAttnLaunch &p, hipStream_t stream) {
     if (p.n_seg > 1) {
-        hipError_t e = launch_linattn_states(p, false, 0, p.n_seg - 1, stream);
+        hipError_t e = launch_linattn_states(p, p.n_seg - 1, p.n_seg, stream);
         if (e == hipSuccess) e = launch_linattn_carry(p, false, stream);
         if (e != hipSuccess) return e;
     }
