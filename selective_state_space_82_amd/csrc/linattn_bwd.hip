@@ -42,20 +42,22 @@ __device__ __forceinline__ float sum_cols(float v) {
 // The four wavefronts share the lower-triangular tiles of both score matrices through LDS; then wavefront w takes
 // the value columns 16w .. of dv, and 16-column jobs of dq and dk.
 template <typename T, int NT, bool VEC>
-__global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && NT < 128 ? 3 : 1)))
+void la_grad_kernel(LinAttnLaunch a) {
     constexpr int SN = NT + kPad<T>, SP = kC + kPad<T>, SV = kPB + kPad<T>;
     constexpr int TILES = NT / 16, JOBS = 2 * TILES / 4;
-    constexpr bool AHEAD = NT < 128;  // at 128 they take 96 registers
     __shared__ __align__(16) T s_q[kC * SN];
     __shared__ __align__(16) T s_k[kC * SN];
+    static_assert(SP == SV, "A1 takes V's place");
     __shared__ __align__(16) T s_v[kC * SV];
     __shared__ __align__(16) T s_d[kC * SV];
     // [t][s]; bf16: one part, half a step of bf16 on each product's size, as the results' own rounding (the terms of dg
     // are taken before it)
-    __shared__ __align__(16) T s_a1[kC * SP];
+    T *const s_a1 = s_v;
     __shared__ __align__(16) T s_a2[kC * SP];
     __shared__ Decays s_g;
-    __shared__ float s_row[4][kC], s_col[4][kC], s_x[TILES][kC], s_y[4][kC], s_z[4];
+    __shared__ __align__(16) float s_col[4][kC];
+    __shared__ float s_row[4][kC], s_x[TILES][kC], s_y[TILES][kC], s_z[4];
 
     int64_t id = work_index(blockIdx.x, gridDim.x);
     const int h = (int)(id % a.H);
@@ -67,6 +69,7 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
     const int64_t len = row_length(a.lengths, ib, a.L);
     const int64_t t0 = ch * kC;
     const int64_t rows = a.L - t0 < kC ? a.L - t0 : kC;
+    const int some = rows_of(t0, len);  // steps of the row in this chunk
     const int npb = (a.P + kPB - 1) / kPB;
 
     float *dgp = (a.g_per_step ? a.dg : a.dg_steps) + (ib * a.L + t0) * a.H + h;
@@ -112,24 +115,12 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
         q.store(s_q);
         k.store(s_k);
     }
-    // the tiles right of the diagonal that a 32-step contraction touches
-    for (int i = tid; i < 2 * 16 * 16; i += kThreads) {
-        const int t = 32 * (i >> 8) + ((i >> 4) & 15), s = 32 * (i >> 8) + 16 + (i & 15);
-        s_a1[t * SP + s] = (T)0;
-        s_a2[t * SP + s] = (T)0;
-    }
-
-    // The wavefront's parts of the entering state and the leaving adjoint, for the first 64 value columns fetched before
-    // the scores are formed: E with a lane's four values along N (for dv), S and E with eight along P (for dq, dk).
+    // The wavefront's parts of the entering state S and the leaving adjoint E: eight values along P at its columns of N.
     const int64_t Pp = (int64_t)npb * kPB;
     const float *Sp = a.S + (bh * a.n_seg + ch) * Pp * NT;
     const float *Ep = a.E + (bh * a.n_seg + ch) * Pp * NT;
-    f4 e[NT / 16];
     f8 x[JOBS][2];
     auto fetch_states = [&](int pb) {
-        const int64_t p = pb * kPB + 16 * w + col;
-#pragma unroll
-        for (int i = 0; i < NT / 16; ++i) e[i] = *reinterpret_cast<const f4 *>(Ep + p * NT + 16 * i + g4);
 #pragma unroll
         for (int j = 0; j < JOBS; ++j) {
             const int job = w + 4 * j;
@@ -141,17 +132,23 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
                 for (int r = 0; r < 8; ++r) x[j][pp][r] = src[(32 * pp + r) * NT];
         }
     };
-    if (AHEAD) fetch_states(0);
 
-    // scores: tile (tb, sb) holds D[s][t] of q·k and do·v
-    f4 aq[3], ad[3];
+    // Over the value columns: the scores' tiles (tb, sb), D[s][t] of q·k and do·v, and the parts of dq and dk that come
+    // through the state and the adjoint (in three bf16 parts: dg's terms X and Y are taken from them).
+    f4 aq[3], ad[3], acc[JOBS][4];
 #pragma unroll
     for (int j = 0; j < 3; ++j) aq[j] = ad[j] = f4{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < JOBS; ++j)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) acc[j][b] = f4{0, 0, 0, 0};
+    float z = 0.0f;
     for (int pb = 0; pb < npb; ++pb) {
-        if (pb) lds_barrier();
         Stage<T, kPB, kThreads, VEC> v((uint32_t)a.v_t, pb * kPB, a.P), d((uint32_t)a.do_t, pb * kPB, a.P);
         v.load(vp + t0 * a.v_t, rows_of(t0, len));
         d.load(dp + t0 * a.do_t, rows_of(t0, len));
+        fetch_states(pb);
+        if (pb) lds_barrier();
         v.store(s_v);
         d.store(s_d);
         lds_barrier();
@@ -167,6 +164,68 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
                 for (int n = 0; n < kPB; n += 32) mma(ad[j], row_frag(s_v, SV, 16 * sb, n), row_frag(s_d, SV, 16 * tb, n));
             }
         }
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j) {
+            const T *tile = w + 4 * j < TILES ? s_d : s_v;
+#pragma unroll
+            for (int pp = 0; pp < 2; ++pp) {
+                const Split<T, 3> xs(x[j][pp]);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) mma(acc[j][b], xs, row_frag(tile, SV, 16 * b, 32 * pp));
+            }
+        }
+        // <S, E>
+        if (JOBS == 1) {  // a wavefront has dq's state or dk's adjoint, not both
+            const int64_t at = (int64_t)(pb * kPB + 16 * w + col) * NT + g4;
+#pragma unroll
+            for (int i = 0; i < NT / 16; ++i) {
+                const f4 u = *reinterpret_cast<const f4 *>(Sp + at + 16 * i), v4 = *reinterpret_cast<const f4 *>(Ep + at + 16 * i);
+                z += (u[0] * v4[0] + u[1] * v4[1]) + (u[2] * v4[2] + u[3] * v4[3]);
+            }
+        } else {  // the same columns of N in its job of dq and in that of dk
+#pragma unroll
+            for (int j = 0; j < JOBS / 2; ++j)
+#pragma unroll
+                for (int pp = 0; pp < 2; ++pp)
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) z = __builtin_fmaf(x[j][pp][r], x[j + JOBS / 2][pp][r], z);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < JOBS; ++j) {
+        const int job = w + 4 * j;
+        const bool is_q = job < TILES;
+        const int tile = is_q ? job : job - TILES;
+        const T *rows_n = is_q ? s_q : s_k;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int t = 16 * b + col;
+            f4 &v = acc[j][b];
+            v *= is_q ? s_g.in[t] : s_g.out[t];
+            const T *r = rows_n + t * SN + 16 * tile + g4;
+            const float xy = sum_groups((v[0] * widen(r[0]) + v[1] * widen(r[1])) + (v[2] * widen(r[2]) + v[3] * widen(r[3])));
+            if (l < 16) (is_q ? s_x : s_y)[tile][t] = xy;
+        }
+    }
+    z = sum_groups(sum_cols(z));
+    if (l == 0) s_z[w] = z;
+
+    // E once more, four values along N at the wavefront's value columns (for dv, one bf16 part), and the first dv block's
+    // do, on their way while the scores are weighted
+    f4 e[NT / 16];
+    auto fetch_adjoint = [&](int pb) {
+        const float *src = Ep + (int64_t)(pb * kPB + 16 * w + col) * NT + g4;
+#pragma unroll
+        for (int i = 0; i < NT / 16; ++i) e[i] = *reinterpret_cast<const f4 *>(src + 16 * i);
+    };
+    fetch_adjoint(0);
+    lds_barrier();  // V's tile is free: A1 takes its place
+
+    // the tiles right of the diagonal that a 32-step contraction touches
+    for (int i = tid; i < 2 * 16 * 16; i += kThreads) {
+        const int t = 32 * (i >> 8) + ((i >> 4) & 15), s = 32 * (i >> 8) + 16 + (i & 15);
+        s_a1[t * SP + s] = (T)0;
+        s_a2[t * SP + s] = (T)0;
     }
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
@@ -175,20 +234,27 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
             const int tb = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3, sb = i - tb * (tb + 1) / 2;
             const int t = 16 * tb + col, s = 16 * sb + g4;
             const float th = s_g.c.hi[t], tl = s_g.c.lo[t];
-            f4 a1, a2;
-            float row = 0.0f;
+            const f4 sh = *reinterpret_cast<const f4 *>(&s_g.c.hi[s]), sl = *reinterpret_cast<const f4 *>(&s_g.c.lo[s]);
+            f4 a1, a2, wv;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float d = a.scale * exp2_fast((th - s_g.c.hi[s + r]) + (tl - s_g.c.lo[s + r]));
-                a1[r] = s + r <= t ? aq[j][r] * d : 0.0f;
-                a2[r] = s + r <= t ? ad[j][r] * d : 0.0f;
-                const float wv = s + r < t ? a1[r] * ad[j][r] : 0.0f;
-                row += wv;
-                const float cs = sum_cols(wv);
-                if (col == 0) s_col[tb][s + r] = cs;
+                const float d = a.scale * exp2_fast((th - sh[r]) + (tl - sl[r]));
+                a1[r] = aq[j][r] * d;
+                a2[r] = ad[j][r] * d;
+                wv[r] = a1[r] * ad[j][r];
             }
-            row = sum_groups(row);
+            if (sb == tb)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    a1[r] = s + r <= t ? a1[r] : 0.0f;
+                    a2[r] = s + r <= t ? a2[r] : 0.0f;
+                    wv[r] = s + r < t ? wv[r] : 0.0f;
+                }
+            const float row = sum_groups((wv[0] + wv[1]) + (wv[2] + wv[3]));
             if (l < 16) s_row[sb][t] = row;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) wv[r] = sum_cols(wv[r]);
+            if (col == 0) *reinterpret_cast<f4 *>(&s_col[tb][s]) = wv;
             if constexpr (sizeof(T) == 2) {
                 *reinterpret_cast<bf4 *>(&s_a1[t * SP + s]) = __builtin_convertvector(a1, bf4);
                 *reinterpret_cast<bf4 *>(&s_a2[t * SP + s]) = __builtin_convertvector(a2, bf4);
@@ -198,76 +264,22 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
             }
         }
     }
+    lds_barrier();
 
-    f4 acc[JOBS][4];
+    if (w == 0) {  // dg
+        const int b = l >> 4;
+        double after = 0.0, ys = 0.0;
+        for (int i = 0; i <= b; ++i) after += s_row[i][l];
+        for (int i = b; i < 4; ++i) after -= s_col[i][l];
 #pragma unroll
-    for (int j = 0; j < JOBS; ++j)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) acc[j][b] = f4{0, 0, 0, 0};
-    float y[4] = {0, 0, 0, 0}, z = 0.0f;
-    for (int pb = 0; pb < npb; ++pb) {
-        lds_barrier();
-        if (!AHEAD || pb) fetch_states(pb);
-        if (npb > 1) {
-            Stage<T, kPB, kThreads, VEC> v((uint32_t)a.v_t, pb * kPB, a.P), d((uint32_t)a.do_t, pb * kPB, a.P);
-            v.load(vp + t0 * a.v_t, rows_of(t0, len));
-            d.load(dp + t0 * a.do_t, rows_of(t0, len));
-            v.store(s_v);
-            d.store(s_d);
-            lds_barrier();
+        for (int i = 0; i < TILES; ++i) {
+            after += s_x[i][l];
+            ys += s_y[i][l];
         }
-        // dv: value columns 16w ..
-        {
-            if (JOBS == 1) {  // a wavefront has dq's state or dk's adjoint, not both
-                const int64_t p = pb * kPB + 16 * w + col;
-#pragma unroll
-                for (int i = 0; i < NT / 16; ++i) {
-                    const f4 s = *reinterpret_cast<const f4 *>(Sp + p * NT + 16 * i + g4);
-                    z += (e[i][0] * s[0] + e[i][1] * s[1]) + (e[i][2] * s[2] + e[i][3] * s[3]);
-                }
-            } else {  // the same columns of N in its job of dq and in that of dk
-#pragma unroll
-                for (int j = 0; j < JOBS / 2; ++j)
-#pragma unroll
-                    for (int pp = 0; pp < 2; ++pp)
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) z = __builtin_fmaf(x[j][pp][r], x[j + JOBS / 2][pp][r], z);
-            }
-            f4 dv[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) dv[b] = f4{0, 0, 0, 0};
-#pragma unroll
-            for (int n = 0; n < NT / 32; ++n) {
-                const Split<T, 3> es(join(e[2 * n], e[2 * n + 1]));
-#pragma unroll
-                for (int b = 0; b < 4; ++b) mma(dv[b], es, half_frag(s_k, SN, 16 * b, 32 * n));
-            }
-            const Frag<T> d0 = col_frag(s_d, SV, 0, 16 * w), d1 = col_frag(s_d, SV, 32, 16 * w);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int s = 16 * b + col;
-                dv[b] *= s_g.out[s];
-                const T *vr = &s_v[s * SV + 16 * w + g4];
-                y[b] += (dv[b][0] * widen(vr[0]) + dv[b][1] * widen(vr[1])) + (dv[b][2] * widen(vr[2]) + dv[b][3] * widen(vr[3]));
-                if (b < 2) mma(dv[b], d0, col_frag(s_a1, SP, 0, 16 * b));
-                mma(dv[b], d1, col_frag(s_a1, SP, 32, 16 * b));
-                if (t0 + s >= len) dv[b] = f4{0, 0, 0, 0};
-                store4<T, VEC>(dv_buf, (uint32_t)dv_t, s, pb * kPB + 16 * w + g4, a.P, dv[b]);
-            }
-        }
-        // dq, dk: the parts through the entering state and the leaving adjoint
-#pragma unroll
-        for (int j = 0; j < JOBS; ++j) {
-            const int job = w + 4 * j;
-            const bool is_q = job < TILES;
-            const T *tile = is_q ? s_d : s_v;
-#pragma unroll
-            for (int pp = 0; pp < 2; ++pp) {
-                const Split<T, 3> xs(x[j][pp]);
-#pragma unroll
-                for (int b = 0; b < 4; ++b) mma(acc[j][b], xs, row_frag(tile, SV, 16 * b, 32 * pp));
-            }
-        }
+        const double upto = wave_running_sum(after), yto = wave_running_sum(ys);
+        const double zs = (((double)s_z[0] + s_z[1]) + ((double)s_z[2] + s_z[3])) * s_g.end;
+        const double v = (lane_value(upto, 63) - upto + after) + (yto - ys) + zs;
+        if (l < rows) dgp[(int64_t)l * a.H] = t0 + l < len ? (float)v : 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < JOBS; ++j) {
@@ -280,43 +292,49 @@ __global__ __launch_bounds__(kThreads) void la_grad_kernel(LinAttnLaunch a) {
         for (int b = 0; b < 4; ++b) {
             const int t = 16 * b + col;
             f4 &v = acc[j][b];
-            v *= is_q ? s_g.in[t] : s_g.out[t];
             if (is_q) {
-                const T *qr = &s_q[t * SN + n0 + g4];
-                const float x = sum_groups((v[0] * widen(qr[0]) + v[1] * widen(qr[1])) + (v[2] * widen(qr[2]) + v[3] * widen(qr[3])));
-                if (l < 16) s_x[job][t] = x;
                 mma(v, f0, row_frag(s_a2, SP, 16 * b, 0));
                 if (b >= 2) mma(v, f1, row_frag(s_a2, SP, 16 * b, 32));
             } else {
                 if (b < 2) mma(v, f0, col_frag(s_a2, SP, 0, 16 * b));
                 mma(v, f1, col_frag(s_a2, SP, 32, 16 * b));
             }
-            if (t0 + t >= len) v = f4{0, 0, 0, 0};
+            if (some < kC && t >= some) v = f4{0, 0, 0, 0};
             const Buffer &buf = is_q ? dq_buf : dk_buf;
             if (part) store4<float, VEC>(buf, (uint32_t)n_t, t, n0 + g4, a.N, v);
             else store4<T, VEC>(buf, (uint32_t)n_t, t, n0 + g4, a.N, v);
         }
     }
+    for (int pb = 0; pb < npb; ++pb) {  // dv: value columns 16w .. of each block
+        if (npb > 1) {
+            Stage<T, kPB, kThreads, VEC> d((uint32_t)a.do_t, pb * kPB, a.P);
+            d.load(dp + t0 * a.do_t, some);
+            if (pb) {
+                fetch_adjoint(pb);
+                lds_barrier();
+            }
+            d.store(s_d);
+            lds_barrier();
+        }
+        f4 dv[4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const float v = sum_groups(y[b]);
-        if (l < 16) s_y[w][16 * b + l] = v;
-    }
-    z = sum_groups(sum_cols(z));
-    if (l == 0) s_z[w] = z;
-    lds_barrier();
-    if (w == 0) {
-        const int b = l >> 4;
-        double after = 0.0;
-        for (int i = 0; i <= b; ++i) after += s_row[i][l];
-        for (int i = b; i < 4; ++i) after -= s_col[i][l];
+        for (int b = 0; b < 4; ++b) dv[b] = f4{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < TILES; ++i) after += s_x[i][l];
-        const double ys = ((double)s_y[0][l] + s_y[1][l]) + ((double)s_y[2][l] + s_y[3][l]);
-        const double upto = wave_running_sum(after), yto = wave_running_sum(ys);
-        const double zs = (((double)s_z[0] + s_z[1]) + ((double)s_z[2] + s_z[3])) * s_g.end;
-        const double v = (__shfl(upto, 63) - upto + after) + (yto - ys) + zs;
-        if (l < rows) dgp[(int64_t)l * a.H] = t0 + l < len ? (float)v : 0.0f;
+        for (int n = 0; n < NT / 32; ++n) {
+            const Split<T, 1> es(join(e[2 * n], e[2 * n + 1]));
+#pragma unroll
+            for (int b = 0; b < 4; ++b) mma(dv[b], es, half_frag(s_k, SN, 16 * b, 32 * n));
+        }
+        const Frag<T> d0 = col_frag(s_d, SV, 0, 16 * w), d1 = col_frag(s_d, SV, 32, 16 * w);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int s = 16 * b + col;
+            dv[b] *= s_g.out[s];
+            if (b < 2) mma(dv[b], d0, col_frag(s_a1, SP, 0, 16 * b));
+            mma(dv[b], d1, col_frag(s_a1, SP, 32, 16 * b));
+            if (some < kC && s >= some) dv[b] = f4{0, 0, 0, 0};
+            store4<T, VEC>(dv_buf, (uint32_t)dv_t, s, pb * kPB + 16 * w + g4, a.P, dv[b]);
+        }
     }
 }
 
