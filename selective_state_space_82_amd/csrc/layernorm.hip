@@ -322,7 +322,10 @@ int64_t groups(int64_t rows, int64_t w_rows, int slots, int64_t most) {
     const int64_t cap = most / w_rows > 1 ? most / w_rows : 1;
     return need < cap ? need : cap;
 }
-constexpr int64_t kFwdGroups = 2048, kBwdGroups = 1024;
+constexpr int64_t kFwdGroups = 2048;
+// The gradient's workgroups also write a row of partial sums each: 512 of them (8192 rows of 768 in fp32: 21.5 us; 1024
+// took 26), but 1024 where rows are short, of sixteen lanes or few more (524288 rows of 128 in bf16: 88 us; 512 took 92).
+int64_t bwd_groups(int64_t d) { return d <= 256 ? 1024 : 512; }
 
 // f(LR, K): the lanes of a row and their pieces; at most 16 elements of a row to a lane, so that the gradient's row,
 // its weight and its two partial sums stay in registers with the next row on its way.
@@ -359,7 +362,7 @@ template <typename T> hipError_t bwd(const NormLaunch &p, hipStream_t stream) {
     return by_width<T>(p.d, [&](auto lr, auto k) {
         constexpr int LR = decltype(lr)::value, K = decltype(k)::value;
         typedef Lay<T, LR, K> Y;
-        const int64_t per = groups(p.rows, p.w_rows, Y::SLOTS, kBwdGroups);
+        const int64_t per = groups(p.rows, p.w_rows, Y::SLOTS, bwd_groups(p.d));
         const dim3 grid((unsigned)(per * p.w_rows));
         if (p.vec) norm_bwd_kernel<T, LR, K, true><<<grid, Y::THREADS, 0, stream>>>(p);
         else norm_bwd_kernel<T, LR, K, false><<<grid, Y::THREADS, 0, stream>>>(p);
@@ -378,7 +381,7 @@ template <typename T> hipError_t bwd(const NormLaunch &p, hipStream_t stream) {
 
 int64_t layernorm_part_floats(int64_t rows, int64_t d, int64_t w_rows) {
     // the most workgroups any layout launches: one row each, or the cap, or one per weight row
-    const int64_t per = ln::groups(rows, w_rows, 1, ln::kBwdGroups);
+    const int64_t per = ln::groups(rows, w_rows, 1, ln::bwd_groups(d));
     return 2 * per * w_rows * d;
 }
 
