@@ -55,10 +55,10 @@ struct Scratch {
 
 // Hands out pieces of the scratch, 256 bytes apart.
 struct Pieces {
-    char *base;
+    uintptr_t base;
     int64_t at = 0;
     template <typename T> T *next(int64_t n) {
-        T *r = reinterpret_cast<T *>(base + at);
+        T *r = reinterpret_cast<T *>(base + (uintptr_t)at);
         at += ceil_div(n * (int64_t)sizeof(T), 256) * 256;
         return r;
     }
@@ -117,7 +117,7 @@ void plan(const AttnSizes &z, bool gradient, LinAttnLaunch *p) {
 
 // Cuts the scratch at `base` (which may be null: for the size alone) into the call's pieces.
 int64_t layout(const AttnSizes &z, bool gradient, bool g_per_step, void *base, LinAttnLaunch *p) {
-    Pieces s{static_cast<char *>(base)};
+    Pieces s{reinterpret_cast<uintptr_t>(base)};
     const int64_t state = ceil_div(z.P, kBlockP) * kBlockP * ssm::linattn_nt(z.N), n = z.b * z.H * p->n_seg;
     if (p->n_seg == 0 || (!gradient && p->n_seg == 1)) return 0;
     p->S = s.next<float>(n * state);

@@ -41,8 +41,12 @@ __device__ __forceinline__ float sum_cols(float v) {
 //
 // The four wavefronts share the lower-triangular tiles of both score matrices through LDS; then wavefront w takes
 // the value columns 16w .. of dv, and 16-column jobs of dq and dk.
-template <typename T, int NT, bool VEC>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && NT < 128 ? 3 : 1)))
+// PARTS: bf16 parts of the scores A1 and A2. One in general: half a step of bf16 on each product's size, as the results'
+// own rounding (dq, dk and dv are then 1.4 times as far off as by that alone). Two where that is not all: where a group's
+// heads are summed in fp32, whose shares cancel while their roundings do not (twice as far off), and in a single chunk,
+// where a result may hang on one score.
+template <typename T, int NT, bool VEC, int PARTS>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && NT < 128 ? 4 - PARTS : 1)))
 void la_grad_kernel(LinAttnLaunch a) {
     constexpr int SN = NT + kPad<T>, SP = kC + kPad<T>, SV = kPB + kPad<T>;
     constexpr int TILES = NT / 16, JOBS = 2 * TILES / 4;
@@ -51,10 +55,10 @@ void la_grad_kernel(LinAttnLaunch a) {
     static_assert(SP == SV, "A1 takes V's place");
     __shared__ __align__(16) T s_v[kC * SV];
     __shared__ __align__(16) T s_d[kC * SV];
-    // [t][s]; bf16: one part, half a step of bf16 on each product's size, as the results' own rounding (the terms of dg
-    // are taken before it)
-    T *const s_a1 = s_v;
-    __shared__ __align__(16) T s_a2[kC * SP];
+    // [t][s]; the terms of dg are taken before these are rounded
+    __shared__ __align__(16) T s_a1_low[(PARTS - 1) * kC * SP + 1];
+    T *const s_a1[2] = {s_v, s_a1_low};
+    __shared__ __align__(16) T s_a2[PARTS][kC * SP];
     __shared__ Decays s_g;
     __shared__ __align__(16) float s_col[4][kC];
     __shared__ float s_row[4][kC], s_x[TILES][kC], s_y[TILES][kC], s_z[4];
@@ -224,8 +228,8 @@ void la_grad_kernel(LinAttnLaunch a) {
     // the tiles right of the diagonal that a 32-step contraction touches
     for (int i = tid; i < 2 * 16 * 16; i += kThreads) {
         const int t = 32 * (i >> 8) + ((i >> 4) & 15), s = 32 * (i >> 8) + 16 + (i & 15);
-        s_a1[t * SP + s] = (T)0;
-        s_a2[t * SP + s] = (T)0;
+#pragma unroll
+        for (int e = 0; e < PARTS; ++e) s_a1[e][t * SP + s] = s_a2[e][t * SP + s] = (T)0;
     }
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
@@ -256,11 +260,17 @@ void la_grad_kernel(LinAttnLaunch a) {
             for (int r = 0; r < 4; ++r) wv[r] = sum_cols(wv[r]);
             if (col == 0) *reinterpret_cast<f4 *>(&s_col[tb][s]) = wv;
             if constexpr (sizeof(T) == 2) {
-                *reinterpret_cast<bf4 *>(&s_a1[t * SP + s]) = __builtin_convertvector(a1, bf4);
-                *reinterpret_cast<bf4 *>(&s_a2[t * SP + s]) = __builtin_convertvector(a2, bf4);
+#pragma unroll
+                for (int e = 0; e < PARTS; ++e) {
+                    const bf4 u = __builtin_convertvector(a1, bf4), v = __builtin_convertvector(a2, bf4);
+                    *reinterpret_cast<bf4 *>(&s_a1[e][t * SP + s]) = u;
+                    *reinterpret_cast<bf4 *>(&s_a2[e][t * SP + s]) = v;
+                    a1 -= __builtin_convertvector(u, f4);
+                    a2 -= __builtin_convertvector(v, f4);
+                }
             } else {
-                *reinterpret_cast<f4 *>(&s_a1[t * SP + s]) = a1;
-                *reinterpret_cast<f4 *>(&s_a2[t * SP + s]) = a2;
+                *reinterpret_cast<f4 *>(&s_a1[0][t * SP + s]) = a1;
+                *reinterpret_cast<f4 *>(&s_a2[0][t * SP + s]) = a2;
             }
         }
     }
@@ -292,12 +302,15 @@ void la_grad_kernel(LinAttnLaunch a) {
         for (int b = 0; b < 4; ++b) {
             const int t = 16 * b + col;
             f4 &v = acc[j][b];
-            if (is_q) {
-                mma(v, f0, row_frag(s_a2, SP, 16 * b, 0));
-                if (b >= 2) mma(v, f1, row_frag(s_a2, SP, 16 * b, 32));
-            } else {
-                if (b < 2) mma(v, f0, col_frag(s_a2, SP, 0, 16 * b));
-                mma(v, f1, col_frag(s_a2, SP, 32, 16 * b));
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+                if (is_q) {
+                    mma(v, f0, row_frag(s_a2[p], SP, 16 * b, 0));
+                    if (b >= 2) mma(v, f1, row_frag(s_a2[p], SP, 16 * b, 32));
+                } else {
+                    if (b < 2) mma(v, f0, col_frag(s_a2[p], SP, 0, 16 * b));
+                    mma(v, f1, col_frag(s_a2[p], SP, 32, 16 * b));
+                }
             }
             if (some < kC && t >= some) v = f4{0, 0, 0, 0};
             const Buffer &buf = is_q ? dq_buf : dk_buf;
@@ -330,8 +343,11 @@ void la_grad_kernel(LinAttnLaunch a) {
         for (int b = 0; b < 4; ++b) {
             const int s = 16 * b + col;
             dv[b] *= s_g.out[s];
-            if (b < 2) mma(dv[b], d0, col_frag(s_a1, SP, 0, 16 * b));
-            mma(dv[b], d1, col_frag(s_a1, SP, 32, 16 * b));
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+                if (b < 2) mma(dv[b], d0, col_frag(s_a1[p], SP, 0, 16 * b));
+                mma(dv[b], d1, col_frag(s_a1[p], SP, 32, 16 * b));
+            }
             if (some < kC && s >= some) dv[b] = f4{0, 0, 0, 0};
             store4<T, VEC>(dv_buf, (uint32_t)dv_t, s, pb * kPB + 16 * w + g4, a.P, dv[b]);
         }
@@ -371,15 +387,18 @@ template <typename T>
 hipError_t grads(const LinAttnLaunch &p, hipStream_t stream) {
     const int nt = linattn_nt(p.N);
     const dim3 grid((unsigned)(p.b * p.H * p.n_seg));
-    if (p.vec) {
-        if (nt == 32) la_grad_kernel<T, 32, true><<<grid, kThreads, 0, stream>>>(p);
-        else if (nt == 64) la_grad_kernel<T, 64, true><<<grid, kThreads, 0, stream>>>(p);
-        else la_grad_kernel<T, 128, true><<<grid, kThreads, 0, stream>>>(p);
-    } else {
-        if (nt == 32) la_grad_kernel<T, 32, false><<<grid, kThreads, 0, stream>>>(p);
-        else if (nt == 64) la_grad_kernel<T, 64, false><<<grid, kThreads, 0, stream>>>(p);
-        else la_grad_kernel<T, 128, false><<<grid, kThreads, 0, stream>>>(p);
-    }
+    auto launch = [&](auto vec, auto parts) {
+        constexpr bool VEC = decltype(vec)::value;
+        constexpr int PARTS = decltype(parts)::value;
+        if (nt == 32) la_grad_kernel<T, 32, VEC, PARTS><<<grid, kThreads, 0, stream>>>(p);
+        else if (nt == 64) la_grad_kernel<T, 64, VEC, PARTS><<<grid, kThreads, 0, stream>>>(p);
+        else la_grad_kernel<T, 128, VEC, PARTS><<<grid, kThreads, 0, stream>>>(p);
+    };
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, sizeof(T) == 2 ? 2 : 1> two;
+    const bool exact = p.G < p.H || p.L <= kC;
+    if (p.vec) exact ? launch(std::true_type{}, two) : launch(std::true_type{}, one);
+    else exact ? launch(std::false_type{}, two) : launch(std::false_type{}, one);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.G < p.H) {
         const int64_t n = p.b * p.L * p.G * p.N, blocks = (n + kThreads - 1) / kThreads;

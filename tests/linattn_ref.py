@@ -9,8 +9,9 @@ exact, is off by at most n·u·M. n counts, for every path from an input to the 
 taken of a difference of sums rounded to fp32 and multiplied by log2 e, so it is off by (2|d| + 2)·u, summed over the
 path 2·104 + 2 per chunk at most (past |d| = 104 e^d is below fp32's range, and the product is 0, an absolute error
 below 2^-125 times the operands). bf16 adds, for results in bf16, the one rounding of the state or adjoint on a path
-through it (2^-8 of the product), the scores cut into two parts (2^-16, at most two on a path), and the rounding of the
-result (2^-8 of it); fp32 results take their fp32 operands in three parts (2^-24).
+through it, or of the scores on a path through them (2^-8 of the product; a path takes one of the two), operands cut into
+two parts (2^-16, at most two on a path), and the rounding of the result (2^-8 of it); fp32 results take their fp32
+operands in three parts (2^-24).
 """
 import math
 
