@@ -24,8 +24,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-fvisibility=
 
 
 # The sources that decide the prefill kernels and their launch shapes.
-FWD_KERNEL_SOURCES = ("abi.cpp", "agg_rev.hip", "device_common.h", "launch.h", "scan_fwd.hip", "scan_small.hip",
-                      "tile_common.h")
+FWD_KERNEL_SOURCES = ("abi.cpp", "agg_rev.hip", "device_common.h", "host_util.h", "launch.h", "scan_fwd.hip",
+                      "scan_small.hip", "tile_common.h")
 # The sources behind each group of kernels a profile under profiles/ covers.
 PROFILE_SOURCES = {
     "scan_fwd": FWD_KERNEL_SOURCES,

@@ -39,8 +39,10 @@ __device__ __forceinline__ float sum_cols(float v) {
 
 // ---- one workgroup per (row, head, chunk), all value columns -----------------------------------------------------
 //
-// The four wavefronts share the lower-triangular tiles of both score matrices through LDS; then wavefront w takes
-// the value columns 16w .. of dv, and 16-column jobs of dq and dk.
+// The four wavefronts share the lower-triangular tiles of both score matrices through LDS; wavefront w takes the value
+// columns 16w .. of dv, and 16-column jobs of dq and dk, whose parts through state and adjoint come first: V is free then
+// and A1 takes its place, which leaves room for three workgroups on a compute unit. Bound: memory and its latency. b 4,
+// L 2048, 24 heads, N = P = 64 in bf16 takes 62 us for 0.28 GB (4.4 TB/s); eight wavefronts to a workgroup took 13 us more.
 // PARTS: bf16 parts of the scores A1 and A2. One in general: half a step of bf16 on each product's size, as the results'
 // own rounding (dq, dk and dv are then 1.4 times as far off as by that alone). Two where that is not all: where a group's
 // heads are summed in fp32, whose shares cancel while their roundings do not (twice as far off), and in a single chunk,
@@ -214,13 +216,14 @@ void la_grad_kernel(LinAttnLaunch a) {
     z = sum_groups(sum_cols(z));
     if (l == 0) s_z[w] = z;
 
-    // E once more, four values along N at the wavefront's value columns (for dv, one bf16 part), and the first dv block's
-    // do, on their way while the scores are weighted
-    f4 e[NT / 16];
+    // E once more, eight values along N at the wavefront's value columns (for dv, one bf16 part), on their way while the
+    // scores are weighted
+    f8 e[NT / 32];
     auto fetch_adjoint = [&](int pb) {
-        const float *src = Ep + (int64_t)(pb * kPB + 16 * w + col) * NT + g4;
+        const float *src = Ep + (int64_t)(pb * kPB + 16 * w + col) * NT + 2 * g4;
 #pragma unroll
-        for (int i = 0; i < NT / 16; ++i) e[i] = *reinterpret_cast<const f4 *>(src + 16 * i);
+        for (int n = 0; n < NT / 32; ++n)
+            e[n] = join(*reinterpret_cast<const f4 *>(src + 32 * n), *reinterpret_cast<const f4 *>(src + 32 * n + 4));
     };
     fetch_adjoint(0);
     lds_barrier();  // V's tile is free: A1 takes its place
@@ -334,9 +337,9 @@ void la_grad_kernel(LinAttnLaunch a) {
         for (int b = 0; b < 4; ++b) dv[b] = f4{0, 0, 0, 0};
 #pragma unroll
         for (int n = 0; n < NT / 32; ++n) {
-            const Split<T, 1> es(join(e[2 * n], e[2 * n + 1]));
+            const Split<T, 1> es(e[n]);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) mma(dv[b], es, half_frag(s_k, SN, 16 * b, 32 * n));
+            for (int b = 0; b < 4; ++b) mma(dv[b], es, row_frag(s_k, SN, 16 * b, 32 * n));
         }
         const Frag<T> d0 = col_frag(s_d, SV, 0, 16 * w), d1 = col_frag(s_d, SV, 32, 16 * w);
 #pragma unroll

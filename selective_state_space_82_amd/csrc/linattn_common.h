@@ -4,13 +4,11 @@
 // Every product is a sum of 16×16 tiles D = A·Bᵀ over a contraction axis taken 32 at a time. Lane l = 16·grp + col
 // of a wavefront supplies, for row `col` of A (and of B), 8 of the 32 contraction values, and receives
 // D[4·grp + r][col], r < 4. The order of a contraction axis is free as long as both operands use the same:
-//   plain    values 8·grp .. 8·grp + 7: one 16-byte LDS read along a row (bf16);
-//   halves   4·grp + j and 16 + 4·grp + j, j < 4: what two neighbouring result tiles hold in each lane, so that the
-//            state, kept as result tiles, is an operand without being moved;
-//   spread   8·(grp % 2) + grp / 2 + 2j, and the same + 16: rows two apart, which lie 8 LDS banks apart at the row
+//   plain    values 8·grp .. 8·grp + 7: one 16-byte LDS read along a row (bf16), which moves 128 bytes a clock (two of
+//            8 bytes each: 64);
+//   spread   8·(grp % 2) + grp / 2 + 2j, and the same + 16, j < 4: rows two apart, which lie 8 LDS banks apart at the row
 //            distances used here, so that the 32 lanes of a transposing read down 16 columns touch 64 different
-//            banks (with neighbouring rows they meet in half of them, which the counters showed as the largest
-//            part of all LDS conflicts).
+//            banks (8.5 clocks for 1 KB; in the plain order, where they meet in half of them, 12).
 #pragma once
 
 #include <type_traits>
@@ -22,7 +20,7 @@ namespace ssm {
 namespace la {
 
 constexpr int kC = 64;        // steps per chunk
-constexpr int kPB = 64;       // value columns per four wavefronts (16 each); P is padded to it in scratch
+constexpr int kPB = 64;       // value columns per workgroup; P is padded to it in scratch
 constexpr int kThreads = 256; // four wavefronts
 // Log-decays below this count as this: e^-1e4 is 0 in fp32, and so is every product with it, while running sums
 // stay finite (−inf would turn differences of sums into NaN).
@@ -69,20 +67,6 @@ __device__ __forceinline__ f8 row_frag(const float *tile, int stride, int row0, 
     const int l = threadIdx.x & 63;
     const float *p = tile + (row0 + (l & 15)) * stride + n0 + 8 * (l >> 4);
     const f4 u = *reinterpret_cast<const f4 *>(p), v = *reinterpret_cast<const f4 *>(p + 4);
-    return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-// The same in the order `halves`.
-__device__ __forceinline__ bf8 half_frag(const uint16_t *tile, int stride, int row0, int n0) {
-    const int l = threadIdx.x & 63;
-    const uint16_t *p = tile + (row0 + (l & 15)) * stride + n0 + 4 * (l >> 4);
-    const bf4 u = *reinterpret_cast<const bf4 *>(p), v = *reinterpret_cast<const bf4 *>(p + 16);
-    return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-__device__ __forceinline__ f8 half_frag(const float *tile, int stride, int row0, int n0) {
-    const int l = threadIdx.x & 63;
-    const float *p = tile + (row0 + (l & 15)) * stride + n0 + 4 * (l >> 4);
-    const f4 u = *reinterpret_cast<const f4 *>(p), v = *reinterpret_cast<const f4 *>(p + 16);
     return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
