@@ -263,3 +263,22 @@ def test_a_block_of_norm_mixer_and_head_norm(dtype):
                            (ga["dg"], refs[5], "dg")):
         err = float((got.double().cpu() - ref).norm() / ref.norm())
         assert err <= tol, (what, err)
+
+
+def test_offsets_past_32_bits():
+    rows, d = 2 ** 20 + 3, 2048
+    x = torch.zeros(rows, d, dtype=BF16, device="cuda")
+    tail = torch.randn(3, d, generator=torch.Generator().manual_seed(3)).to(BF16).cuda()
+    x[-3:] = tail
+    w = torch.full((d,), 2.0, device="cuda")
+    y, m, r = api.ssm_layernorm_fwd(x, w, return_stats=True)
+    y2, m2, r2 = api.ssm_layernorm_fwd(tail, w, return_stats=True)
+    assert torch.equal(y[-3:], y2) and torch.equal(m[-3:], m2) and torch.equal(r[-3:], r2)
+    assert not y[:1000].any() and not y[-1000:-3].any()
+    g = api.ssm_layernorm_bwd(x, w, dy=x, mean=m, rstd=r)
+    g2 = api.ssm_layernorm_bwd(tail, w, dy=tail, mean=m2, rstd=r2)
+    assert torch.equal(g["dx"][-3:], g2["dx"])
+    # the rows of zeros add nothing; the last three are summed in another order
+    size = (tail.double().abs() * 4).sum(0)
+    for n in ("dw", "dbias"):
+        assert ((g[n] - g2[n]).abs().double() <= 8 * U * size * 4).all(), n

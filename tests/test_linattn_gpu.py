@@ -435,3 +435,65 @@ def test_no_workspace_takes_the_librarys_scratch():
     assert st == 0
     torch.cuda.synchronize()
     assert torch.equal(o, o2) and torch.equal(S, S2)
+
+
+def test_widest_values():
+    check_fwd(make(1, 70, 2, 1, 24, 1024, dtype=BF16, seed=71), "P 1024")
+    check_bwd(make(1, 70, 2, 1, 24, 1024, dtype=BF16, seed=71), "P 1024")
+
+
+def test_offsets_past_32_bits():
+    """Rows of the batch more than 2^31 elements apart, and a state of more than 2^31 elements."""
+    b, L, H, N, P = 2, 70, 2, 16, 24
+    x = gpu(make(b, L, H, H, N, P, dtype=BF16, seed=81))
+    far = torch.zeros(2 ** 31 + 2 * L * H * P, dtype=BF16, device="cuda")
+    v = far.as_strided((b, L, H, P), (2 ** 31 + 8, H * P, P, 1))
+    v.copy_(x["v"])
+    o, S = api.ssm_linattn_fwd(x["q"], x["k"], x["v"], x["g"])
+    o2, S2 = api.ssm_linattn_fwd(x["q"], x["k"], v, x["g"])
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    a = api.ssm_linattn_bwd(x["q"], x["k"], x["v"], x["g"], do=x["do"])
+    c = api.ssm_linattn_bwd(x["q"], x["k"], v, x["g"], do=x["do"])
+    assert all(torch.equal(a[n], c[n]) for n in a)
+    del far, v
+    b, H, N, P = 520, 64, 128, 512  # 2.18e9 state elements
+    state = torch.zeros(b, H, P, N, dtype=F32, device="cuda")
+    state[-1, -1] = 2.0
+    q, k, v = torch.ones(b, 1, N, device="cuda"), torch.ones(b, 1, N, device="cuda"), torch.ones(b, H, P, device="cuda")
+    o = api.ssm_linattn_step(state, q, k, v, torch.zeros(H, device="cuda"))
+    assert (o[-1, -1] == 3.0 * N).all() and (o[:-1] == N).all() and (o[-1, :-1] == N).all()
+    assert (state[-1, -1] == 3.0).all() and (state[-1, 0] == 1.0).all() and (state[0] == 1.0).all()
+
+
+def test_calls_at_once_on_two_streams():
+    """Two streams, each with its own workspace, at the same time: each call's own result."""
+    xs = [gpu(make(1, 1500, 2, 1, 32, 32, first=True, seed=90 + i)) for i in range(2)]
+    run = lambda x: list(api.ssm_linattn_bwd(x["q"], x["k"], x["v"], x["g"], do=x["do"], initial_state=x["first"],  # noqa: E731
+                                             d_final_state=x["d_final"]).values()) + \
+        list(api.ssm_linattn_fwd(x["q"], x["k"], x["v"], x["g"], initial_state=x["first"]))
+    want = [run(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = run(xs[i])
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, c) for a, c in zip(w, g))
+
+
+def test_short_calls_keep_their_accuracy():
+    """A result that hangs on one score (one step, heads of a group that cancel) keeps the accuracy of its own rounding:
+    against 64 bits at most 1.5 times as far off as rounding the 64-bit result to bf16."""
+    for seed, (b, L, H, G, N, P) in enumerate([(5, 1, 40, 5, 64, 128), (2, 2, 64, 8, 64, 128), (4, 4, 8, 8, 64, 128),
+                                               (3, 13, 16, 2, 32, 32)]):
+        x = make(b, L, H, G, N, P, dtype=BF16, seed=seed)
+        t, w = gpu(x), wide(x)
+        got = api.ssm_linattn_bwd(t["q"], t["k"], t["v"], t["g"], do=t["do"], scale=t["scale"])
+        ref = R.grads(w["q"], w["k"], w["v"], w["g"], w["scale"], w["do"])
+        for n in ("dq", "dk", "dv"):
+            mine = float((got[n].double().cpu() - ref[n]).norm())
+            own = float((ref[n].to(BF16).double() - ref[n]).norm())
+            assert mine <= 1.5 * own, (n, L, mine / own)
