@@ -565,13 +565,23 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def ssm_linattn_workspace(b, L, H, G, N, P, dtype=torch.float32, *, gradient=False, g_per_step=True) -> int:
-    """Workspace bytes of ssm_linattn_fwd (or ssm_linattn_bwd) for this shape (host only)."""
+def _linattn_bytes(gradient, b, L, H, G, N, P, code, per_step) -> int:
     n = ctypes.c_int64()
-    status = lib().ssm_linattn_workspace(int(bool(gradient)), b, L, H, G, N, P, _dtype_code(dtype),
-                                         int(bool(g_per_step)), ctypes.byref(n))
+    status = lib().ssm_linattn_workspace(gradient, b, L, H, G, N, P, code, per_step, ctypes.byref(n))
     _raise(status, "ssm_linattn_workspace")
     return n.value
+
+
+def _layernorm_bytes(rows, d, w_rows) -> int:
+    n = ctypes.c_int64()
+    status = lib().ssm_layernorm_bwd_workspace(rows, d, w_rows, ctypes.byref(n))
+    _raise(status, "ssm_layernorm_bwd_workspace")
+    return n.value
+
+
+def ssm_linattn_workspace(b, L, H, G, N, P, dtype=torch.float32, *, gradient=False, g_per_step=True) -> int:
+    """Workspace bytes of ssm_linattn_fwd (or ssm_linattn_bwd) for this shape (host only)."""
+    return _linattn_bytes(int(bool(gradient)), b, L, H, G, N, P, _dtype_code(dtype), int(bool(g_per_step)))
 
 
 def ssm_linattn_fwd(q, k, v, g, *, scale=1.0, initial_state=None, lengths=None, o=None, final_state=None,
@@ -592,16 +602,17 @@ def ssm_linattn_fwd(q, k, v, g, *, scale=1.0, initial_state=None, lengths=None, 
     with _on_device(dev):
         if o is None:
             o = torch.empty((b, L, H, P), dtype=v.dtype, device=dev)
-        _check("o", o, (b, L, H, P), v.dtype, dev)
-        if final_state is None and return_final_state:
+        else:
+            _check("o", o, (b, L, H, P), v.dtype, dev)
+        if final_state is not None:
+            _check("final_state", final_state, (b, H, P, N), torch.float32, dev)
+        elif return_final_state:
             final_state = torch.empty((b, H, P, N), dtype=torch.float32, device=dev)
-        _check("final_state", final_state, (b, H, P, N), torch.float32, dev)
-        need = ctypes.c_int64()
-        _raise(lib().ssm_linattn_workspace(0, b, L, H, G, N, P, code, per_step, ctypes.byref(need)), "ssm_linattn_fwd")
-        ws = _workspace(need.value, dev)
+        need = _linattn_bytes(0, b, L, H, G, N, P, code, per_step)
+        ws = _workspace(need, dev)
         status = lib().ssm_linattn_fwd(_at(q), _at(k), _at(v), _at(g), per_step, float(scale), _at(initial_state),
                                        _at(lengths), _at(o), _at(final_state), b, L, H, G, N, P, code,
-                                       _linattn_strides(q, k, v), _at(ws), need.value, _raw_stream(dev))
+                                       _linattn_strides(q, k, v), _at(ws), need, _raw_stream(dev))
     _raise(status, "ssm_linattn_fwd")
     return o, final_state
 
@@ -620,7 +631,8 @@ def ssm_linattn_step(state, q, k, v, g, *, scale=1.0, o=None):
     with _on_device(dev):
         if o is None:
             o = torch.empty((b, H, P), dtype=v.dtype, device=dev)
-        _check("o", o, (b, H, P), v.dtype, dev)
+        else:
+            _check("o", o, (b, H, P), v.dtype, dev)
         status = lib().ssm_linattn_step(_at(state), _at(q), _at(k), _at(v), _at(g), per_step, float(scale), _at(o),
                                         b, H, G, N, P, code, _linattn_strides(q, k, v), _raw_stream(dev))
     _raise(status, "ssm_linattn_step")
@@ -645,13 +657,12 @@ def ssm_linattn_bwd(q, k, v, g, *, do, scale=1.0, initial_state=None, d_final_st
         out = {"dq": torch.empty((b, L, G, N), dtype=st, device=dev), "dk": torch.empty((b, L, G, N), dtype=st, device=dev),
                "dv": torch.empty((b, L, H, P), dtype=st, device=dev), "dg": torch.empty(g.shape, dtype=f32, device=dev),
                "d_initial_state": torch.empty((b, H, P, N), dtype=f32, device=dev) if want_d_initial_state else None}
-        need = ctypes.c_int64()
-        _raise(lib().ssm_linattn_workspace(1, b, L, H, G, N, P, code, per_step, ctypes.byref(need)), "ssm_linattn_bwd")
-        ws = _workspace(need.value, dev)
+        need = _linattn_bytes(1, b, L, H, G, N, P, code, per_step)
+        ws = _workspace(need, dev)
         status = lib().ssm_linattn_bwd(_at(q), _at(k), _at(v), _at(g), per_step, float(scale), _at(initial_state),
                                        _at(lengths), _at(do), _at(d_final_state), _at(out["dq"]), _at(out["dk"]),
                                        _at(out["dv"]), _at(out["dg"]), _at(out["d_initial_state"]), b, L, H, G, N, P,
-                                       code, _linattn_strides(q, k, v, do), _at(ws), need.value, _raw_stream(dev))
+                                       code, _linattn_strides(q, k, v, do), _at(ws), need, _raw_stream(dev))
     _raise(status, "ssm_linattn_bwd")
     return out
 
@@ -690,9 +701,12 @@ def ssm_layernorm_fwd(x, w=None, bias=None, *, eps=1e-5, y=None, return_stats=Fa
     with _on_device(dev):
         if y is None:
             y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        _check("y", y, x.shape, x.dtype, dev)
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if return_stats else None
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if return_stats else None
+        else:
+            _check("y", y, x.shape, x.dtype, dev)
+        mean = rstd = None
+        if return_stats:
+            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            rstd = torch.empty_like(mean)
         status = lib().ssm_layernorm_fwd(_at(x), _at(w), _at(bias), _at(y), _at(mean), _at(rstd), rows,
                                          x.shape[-1], k, stride, float(eps), code, _raw_stream(dev))
     _raise(status, "ssm_layernorm_fwd")
@@ -724,12 +738,10 @@ def ssm_layernorm_bwd(x, w=None, *, dy, mean, rstd, want_dw=True, want_dbias=Tru
         out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
                "dw": torch.empty(shape, dtype=torch.float32, device=dev) if want_dw else None,
                "dbias": torch.empty(shape, dtype=torch.float32, device=dev) if want_dbias else None}
-        need = ctypes.c_int64()
-        if want_dw or want_dbias:
-            _raise(lib().ssm_layernorm_bwd_workspace(rows, d, k, ctypes.byref(need)), "ssm_layernorm_bwd")
-        ws = _workspace(need.value, dev)
+        need = _layernorm_bytes(rows, d, k) if want_dw or want_dbias else 0
+        ws = _workspace(need, dev)
         status = lib().ssm_layernorm_bwd(_at(x), _at(w), _at(dy), _at(mean), _at(rstd), _at(out["dx"]),
                                          _at(out["dw"]), _at(out["dbias"]), rows, d, k, stride, dy_stride, code,
-                                         _at(ws), need.value, _raw_stream(dev))
+                                         _at(ws), need, _raw_stream(dev))
     _raise(status, "ssm_layernorm_bwd")
     return out
