@@ -305,9 +305,9 @@ SSM_API ssm_status_t ssm_ssd_fwd(const void *x, const void *delta, const float *
  *                     may overlap (other streams, captured graphs replayed at once) need one each.
  * Products are exact bf16 products summed in fp32 (bf16; fp32 operands, that is states and decayed scores, enter
  * as one or two bf16 parts where the result is bf16, as three where it is fp32) or fp32 products (f32). All sums,
- * decays and states are fp32, the running sum of g in a chunk fp64. Results are deterministic. A NaN or Inf at one step reaches outputs and gradients as the
- * formulas say, except that an Inf may come out as NaN, and that gradients (dq, dk, dv, dg) may become NaN at every
- * step of the 64-step chunk it is in.
+ * decays and states are fp32, the running sum of g in a chunk fp64. Results are deterministic. A NaN or Inf at one
+ * step reaches outputs and gradients as the formulas say, except that an Inf may come out as NaN, and that gradients
+ * (dq, dk, dv, dg) may become NaN at every step of the 64-step chunk it is in.
  * b, H, G, N, P >= 1; G divides H; H times the larger of 128 and P (rounded up to 64) is at most 2^24;
  * N <= SSM_LINATTN_MAX_N, P <= SSM_LINATTN_MAX_P (SSM_ERR_UNSUPPORTED above); L >= 0. With L = 0 the
  * forward call copies the initial state (or zeros) to final_state, the gradient call d_final_state (or zeros) to

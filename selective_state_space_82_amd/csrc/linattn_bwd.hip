@@ -46,7 +46,9 @@ __device__ __forceinline__ float sum_cols(float v) {
 // PARTS: bf16 parts of the scores A1 and A2. One in general: half a step of bf16 on each product's size, as the results'
 // own rounding (dq, dk and dv are then 1.4 times as far off as by that alone). Two where that is not all: where a group's
 // heads are summed in fp32, whose shares cancel while their roundings do not (twice as far off), and in a single chunk,
-// where a result may hang on one score.
+// where a result may hang on one score. Calls of few workgroups take two for the adjoint in dv too, as few results can be
+// further off than 1.4 times by chance: 1 row of 2048 steps, 8 heads, 128 by 128 takes 54 us against 52. With many it
+// costs more: the 62 us above become 74, a group's adjoint in two parts 9 % of all (4 rows of 2048, 24 heads on 4, 64 by 64).
 template <typename T, int NT, bool VEC, int PARTS>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && NT < 128 ? 4 - PARTS : 1)))
 void la_grad_kernel(LinAttnLaunch a) {
@@ -216,8 +218,8 @@ void la_grad_kernel(LinAttnLaunch a) {
     z = sum_groups(sum_cols(z));
     if (l == 0) s_z[w] = z;
 
-    // E once more, eight values along N at the wavefront's value columns (for dv, one bf16 part), on their way while the
-    // scores are weighted
+    // E once more, eight values along N at the wavefront's value columns (for dv, one bf16 part, or two in a call of few
+    // workgroups), on their way while the scores are weighted
     f8 e[NT / 32];
     auto fetch_adjoint = [&](int pb) {
         const float *src = Ep + (int64_t)(pb * kPB + 16 * w + col) * NT + 2 * g4;
@@ -226,6 +228,7 @@ void la_grad_kernel(LinAttnLaunch a) {
             e[n] = join(*reinterpret_cast<const f4 *>(src + 32 * n), *reinterpret_cast<const f4 *>(src + 32 * n + 4));
     };
     fetch_adjoint(0);
+    const bool few = gridDim.x <= kFewBlocks;
     lds_barrier();  // V's tile is free: A1 takes its place
 
     // the tiles right of the diagonal that a 32-step contraction touches
@@ -337,9 +340,12 @@ void la_grad_kernel(LinAttnLaunch a) {
         for (int b = 0; b < 4; ++b) dv[b] = f4{0, 0, 0, 0};
 #pragma unroll
         for (int n = 0; n < NT / 32; ++n) {
-            const Split<T, 1> es(e[n]);
+            auto through = [&](const auto &es) {
 #pragma unroll
-            for (int b = 0; b < 4; ++b) mma(dv[b], es, row_frag(s_k, SN, 16 * b, 32 * n));
+                for (int b = 0; b < 4; ++b) mma(dv[b], es, row_frag(s_k, SN, 16 * b, 32 * n));
+            };
+            if (PARTS == 2 && few) through(Split<T, 2>(e[n]));
+            else through(Split<T, 1>(e[n]));
         }
         const Frag<T> d0 = col_frag(s_d, SV, 0, 16 * w), d1 = col_frag(s_d, SV, 32, 16 * w);
 #pragma unroll
@@ -399,7 +405,7 @@ hipError_t grads(const LinAttnLaunch &p, hipStream_t stream) {
     };
     const std::integral_constant<int, 1> one;
     const std::integral_constant<int, sizeof(T) == 2 ? 2 : 1> two;
-    const bool exact = p.G < p.H || p.L <= kC;
+    const bool exact = p.G < p.H || p.L <= kC || grid.x <= kFewBlocks;
     if (p.vec) exact ? launch(std::true_type{}, two) : launch(std::true_type{}, one);
     else exact ? launch(std::false_type{}, two) : launch(std::false_type{}, one);
     hipError_t e = hipGetLastError();

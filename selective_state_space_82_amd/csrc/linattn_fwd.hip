@@ -49,8 +49,11 @@ __device__ __forceinline__ const float *decays_of(const LinAttnLaunch &a, const 
 // scores and state products 10 %, without the stores 8 %. Of the bf16 matrix rate it reaches 7 % by the recurrence's
 // operations (222 Tflop/s), about three times that by the products it makes. Three 64-step tiles, the scores in two parts
 // and the state's fragments fill half a compute unit's LDS, so 128 steps per chunk would leave one workgroup on it.
-template <typename T, int NT, bool VEC>
-__global__ __launch_bounds__(kOutThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && VEC ? 4 : 2))) void la_out_kernel(LinAttnLaunch a) {
+// SPARTS: bf16 parts in which the state enters the outputs. One in general: half a step of bf16 on each product's size, as
+// their own rounding (o is then up to 1.4 times as far off as by that alone). Two where that costs little: see outputs().
+template <typename T, int NT, bool VEC, int SPARTS>
+__global__ __launch_bounds__(kOutThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && VEC && SPARTS == 1 ? 4 : 2)))
+void la_out_kernel(LinAttnLaunch a) {
     constexpr int SN = NT + kPad<T>, SP = kC + kPad<T>, SV = kPB + kPad<T>;
     constexpr int PARTS = sizeof(T) == 2 ? 2 : 1, NF = NT / 32;
     typedef typename std::conditional<sizeof(T) == 2, bf4, f4>::type Half;  // a lane's part of one result tile
@@ -58,7 +61,7 @@ __global__ __launch_bounds__(kOutThreads) __attribute__((amdgpu_waves_per_eu(siz
     __shared__ __align__(16) T s_k[kC * SN];
     __shared__ __align__(16) T s_v[kC * SV];
     __shared__ __align__(16) T s_p[PARTS][kC * SP];  // decayed scores [t][s], s in the order spread
-    __shared__ __align__(16) Half s_s[4][NF][64][2]; // the state's operand fragments
+    __shared__ __align__(16) Half s_s[SPARTS][4][NF][64][2];  // the state's operand fragments
     __shared__ Decays s_g[2];
 
     const Work wk = work_of<4>(a, work_index(blockIdx.x, gridDim.x), a.n_seg);
@@ -93,13 +96,18 @@ __global__ __launch_bounds__(kOutThreads) __attribute__((amdgpu_waves_per_eu(siz
                               ? a.initial_state[(wk.bh * a.P + p_lane) * a.N + n] : 0.0f;
             }
     }
-    // the state enters the outputs as one bf16 part: half a step of bf16 on each product's size, as their own rounding
     auto put_state = [&]() {
 #pragma unroll
         for (int i = 0; i < NF; ++i) {
             // four values of N of column col, 16·(tile % 2) + 4·grp into their 32, where the plain order has them
             const int tile = tw * NF + i;
-            s_s[pw][tile >> 1][16 * (2 * (tile & 1) + (g4 >> 3)) + col][g4 >> 2 & 1] = __builtin_convertvector(S[i], Half);
+            f4 left = S[i];
+#pragma unroll
+            for (int e = 0; e < SPARTS; ++e) {
+                const Half part = __builtin_convertvector(left, Half);
+                s_s[e][pw][tile >> 1][16 * (2 * (tile & 1) + (g4 >> 3)) + col][g4 >> 2 & 1] = part;
+                if (e + 1 < SPARTS) left -= __builtin_convertvector(part, f4);
+            }
         }
     };
     put_state();
@@ -166,9 +174,11 @@ __global__ __launch_bounds__(kOutThreads) __attribute__((amdgpu_waves_per_eu(siz
         // D[s][t] = k_s·q_t; a wavefront takes those of its two blocks of t and of s block pw, in two bf16 parts.
         f4 acc[2];
         __builtin_amdgcn_s_setprio(1);  // the workgroup that computes goes before the one that loads and stores: 3 % less time
-        Frag<T> sf[NF];
+        Frag<T> sf[SPARTS][NF];
 #pragma unroll
-        for (int n = 0; n < NF; ++n) sf[n] = *reinterpret_cast<const Frag<T> *>(&s_s[pw][n][l][0]);
+        for (int e = 0; e < SPARTS; ++e)
+#pragma unroll
+            for (int n = 0; n < NF; ++n) sf[e][n] = *reinterpret_cast<const Frag<T> *>(&s_s[e][pw][n][l][0]);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const int tb = 2 * tw + b;
@@ -177,7 +187,9 @@ __global__ __launch_bounds__(kOutThreads) __attribute__((amdgpu_waves_per_eu(siz
             for (int n = 0; n < NF; ++n) qf[n] = row_frag(s_q, SN, 16 * tb, 32 * n);
             acc[b] = f4{0, 0, 0, 0};
 #pragma unroll
-            for (int n = 0; n < NF; ++n) mma(acc[b], sf[n], qf[n]);
+            for (int e = 0; e < SPARTS; ++e)
+#pragma unroll
+                for (int n = 0; n < NF; ++n) mma(acc[b], sf[e][n], qf[n]);
             acc[b] *= dec.in[16 * tb + col];
             if (tb >= pw) {
                 f4 sc = {0, 0, 0, 0};
@@ -234,7 +246,9 @@ __global__ __launch_bounds__(kOutThreads) __attribute__((amdgpu_waves_per_eu(siz
                 for (int n = 0; n < NF; ++n) qf[n] = row_frag(s_q, SN, 16 * (2 * tw + b), 32 * n);
                 f4 v = {0, 0, 0, 0};
 #pragma unroll
-                for (int n = 0; n < NF; ++n) mma(v, *reinterpret_cast<const Frag<T> *>(&s_s[pw][n][l][0]), qf[n]);
+                for (int e = 0; e < SPARTS; ++e)
+#pragma unroll
+                    for (int n = 0; n < NF; ++n) mma(v, *reinterpret_cast<const Frag<T> *>(&s_s[e][pw][n][l][0]), qf[n]);
                 v *= dec.in[tl];
                 for (int s = 0; s <= tl; ++s) {
                     float pr = 0.0f;
@@ -461,8 +475,16 @@ hipError_t states(const LinAttnLaunch &p, int64_t n_states, int64_t first_adjoin
 template <typename T>
 hipError_t outputs(const LinAttnLaunch &p, hipStream_t stream) {
     const dim3 grid((unsigned)(p.b * p.H * p.n_seg) * (unsigned)((p.P + kPB - 1) / kPB));
+    constexpr int TWO = sizeof(T) == 2 ? 2 : 1;
+    // Few workgroups: two parts cost 2 % (1 row of 512 steps, 16 heads, 64 by 64: 18.3 us against 18.1), and so few results
+    // can be further off than 1.4 times by chance. Many: their LDS leaves one workgroup of two on a compute unit (64 rows
+    // of 64 steps, 32 heads, 128 by 64: 106 us against 82).
+    const bool two = grid.x <= kFewBlocks && (p.initial_state || p.L > kC);
     return by_width(p, [&](auto nt, auto, auto vec) {
-        la_out_kernel<T, decltype(nt)::value, decltype(vec)::value><<<grid, kOutThreads, 0, stream>>>(p);
+        constexpr int NT = decltype(nt)::value;
+        constexpr bool VEC = decltype(vec)::value;
+        if (two) la_out_kernel<T, NT, VEC, TWO><<<grid, kOutThreads, 0, stream>>>(p);
+        else la_out_kernel<T, NT, VEC, 1><<<grid, kOutThreads, 0, stream>>>(p);
         return hipGetLastError();
     });
 }
