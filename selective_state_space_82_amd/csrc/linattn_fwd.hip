@@ -224,6 +224,8 @@ void la_out_kernel(LinAttnLaunch a) {
         if (w == 3) s_g[(ch + 1 - ch0) & 1].set<true>(log_decay(g_now), a.scale);
         lds_barrier();
 
+        // From here to the next barrier s_s is written by the wavefronts that are done: nothing below reads it.
+        const f4 through[2] = {acc[0], acc[1]};
         Frag<T> vf[2];
 #pragma unroll
         for (int sp = 0; sp < 2; ++sp) vf[sp] = col_frag<true>(s_v, SV, 32 * sp, 16 * pw);
@@ -241,15 +243,7 @@ void la_out_kernel(LinAttnLaunch a) {
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 const int tl = 16 * (2 * tw + b) + col;
-                Frag<T> qf[NF];
-#pragma unroll
-                for (int n = 0; n < NF; ++n) qf[n] = row_frag(s_q, SN, 16 * (2 * tw + b), 32 * n);
-                f4 v = {0, 0, 0, 0};
-#pragma unroll
-                for (int e = 0; e < SPARTS; ++e)
-#pragma unroll
-                    for (int n = 0; n < NF; ++n) mma(v, *reinterpret_cast<const Frag<T> *>(&s_s[e][pw][n][l][0]), qf[n]);
-                v *= dec.in[tl];
+                f4 v = b == 0 ? through[0] : through[1];
                 for (int s = 0; s <= tl; ++s) {
                     float pr = 0.0f;
 #pragma unroll
@@ -281,7 +275,7 @@ void la_out_kernel(LinAttnLaunch a) {
             else update(Split<T, 2>(wide(vf[sp]) * join(u, v)));
         }
         __builtin_amdgcn_s_setprio(0);
-        put_state();  // its readers passed the last barrier
+        put_state();  // its readers, above the last barrier, are past it
         lds_barrier();
     }
     store_res();
