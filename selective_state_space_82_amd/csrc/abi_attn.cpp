@@ -122,6 +122,8 @@ int64_t layout(const AttnSizes &z, bool gradient, bool g_per_step, void *base, L
     if (p->n_seg == 0 || (!gradient && p->n_seg == 1)) return 0;
     p->S = s.next<float>(n * state);
     p->gsum = s.next<double>(n);
+    // a segment of one chunk has no chunks that the walk over its own state could leave out
+    if (!gradient && p->seg_chunks > 1) p->bad = s.next<uint32_t>(n * ceil_div(z.P, kBlockP) * 8);
     if (gradient) {
         p->E = s.next<float>(n * state);
         if (!g_per_step) p->dg_steps = s.next<float>(z.b * z.L * z.H);

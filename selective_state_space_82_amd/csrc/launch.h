@@ -240,6 +240,7 @@ struct LinAttnLaunch {
     int64_t seg_chunks, n_seg;
     float *S, *E;
     double *gsum;          // [b·H][n_seg] sums of g
+    uint32_t *bad;         // [b·H][n_seg][⌈P/64⌉][8 wavefronts]: whether the state a segment leaves holds a NaN or Inf
     float *dg_steps;       // [b][L][H] when g_per_step is false
     float *dq_part, *dk_part;  // [b][L][H][N] when G < H
     bool vec;              // every input and output row takes 16-byte accesses at multiples of 16 bytes

@@ -288,6 +288,22 @@ void la_out_kernel(LinAttnLaunch a) {
             store4<T, VEC>(rest, o_t, 16 * (2 * tw + b) + col, p_wave + g4, a.P, f4{0, 0, 0, 0});
     }
 
+    // what la_nonfinite_kernel asks for: whether the wavefront's part of the state the segment leaves is finite, and if it is
+    // not, that part, where the lane itself had read the state entering
+    if (a.bad && wk.seg + 1 < a.n_seg) {
+        float probe = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NF; ++i) probe += (S[i][0] * 0.0f + S[i][1] * 0.0f) + (S[i][2] * 0.0f + S[i][3] * 0.0f);
+        const bool bad = __any(probe != 0.0f);
+        const int64_t Pp = (a.P + kPB - 1) / kPB * kPB, at = wk.bh * a.n_seg + wk.seg;
+        if (l == 0) a.bad[(at * (Pp / kPB) + p0 / kPB) * 8 + w] = bad;
+        if (bad) {
+            float *dst = a.S + (at * Pp + p_lane) * NT + n0 + g4;
+#pragma unroll
+            for (int i = 0; i < NF; ++i) *reinterpret_cast<f4 *>(dst + 16 * i) = S[i];
+        }
+    }
+
     if (is_result && p_lane < a.P) {
         float *dst = a.final_state + (wk.bh * a.P + p_lane) * a.N;
 #pragma unroll
@@ -305,7 +321,8 @@ void la_out_kernel(LinAttnLaunch a) {
 // segment) as above. Both walk the chunks from the far end of the decay to the near one, S from the last chunk back
 // and E from the first on, so that each chunk's weights carry the decay of all chunks walked before it. The walk ends
 // where that decay is below e^-200: what the rest would add is it times a state (adjoint) of the recurrence, which as
-// an fp32 number is at most e^88.8, and the product is 0 in fp32 (smallest positive value e^-103.3).
+// an fp32 number is at most e^88.8, and the product is 0 in fp32 (smallest positive value e^-103.3). A NaN or Inf in the
+// rest is what that leaves out: la_nonfinite_kernel sees to it. (The gradient's segments have one chunk each.)
 template <typename T, int NT, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int64_t n_states, int64_t first_adjoint) {
     constexpr int THREADS = 64 * NW, PB = 16 * NW;
@@ -436,6 +453,45 @@ __global__ __launch_bounds__(kThreads) void la_carry_kernel(LinAttnLaunch a, int
             if (n + r < a.N) a.d_initial_state[(bh * a.P + p) * a.N + n + r] = carry[r];
 }
 
+// ---- a NaN or Inf that a walk over a segment's own state did not reach -------------------------------------------
+//
+// e^-200 times a NaN or Inf is not 0: once an element of the state is one, it stays one (Inf or NaN) for all later steps, and
+// so does its column of the outputs. The walk that gives the outputs meets every step and says which segments it left with
+// such an element; here one workgroup per (row, head, 64 value columns) carries it into the segments after. It costs a
+// launch in calls of more than one segment of more than one chunk, and a look at the words where all is finite.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void la_nonfinite_kernel(LinAttnLaunch a, int NT) {
+    const int64_t npb = (a.P + kPB - 1) / kPB, pb = blockIdx.x % npb, bh = blockIdx.x / npb;
+    const int64_t ib = bh / a.H, h = bh % a.H, last = a.n_seg - 1;
+    const int tid = threadIdx.x;
+    auto word = [&](int64_t seg, int w) { return a.bad[((bh * a.n_seg + seg) * npb + pb) * 8 + w]; };
+    uint32_t any = 0;
+    for (int64_t i = tid; i < last * 8; i += kThreads) any |= word(i / 8, (int)(i % 8));
+    if (!__syncthreads_or((int)any)) return;
+
+    __shared__ int s_from[kPB];  // the first segment that a column enters with a NaN or Inf
+    if (tid < kPB) s_from[tid] = (int)a.n_seg;
+    __syncthreads();
+    const float nan = __uint_as_float(0x7fc00000u);
+    for (int64_t seg = 0; seg < last; ++seg) {
+        const float *left = a.S + ((bh * a.n_seg + seg) * npb + pb) * kPB * NT;
+        for (int i = tid; i < kPB * NT; i += kThreads) {
+            const int p = i / NT, n = i % NT;
+            if (!word(seg, p / 16 + (2 * n >= NT ? 4 : 0)) || left[i] * 0.0f == 0.0f) continue;
+            atomicMin(&s_from[p], (int)seg + 1);
+            if (a.final_state && pb * kPB + p < a.P && n < a.N)
+                a.final_state[(bh * a.P + pb * kPB + p) * a.N + n] = nan;
+        }
+    }
+    __syncthreads();
+    const int64_t len = row_length(a.lengths, ib, a.L);
+    T *o = static_cast<T *>(a.o) + (ib * a.L * a.H + h) * a.P + pb * kPB;
+    const int p = tid % kPB;
+    if (pb * kPB + p < a.P)
+        for (int64_t t = s_from[p] * a.seg_chunks * kC + tid / kPB; t < len; t += kThreads / kPB)
+            o[t * a.H * a.P + p] = narrow<T>(nan);
+}
+
 // f(NT, NW, VEC): the padded width of N, wavefronts per workgroup, and whether all rows take 16-byte accesses. Eight
 // wavefronts share the scores, queries and keys of 128 value columns where P is that wide.
 template <typename F> hipError_t by_width(const LinAttnLaunch &p, F f) {
@@ -464,6 +520,13 @@ hipError_t states(const LinAttnLaunch &p, int64_t n_states, int64_t first_adjoin
         la_states_kernel<T, NT, NW, VEC><<<grid, 64 * NW, 0, stream>>>(p, n_states, first_adjoint);
         return hipGetLastError();
     });
+}
+
+template <typename T>
+hipError_t nonfinite(const LinAttnLaunch &p, hipStream_t stream) {
+    const dim3 grid((unsigned)(p.b * p.H) * (unsigned)((p.P + kPB - 1) / kPB));
+    la_nonfinite_kernel<T><<<grid, kThreads, 0, stream>>>(p, linattn_nt(p.N));
+    return hipGetLastError();
 }
 
 template <typename T>
@@ -505,7 +568,9 @@ hipError_t launch_linattn_fwd(const LinAttnLaunch &p, hipStream_t stream) {
         if (e == hipSuccess) e = launch_linattn_carry(p, false, stream);
         if (e != hipSuccess) return e;
     }
-    return p.bf16 ? la::outputs<uint16_t>(p, stream) : la::outputs<float>(p, stream);
+    hipError_t e = p.bf16 ? la::outputs<uint16_t>(p, stream) : la::outputs<float>(p, stream);
+    if (e == hipSuccess && p.bad) e = p.bf16 ? la::nonfinite<uint16_t>(p, stream) : la::nonfinite<float>(p, stream);
+    return e;
 }
 
 }  // namespace ssm

@@ -81,3 +81,57 @@ def test_one_walk_over_several_chunks(b, H, G, N, P, dtype):
         for bad in BAD:
             spots = [(i % b, t, 5 * i % heads, 7 * i % width) for i, t in enumerate(steps)]
             check(x, spots, name, bad, want)
+
+
+@pytest.mark.parametrize("rate", [0.01, 8.0], ids=["weak", "strong"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_segments_of_several_chunks(dtype, rate):
+    """Six segments of three chunks. With strong decays the walk over a segment's own state ends after its last chunk; what
+    is bad before that stays bad all the same, as it does in one walk over all steps."""
+    b, L, H, G, N, P = 3, 1003, 12, 4, 40, 72
+    x = make(b, L, H, G, N, P, dtype=dtype, rate=rate, first=True, seed=7)
+    assert segments(x) == 6
+    want = bounds(x)
+    # in the first, a middle and the last chunk of the first, a middle and the last segment
+    steps = [0, 70, 191, 192, 200, 300, 383, 700, 767, 768, 800, 900, 1002]
+    for name, width, heads in (("v", P, H), ("k", N, G), ("q", N, G)):
+        for bad in BAD:
+            at = steps if name == "v" else steps[::3]
+            spots = [(i % b, t, 5 * i % heads, 7 * i % width) for i, t in enumerate(at)]
+            check(x, spots, name, bad, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_bad_initial_state_stays(dtype):
+    """A NaN in the initial state: its column of the outputs and its element of the final state, in every segment."""
+    b, L, H, G, N, P = 3, 1003, 12, 4, 40, 72
+    x = make(b, L, H, G, N, P, dtype=dtype, rate=8.0, first=True, seed=7)
+    ro, tol, rS, tolS = bounds(x)
+    y = gpu(x)
+    y["first"][1, 5, 70, 33] = math.nan
+    o, S = api.ssm_linattn_fwd(y["q"], y["k"], y["v"], y["g"], scale=y["scale"], initial_state=y["first"])
+    o, S = o.cpu(), S.cpu()
+    assert bool(o[1, :, 5, 70].isnan().all()) and bool(S[1, 5, 70, 33].isnan())
+    o[1, :, 5, 70], S[1, 5, 70, 33] = ro[1, :, 5, 70].to(dtype), rS[1, 5, 70, 33].float()
+    R.assert_within(o, ro, tol, "o")
+    R.assert_within(S, rS, tolS, "state")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_bad_value_in_a_padded_batch_of_segments(dtype):
+    """Rows that end in the bad value's segment, in the one after it and before it: outputs past a row's end stay 0."""
+    b, L, H, G, N, P = 3, 1003, 12, 4, 40, 72
+    lens = [250, 700, 100]
+    x = make(b, L, H, G, N, P, dtype=dtype, rate=8.0, lengths=lens, seed=8)
+    assert segments(x) == 6
+    y = gpu(x)
+    y["v"][:, 200, 3, 7] = math.nan
+    want = api.ssm_linattn_fwd(gpu(x)["q"], y["k"], gpu(x)["v"], y["g"], lengths=y["lengths"])
+    o, S = api.ssm_linattn_fwd(y["q"], y["k"], y["v"], y["g"], lengths=y["lengths"])
+    for i, n in enumerate(lens):
+        assert not o[i, n:].any()
+        assert torch.isfinite(o[i, :200]).all()
+        assert bool(o[i, 200:n, 3, 7].isnan().all()) and bool(S[i, 3, 7].isnan().all()) == (n > 200)
+        o[i, 200:n, 3, 7] = want[0][i, 200:n, 3, 7]
+        S[i, 3, 7] = want[1][i, 3, 7]
+    assert torch.isfinite(o).all() and torch.isfinite(S).all()
