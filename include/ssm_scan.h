@@ -309,7 +309,10 @@ SSM_API ssm_status_t ssm_ssd_fwd(const void *x, const void *delta, const float *
  * step reaches outputs and gradients as the formulas say, except that an Inf may come out as NaN, and that gradients
  * (dq, dk, dv, dg) may become NaN at every step of the 64-step chunk it is in.
  * b, H, G, N, P >= 1; G divides H; H times the larger of 128 and P (rounded up to 64) is at most 2^24;
- * N <= SSM_LINATTN_MAX_N, P <= SSM_LINATTN_MAX_P (SSM_ERR_UNSUPPORTED above); L >= 0. With L = 0 the
+ * N <= SSM_LINATTN_MAX_N, P <= SSM_LINATTN_MAX_P (SSM_ERR_UNSUPPORTED above); L >= 0. A launch takes fewer than 2^32
+ * threads: SSM_ERR_SHAPE where b·H·⌈P/64⌉ (forward: times the segments the steps are cut into, one where b·H is large)
+ * reaches 2^23, in the step 2^24; and in the gradient where 2·b·H·⌈L/64⌉ reaches 2^24 (times ⌈P/128⌉, 2^23 where P > 64)
+ * or b·H·P·N, P padded to 64s and N to 32, 64 or 128, reaches 2^33. With L = 0 the
  * forward call copies the initial state (or zeros) to final_state, the gradient call d_final_state (or zeros) to
  * d_initial_state and zeros to a g_per_step = 0 dg. No output may overlap an input,
  * the workspace or another output. Errors as for ssm_scan_fwd; SSM_ERR_SCRATCH: workspace_bytes is too small.

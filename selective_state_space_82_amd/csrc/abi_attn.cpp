@@ -78,8 +78,7 @@ ssm_status_t check_sizes(const AttnSizes &z, ssm_dtype_t dtype) {
     int64_t bl = 0, bh = 0, n = 0;
     const int64_t L = z.L > 0 ? z.L : 1;
     if (!mul_ok(z.b, L, &bl) || !mul_ok(z.b, z.H, &bh) || bl > kMost || bh > kMost) return SSM_ERR_SHAPE;
-    // the padded widths bound every tensor, the states of all chunks and every grid (one workgroup per 64 value
-    // columns of a chunk)
+    // the padded widths bound every tensor and the states of all chunks
     const int64_t width = ceil_div(z.P, kBlockP) * kBlockP;
     if (z.H > kMostStep / (width > 128 ? width : 128)) return SSM_ERR_SHAPE;
     if (!mul_ok(bl, z.H * (width > 128 ? width : 128), &n) || n > kMost) return SSM_ERR_SHAPE;
@@ -113,6 +112,18 @@ void plan(const AttnSizes &z, bool gradient, LinAttnLaunch *p) {
         }
     }
     p->n_seg = p->seg_chunks > 0 ? ceil_div(chunks, p->seg_chunks) : 0;
+}
+
+// Whether HIP takes every launch of the planned call (launchable() in launch.h).
+bool launches(const AttnSizes &z, bool gradient, const LinAttnLaunch &p) {
+    if (p.n_seg == 0) return true;
+    const int64_t bh = z.b * z.H, blocks = ceil_div(z.P, kBlockP), cols = ssm::linattn_cols(z.P);
+    const int64_t walks = gradient ? 2 * p.n_seg - 1 : p.n_seg - 1;  // over the segments' own states and adjoints
+    const int64_t carries = bh * (blocks * kBlockP * ssm::linattn_nt(z.N) / (4 * ssm::kLinAttnThreads)) * (gradient ? 2 : 1);
+    if (!ssm::launchable(bh * walks * ceil_div(z.P, cols), 4 * cols)) return false;
+    if ((gradient || p.n_seg > 1) && !ssm::launchable(carries, ssm::kLinAttnThreads)) return false;
+    return gradient ? ssm::launchable(bh * p.n_seg, ssm::kLinAttnThreads)
+                    : ssm::launchable(bh * p.n_seg * blocks, ssm::kLinAttnOutThreads);
 }
 
 // Cuts the scratch at `base` (which may be null: for the size alone) into the call's pieces.
@@ -185,8 +196,10 @@ void set_common(const AttnSizes &z, ssm_dtype_t dtype, LinAttnLaunch *p) {
 
 ssm_status_t fill_state(const float *src, float *dst, int64_t n, hipStream_t stream) {
     if (!dst) return SSM_OK;
-    const hipError_t e = src ? hipMemcpyAsync(dst, src, (size_t)n * 4, hipMemcpyDeviceToDevice, stream)
-                             : ssm::launch_fill_zero(dst, n, stream);
+    hipError_t e = src ? hipMemcpyAsync(dst, src, (size_t)n * 4, hipMemcpyDeviceToDevice, stream) : hipSuccess;
+    constexpr int64_t kPiece = INT64_C(1) << 31;  // of the threads that HIP takes to a launch
+    for (int64_t i = 0; !src && i < n && e == hipSuccess; i += kPiece)
+        e = ssm::launch_fill_zero(dst + i, n - i < kPiece ? n - i : kPiece, stream);
     return e == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
@@ -213,6 +226,7 @@ ssm_status_t ssm_linattn_workspace(int32_t gradient, int64_t b, int64_t L, int64
     LinAttnLaunch p{};
     p.bf16 = dtype == SSM_BF16;
     plan(z, gradient != 0, &p);
+    if (!launches(z, gradient != 0, p)) return SSM_ERR_SHAPE;
     *bytes = layout(z, gradient != 0, g_per_step != 0, nullptr, &p);
     return SSM_OK;
 }
@@ -226,11 +240,11 @@ ssm_status_t ssm_linattn_fwd(const void *q, const void *k, const void *v, const 
     ssm_status_t st = check_sizes(z, dtype);
     if (st != SSM_OK) return st;
     LinAttnLaunch p{};
-    if (!set_strides(z, strides, false, &p)) return SSM_ERR_SHAPE;
-    if (L > 0 && (!q || !k || !v || !g || !o)) return SSM_ERR_NULL;
-    const int64_t es = dtype == SSM_BF16 ? 2 : 4, state = b * H * P * N;
     p.bf16 = dtype == SSM_BF16;
     plan(z, false, &p);
+    if (!launches(z, false, p) || !set_strides(z, strides, false, &p)) return SSM_ERR_SHAPE;
+    if (L > 0 && (!q || !k || !v || !g || !o)) return SSM_ERR_NULL;
+    const int64_t es = dtype == SSM_BF16 ? 2 : 4, state = b * H * P * N;
     const int64_t need = layout(z, false, g_per_step != 0, nullptr, &p);
     const Span outs[] = {{L > 0 ? o : nullptr, b * L * H * P * es}, {final_state, state * 4}, {workspace, need}};
     const Span ins[] = {{L > 0 ? q : nullptr, extent(b, L, G, N, p.q_b, p.q_t, p.q_h, es)},
@@ -259,6 +273,7 @@ ssm_status_t ssm_linattn_step(float *state, const void *q, const void *k, const 
     const ssm_status_t st = check_sizes(z, dtype);
     if (st != SSM_OK) return st;
     LinAttnLaunch p{};
+    if (!ssm::launchable(b * H * ceil_div(P, kBlockP), ssm::kLinAttnThreads)) return SSM_ERR_SHAPE;
     if (!set_strides(z, strides, true, &p)) return SSM_ERR_SHAPE;
     if (!state || !q || !k || !v || !g || !o) return SSM_ERR_NULL;
     const int64_t es = dtype == SSM_BF16 ? 2 : 4;
@@ -285,11 +300,11 @@ ssm_status_t ssm_linattn_bwd(const void *q, const void *k, const void *v, const 
     ssm_status_t st = check_sizes(z, dtype);
     if (st != SSM_OK) return st;
     LinAttnLaunch p{};
-    if (!set_strides(z, strides, false, &p)) return SSM_ERR_SHAPE;
+    plan(z, true, &p);
+    if (!launches(z, true, p) || !set_strides(z, strides, false, &p)) return SSM_ERR_SHAPE;
     if (L > 0 && (!q || !k || !v || !g || !do_ || !dq || !dk || !dv || !dg)) return SSM_ERR_NULL;
     if (L == 0 && !g_per_step && !dg) return SSM_ERR_NULL;
     const int64_t es = dtype == SSM_BF16 ? 2 : 4, state = b * H * P * N;
-    plan(z, true, &p);
     const int64_t need = layout(z, true, g_per_step != 0, nullptr, &p);
     const bool some = L > 0;
     const Span outs[] = {{some ? dq : nullptr, b * L * G * N * es}, {some ? dk : nullptr, b * L * G * N * es},

@@ -245,7 +245,10 @@ struct LinAttnLaunch {
     float *dq_part, *dk_part;  // [b][L][H][N] when G < H
     bool vec;              // every input and output row takes 16-byte accesses at multiples of 16 bytes
 };
-// Value columns per workgroup of the segment states' walk.
+// HIP takes fewer than 2^32 threads to a launch; the ABI layer refuses what would need more.
+inline bool launchable(int64_t workgroups, int64_t threads) { return workgroups <= ((INT64_C(1) << 32) - 1) / threads; }
+constexpr int kLinAttnThreads = 256, kLinAttnOutThreads = 512;
+// Value columns per workgroup of the segment states' walk, 16 to a wavefront.
 inline int64_t linattn_cols(int64_t P) { return P > 64 ? 128 : 64; }
 inline int linattn_nt(int64_t N) { return N <= 32 ? 32 : N <= 64 ? 64 : 128; }
 hipError_t launch_linattn_fwd(const LinAttnLaunch &p, hipStream_t stream);

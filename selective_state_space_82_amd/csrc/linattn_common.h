@@ -21,7 +21,7 @@ namespace la {
 
 constexpr int kC = 64;        // steps per chunk
 constexpr int kPB = 64;       // value columns per workgroup; P is padded to it in scratch
-constexpr int kThreads = 256; // four wavefronts
+constexpr int kThreads = kLinAttnThreads;  // four wavefronts
 // Up to this many workgroups each has a compute unit to itself: a call of so few takes a second bf16 part of its scores
 // (gradient) or its state (outputs) for little.
 constexpr unsigned kFewBlocks = 256;

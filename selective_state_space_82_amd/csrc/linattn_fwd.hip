@@ -11,7 +11,7 @@ namespace ssm {
 namespace la {
 namespace {
 
-constexpr int kOutThreads = 512;
+constexpr int kOutThreads = kLinAttnOutThreads;
 
 struct Work {
     int64_t ib, seg, bh;

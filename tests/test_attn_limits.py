@@ -1,0 +1,61 @@
+"""The largest calls of linear attention and layer norm: HIP takes fewer than 2^32 threads to a launch, so what would need
+more is refused before anything is launched, and what is just below runs."""
+import ctypes
+
+import pytest
+import torch
+
+from selective_state_space_82_amd import api
+from test_attn_abi_host import SHAPE, bwd, fwd, step
+
+I64 = ctypes.c_int64
+
+
+def workspace(gradient, b, L, H, G, N, P, dtype=0):
+    return api.lib().ssm_linattn_workspace(gradient, b, L, H, G, N, P, dtype, 1, ctypes.byref(I64()))
+
+
+def test_linear_attention_launches():
+    one = dict(G=1, N=4, P=4, L=1)
+    assert fwd(b=1 << 17, H=64, **one) == SHAPE             # 2^23 workgroups of 512 threads
+    assert workspace(0, 1 << 17, 1, 64, 1, 4, 4) == SHAPE
+    assert workspace(0, (1 << 17) - 1, 1, 64, 1, 4, 4) == 0
+    assert workspace(0, 1 << 16, 1, 64, 1, 4, 65) == SHAPE  # two blocks of value columns each
+    assert workspace(0, (1 << 16) - 1, 1, 64, 1, 4, 65) == 0
+    assert step(b=1 << 18, H=64, G=1, N=1, P=1) == SHAPE    # 2^24 workgroups of 256
+    assert step(b=1 << 16, H=64, G=1, N=1, P=193) == SHAPE
+    for L, b, P in ((1, 1 << 18, 4), (4097, 2048, 4), (4097, 1024, 128)):  # states and adjoints of every chunk
+        assert bwd(b=b, H=64, G=1, N=4, P=P, L=L) == SHAPE
+        assert workspace(1, b, L, 64, 1, 4, P) == SHAPE
+    assert workspace(1, 2016, 4097, 64, 1, 4, 4) == 0       # 64 · 2016 rows of 65 chunks: 129 walks each, below 2^24
+    assert workspace(1, 2 ** 14, 1, 64, 1, 128, 64) == SHAPE  # 2^33 state elements: 2^24 workgroups of the carry
+    assert workspace(1, 2 ** 14 - 1, 1, 64, 1, 128, 64) == 0
+
+
+@pytest.mark.gpu
+def test_linear_attention_up_to_the_limit():
+    """Just below the limits: 2^24 - 64 and 2^23 - 64 workgroups."""
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm GPU visible")
+    one = lambda *s: torch.ones(s, device="cuda")  # noqa: E731
+    b, H, g = 2 ** 18 - 1, 64, torch.zeros(64, device="cuda")
+    state = one(b, H, 1, 1)
+    o = api.ssm_linattn_step(state, one(b, 1, 1), one(b, 1, 1), one(b, H, 1), g)
+    assert bool((o == 2).all()) and bool((state == 2).all())
+    b = 2 ** 17 - 1
+    o, _ = api.ssm_linattn_fwd(one(b, 1, 1, 4), one(b, 1, 1, 4), one(b, 1, H, 4), g, return_final_state=False)
+    assert bool((o == 4).all())
+    with pytest.raises(api.SsmError) as e:
+        api.ssm_linattn_fwd(one(b + 1, 1, 1, 4), one(b + 1, 1, 1, 4), one(b + 1, 1, H, 4), g, return_final_state=False)
+    assert e.value.status == SHAPE
+
+
+@pytest.mark.gpu
+def test_no_steps_and_a_state_of_more_than_2_to_the_32_elements():
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm GPU visible")
+    b, H, N, P = 520, 64, 128, 1024  # 4.4e9 elements
+    z = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    S = torch.full((b, H, P, N), 7.0, device="cuda")
+    api.ssm_linattn_fwd(z(b, 0, 1, N), z(b, 0, 1, N), z(b, 0, H, P), z(H), final_state=S)
+    assert all(not bool(S[i].any()) for i in (0, 1, 255, 256, 257, 511, 512, 518, 519))
