@@ -369,8 +369,9 @@ SSM_API ssm_status_t ssm_linattn_bwd(const void *q, const void *k, const void *v
  *   dx                [rows][d] dtype, required; dw, dbias [w_rows][d] fp32 or NULL, summed in a fixed order
  *   workspace         as for ssm_linattn_fwd, of the bytes ssm_layernorm_bwd_workspace gives (0 without dw and dbias)
  * All sums are fp32 or wider. rows >= 0 (0: only dw and dbias are written, with zeros), d, w_rows >= 1,
- * d <= SSM_LAYERNORM_MAX_D (SSM_ERR_UNSUPPORTED above), rows·d <= 2^40. y may be x itself (x dense), dx may be dy or x itself (dense); other overlaps are refused. Errors
- * as for ssm_scan_fwd and ssm_linattn_fwd.
+ * d <= SSM_LAYERNORM_MAX_D (SSM_ERR_UNSUPPORTED above), rows times the distance of rows <= 2^40,
+ * w_rows below 2^24 (2^22 where d > 4096: a launch takes fewer than 2^32 threads). y may be x itself (x dense), dx may
+ * be dy or x itself (dense); other overlaps are refused. Errors as for ssm_scan_fwd and ssm_linattn_fwd.
  */
 #define SSM_LAYERNORM_MAX_D 16384
 SSM_API ssm_status_t ssm_layernorm_fwd(const void *x, const float *w, const float *bias, void *y, float *mean,

@@ -342,8 +342,7 @@ static ssm_status_t check_norm(int64_t rows, int64_t d, int64_t w_rows, int64_t 
     if (!valid_dtype(dtype)) return SSM_ERR_UNSUPPORTED;
     if (rows < 0 || d < 1 || w_rows < 1 || rows % w_rows != 0) return SSM_ERR_SHAPE;
     if (d > SSM_LAYERNORM_MAX_D) return SSM_ERR_UNSUPPORTED;
-    // one workgroup at least for each weight row
-    if (w_rows > (INT64_C(1) << 24) || w_rows * ceil_div(d, 16) >= (INT64_C(1) << 31)) return SSM_ERR_SHAPE;
+    if (!ssm::launchable(w_rows, ssm::layernorm_threads(d))) return SSM_ERR_SHAPE;
     if (*stride == 0) *stride = d;
     if (*stride < d || !mul_ok(rows, *stride, &n) || n > kMost) return SSM_ERR_SHAPE;
     return SSM_OK;

@@ -271,6 +271,8 @@ struct NormLaunch {
     float *part;             // gradient: partial sums of dw, dbias
     bool vec;                // 16-byte accesses allowed on every row
 };
+// Threads of a workgroup; there is one at least for each weight row.
+inline int64_t layernorm_threads(int64_t d) { return d > 4096 ? 1024 : 256; }
 hipError_t launch_layernorm_fwd(const NormLaunch &p, hipStream_t stream);
 hipError_t launch_layernorm_bwd(const NormLaunch &p, hipStream_t stream);
 int64_t layernorm_part_floats(int64_t rows, int64_t d, int64_t w_rows);

@@ -284,38 +284,41 @@ __global__ __launch_bounds__((Lay<T, LR, K>::THREADS)) void norm_bwd_kernel(Norm
 __global__ __launch_bounds__(1024) void norm_part_sum_kernel(const float *part, float *dw, float *dbias, int64_t d,
                                                              int64_t w_rows, int64_t per) {
     __shared__ float s[2][64][17];
-    const int64_t blocks = (d + 15) / 16, wr = blockIdx.x / blocks;
+    const int64_t blocks = (d + 15) / 16;
     const int col = threadIdx.x & 15, run = threadIdx.x >> 4;
-    const int64_t c = blockIdx.x % blocks * 16 + col;
-    float u = 0.0f, v = 0.0f;
-    if (c < d) {
+    for (int64_t block = blockIdx.x; block < w_rows * blocks; block += gridDim.x) {
+        const int64_t wr = block / blocks, c = block % blocks * 16 + col;
+        float u = 0.0f, v = 0.0f;
+        if (c < d) {
 #pragma unroll 4
-        for (int64_t i = run; i < per; i += 64) {
-            const float *p = part + 2 * (i * w_rows + wr) * d + c;
-            u += p[0];
-            v += p[d];
+            for (int64_t i = run; i < per; i += 64) {
+                const float *p = part + 2 * (i * w_rows + wr) * d + c;
+                u += p[0];
+                v += p[d];
+            }
         }
-    }
-    s[0][run][col] = u;
-    s[1][run][col] = v;
-    for (int h = 32; h > 0; h >>= 1) {
-        __syncthreads();
-        if (run < h) {
-            s[0][run][col] += s[0][run + h][col];
-            s[1][run][col] += s[1][run + h][col];
+        s[0][run][col] = u;
+        s[1][run][col] = v;
+        for (int h = 32; h > 0; h >>= 1) {
+            __syncthreads();
+            if (run < h) {
+                s[0][run][col] += s[0][run + h][col];
+                s[1][run][col] += s[1][run + h][col];
+            }
         }
-    }
-    if (run == 0 && c < d) {
-        if (dw) dw[wr * d + c] = s[0][0][col];
-        if (dbias) dbias[wr * d + c] = s[1][0][col];
+        if (run == 0 && c < d) {
+            if (dw) dw[wr * d + c] = s[0][0][col];
+            if (dbias) dbias[wr * d + c] = s[1][0][col];
+        }
+        __syncthreads();  // every sum of this block is read
     }
 }
 
 __global__ __launch_bounds__(256) void norm_zero_kernel(float *dw, float *dbias, int64_t n) {
-    const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
-    if (i >= n) return;
-    if (dw) dw[i] = 0.0f;
-    if (dbias) dbias[i] = 0.0f;
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += gridDim.x * (int64_t)256) {
+        if (dw) dw[i] = 0.0f;
+        if (dbias) dbias[i] = 0.0f;
+    }
 }
 
 // Workgroups per weight row: enough to give the device `most` workgroups in all, no more than have rows.
@@ -325,6 +328,8 @@ int64_t groups(int64_t rows, int64_t w_rows, int slots, int64_t most) {
     return need < cap ? need : cap;
 }
 constexpr int64_t kFwdGroups = 2048;
+// Workgroups of the launches that walk over columns in steps of the grid, far below HIP's limit of threads.
+unsigned walking(int64_t n) { return (unsigned)(n < 65536 ? n : 65536); }
 // The gradient's workgroups also write a row of partial sums each: 512 of them (8192 rows of 768 in fp32: 21.5 us; 1024
 // took 26), but 1024 where rows are short, of sixteen lanes or few more (524288 rows of 128 in bf16: 88 us; 512 took 92).
 int64_t bwd_groups(int64_t d) { return d <= 256 ? 1024 : 512; }
@@ -370,7 +375,7 @@ template <typename T> hipError_t bwd(const NormLaunch &p, hipStream_t stream) {
         else norm_bwd_kernel<T, LR, K, false><<<grid, Y::THREADS, 0, stream>>>(p);
         hipError_t e = hipGetLastError();
         if (e == hipSuccess && p.part) {
-            norm_part_sum_kernel<<<dim3((unsigned)(p.w_rows * ((p.d + 15) / 16))), 1024, 0, stream>>>(
+            norm_part_sum_kernel<<<dim3(walking(p.w_rows * ((p.d + 15) / 16))), 1024, 0, stream>>>(
                 p.part, p.dw, p.dbias, p.d, p.w_rows, per);
             e = hipGetLastError();
         }
@@ -394,7 +399,7 @@ hipError_t launch_layernorm_fwd(const NormLaunch &p, hipStream_t stream) {
 hipError_t launch_layernorm_bwd(const NormLaunch &p, hipStream_t stream) {
     if (p.rows == 0) {
         const int64_t n = p.w_rows * p.d;
-        ln::norm_zero_kernel<<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(p.dw, p.dbias, n);
+        ln::norm_zero_kernel<<<dim3(ln::walking((n + 255) / 256)), 256, 0, stream>>>(p.dw, p.dbias, n);
         return hipGetLastError();
     }
     return p.bf16 ? ln::bwd<uint16_t>(p, stream) : ln::bwd<float>(p, stream);
