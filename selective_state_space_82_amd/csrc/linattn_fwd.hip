@@ -44,24 +44,30 @@ __device__ __forceinline__ const float *decays_of(const LinAttnLaunch &a, const 
 // of its columns and steps need all of N, so the state's bf16 parts pass through LDS (a sixteenth of what is read
 // there). The decayed scores, 10 lower-triangular 16×16 tiles, are shared through LDS too. The next chunk's rows are
 // fetched into registers, and its decays formed by a wavefront without score tiles, while this chunk is computed.
-// Bound: instruction issue and LDS, not memory. b 8, L 4096, 64 heads, N 128, P 64 in bf16 takes 310 us for 0.70 GB that a
-// copy moves in 134 us; with the loads taken from one chunk it takes 6 % less, without the state's update 15 %, without
-// scores and state products 10 %, without the stores 8 %. Of the bf16 matrix rate it reaches 7 % by the recurrence's
-// operations (222 Tflop/s), about three times that by the products it makes. Three 64-step tiles, the scores in two parts
-// and the state's fragments fill half a compute unit's LDS, so 128 steps per chunk would leave one workgroup on it.
-// SPARTS: bf16 parts in which the state enters the outputs. One in general: half a step of bf16 on each product's size, as
-// their own rounding (o is then up to 1.4 times as far off as by that alone). Two where that costs little: see outputs().
-template <typename T, int NT, bool VEC, int SPARTS>
-__global__ __launch_bounds__(kOutThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && VEC && SPARTS == 1 ? 4 : 2)))
+// Bound: instruction issue and LDS, not memory. b 8, L 4096, 64 heads, N 128, P 64 in bf16 takes 355 us for 0.70 GB that a
+// copy moves in 134 us. Three 64-step tiles, the scores in two parts and the state's first parts fill half a compute unit's
+// LDS, so 128 steps per chunk would leave one workgroup on it.
+// PARTS: bf16 parts of the state, as it enters the outputs, and of the scores. Two leave 2^-17 of each product; the outputs
+// are then as far off as rounding them to bf16 alone. The state in one part takes 316 us here and puts them up to 1.4
+// times as far off; its second part in LDS of its own, with one workgroup on a compute unit, takes 106 us where this takes
+// 68 (64 rows of 64 steps, 32 heads, 128 by 64).
+template <typename T, int NT, bool VEC>
+__global__ __launch_bounds__(kOutThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && VEC ? 4 : 2)))
 void la_out_kernel(LinAttnLaunch a) {
     constexpr int SN = NT + kPad<T>, SP = kC + kPad<T>, SV = kPB + kPad<T>;
-    constexpr int PARTS = sizeof(T) == 2 ? 2 : 1, NF = NT / 32;
+    constexpr int PARTS = sizeof(T) == 2 ? 2 : 1, NF = NT / 32;  // PARTS: of the state and of the scores
     typedef typename std::conditional<sizeof(T) == 2, bf4, f4>::type Half;  // a lane's part of one result tile
     __shared__ __align__(16) T s_q[kC * SN];
     __shared__ __align__(16) T s_k[kC * SN];
     __shared__ __align__(16) T s_v[kC * SV];
     __shared__ __align__(16) T s_p[PARTS][kC * SP];  // decayed scores [t][s], s in the order spread
-    __shared__ __align__(16) Half s_s[SPARTS][4][NF][64][2];  // the state's operand fragments
+    // the state's operand fragments. Their second parts stand in Q's place: Q's readers are done by the barrier before they are
+    // written, and the next Q is stored past a barrier after they are read. That barrier saves the 16 KB without which two
+    // workgroups do not fit on a compute unit.
+    typedef Half StateParts[4][NF][64][2];
+    __shared__ __align__(16) StateParts s_s;
+    StateParts &s_low = *reinterpret_cast<StateParts *>(&s_q[0]);
+    static_assert(PARTS == 1 || sizeof(StateParts) <= sizeof(s_q), "the second parts fit in Q's place");
     __shared__ Decays s_g[2];
 
     const Work wk = work_of<4>(a, work_index(blockIdx.x, gridDim.x), a.n_seg);
@@ -101,13 +107,11 @@ void la_out_kernel(LinAttnLaunch a) {
         for (int i = 0; i < NF; ++i) {
             // four values of N of column col, 16·(tile % 2) + 4·grp into their 32, where the plain order has them
             const int tile = tw * NF + i;
-            f4 left = S[i];
-#pragma unroll
-            for (int e = 0; e < SPARTS; ++e) {
-                const Half part = __builtin_convertvector(left, Half);
-                s_s[e][pw][tile >> 1][16 * (2 * (tile & 1) + (g4 >> 3)) + col][g4 >> 2 & 1] = part;
-                if (e + 1 < SPARTS) left -= __builtin_convertvector(part, f4);
-            }
+            const int at = 16 * (2 * (tile & 1) + (g4 >> 3)) + col, half = g4 >> 2 & 1;
+            const Half part = __builtin_convertvector(S[i], Half);
+            s_s[pw][tile >> 1][at][half] = part;
+            if constexpr (PARTS == 2)
+                s_low[pw][tile >> 1][at][half] = __builtin_convertvector(S[i] - __builtin_convertvector(part, f4), Half);
         }
     };
     put_state();
@@ -118,6 +122,7 @@ void la_out_kernel(LinAttnLaunch a) {
 #pragma unroll
         for (int e = 0; e < PARTS; ++e) s_p[e][t * SP + spread_of(s)] = (T)0;
     }
+    lds_barrier();
 
     const int64_t n_chunks = (a.L + kC - 1) / kC, live = (len + kC - 1) / kC;
     const int64_t ch0 = wk.seg * a.seg_chunks, ch1 = ch0 + a.seg_chunks < n_chunks ? ch0 + a.seg_chunks : n_chunks;
@@ -159,12 +164,24 @@ void la_out_kernel(LinAttnLaunch a) {
         const Decays &dec = s_g[(ch - ch0) & 1];
         const int all = outs.next(), some = ch + 1 == live ? (int)(len - ch * kC) : kC;
         if (!VEC) fetch();
-        rq.store(s_q);
+        Frag<T> sf[PARTS][NF];
+        if constexpr (PARTS == 2)
+#pragma unroll
+            for (int n = 0; n < NF; ++n) sf[1][n] = *reinterpret_cast<const Frag<T> *>(&s_low[pw][n][l][0]);
         rk.store(s_k);
         rv.store(s_v);
+        if constexpr (PARTS == 2) lds_barrier();  // the second parts are read
+        rq.store(s_q);
         float g_now = g_next;
         asm volatile("" : "+v"(g_now));  // it has arrived with the rest: no wait for it behind the next loads
         lds_barrier();
+        // the state's second parts go first, before the next chunk's rows take registers
+        f4 acc[2] = {f4{0, 0, 0, 0}, f4{0, 0, 0, 0}};
+        if constexpr (PARTS == 2)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int n = 0; n < NF; ++n) mma(acc[b], sf[1][n], row_frag(s_q, SN, 16 * (2 * tw + b), 32 * n));
         store_res();
         out = co.next(all);
         g_next = fetch_g();
@@ -172,24 +189,17 @@ void la_out_kernel(LinAttnLaunch a) {
 
         // Through the state, and the decayed scores: a query fragment serves both. Score tile (tb, sb) holds
         // D[s][t] = k_s·q_t; a wavefront takes those of its two blocks of t and of s block pw, in two bf16 parts.
-        f4 acc[2];
         __builtin_amdgcn_s_setprio(1);  // the workgroup that computes goes before the one that loads and stores: 3 % less time
-        Frag<T> sf[SPARTS][NF];
 #pragma unroll
-        for (int e = 0; e < SPARTS; ++e)
-#pragma unroll
-            for (int n = 0; n < NF; ++n) sf[e][n] = *reinterpret_cast<const Frag<T> *>(&s_s[e][pw][n][l][0]);
+        for (int n = 0; n < NF; ++n) sf[0][n] = *reinterpret_cast<const Frag<T> *>(&s_s[pw][n][l][0]);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const int tb = 2 * tw + b;
             Frag<T> qf[NF];
 #pragma unroll
             for (int n = 0; n < NF; ++n) qf[n] = row_frag(s_q, SN, 16 * tb, 32 * n);
-            acc[b] = f4{0, 0, 0, 0};
 #pragma unroll
-            for (int e = 0; e < SPARTS; ++e)
-#pragma unroll
-                for (int n = 0; n < NF; ++n) mma(acc[b], sf[e][n], qf[n]);
+            for (int n = 0; n < NF; ++n) mma(acc[b], sf[0][n], qf[n]);
             acc[b] *= dec.in[16 * tb + col];
             if (tb >= pw) {
                 f4 sc = {0, 0, 0, 0};
@@ -224,7 +234,7 @@ void la_out_kernel(LinAttnLaunch a) {
         if (w == 3) s_g[(ch + 1 - ch0) & 1].set<true>(log_decay(g_now), a.scale);
         lds_barrier();
 
-        // From here to the next barrier s_s is written by the wavefronts that are done: nothing below reads it.
+        // From here to the next barrier the state's parts are written by the wavefronts that are done: nothing below reads them, or Q.
         const f4 through[2] = {acc[0], acc[1]};
         Frag<T> vf[2];
 #pragma unroll
@@ -275,7 +285,7 @@ void la_out_kernel(LinAttnLaunch a) {
             else update(Split<T, 2>(wide(vf[sp]) * join(u, v)));
         }
         __builtin_amdgcn_s_setprio(0);
-        put_state();  // its readers, above the last barrier, are past it
+        put_state();  // its readers, and Q's, are past the last barrier
         lds_barrier();
     }
     store_res();
@@ -532,16 +542,10 @@ hipError_t nonfinite(const LinAttnLaunch &p, hipStream_t stream) {
 template <typename T>
 hipError_t outputs(const LinAttnLaunch &p, hipStream_t stream) {
     const dim3 grid((unsigned)(p.b * p.H * p.n_seg) * (unsigned)((p.P + kPB - 1) / kPB));
-    constexpr int TWO = sizeof(T) == 2 ? 2 : 1;
-    // Few workgroups: two parts cost 2 % (1 row of 512 steps, 16 heads, 64 by 64: 18.3 us against 18.1), and so few results
-    // can be further off than 1.4 times by chance. Many: their LDS leaves one workgroup of two on a compute unit (64 rows
-    // of 64 steps, 32 heads, 128 by 64: 106 us against 82).
-    const bool two = grid.x <= kFewBlocks && (p.initial_state || p.L > kC);
     return by_width(p, [&](auto nt, auto, auto vec) {
         constexpr int NT = decltype(nt)::value;
         constexpr bool VEC = decltype(vec)::value;
-        if (two) la_out_kernel<T, NT, VEC, TWO><<<grid, kOutThreads, 0, stream>>>(p);
-        else la_out_kernel<T, NT, VEC, 1><<<grid, kOutThreads, 0, stream>>>(p);
+        la_out_kernel<T, NT, VEC><<<grid, kOutThreads, 0, stream>>>(p);
         return hipGetLastError();
     });
 }

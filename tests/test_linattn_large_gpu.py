@@ -1,0 +1,79 @@
+"""Linear attention in calls of many workgroups, walks of many chunks and segments of several: the launches that long prompts
+and training batches make, with their plan asserted, element by element against the recurrence in 64 bits.
+
+The bound is linattn_ref.py's without its 2^-8 for an operand in one bf16 part: every fp32 operand of a product is taken in
+two bf16 parts or more, each the rounded remainder of those before, so it is off by 2^-16 of itself at most, and at most
+two such operands lie on a path from an input to a result (the decayed value in the state's update, then the state)."""
+import pytest
+import torch
+
+import linattn_ref as R
+from selective_state_space_82_amd import api
+from test_linattn_gpu import BF16, F32, SHAPES, gpu, make, reference
+from test_linattn_nonfinite_gpu import segments
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm GPU visible")
+    api.lib()
+
+
+def tight(ref, mag, x, ratio=1):
+    L, N, P = x["v"].shape[1], x["q"].shape[3], x["v"].shape[3]
+    return R.bound(ref, mag, x["v"].dtype, L, N, P, ratio=ratio) - (2.0 ** -8 * mag if x["v"].dtype == BF16 else 0.0)
+
+
+def check_forward(x, what=""):
+    L, N, P = x["v"].shape[1], x["q"].shape[3], x["v"].shape[3]
+    t = gpu(x)
+    o, S = api.ssm_linattn_fwd(t["q"], t["k"], t["v"], t["g"], scale=t["scale"], initial_state=t["first"],
+                               lengths=t["lengths"])
+    (ro, rS), (mo, mS) = reference(x), reference(x, True)
+    R.assert_within(o, ro, tight(ro, mo, x), what + " o")
+    R.assert_within(S, rS, R.bound(rS, mS, x["v"].dtype, L, N, P, F32), what + " state")
+
+
+def workgroups(x, columns=64):
+    b, _, H, P = x["v"].shape
+    return b * H * -(-P // columns)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "b%d_L%d_H%d_G%d_N%d_P%d" % s)
+def test_forward_of_few_workgroups(shape):
+    check_forward(make(*shape, dtype=BF16, first=True, seed=sum(shape) + 2))
+
+
+@pytest.mark.parametrize("lengths", [None, "ragged"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("b,L,H,G,N,P", [(2, 330, 256, 128, 16, 40), (3, 400, 100, 50, 64, 64), (1, 330, 136, 17, 128, 128)])
+def test_forward_of_many_workgroups(b, L, H, G, N, P, dtype, lengths):
+    """More workgroups than compute units, each walking five chunks and more."""
+    lengths = None if lengths is None else [L - 130, L, 63][:b]
+    x = make(b, L, H, G, N, P, dtype=dtype, rate=0.1, first=True, lengths=lengths, seed=N)
+    # fp32 tiles of N > 32 leave one workgroup on a compute unit: two rounds of them go in segments of two chunks
+    assert workgroups(x) > 256 and segments(x) <= (4 if dtype == F32 and N > 32 else 1)
+    check_forward(x)
+
+
+@pytest.mark.parametrize("rate", [0.01, 0.5, 8.0], ids=["weak", "between", "strong"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("b,L,H,G,N,P", [(3, 1003, 12, 4, 40, 72), (1, 1600, 100, 20, 16, 64)])
+def test_forward_in_segments_of_several_chunks(b, L, H, G, N, P, dtype, rate):
+    """Segments of three chunks and more, whose own states' walks go on past the first chunk (weak decays) or end by the decay
+    (strong: 4 a step, 256 a chunk)."""
+    x = make(b, L, H, G, N, P, dtype=dtype, rate=rate, first=True, seed=P)
+    n = segments(x)
+    assert n > 1 and -(-L // 64) // n >= 2, n
+    check_forward(x)
+    check_forward(make(b, L, H, G, N, P, dtype=dtype, decay="head", rate=rate, seed=P + 1,
+                       lengths=[L, L - 500, 130][:b]), "lengths")
+
+
+def test_forward_in_segments_of_wide_states():
+    x = make(1, 1003, 72, 9, 128, 64, dtype=BF16, rate=0.05, seed=9)
+    assert segments(x) == 6
+    check_forward(x)
