@@ -304,7 +304,7 @@ SSM_API ssm_status_t ssm_ssd_fwd(const void *x, const void *delta, const float *
  *                     may refuse. A call writes what it reads there, and keeps nothing in it; calls that
  *                     may overlap (other streams, captured graphs replayed at once) need one each.
  * Products are exact bf16 products summed in fp32 (bf16; fp32 operands, that is states and decayed scores, enter
- * as one or two bf16 parts where the result is bf16, as three where it is fp32) or fp32 products (f32). All sums,
+ * as two bf16 parts, 2^-16 of the operand, where the result is bf16, as three where it is fp32) or fp32 products (f32). All sums,
  * decays and states are fp32, the running sum of g in a chunk fp64. Results are deterministic. A NaN or Inf at one
  * step reaches outputs and gradients as the formulas say, except that an Inf may come out as NaN, and that gradients
  * (dq, dk, dv, dg) may become NaN at every step of the 64-step chunk it is in.

@@ -42,16 +42,16 @@ __device__ __forceinline__ float sum_cols(float v) {
 // The four wavefronts share the lower-triangular tiles of both score matrices through LDS; wavefront w takes the value
 // columns 16w .. of dv, and 16-column jobs of dq and dk, whose parts through state and adjoint come first: V is free then
 // and A1 takes its place, which leaves room for three workgroups on a compute unit. Bound: memory and its latency. b 4,
-// L 2048, 24 heads, N = P = 64 in bf16 takes 62 us for 0.28 GB (4.4 TB/s); eight wavefronts to a workgroup took 13 us more.
-// PARTS: bf16 parts of the scores A1 and A2. One in general: half a step of bf16 on each product's size, as the results'
-// own rounding (dq, dk and dv are then 1.4 times as far off as by that alone). Two where that is not all: where a group's
-// heads are summed in fp32, whose shares cancel while their roundings do not (twice as far off), and in a single chunk,
-// where a result may hang on one score. Calls of few workgroups take two for the adjoint in dv too, as few results can be
-// further off than 1.4 times by chance: 1 row of 2048 steps, 8 heads, 128 by 128 takes 54 us against 52. With many it
-// costs more: the 62 us above become 74, a group's adjoint in two parts 9 % of all (4 rows of 2048, 24 heads on 4, 64 by 64).
-template <typename T, int NT, bool VEC, int PARTS>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && NT < 128 ? 4 - PARTS : 1)))
+// L 2048, 24 heads, N = P = 64 in bf16 takes 64 us for 0.28 GB (4.4 TB/s); eight wavefronts to a workgroup took 13 us more.
+// PARTS: bf16 parts of the scores A1 and A2 (E, as it enters dv, takes as many; S and E in dq and dk take three, because dg's
+// terms come from them). Two leave 2^-16 of each product, and dq, dk and dv as far off as rounding them to bf16 alone; one
+// leaves them 1.4 times as far off, twice where a group's heads are summed. The second parts wait in registers and take
+// A2's place one after the other, four barriers more: the call above takes 131 us, with one part 128, with all four tiles
+// in LDS, which leave room for two workgroups, 141.
+template <typename T, int NT, bool VEC>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && NT < 128 ? 3 : 1)))
 void la_grad_kernel(LinAttnLaunch a) {
+    constexpr int PARTS = sizeof(T) == 2 ? 2 : 1;
     constexpr int SN = NT + kPad<T>, SP = kC + kPad<T>, SV = kPB + kPad<T>;
     constexpr int TILES = NT / 16, JOBS = 2 * TILES / 4;
     __shared__ __align__(16) T s_q[kC * SN];
@@ -59,10 +59,9 @@ void la_grad_kernel(LinAttnLaunch a) {
     static_assert(SP == SV, "A1 takes V's place");
     __shared__ __align__(16) T s_v[kC * SV];
     __shared__ __align__(16) T s_d[kC * SV];
-    // [t][s]; the terms of dg are taken before these are rounded
-    __shared__ __align__(16) T s_a1_low[(PARTS - 1) * kC * SP + 1];
-    T *const s_a1[2] = {s_v, s_a1_low};
-    __shared__ __align__(16) T s_a2[PARTS][kC * SP];
+    // A2 [t][s], then the second parts of A2 and of A1; the terms of dg are taken before any is rounded
+    __shared__ __align__(16) T s_a2[kC * SP];
+    T *const s_a1 = s_v;
     __shared__ Decays s_g;
     __shared__ __align__(16) float s_col[4][kC];
     __shared__ float s_row[4][kC], s_x[TILES][kC], s_y[TILES][kC], s_z[4];
@@ -218,8 +217,7 @@ void la_grad_kernel(LinAttnLaunch a) {
     z = sum_groups(sum_cols(z));
     if (l == 0) s_z[w] = z;
 
-    // E once more, eight values along N at the wavefront's value columns (for dv, one bf16 part, or two in a call of few
-    // workgroups), on their way while the scores are weighted
+    // E once more, eight values along N at the wavefront's value columns (for dv), on their way while the scores are weighted
     f8 e[NT / 32];
     auto fetch_adjoint = [&](int pb) {
         const float *src = Ep + (int64_t)(pb * kPB + 16 * w + col) * NT + 2 * g4;
@@ -228,15 +226,14 @@ void la_grad_kernel(LinAttnLaunch a) {
             e[n] = join(*reinterpret_cast<const f4 *>(src + 32 * n), *reinterpret_cast<const f4 *>(src + 32 * n + 4));
     };
     fetch_adjoint(0);
-    const bool few = gridDim.x <= kFewBlocks;
     lds_barrier();  // V's tile is free: A1 takes its place
 
     // the tiles right of the diagonal that a 32-step contraction touches
     for (int i = tid; i < 2 * 16 * 16; i += kThreads) {
         const int t = 32 * (i >> 8) + ((i >> 4) & 15), s = 32 * (i >> 8) + 16 + (i & 15);
-#pragma unroll
-        for (int e = 0; e < PARTS; ++e) s_a1[e][t * SP + s] = s_a2[e][t * SP + s] = (T)0;
+        s_a1[t * SP + s] = s_a2[t * SP + s] = (T)0;
     }
+    bf4 a1_low[3], a2_low[3];
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
         const int i = w + 4 * j;
@@ -265,21 +262,31 @@ void la_grad_kernel(LinAttnLaunch a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) wv[r] = sum_cols(wv[r]);
             if (col == 0) *reinterpret_cast<f4 *>(&s_col[tb][s]) = wv;
-            if constexpr (sizeof(T) == 2) {
-#pragma unroll
-                for (int e = 0; e < PARTS; ++e) {
-                    const bf4 u = __builtin_convertvector(a1, bf4), v = __builtin_convertvector(a2, bf4);
-                    *reinterpret_cast<bf4 *>(&s_a1[e][t * SP + s]) = u;
-                    *reinterpret_cast<bf4 *>(&s_a2[e][t * SP + s]) = v;
-                    a1 -= __builtin_convertvector(u, f4);
-                    a2 -= __builtin_convertvector(v, f4);
-                }
+            if constexpr (PARTS == 2) {
+                const bf4 u = __builtin_convertvector(a1, bf4), v = __builtin_convertvector(a2, bf4);
+                *reinterpret_cast<bf4 *>(&s_a1[t * SP + s]) = u;
+                *reinterpret_cast<bf4 *>(&s_a2[t * SP + s]) = v;
+                a1_low[j] = __builtin_convertvector(a1 - __builtin_convertvector(u, f4), bf4);
+                a2_low[j] = __builtin_convertvector(a2 - __builtin_convertvector(v, f4), bf4);
             } else {
-                *reinterpret_cast<f4 *>(&s_a1[0][t * SP + s]) = a1;
-                *reinterpret_cast<f4 *>(&s_a2[0][t * SP + s]) = a2;
+                *reinterpret_cast<f4 *>(&s_a1[t * SP + s]) = a1;
+                *reinterpret_cast<f4 *>(&s_a2[t * SP + s]) = a2;
             }
         }
     }
+    // the scores' second parts, in A2's place when what is there has been read
+    auto put_low = [&](const bf4 (&low)[3]) {
+        lds_barrier();
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            const int i = w + 4 * j;
+            if (i < 10) {
+                const int tb = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3, sb = i - tb * (tb + 1) / 2;
+                *reinterpret_cast<bf4 *>(&s_a2[(16 * tb + col) * SP + 16 * sb + g4]) = low[j];
+            }
+        }
+        lds_barrier();
+    };
     lds_barrier();
 
     if (w == 0) {  // dg
@@ -297,33 +304,48 @@ void la_grad_kernel(LinAttnLaunch a) {
         const double v = (lane_value(upto, 63) - upto + after) + (yto - ys) + zs;
         if (l < rows) dgp[(int64_t)l * a.H] = t0 + l < len ? (float)v : 0.0f;
     }
+    // dq and dk through the scores
+    auto add_scores = [&]() {
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j) {
+            const int job = w + 4 * j;
+            const bool is_q = job < TILES;
+            const int n0 = 16 * (is_q ? job : job - TILES);
+            const T *tile = is_q ? s_k : s_q;
+            const Frag<T> f0 = col_frag(tile, SN, 0, n0), f1 = col_frag(tile, SN, 32, n0);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (is_q) {
+                    mma(acc[j][b], f0, row_frag(s_a2, SP, 16 * b, 0));
+                    if (b >= 2) mma(acc[j][b], f1, row_frag(s_a2, SP, 16 * b, 32));
+                } else {
+                    if (b < 2) mma(acc[j][b], f0, col_frag(s_a2, SP, 0, 16 * b));
+                    mma(acc[j][b], f1, col_frag(s_a2, SP, 32, 16 * b));
+                }
+            }
+        }
+    };
+    add_scores();
+    if constexpr (PARTS == 2) {
+        put_low(a2_low);
+        add_scores();
+    }
 #pragma unroll
     for (int j = 0; j < JOBS; ++j) {
         const int job = w + 4 * j;
         const bool is_q = job < TILES;
         const int n0 = 16 * (is_q ? job : job - TILES);
-        const T *tile = is_q ? s_k : s_q;
-        const Frag<T> f0 = col_frag(tile, SN, 0, n0), f1 = col_frag(tile, SN, 32, n0);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const int t = 16 * b + col;
             f4 &v = acc[j][b];
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p) {
-                if (is_q) {
-                    mma(v, f0, row_frag(s_a2[p], SP, 16 * b, 0));
-                    if (b >= 2) mma(v, f1, row_frag(s_a2[p], SP, 16 * b, 32));
-                } else {
-                    if (b < 2) mma(v, f0, col_frag(s_a2[p], SP, 0, 16 * b));
-                    mma(v, f1, col_frag(s_a2[p], SP, 32, 16 * b));
-                }
-            }
             if (some < kC && t >= some) v = f4{0, 0, 0, 0};
             const Buffer &buf = is_q ? dq_buf : dk_buf;
             if (part) store4<float, VEC>(buf, (uint32_t)n_t, t, n0 + g4, a.N, v);
             else store4<T, VEC>(buf, (uint32_t)n_t, t, n0 + g4, a.N, v);
         }
     }
+    if constexpr (PARTS == 2) put_low(a1_low);
     for (int pb = 0; pb < npb; ++pb) {  // dv: value columns 16w .. of each block
         if (npb > 1) {
             Stage<T, kPB, kThreads, VEC> d((uint32_t)a.do_t, pb * kPB, a.P);
@@ -340,12 +362,9 @@ void la_grad_kernel(LinAttnLaunch a) {
         for (int b = 0; b < 4; ++b) dv[b] = f4{0, 0, 0, 0};
 #pragma unroll
         for (int n = 0; n < NT / 32; ++n) {
-            auto through = [&](const auto &es) {
+            const Split<T, 2> es(e[n]);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) mma(dv[b], es, row_frag(s_k, SN, 16 * b, 32 * n));
-            };
-            if (PARTS == 2 && few) through(Split<T, 2>(e[n]));
-            else through(Split<T, 1>(e[n]));
+            for (int b = 0; b < 4; ++b) mma(dv[b], es, row_frag(s_k, SN, 16 * b, 32 * n));
         }
         const Frag<T> d0 = col_frag(s_d, SV, 0, 16 * w), d1 = col_frag(s_d, SV, 32, 16 * w);
 #pragma unroll
@@ -354,8 +373,9 @@ void la_grad_kernel(LinAttnLaunch a) {
             dv[b] *= s_g.out[s];
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
-                if (b < 2) mma(dv[b], d0, col_frag(s_a1[p], SP, 0, 16 * b));
-                mma(dv[b], d1, col_frag(s_a1[p], SP, 32, 16 * b));
+                const T *a1 = p ? s_a2 : s_a1;
+                if (b < 2) mma(dv[b], d0, col_frag(a1, SP, 0, 16 * b));
+                mma(dv[b], d1, col_frag(a1, SP, 32, 16 * b));
             }
             if (some < kC && s >= some) dv[b] = f4{0, 0, 0, 0};
             store4<T, VEC>(dv_buf, (uint32_t)dv_t, s, pb * kPB + 16 * w + g4, a.P, dv[b]);
@@ -396,18 +416,14 @@ template <typename T>
 hipError_t grads(const LinAttnLaunch &p, hipStream_t stream) {
     const int nt = linattn_nt(p.N);
     const dim3 grid((unsigned)(p.b * p.H * p.n_seg));
-    auto launch = [&](auto vec, auto parts) {
+    auto launch = [&](auto vec) {
         constexpr bool VEC = decltype(vec)::value;
-        constexpr int PARTS = decltype(parts)::value;
-        if (nt == 32) la_grad_kernel<T, 32, VEC, PARTS><<<grid, kThreads, 0, stream>>>(p);
-        else if (nt == 64) la_grad_kernel<T, 64, VEC, PARTS><<<grid, kThreads, 0, stream>>>(p);
-        else la_grad_kernel<T, 128, VEC, PARTS><<<grid, kThreads, 0, stream>>>(p);
+        if (nt == 32) la_grad_kernel<T, 32, VEC><<<grid, kThreads, 0, stream>>>(p);
+        else if (nt == 64) la_grad_kernel<T, 64, VEC><<<grid, kThreads, 0, stream>>>(p);
+        else la_grad_kernel<T, 128, VEC><<<grid, kThreads, 0, stream>>>(p);
     };
-    const std::integral_constant<int, 1> one;
-    const std::integral_constant<int, sizeof(T) == 2 ? 2 : 1> two;
-    const bool exact = p.G < p.H || p.L <= kC || grid.x <= kFewBlocks;
-    if (p.vec) exact ? launch(std::true_type{}, two) : launch(std::true_type{}, one);
-    else exact ? launch(std::false_type{}, two) : launch(std::false_type{}, one);
+    if (p.vec) launch(std::true_type{});
+    else launch(std::false_type{});
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.G < p.H) {
         const int64_t n = p.b * p.L * p.G * p.N, blocks = (n + kThreads - 1) / kThreads;

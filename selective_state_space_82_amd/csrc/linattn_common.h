@@ -22,9 +22,6 @@ namespace la {
 constexpr int kC = 64;        // steps per chunk
 constexpr int kPB = 64;       // value columns per workgroup; P is padded to it in scratch
 constexpr int kThreads = kLinAttnThreads;  // four wavefronts
-// Up to this many workgroups each has a compute unit to itself: a gradient of so few takes a second bf16 part of its scores
-// for little.
-constexpr unsigned kFewBlocks = 256;
 // Log-decays below this count as this: e^-1e4 is 0 in fp32, and so is every product with it, while running sums
 // stay finite (−inf would turn differences of sums into NaN).
 constexpr float kMinG = -1e4f;

@@ -9,7 +9,7 @@ import torch
 
 import linattn_ref as R
 from selective_state_space_82_amd import api
-from test_linattn_gpu import BF16, F32, SHAPES, gpu, make, reference
+from test_linattn_gpu import BF16, F32, SHAPES, gpu, grad_bounds, make, reference, wide
 from test_linattn_nonfinite_gpu import segments
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +77,34 @@ def test_forward_in_segments_of_wide_states():
     x = make(1, 1003, 72, 9, 128, 64, dtype=BF16, rate=0.05, seed=9)
     assert segments(x) == 6
     check_forward(x)
+
+
+def check_gradient(x, what=""):
+    t, w, u = gpu(x), wide(x), wide(x, True)
+    names = ("dq", "dk", "dv", "dg", "d_initial_state")
+    got = api.ssm_linattn_bwd(t["q"], t["k"], t["v"], t["g"], do=t["do"], scale=t["scale"], initial_state=t["first"],
+                              d_final_state=t["d_final"], lengths=t["lengths"])
+    ref = R.grads(w["q"], w["k"], w["v"], w["g"], w["scale"], w["do"], w["first"], w["d_final"], w["lengths"])
+    mag = R.grads(u["q"], u["k"], u["v"], w["g"], u["scale"], u["do"], u["first"], u["d_final"], u["lengths"])
+    tol = grad_bounds(x, ref)
+    for n in ("dq", "dk", "dv"):
+        tol[n] = tight(ref[n], mag[n], x, x["v"].shape[2] // x["q"].shape[2])
+    for n in names:
+        R.assert_within(got[n], ref[n], tol[n], f"{what} {n}")
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "b%d_L%d_H%d_G%d_N%d_P%d" % s)
+def test_gradient_of_few_workgroups(shape):
+    check_gradient(make(*shape, dtype=BF16, first=True, seed=sum(shape) + 2))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("b,L,H,G,N,P", [(2, 330, 48, 48, 64, 64), (4, 200, 24, 24, 20, 40), (1, 300, 56, 56, 100, 70),
+                                         (1, 300, 56, 8, 128, 64)])
+def test_gradient_of_many_workgroups(b, L, H, G, N, P, dtype):
+    """More workgroups than compute units, with and without states, heads of their own and in groups."""
+    x = make(b, L, H, G, N, P, dtype=dtype, rate=0.1, first=True, seed=N)
+    assert b * H * -(-L // 64) > 256
+    check_gradient(x, "states")
+    check_gradient(make(b, L, H, G, N, P, dtype=dtype, decay="head", rate=0.1, seed=N + 1,
+                        lengths=[L - 70, L, 64, 1][:b]), "lengths")

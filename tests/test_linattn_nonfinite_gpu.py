@@ -22,11 +22,11 @@ def _need_gpu():
     api.lib()
 
 
-def segments(x, gradient=False):
-    """Segments that a call's plan cuts the steps into: its workspace holds one state of each."""
+def segments(x):
+    """Segments that a forward call's plan cuts the steps into: its workspace holds one state of each."""
     b, L, G, N = x["q"].shape
     H, P = x["v"].shape[2:]
-    n = api.ssm_linattn_workspace(b, L, H, G, N, P, x["v"].dtype, gradient=gradient)
+    n = api.ssm_linattn_workspace(b, L, H, G, N, P, x["v"].dtype)
     state = -(-P // 64) * 64 * (32 if N <= 32 else 64 if N <= 64 else 128)
     return n // (b * H * state * 4) or 1
 
