@@ -10,9 +10,9 @@
 //     dv_s = Σ_t A1_ts do_t + e^{c_end − c_s} E k_s,
 //     dg_t = Σ_{u>=t} (Σ_{s<u} W_us − Σ_{s>u} W_su + X_u) + Σ_{s<t} Y_s + e^{c_end}<S, E>
 // with W_us = A1_us·(do_u·v_s), X_u = q_u·(scale·e^{c_u} Sᵀdo_u), Y_s = v_s·(e^{c_end − c_s} E k_s): the paths from a
-// step before t to one at or after it, by whether either end lies outside the chunk. The W terms come from the same
-// fp32 products in the sum over rows and the one over columns, so the pairs that do not span t cancel in them, and
-// no sum runs past the chunk.
+// step before t to one at or after it, by whether either end lies outside the chunk. The pairs that do not span t cancel
+// between the sums over rows and over columns: both are of the same fp32 terms and taken in fp64, so that 2^-53 of them is
+// left, and no sum runs past the chunk.
 #include "linattn_common.h"
 
 namespace ssm {
@@ -31,6 +31,31 @@ template <int N> __device__ __forceinline__ float row_rotate(float v) {
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x120 + N, 0xf, 0xf, false));
 }
 __device__ __forceinline__ float sum_cols(float v) {
+    v += row_rotate<8>(v);
+    v += row_rotate<4>(v);
+    v += row_rotate<2>(v);
+    return v + row_rotate<1>(v);
+}
+
+// The same for fp64 values, word by word.
+__device__ __forceinline__ double of_words(uint32_t lo, uint32_t hi) {
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double sum_groups(double v) {
+    uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const auto a = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+    u = __builtin_bit_cast(uint64_t, of_words(a[0], b[0]) + of_words(a[1], b[1]));
+    const auto c = __builtin_amdgcn_permlane32_swap((uint32_t)u, (uint32_t)u, false, false);
+    const auto d = __builtin_amdgcn_permlane32_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+    return of_words(c[0], d[0]) + of_words(c[1], d[1]);
+}
+template <int N> __device__ __forceinline__ double row_rotate(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return of_words(__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, 0x120 + N, 0xf, 0xf, false),
+                    __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), 0x120 + N, 0xf, 0xf, false));
+}
+__device__ __forceinline__ double sum_cols(double v) {
     v += row_rotate<8>(v);
     v += row_rotate<4>(v);
     v += row_rotate<2>(v);
@@ -63,8 +88,8 @@ void la_grad_kernel(LinAttnLaunch a) {
     __shared__ __align__(16) T s_a2[kC * SP];
     T *const s_a1 = s_v;
     __shared__ Decays s_g;
-    __shared__ __align__(16) float s_col[4][kC];
-    __shared__ float s_row[4][kC], s_x[TILES][kC], s_y[TILES][kC], s_z[4];
+    __shared__ double s_row[4][kC], s_col[4][kC];
+    __shared__ float s_x[TILES][kC], s_y[TILES][kC], s_z[4];
 
     int64_t id = work_index(blockIdx.x, gridDim.x);
     const int h = (int)(id % a.H);
@@ -257,11 +282,14 @@ void la_grad_kernel(LinAttnLaunch a) {
                     a2[r] = s + r <= t ? a2[r] : 0.0f;
                     wv[r] = s + r < t ? wv[r] : 0.0f;
                 }
-            const float row = sum_groups((wv[0] + wv[1]) + (wv[2] + wv[3]));
+            // in fp64: most of a row's sum goes out against the columns' (pairs of steps that do not span t)
+            const double row = sum_groups(((double)wv[0] + wv[1]) + ((double)wv[2] + wv[3]));
             if (l < 16) s_row[sb][t] = row;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) wv[r] = sum_cols(wv[r]);
-            if (col == 0) *reinterpret_cast<f4 *>(&s_col[tb][s]) = wv;
+            for (int r = 0; r < 4; ++r) {
+                const double column = sum_cols((double)wv[r]);
+                if (col == 0) s_col[tb][s + r] = column;
+            }
             if constexpr (PARTS == 2) {
                 const bf4 u = __builtin_convertvector(a1, bf4), v = __builtin_convertvector(a2, bf4);
                 *reinterpret_cast<bf4 *>(&s_a1[t * SP + s]) = u;

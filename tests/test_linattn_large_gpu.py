@@ -108,3 +108,27 @@ def test_gradient_of_many_workgroups(b, L, H, G, N, P, dtype):
     check_gradient(x, "states")
     check_gradient(make(b, L, H, G, N, P, dtype=dtype, decay="head", rate=0.1, seed=N + 1,
                         lengths=[L - 70, L, 64, 1][:b]), "lengths")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("b,L,H,G,N,P", [(1, 200, 4, 4, 64, 64), (2, 150, 4, 2, 20, 72), (1, 130, 2, 1, 128, 100)])
+def test_decay_gradient_at_a_restart(b, L, H, G, N, P, dtype):
+    """dg_t = e^{g_t} <S_{t-1}, E_t> is 0 where the decay is, and small where it is: what the chunk's other pairs of steps add
+    to it goes out in fp64. Each of the sums has at most 2·64 + 16 terms, of which fp64 leaves 144·2^-53 < 2^-45."""
+    x = make(b, L, H, G, N, P, dtype=dtype, rate=0.1, first=True, seed=N + P)
+    at = [0, 1, 31, 63, 64, 70, 100, 127, L - 1]
+    x["g"][:, at] = -float("inf")
+    x["g"][:, 40] = -25.0
+    t = gpu(x)
+    got = api.ssm_linattn_bwd(t["q"], t["k"], t["v"], t["g"], do=t["do"], scale=t["scale"], initial_state=t["first"],
+                              d_final_state=t["d_final"])["dg"].cpu().double()
+    x["g"] = x["g"].clamp(min=-1e4)
+    w, u = wide(x), wide(x, True)
+    ref = R.grads(w["q"], w["k"], w["v"], w["g"], w["scale"], w["do"], w["first"], w["d_final"])["dg"]
+    mag = R.grads(u["q"], u["k"], u["v"], w["g"], u["scale"], u["do"], u["first"], u["d_final"])["dg"]
+    # grad_bounds' for dg is n·2^-24 of the chunk's magnitudes and of dg's own
+    n = R.paths(L, N, P) + 2 * 64
+    chunk = (grad_bounds(x, {k: torch.zeros(()) for k in ("dq", "dk", "dv", "d_initial_state")} | {"dg": ref})["dg"] -
+             n * R.U * mag - R.U * ref.abs()) / (n * R.U)
+    R.assert_within(got, ref, n * R.U * mag + R.U * ref.abs() + 2.0 ** -45 * chunk, "dg")
+    assert bool((ref[:, at] == 0).all())
