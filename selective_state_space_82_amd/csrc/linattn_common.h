@@ -131,8 +131,13 @@ template <int PARTS> __device__ __forceinline__ void mma(f4 &acc, const bf8 &a, 
 __device__ __forceinline__ void mma(f4 &acc, const Whole &a, const f8 &b) { mma(acc, a.v, b); }
 __device__ __forceinline__ void mma(f4 &acc, const f8 &a, const Whole &b) { mma(acc, a, b.v); }
 
-// e^v for a difference of running sums.
-__device__ __forceinline__ float exp_of(float v) { return exp2_fast(kLog2e * v); }
+// e^v of a running sum or a difference of two: 2^(hi + lo) = 2^hi·(1 + lo·ln 2), so that neither v's nor its product's
+// rounding to fp32 is left, which at v = -60 would be 4e-6 of the result. (A factor near 1 keeps 0 and Inf what they are.)
+__device__ __forceinline__ float exp_of(double v) {
+    const double e = v * 1.4426950408889634074;
+    const float hi = (float)e, lo = (float)(e - (double)hi);
+    return exp2_fast(hi) * (1.0f + 0.69314718055994530942f * lo);
+}
 
 // Inclusive running sum over the 64 lanes of a wavefront, fp64: data-parallel moves inside each row of 16 lanes (lanes
 // shifted in from outside add 0), then the totals of the rows before.
@@ -183,9 +188,9 @@ struct Decays {
         const int l = threadIdx.x & 63;
         const double sum = wave_running_sum(g), total = lane_value(sum, 63);
         c.set(l, sum);
-        in[l] = factor * exp_of((float)sum);
-        out[SPREAD ? spread_of(l) : l] = exp_of((float)(total - sum));
-        if (l == 63) end = exp_of((float)total);
+        in[l] = factor * exp_of(sum);
+        out[SPREAD ? spread_of(l) : l] = exp_of(total - sum);
+        if (l == 63) end = exp_of(total);
     }
 };
 

@@ -386,7 +386,7 @@ __global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int
         rv.store(s_v);
         const double sum = wave_running_sum(log_decay(g_next)), total = lane_value(sum, 63);  // before the next loads
         // the weight of the lane's step, from all chunks walked and from this one
-        const float wt = (rev ? a.scale : 1.0f) * exp_of((float)(passed + (rev ? sum : total - sum)));
+        const float wt = (rev ? a.scale : 1.0f) * exp_of(passed + (rev ? sum : total - sum));
         if (w == 0) s_g.out[spread_of(l)] = wt;
         passed += total;
         lds_barrier();
@@ -446,7 +446,7 @@ __global__ __launch_bounds__(kThreads) void la_carry_kernel(LinAttnLaunch a, int
             const int64_t j = j0 + u, s = rev ? a.n_seg - 1 - j : j;
             const bool need = j < a.n_seg && (j + 1 < a.n_seg || (rev && a.d_initial_state));
             own[u] = need ? base[s * per] : f4{0, 0, 0, 0};
-            d[u] = need ? exp_of((float)gs[s]) : 0.0f;
+            d[u] = need ? exp_of(gs[s]) : 0.0f;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {

@@ -63,7 +63,7 @@ __global__ __launch_bounds__(kThreads) void la_step_kernel(float *state, LinAttn
             k[i][r] = n < a.N ? widen(kp[n]) : 0.0f;
         }
     const float gv = a.g_per_step ? a.g[ib * a.H + h] : a.g[h];
-    const float decay = exp_of(gv < kMinG ? kMinG : gv);
+    const float decay = exp_of(log_decay(gv));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int p = p0 + u * RW;

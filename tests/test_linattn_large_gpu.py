@@ -132,3 +132,53 @@ def test_decay_gradient_at_a_restart(b, L, H, G, N, P, dtype):
              n * R.U * mag - R.U * ref.abs()) / (n * R.U)
     R.assert_within(got, ref, n * R.U * mag + R.U * ref.abs() + 2.0 ** -45 * chunk, "dg")
     assert bool((ref[:, at] == 0).all())
+
+
+def test_decays_keep_fp32_accuracy():
+    """One path at a time, so that a result is a product of decays with exact values (powers of two): each decay is e^v of an
+    fp64 sum, with 1 ulp (2 half steps u = 2^-24) from the exponential and 3u from its correction and the factors it is
+    multiplied by, also where |v| is 20 to 70. A path takes at most four: the step's own to its chunk's end, the chunk's in
+    between, the state's or adjoint's own, and the one to the other step."""
+    b, H, N, P, L = 1, 512, 2, 2, 192
+    r = torch.Generator().manual_seed(3)
+    z = lambda *s: torch.zeros(s)  # noqa: E731
+    x = {"q": z(b, L, H, N), "k": z(b, L, H, N), "v": z(b, L, H, P), "do": z(b, L, H, P), "scale": 0.5, "lengths": None,
+         "d_final": None}
+    u = R.U
+
+    def near(got, want, n, what):
+        want = want.expand(got.shape)
+        err = ((got.double().cpu() - want).abs() / want).max()
+        assert float(err) <= n * u, (what, float(err) / u)
+
+    # one chunk: the entering state to an output and to the final state, and a step to the final state
+    g = -1.2 * torch.rand(b, 64, H, generator=r)
+    c = g.double().cumsum(1)
+    one = torch.ones(b, 64, H, N)
+    first = torch.ones(b, H, P, N)
+    o, S = api.ssm_linattn_fwd(one.cuda(), z(b, 64, H, N).cuda(), z(b, 64, H, P).cuda(), g.cuda(), initial_state=first.cuda())
+    near(o, N * c.exp()[..., None], 5, "o")
+    near(S, c[:, -1].exp()[..., None, None], 5, "state")
+    k = z(b, 64, H, N)
+    k[:, 3] = 1.0
+    _, S = api.ssm_linattn_fwd(one.cuda(), k.cuda(), one.cuda(), g.cuda())
+    near(S, (c[:, -1] - c[:, 3]).exp()[..., None, None], 5, "own state")
+    # a token
+    state, gs = torch.ones(b, H, P, N), -70.0 * torch.rand(b, H, generator=r)
+    state = state.cuda()
+    api.ssm_linattn_step(state, z(b, H, N).cuda(), z(b, H, N).cuda(), z(b, H, P).cuda(), gs.cuda())
+    near(state, gs.double().exp()[..., None, None], 5, "step")
+    # three chunks: from step 50 of the first to step 20 of the last, over a chunk whose decay is e^-30 to e^-60
+    g = torch.cat([-0.6 * torch.rand(b, 64, H, generator=r), -0.5 - 0.4 * torch.rand(b, 64, H, generator=r),
+                   -0.6 * torch.rand(b, 64, H, generator=r)], 1)
+    c = g.double().cumsum(1)
+    s, t = 50, 148
+    x["k"][:, s], x["v"][:, s], x["q"][:, t], x["do"][:, t] = 1.0, 1.0, 1.0, 1.0
+    y = gpu(x)
+    got = api.ssm_linattn_bwd(y["q"], y["k"], y["v"], g.cuda(), do=y["do"], scale=0.5)
+    w = 0.5 * (c[:, t] - c[:, s]).exp()
+    near(got["dq"][:, t], P * w[..., None], 20, "dq")
+    near(got["dk"][:, s], P * w[..., None], 20, "dk")
+    near(got["dv"][:, s], N * w[..., None], 20, "dv")
+    near(got["dg"][:, s + 1:t + 1].permute(1, 0, 2), P * N * w, 24, "dg")
+    assert not bool(got["dg"][:, t + 1:].any()) and not bool(got["dg"][:, :s + 1].any())
