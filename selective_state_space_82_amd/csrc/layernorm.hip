@@ -335,7 +335,8 @@ unsigned walking(int64_t n) { return (unsigned)(n < 65536 ? n : 65536); }
 int64_t bwd_groups(int64_t d) { return d <= 256 ? 1024 : 512; }
 
 // f(LR, K): the lanes of a row and their pieces; at most 16 elements of a row to a lane, so that the gradient's row,
-// its weight and its two partial sums stay in registers with the next row on its way.
+// its weight and its two partial sums stay in registers with the next row on its way. Past d = 8192 they do not quite: the
+// 1024 lanes have 128 registers each, and the gradient spills 59 (bf16) to 113 (fp32, rows of odd width) of them.
 template <typename T, typename F> hipError_t by_width(int64_t d, F f) {
     const int64_t n = (d + kV<T> - 1) / kV<T>;
 #define SSM_LN(LR, K) if (n <= (LR) * (K)) return f(std::integral_constant<int, LR>{}, std::integral_constant<int, K>{})
@@ -344,10 +345,10 @@ template <typename T, typename F> hipError_t by_width(int64_t d, F f) {
     SSM_LN(64, 1);
     SSM_LN(64, 2);
     if constexpr (sizeof(T) == 4) SSM_LN(64, 4);
-    SSM_LN(256, 1);
+    if constexpr (sizeof(T) == 2) SSM_LN(256, 1);  // fp32: no wider than the one before
     SSM_LN(256, 2);
     if constexpr (sizeof(T) == 4) SSM_LN(256, 4);
-    SSM_LN(1024, 1);
+    if constexpr (sizeof(T) == 2) SSM_LN(1024, 1);
     SSM_LN(1024, 2);
     if constexpr (sizeof(T) == 4) SSM_LN(1024, 4);
 #undef SSM_LN
