@@ -182,3 +182,81 @@ def test_decays_keep_fp32_accuracy():
     near(got["dv"][:, s], N * w[..., None], 20, "dv")
     near(got["dg"][:, s + 1:t + 1].permute(1, 0, 2), P * N * w, 24, "dg")
     assert not bool(got["dg"][:, t + 1:].any()) and not bool(got["dg"][:, :s + 1].any())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("H,G,N,P", [(8, 8, 64, 64), (8, 2, 20, 100)])
+def test_a_row_alone_and_in_a_batch(H, G, N, P, dtype):
+    """The gradient of a row, and a prompt of one chunk, have the same bits alone (few workgroups) and in a batch of many."""
+    b, L = 24, 130
+    x = gpu(make(b, L, H, G, N, P, dtype=dtype, first=True, seed=N))
+    names = ("q", "k", "v", "g", "do", "first", "d_final")
+
+    def grad(z):
+        return api.ssm_linattn_bwd(z["q"], z["k"], z["v"], z["g"], do=z["do"], scale=x["scale"], initial_state=z["first"],
+                                   d_final_state=z["d_final"])
+
+    def short(z):
+        cut = [z[n][:, :64].contiguous() for n in ("q", "k", "v", "g")]
+        return api.ssm_linattn_fwd(*cut, scale=x["scale"], initial_state=z["first"])
+
+    many, prompt = grad(x), short(x)
+    for i in (0, 13):
+        one = {n: x[n][i:i + 1] for n in names}
+        got = grad(one)
+        assert all(torch.equal(got[n], many[n][i:i + 1]) for n in many), i
+        assert all(torch.equal(a, c[i:i + 1]) for a, c in zip(short(one), prompt)), i
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("H,G,N,P", [(6, 2, 24, 40), (4, 4, 128, 64), (5, 1, 33, 70)])
+def test_a_token_out_of_a_packed_projection(H, G, N, P, dtype):
+    """Queries, keys and values of a token side by side in one buffer, head-major values, and a key for the whole batch."""
+    b = 3
+    x = gpu(make(b, 1, H, G, N, P, dtype=dtype, first=True, seed=N))
+    q, k, v, g = (x[n][:, 0].contiguous() for n in ("q", "k", "v", "g"))
+
+    def step(q, k, v):
+        state = x["first"].clone()
+        return api.ssm_linattn_step(state, q, k, v, g, scale=x["scale"]), state
+
+    buf = torch.cat([q.flatten(1), k.flatten(1), v.flatten(1)], -1)
+    views = (buf[:, :G * N].unflatten(-1, (G, N)), buf[:, G * N:2 * G * N].unflatten(-1, (G, N)),
+             buf[:, 2 * G * N:].unflatten(-1, (H, P)))
+    assert not views[0].is_contiguous()
+    major = v.transpose(0, 1).contiguous().transpose(0, 1)
+    shared = k[:1].expand(b, G, N)
+    for dense, strided in (((q, k, v), views), ((q, k, v), (q, k, major)), ((q, shared.contiguous(), v), (q, shared, v))):
+        for a, c in zip(step(*dense), step(*strided)):
+            assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_gradient_of_a_value_that_is_nan(dtype):
+    """A NaN in v or do at one step: gradients of other heads keep their bits; of its own head, those of other chunks that the
+    formulas keep it from (dv and dk of v's, dv's and dk's later, dq's and dv's own later ones of do's) stay as they were."""
+    b, L, H, N, P = 1, 260, 3, 32, 40
+    x = gpu(make(b, L, H, H, N, P, dtype=dtype, rate=0.05, seed=5))
+
+    def grad(z):
+        return api.ssm_linattn_bwd(z["q"], z["k"], z["v"], z["g"], do=z["do"], scale=x["scale"])
+
+    want = grad(x)
+    for name in ("v", "do"):
+        y = dict(x)
+        y[name] = x[name].clone()
+        y[name][0, 100, 1, 7] = float("nan")
+        got = grad(y)
+        for n in ("dq", "dk", "dv", "dg"):
+            assert torch.equal(got[n][:, :, [0, 2]], want[n][:, :, [0, 2]]), (name, n)
+        own = {n: (got[n][0, :, 1], want[n][0, :, 1]) for n in ("dq", "dk", "dv", "dg")}
+        same = lambda n, s: torch.equal(own[n][0][s], own[n][1][s])  # noqa: E731
+        before, after = slice(0, 64), slice(128, None)
+        if name == "v":  # S_t from step 100 on: dq later; E is untouched
+            assert same("dv", before) and same("dv", after) and same("dk", before) and same("dk", after)
+            assert same("dq", before) and bool(own["dq"][0][100:].isnan().all())
+            assert bool(own["dk"][0][100].isnan().all()) and bool(own["dg"][0][101:].isnan().all())
+        else:            # E_t up to step 100: dk, dv and dg earlier; S is untouched
+            assert same("dq", before) and same("dq", after) and same("dk", after) and same("dv", after) and same("dg", after)
+            assert bool(own["dq"][0][100].isnan().all()) and bool(own["dk"][0][:101].isnan().all())
+            assert bool(own["dv"][0][:101, 7].isnan().all()) and bool(own["dg"][0][:101].isnan().all())
