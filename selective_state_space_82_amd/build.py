@@ -35,9 +35,9 @@ PROFILE_SOURCES = {
     "conv1d": ("abi.cpp", "device_common.h", "launch.h", "conv1d.hip", "tile_common.h"),
     "frontend": ("abi.cpp", "conv1d.hip", "device_common.h", "launch.h", "scan_fwd.hip", "tile_common.h"),
     "lti": ("abi.cpp", "device_common.h", "launch.h", "lti.hip", "tile_common.h"),
-    "linattn": ("abi_attn.cpp", "device_common.h", "host_util.h", "launch.h", "linattn_bwd.hip", "linattn_common.h",
-                "linattn_fwd.hip", "linattn_step.hip"),
-    "layernorm": ("abi_attn.cpp", "device_common.h", "host_util.h", "launch.h", "layernorm.hip"),
+    "linattn": ("abi_attn.cpp", "device_common.h", "host_util.h", "launch_attn.h", "linattn_bwd.hip",
+                "linattn_common.h", "linattn_fwd.hip", "linattn_step.hip"),
+    "layernorm": ("abi_attn.cpp", "device_common.h", "host_util.h", "launch_attn.h", "layernorm.hip"),
     "ssd": ("abi.cpp", "device_common.h", "launch.h", "ssd.hip", "ssd_common.h", "ssd_scan.hip"),
 }
 

@@ -14,7 +14,7 @@
 #include <type_traits>
 
 #include "device_common.h"
-#include "launch.h"
+#include "launch_attn.h"
 
 namespace ssm {
 namespace la {
