@@ -330,9 +330,15 @@ int64_t groups(int64_t rows, int64_t w_rows, int slots, int64_t most) {
 constexpr int64_t kFwdGroups = 2048;
 // Workgroups of the launches that walk over columns in steps of the grid, far below HIP's limit of threads.
 unsigned walking(int64_t n) { return (unsigned)(n < 65536 ? n : 65536); }
-// The gradient's workgroups also write a row of partial sums each: 512 of them (8192 rows of 768 in fp32: 21.5 us; 1024
-// took 26), but 1024 where rows are short, of sixteen lanes or few more (524288 rows of 128 in bf16: 88 us; 512 took 92).
-int64_t bwd_groups(int64_t d) { return d <= 256 ? 1024 : 512; }
+// The gradient's workgroups also write a row of partial sums each: 512 of them, but 1024 where a lane has one piece of a row
+// of one wavefront or less, whose registers (under 90) let that many be resident at once. Over 2^25 elements, 1024 against 512:
+//   one piece a lane: fp32 d 64 81 us against 87, 192 78 against 108, 256 82 against 88; bf16 d 64 50 against 65, 128 43
+//   against 44, 320 45 against 57, 512 42 against 43;
+//   the rest: fp32 d 128 86 us against 81, 320 82 against 86, 512 86 against 79, 768 91 against 83, 2048 90 against 80, 8192 125
+//   against 102; bf16 d 192 56 against 48, 256 54 against 47, 768 51 against 44, 2048 50 against 50, 8192 104 against 70.
+template <int LR, int K> constexpr int64_t kBwdGroups = K == 1 && LR <= 64 ? 1024 : 512;
+// the most of them for either type: one piece a lane holds rows of up to 64·8
+int64_t most_bwd_groups(int64_t d) { return d <= 512 ? 1024 : 512; }
 
 // f(LR, K): the lanes of a row and their pieces; at most 16 elements of a row to a lane, so that the gradient's row,
 // its weight and its two partial sums stay in registers with the next row on its way. Past d = 8192 they do not quite: the
@@ -370,7 +376,7 @@ template <typename T> hipError_t bwd(const NormLaunch &p, hipStream_t stream) {
     return by_width<T>(p.d, [&](auto lr, auto k) {
         constexpr int LR = decltype(lr)::value, K = decltype(k)::value;
         typedef Lay<T, LR, K> Y;
-        const int64_t per = groups(p.rows, p.w_rows, Y::SLOTS, bwd_groups(p.d));
+        const int64_t per = groups(p.rows, p.w_rows, Y::SLOTS, kBwdGroups<LR, K>);
         const dim3 grid((unsigned)(per * p.w_rows));
         if (p.vec) norm_bwd_kernel<T, LR, K, true><<<grid, Y::THREADS, 0, stream>>>(p);
         else norm_bwd_kernel<T, LR, K, false><<<grid, Y::THREADS, 0, stream>>>(p);
@@ -389,7 +395,7 @@ template <typename T> hipError_t bwd(const NormLaunch &p, hipStream_t stream) {
 
 int64_t layernorm_part_floats(int64_t rows, int64_t d, int64_t w_rows) {
     // the most workgroups any layout launches: one row each, or the cap, or one per weight row
-    const int64_t per = ln::groups(rows, w_rows, 1, ln::bwd_groups(d));
+    const int64_t per = ln::groups(rows, w_rows, 1, ln::most_bwd_groups(d));
     return 2 * per * w_rows * d;
 }
 
