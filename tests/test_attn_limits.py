@@ -102,3 +102,25 @@ def test_norm_of_many_weight_rows():
     assert api.lib().ssm_layernorm_bwd(p(none), p(w), p(none), None, None, None, p(dw), None, 0, d, k, 0, 0, 0, None, 0,
                                        api._stream(w.device)) == 0
     assert not bool(dw[:: 2 ** 18].any()) and not bool(dw[-1].any()) and not bool(dw[k // 2:].any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows,d,k", [(700, 64, 1), (3000, 130, 2), (2100, 2048, 1), (1200, 5000, 4)])
+def test_norm_gradient_in_place(rows, d, k, dtype):
+    """dx written over x, or over dy, as the header allows, with more rows than workgroups."""
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm GPU visible")
+    r = torch.Generator(device="cuda").manual_seed(d)
+    n = lambda *s: torch.randn(s, generator=r, device="cuda")  # noqa: E731
+    x, dy, w = n(rows // k, k, d).to(dtype), n(rows // k, k, d).to(dtype), n(k, d)
+    _, m, rs = api.ssm_layernorm_fwd(x, w, return_stats=True)
+    want = api.ssm_layernorm_bwd(x, w, dy=dy, mean=m, rstd=rs)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    for over in ("x", "dy"):
+        a, c, dw, db = x.clone(), dy.clone(), torch.empty_like(w), torch.empty_like(w)
+        dx = a if over == "x" else c
+        assert api.lib().ssm_layernorm_bwd(p(a), p(w), p(c), p(m), p(rs), p(dx), p(dw), p(db), rows, d, k, 0, 0,
+                                           0 if dtype == torch.float32 else 1, None, 0, api._stream(x.device)) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(dx, want["dx"]) and torch.equal(dw, want["dw"]) and torch.equal(db, want["dbias"]), over

@@ -260,3 +260,18 @@ def test_gradient_of_a_value_that_is_nan(dtype):
             assert same("dq", before) and same("dq", after) and same("dk", after) and same("dv", after) and same("dg", after)
             assert bool(own["dq"][0][100].isnan().all()) and bool(own["dk"][0][:101].isnan().all())
             assert bool(own["dv"][0][:101, 7].isnan().all()) and bool(own["dg"][0][:101].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_inputs_broadcast_over_steps(dtype):
+    """One query, key, value or upstream gradient for all steps of a row (distance 0 between steps): the dense tensors' bits."""
+    b, L, H, G, N, P = 2, 200, 6, 3, 32, 64
+    x = gpu(make(b, L, H, G, N, P, dtype=dtype, seed=17))
+    for name in ("q", "k", "v", "do"):
+        one = x[name][:, :1].expand_as(x[name])
+        calls = [dict(x, **{name: t}) for t in (one, one.contiguous())]
+        got = [api.ssm_linattn_bwd(z["q"], z["k"], z["v"], z["g"], do=z["do"], scale=z["scale"]) for z in calls]
+        assert all(torch.equal(got[0][n], got[1][n]) for n in got[0]), name
+        if name != "do":
+            got = [api.ssm_linattn_fwd(z["q"], z["k"], z["v"], z["g"], scale=z["scale"]) for z in calls]
+            assert all(torch.equal(a, c) for a, c in zip(*got)), name

@@ -135,3 +135,39 @@ def test_bad_value_in_a_padded_batch_of_segments(dtype):
         o[i, 200:n, 3, 7] = want[0][i, 200:n, 3, 7]
         S[i, 3, 7] = want[1][i, 3, 7]
     assert torch.isfinite(o).all() and torch.isfinite(S).all()
+
+
+def test_nothing_bad_is_kept_for_the_next_call():
+    """A captured call of several multi-chunk segments, replayed with clean and with bad inputs in turn between eager calls, and
+    eager calls on one caller-held workspace: each gives what its own inputs give."""
+    import ctypes
+    b, L, H, G, N, P = 3, 1003, 12, 4, 40, 72
+    x = gpu(make(b, L, H, G, N, P, dtype=BF16, rate=8.0, first=True, seed=7))
+    assert segments(x) == 6
+    good, bad = x["v"].clone(), x["v"].clone()
+    bad[1, 200, 3, 7] = math.nan
+    run = lambda: api.ssm_linattn_fwd(x["q"], x["k"], x["v"], x["g"], scale=x["scale"], initial_state=x["first"])  # noqa: E731
+    same = lambda a, c: torch.equal(torch.nan_to_num(a.float(), nan=1e9), torch.nan_to_num(c.float(), nan=1e9))  # noqa: E731
+    run()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = run()
+    need = api.ssm_linattn_workspace(b, L, H, G, N, P, BF16)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    at = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    for i, v in enumerate((good, bad, good, bad, bad, good)):
+        x["v"].copy_(v)
+        want = run()
+        assert bool(torch.isfinite(want[0]).all()) == (v is good)
+        torch.cuda.synchronize()
+        gr.replay()
+        o, S = torch.empty_like(want[0]), torch.empty_like(want[1])
+        assert api.lib().ssm_linattn_fwd(at(x["q"]), at(x["k"]), at(x["v"]), at(x["g"]), 1, x["scale"], at(x["first"]), None,
+                                         at(o), at(S), b, L, H, G, N, P, 1, None, at(ws), need,
+                                         api._stream(o.device)) == 0
+        torch.cuda.synchronize()
+        for got in (out, (o, S)):
+            assert all(same(a, c) for a, c in zip(got, want)), i
+    o, S = api.ssm_linattn_fwd(x["q"], x["k"], bad, x["g"], scale=x["scale"], initial_state=x["first"],
+                               return_final_state=False)
+    assert S is None and bool(o[1, 200:, 3, 7].isnan().all())
