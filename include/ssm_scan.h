@@ -290,7 +290,8 @@ SSM_API ssm_status_t ssm_ssd_fwd(const void *x, const void *delta, const float *
  *   v, o              [b][L][H][P] dtype (step: [b][H][P])
  *   g                 log-decay, fp32: [b][L][H] (step: [b][H]) when g_per_step is 1, [H] (the same at every
  *                     step) when it is 0. Any value; −inf, and everything below −1e4, is a decay of exactly 0
- *                     (the state restarts at that step). Positive values let the state grow.
+ *                     (the state restarts at that step). Positive values let the state grow; where the growth over
+ *                     a chunk, or a run of chunks, passes fp32's range (e^88), results may be Inf or NaN.
  *   states            [b][H][P][N] fp32, as ssm_ssd_fwd's
  *   lengths           [b] int32 on the device or NULL (every row has L steps): row i has lengths[i] steps (taken
  *                     as 0 below 0 and as L above L). Nothing past them is read; outputs past them (o, dq, dk, dv,
@@ -305,9 +306,10 @@ SSM_API ssm_status_t ssm_ssd_fwd(const void *x, const void *delta, const float *
  *                     may overlap (other streams, captured graphs replayed at once) need one each.
  * Products are exact bf16 products summed in fp32 (bf16; fp32 operands, that is states and decayed scores, enter
  * as two bf16 parts, 2^-16 of the operand, where the result is bf16, as three where it is fp32) or fp32 products (f32). All sums,
- * decays and states are fp32, the running sum of g in a chunk fp64. Results are deterministic. A NaN or Inf at one
- * step reaches outputs and gradients as the formulas say, except that an Inf may come out as NaN, and that gradients
- * (dq, dk, dv, dg) may become NaN at every step of the 64-step chunk it is in.
+ * decays and states are fp32, the running sums of g and the sums whose difference makes dg fp64. Results are
+ * deterministic; the forward call's fp32 sums are cut by its segments, which depend on b, H, P and L. A NaN or Inf at one
+ * step reaches outputs and gradients as the formulas say, for all later steps however strong the decay, except that an
+ * Inf may come out as NaN, and that gradients (dq, dk, dv, dg) may become NaN at every step of the 64-step chunk it is in.
  * b, H, G, N, P >= 1; G divides H; H times the larger of 128 and P (rounded up to 64) is at most 2^24;
  * N <= SSM_LINATTN_MAX_N, P <= SSM_LINATTN_MAX_P (SSM_ERR_UNSUPPORTED above); L >= 0. A launch takes fewer than 2^32
  * threads: SSM_ERR_SHAPE where b·H·⌈P/64⌉ (forward: times the segments the steps are cut into, one where b·H is large)

@@ -687,7 +687,8 @@ def _norm_weight_rows(x, *weights):
 
 
 def ssm_layernorm_fwd(x, w=None, bias=None, *, eps=1e-5, y=None, return_stats=False):
-    """Layer norm over the last axis: x [..., d] (float32 or bfloat16, d <= 16384); w, bias: [d] float32, or
+    """Layer norm over the last axis: x [..., d] (float32 or bfloat16, d <= 16384), contiguous, or [rows, d] with
+    contiguous rows (columns of a wider buffer; flatten the leading axes of one first); w, bias: [d] float32, or
     [K, d] with a row per head for x [..., K, d]. Returns y, or (y, mean, rstd) with mean and rstd float32 of x's
     shape without its last axis when return_stats is set. y may be x itself."""
     if x.dim() < 1 or x.shape[-1] < 1:

@@ -91,7 +91,8 @@ ssm_status_t check_sizes(const AttnSizes &z, ssm_dtype_t dtype) {
 // least: the rounds in which the device takes its workgroups (two on a compute unit, or one where fp32 tiles of N > 32
 // fill its LDS), each of a segment's chunks and half a chunk to start and end; and with more than one segment the walk
 // over the segments' own states, 0.4 of a chunk each with four workgroups on a compute unit, and 1.5 for two more
-// launches. (fp32, 72 blocks of 16 chunks: 4 segments, 288 workgroups in two rounds, took 71 us.)
+// launches. (fp32, 72 blocks of 16 chunks: 4 segments, 288 workgroups in two rounds, took 71 us.) Planned, as the scan is,
+// for 256 compute units, and for at most 64 segments, which the carry steps over one after the other.
 void plan(const AttnSizes &z, bool gradient, LinAttnLaunch *p) {
     const int64_t chunks = ceil_div(z.L, kChunk);
     p->seg_chunks = chunks;

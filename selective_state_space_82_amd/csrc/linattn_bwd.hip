@@ -67,7 +67,7 @@ __device__ __forceinline__ double sum_cols(double v) {
 // The four wavefronts share the lower-triangular tiles of both score matrices through LDS; wavefront w takes the value
 // columns 16w .. of dv, and 16-column jobs of dq and dk, whose parts through state and adjoint come first: V is free then
 // and A1 takes its place, which leaves room for three workgroups on a compute unit. Bound: memory and its latency. b 4,
-// L 2048, 24 heads, N = P = 64 in bf16 takes 64 us for 0.28 GB (4.4 TB/s); eight wavefronts to a workgroup took 13 us more.
+// L 2048, 24 heads, N = P = 64 in bf16 takes 67 us for 0.30 GB (4.4 TB/s); eight wavefronts to a workgroup took 13 us more.
 // PARTS: bf16 parts of the scores A1 and A2 (E, as it enters dv, takes as many; S and E in dq and dk take three, because dg's
 // terms come from them). Two leave 2^-16 of each product, and dq, dk and dv as far off as rounding them to bf16 alone; one
 // leaves them 1.4 times as far off, twice where a group's heads are summed. The second parts wait in registers and take

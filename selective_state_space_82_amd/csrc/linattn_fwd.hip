@@ -45,9 +45,11 @@ __device__ __forceinline__ const float *decays_of(const LinAttnLaunch &a, const 
 // there). The decayed scores, 10 lower-triangular 16×16 tiles, are shared through LDS too. The next chunk's rows are
 // fetched into registers, and its decays formed by a wavefront without score tiles, while this chunk is computed.
 // Bound: instruction issue and LDS, not memory. b 8, L 4096, 64 heads, N 128, P 64 in bf16 takes 355 us for 0.70 GB that a
-// copy moves in 134 us. Three 64-step tiles, the scores in two parts and the state's first parts fill half a compute unit's
-// LDS, so 128 steps per chunk would leave one workgroup on it.
-// PARTS: bf16 parts of the state, as it enters the outputs, and of the scores. Two leave 2^-17 of each product; the outputs
+// copy moves in 134 us. By the recurrence's operations (4·N·P a step and head) that is 194 Tflop/s, 15 % of what a large
+// bf16 product reaches; it makes about three times as many. A wavefront issues 390 VALU, 51 MFMA, 78 LDS and 8 memory
+// instructions a chunk, and 150 clocks go to bank conflicts. Three 64-step tiles, the scores in two parts and the state's
+// first parts fill half a compute unit's LDS, so 128 steps per chunk would leave one workgroup on it.
+// PARTS: bf16 parts of the state, as it enters the outputs, and of the scores. Two leave 2^-16 of each product; the outputs
 // are then as far off as rounding them to bf16 alone. The state in one part takes 316 us here and puts them up to 1.4
 // times as far off; its second part in LDS of its own, with one workgroup on a compute unit, takes 106 us where this takes
 // 68 (64 rows of 64 steps, 32 heads, 128 by 64).
@@ -416,7 +418,7 @@ __global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int
 // ---- from the segments' own states to those entering them (adjoints: leaving them), in place ---------------------
 //
 // One thread per four state elements steps over the segments; eight loads are kept in flight. Memory bounds it: the
-// gradient's states and adjoints of 3072 chunks, 0.2 GB both ways, take 32 us (6.3 TB/s). A carry over segments of six
+// gradient's states and adjoints of 3072 chunks, 0.2 GB both ways, take 31 us (30 to 45 over 400 calls; 6.4 TB/s). A carry over segments of six
 // chunks, with the chunks' states formed from zero at their segment's border and put together where they are used,
 // took 8 us, but the walk and the gradient's kernel 37 us more.
 __global__ __launch_bounds__(kThreads) void la_carry_kernel(LinAttnLaunch a, int NT) {
@@ -468,7 +470,7 @@ __global__ __launch_bounds__(kThreads) void la_carry_kernel(LinAttnLaunch a, int
 // e^-200 times a NaN or Inf is not 0: once an element of the state is one, it stays one (Inf or NaN) for all later steps, and
 // so does its column of the outputs. The walk that gives the outputs meets every step and says which segments it left with
 // such an element; here one workgroup per (row, head, 64 value columns) carries it into the segments after. It costs a
-// launch in calls of more than one segment of more than one chunk, and a look at the words where all is finite.
+// launch in calls of more than one segment of more than one chunk, 4.7 us where all is finite.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void la_nonfinite_kernel(LinAttnLaunch a, int NT) {
     const int64_t npb = (a.P + kPB - 1) / kPB, pb = blockIdx.x % npb, bh = blockIdx.x / npb;
