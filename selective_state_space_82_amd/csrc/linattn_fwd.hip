@@ -418,9 +418,10 @@ __global__ __launch_bounds__(64 * NW) void la_states_kernel(LinAttnLaunch a, int
 // ---- from the segments' own states to those entering them (adjoints: leaving them), in place ---------------------
 //
 // One thread per four state elements steps over the segments; eight loads are kept in flight. Memory bounds it: the
-// gradient's states and adjoints of 3072 chunks, 0.2 GB both ways, take 31 us (30 to 45 over 400 calls; 6.4 TB/s). A carry over segments of six
-// chunks, with the chunks' states formed from zero at their segment's border and put together where they are used,
-// took 8 us, but the walk and the gradient's kernel 37 us more.
+// states and adjoints of all chunks of the gradient at b 4, L 2048, 24 heads, N = P = 64, 0.2 GB both ways, take 31 us
+// (30 to 45 over 400 calls; 6.4 TB/s). A carry over segments of six chunks, with the chunks' states formed from zero at
+// their segment's border and put together where they are used, took 8 us, but the walk and the gradient's kernel 37 us
+// more.
 __global__ __launch_bounds__(kThreads) void la_carry_kernel(LinAttnLaunch a, int NT) {
     const int64_t Pp = (a.P + kPB - 1) / kPB * kPB;
     const int64_t per = Pp * NT / 4;                       // four-element groups of one state: a multiple of 256
