@@ -115,7 +115,7 @@ void plan(const AttnSizes &z, bool gradient, LinAttnLaunch *p) {
     p->n_seg = p->seg_chunks > 0 ? ceil_div(chunks, p->seg_chunks) : 0;
 }
 
-// Whether HIP takes every launch of the planned call (launchable() in launch.h).
+// Whether HIP takes every launch of the planned call (launchable() in launch_attn.h).
 bool launches(const AttnSizes &z, bool gradient, const LinAttnLaunch &p) {
     if (p.n_seg == 0) return true;
     const int64_t bh = z.b * z.H, blocks = ceil_div(z.P, kBlockP), cols = ssm::linattn_cols(z.P);
