@@ -386,6 +386,115 @@ SSM_API ssm_status_t ssm_layernorm_bwd(const void *x, const float *w, const void
                                        void *workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Softmax attention, for the attention layers that hybrid stacks set between recurrent ones (page
+ * "State Space Models（SSM）とMamba" §6). Per sequence of nq queries and nk keys, query head h reading key head h·G/H:
+ *     s_ij = scale · q_i·k_j   over the keys j that query i sees: j <= i + nk − nq (causal) or all j < nk
+ *     o_i  = Σ_j p_ij v_j,  p_ij = e^(s_ij − lse_i),  lse_i = log Σ_j e^s_ij
+ * A query that sees no key has o = 0 and lse = −inf.
+ *   q, o, do_         [tokens][H][D] dtype        k, v              [tokens][G][D] dtype
+ *   lse               [tokens][H] fp32, or NULL where it is an output
+ *   rows              where the sequences lie:
+ *                     cu_q, cu_k both given: packed. b + 1 rising offsets each on the device into tokens_q and tokens_k
+ *                       tokens; sequence i has those from cu[i] to cu[i+1]. They may be the same pointer. Lq and Lk are the
+ *                       longest sequences' lengths, or more: a longer one counts as Lq (Lk) long. Outputs of tokens of
+ *                       no sequence are left as they were. Offsets outside of the tokens are taken as the nearest one inside.
+ *                     otherwise b rows of Lq queries and Lk keys, tokens_q and tokens_k unused; len_q and len_k (or NULL: all
+ *                       count), [b] on the device, say how many of each row count. Nothing past them is read; outputs past
+ *                       them (o, dq, dk, dv) are 0, lse −inf.
+ *   strides           NULL: dense. Otherwise as ssm_linattn_strides_t's for q, k, v, do_ (b unused where packed). Outputs, and
+ *                     o and lse as inputs, are always dense.
+ * Products are exact bf16 products summed in fp32 (bf16) or fp32 products (f32); the softmax' statistics and all sums are
+ * fp32. With bf16, weights and their gradients enter products rounded to bf16, 2^-8 each (a second part for each would add half
+ * again to the forward call's products). Results are deterministic. A NaN or Inf reaches the
+ * queries that see its key and no others (an Inf in v may come out as NaN); gradients may become NaN for the 32 tokens of
+ * the same sequence around it.
+ * b, H, G, D >= 1; G divides H; D <= SSM_ATTN_MAX_D and scale finite (SSM_ERR_UNSUPPORTED otherwise); Lq, Lk <= 2^30; H·D and
+ * strides between tokens at most 2^24; a launch takes fewer than 2^32 threads (b·H·⌈Lq/128⌉ and b·G·⌈Lk/128⌉ below 2^24,
+ * queries times H in the gradient below 2^28). No output may overlap an input, the workspace or another output.
+ */
+#define SSM_ATTN_MAX_D 128
+typedef ssm_linattn_strides_t ssm_attn_strides_t;
+typedef struct {
+    const int32_t *cu_q, *cu_k, *len_q, *len_k;
+    int64_t b, Lq, Lk, tokens_q, tokens_k;
+} ssm_attn_rows_t;
+
+SSM_API ssm_status_t ssm_attn_fwd(const void *q, const void *k, const void *v, float scale, int32_t causal,
+                                  const ssm_attn_rows_t *rows, void *o, float *lse, int64_t H, int64_t G, int64_t D,
+                                  ssm_dtype_t dtype, const ssm_attn_strides_t *strides, hipStream_t stream);
+
+/* Gradients for an upstream gradient do_ on o, from the forward call's o and lse. dq [tokens][H][D], dk and dv
+ * [tokens][G][D] (summed over the heads that share a key head, in fp32) dtype, all required. workspace as for
+ * ssm_linattn_bwd, of the bytes ssm_attn_bwd_workspace gives. */
+SSM_API ssm_status_t ssm_attn_bwd_workspace(const ssm_attn_rows_t *rows, int64_t H, int64_t *bytes);
+SSM_API ssm_status_t ssm_attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                                  const void *do_, float scale, int32_t causal, const ssm_attn_rows_t *rows, void *dq,
+                                  void *dk, void *dv, int64_t H, int64_t G, int64_t D, ssm_dtype_t dtype,
+                                  const ssm_attn_strides_t *strides, void *workspace, int64_t workspace_bytes,
+                                  hipStream_t stream);
+
+/*
+ * A paged cache of keys and values: token t of row i is in slot t mod page_size of page
+ * page_table[i·max_pages + t / page_size].
+ *   k_cache, v_cache  [pages][page_size][G][D] dtype; pages k_page and v_page elements apart (0: dense), so that both may
+ *                     lie in one pool
+ *   page_table        [b][max_pages] int32 on the device. An entry outside 0 .. pages − 1 is a page that is not there: its
+ *                     tokens are not attended to, and not stored
+ * pages, page_size, max_pages >= 1, page_size <= 2^20, max_pages·page_size <= 2^30, G·D <= 2^24.
+ */
+typedef struct {
+    const int32_t *page_table;
+    int64_t pages, page_size, max_pages, k_page, v_page;
+} ssm_pages_t;
+
+/* Attention of one new token a row, over the row's tokens in the cache (its own among them, ssm_kv_append stores it):
+ *   q                 [b][H][D] dtype, rows q_b and heads q_h elements apart (0, 0: dense)
+ *   lengths           [b] int32 on the device: tokens of each row in the cache, taken as 0 below 0 and as max_pages·page_size
+ *                     above that. Rows of length 0 have o = 0 and lse = −inf. Nothing past them is read.
+ *   o, lse            [b][H][D] dtype, required; [b][H] fp32 or NULL
+ *   max_len           the longest length the call is planned for (0: max_pages·page_size); rows may be longer
+ *   workspace         as for ssm_linattn_fwd, of the bytes ssm_attn_step_workspace gives (0 where no row is split)
+ * Arithmetic, limits and errors as for ssm_attn_fwd; b·G·⌈H/G/16⌉ times the pieces (up to ⌈max_len/256⌉) and b·H below 2^24. */
+SSM_API ssm_status_t ssm_attn_step_workspace(int64_t b, int64_t H, int64_t G, int64_t D, const ssm_pages_t *pages,
+                                             int64_t max_len, int64_t *bytes);
+SSM_API ssm_status_t ssm_attn_step(const void *q, const void *k_cache, const void *v_cache, const ssm_pages_t *pages,
+                                   const int32_t *lengths, float scale, void *o, float *lse, int64_t b, int64_t H, int64_t G,
+                                   int64_t D, int64_t q_b, int64_t q_h, int64_t max_len, ssm_dtype_t dtype, void *workspace,
+                                   int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * New tokens into the cache, with the position rotation on the way. Coordinates of a head are turned in pairs: pair
+ * m < rotary/2 of a token at position t by the angle t·freq[m] (coordinates m and m + rotary/2, or 2m and 2m + 1 where
+ * interleaved), the others stay:  (x, y) -> (x cos − y sin, y cos + x sin). Angles are formed and reduced in fp64.
+ *   tokens            which rows the T new tokens belong to: cu NULL: b rows of L tokens, T = b·L, of which new_lengths[i] (or
+ *                     NULL: all) count; cu given: b + 1 rising offsets on the device, row i has those from cu[i] to cu[i+1]
+ *   lengths           [b] int32 on the device: tokens of each row with the new ones; the new ones are the row's last.
+ *                     NULL (ssm_rope only): they are all there are
+ *   q, q_out          [T][H][D] dtype: rotated; both NULL, or q_out may be q (dense)
+ *   k, k_out          [T][G][D] dtype: rotated into the cache and, where k_out is not NULL, into it; k_out may be k (dense)
+ *   v                 [T][G][D] dtype: into the cache
+ *   freq              [rotary/2] fp64 on the device, radians a position, or NULL: no rotation. rotary even, 2 .. D
+ *   strides           as for ssm_attn_fwd (do_'s are not used)
+ * Tokens whose position the row's pages do not reach are not stored. Two new tokens on the same slot (rows that share a page)
+ * leave either's values there. Outputs q_out and k_out of tokens that belong to no row are 0 (left as they are in place). T and T·H·D
+ * within ssm_attn_fwd's limits, T below 2^26. Errors as for ssm_attn_fwd.
+ */
+typedef struct {
+    const int32_t *cu, *new_lengths;
+    int64_t b, L, T;
+} ssm_tokens_t;
+SSM_API ssm_status_t ssm_kv_append(const void *q, const void *k, const void *v, void *q_out, void *k_out, void *k_cache,
+                                   void *v_cache, const ssm_pages_t *pages, const int32_t *lengths, const ssm_tokens_t *tokens,
+                                   const double *freq, int64_t rotary, int32_t interleaved, int64_t H, int64_t G, int64_t D,
+                                   ssm_dtype_t dtype, const ssm_attn_strides_t *strides, hipStream_t stream);
+
+/* The rotation alone: x [T][H][D] dtype, x_b, x_t, x_h elements apart (all 0: dense), to out (dense; may be x where that is
+ * dense). inverse: by the opposite angles, which is the gradient. */
+SSM_API ssm_status_t ssm_rope(const void *x, void *out, const int32_t *lengths, const ssm_tokens_t *tokens, const double *freq,
+                              int64_t rotary, int32_t interleaved, int32_t inverse, int64_t H, int64_t D, int64_t x_b,
+                              int64_t x_t, int64_t x_h, ssm_dtype_t dtype, hipStream_t stream);
+
+/*
  * Options of ssm_scan_fwd_ex. Zero-initialise, then set what you need; zero means "choose".
  *   seg_len            time-segment length (multiple of 32) carried across by the chunk-carry
  *                      pass; 0 = chosen from the shape, >= L = one segment

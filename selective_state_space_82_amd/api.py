@@ -50,6 +50,24 @@ class LinAttnStrides(ctypes.Structure):
     _fields_ = [(f"{t}_{a}", ctypes.c_int64) for t in ("q", "k", "v", "do") for a in ("b", "t", "h")]
 
 
+class AttnRows(ctypes.Structure):
+    """ssm_attn_rows_t."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("cu_q", "cu_k", "len_q", "len_k")] + \
+               [(n, ctypes.c_int64) for n in ("b", "Lq", "Lk", "tokens_q", "tokens_k")]
+
+
+class Pages(ctypes.Structure):
+    """ssm_pages_t."""
+    _fields_ = [("page_table", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int64) for n in ("pages", "page_size", "max_pages", "k_page", "v_page")]
+
+
+class Tokens(ctypes.Structure):
+    """ssm_tokens_t."""
+    _fields_ = [("cu", ctypes.c_void_p), ("new_lengths", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int64) for n in ("b", "L", "T")]
+
+
 _lib = None
 
 
@@ -112,6 +130,21 @@ def lib() -> ctypes.CDLL:
     L.ssm_layernorm_bwd_workspace.restype = i32
     L.ssm_layernorm_bwd.argtypes = [vp] * 8 + [i64] * 5 + [i32, vp, i64, vp]
     L.ssm_layernorm_bwd.restype = i32
+    rows, pages, tokens = ctypes.POINTER(AttnRows), ctypes.POINTER(Pages), ctypes.POINTER(Tokens)
+    L.ssm_attn_fwd.argtypes = [vp] * 3 + [f32, i32, rows, vp, vp] + [i64] * 3 + [i32, strides, vp]
+    L.ssm_attn_fwd.restype = i32
+    L.ssm_attn_bwd_workspace.argtypes = [rows, i64, ctypes.POINTER(i64)]
+    L.ssm_attn_bwd_workspace.restype = i32
+    L.ssm_attn_bwd.argtypes = [vp] * 6 + [f32, i32, rows] + [vp] * 3 + [i64] * 3 + [i32, strides, vp, i64, vp]
+    L.ssm_attn_bwd.restype = i32
+    L.ssm_attn_step_workspace.argtypes = [i64] * 4 + [pages, i64, ctypes.POINTER(i64)]
+    L.ssm_attn_step_workspace.restype = i32
+    L.ssm_attn_step.argtypes = [vp] * 3 + [pages, vp, f32, vp, vp] + [i64] * 7 + [i32, vp, i64, vp]
+    L.ssm_attn_step.restype = i32
+    L.ssm_kv_append.argtypes = [vp] * 7 + [pages, vp, tokens, vp, i64, i32] + [i64] * 3 + [i32, strides, vp]
+    L.ssm_kv_append.restype = i32
+    L.ssm_rope.argtypes = [vp] * 3 + [tokens, vp, i64, i32, i32] + [i64] * 5 + [i32, vp]
+    L.ssm_rope.restype = i32
     L.ssm_status_string.argtypes = [i32]
     L.ssm_status_string.restype = ctypes.c_char_p
     L.ssm_abi_version.argtypes = []
@@ -745,4 +778,322 @@ def ssm_layernorm_bwd(x, w=None, *, dy, mean, rstd, want_dw=True, want_dbias=Tru
                                          _at(out["dw"]), _at(out["dbias"]), rows, d, k, stride, dy_stride, code,
                                          _at(ws), need, _raw_stream(dev))
     _raise(status, "ssm_layernorm_bwd")
+    return out
+
+
+def _on_gpu(t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError("tensors must live on a ROCm GPU")
+
+
+def _attn_rows(q, k, cu_seqlens, max_len, cu_seqlens_k, max_len_k, lengths, lengths_k):
+    """Where the sequences of q and k lie: the descriptor of a packed batch [T, heads, D] or of rows [b, L, heads, D]."""
+    r, dev = AttnRows(), q.device
+    if q.dim() != k.dim() or q.dim() not in (3, 4):
+        raise ValueError("q, k and v must be [b, L, heads, D], or [T, heads, D] with cu_seqlens")
+    if q.dim() == 3:
+        if cu_seqlens is None or max_len is None:
+            raise ValueError("packed sequences [T, heads, D] need cu_seqlens and max_len")
+        if lengths is not None or lengths_k is not None:
+            raise ValueError("lengths are for rows [b, L, heads, D]")
+        if (cu_seqlens_k is None) != (max_len_k is None):
+            raise ValueError("cu_seqlens_k and max_len_k go together")
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+            raise ValueError("cu_seqlens must be [b + 1]")
+        r.b = cu_seqlens.shape[0] - 1
+        _check("cu_seqlens", cu_seqlens, (r.b + 1,), torch.int32, dev)
+        _check("cu_seqlens_k", cu_seqlens_k, (r.b + 1,), torch.int32, dev)
+        r.cu_q = cu_seqlens.data_ptr()
+        r.cu_k = r.cu_q if cu_seqlens_k is None else cu_seqlens_k.data_ptr()
+        r.Lq, r.Lk = max_len, max_len if max_len_k is None else max_len_k
+        r.tokens_q, r.tokens_k = q.shape[0], k.shape[0]
+        return r
+    if cu_seqlens is not None or cu_seqlens_k is not None or max_len is not None or max_len_k is not None:
+        raise ValueError("cu_seqlens and max_len are for packed sequences [T, heads, D]")
+    r.b, r.Lq = q.shape[:2]
+    r.Lk = k.shape[1]
+    if lengths is not None and lengths_k is None:
+        if r.Lk != r.Lq:
+            raise ValueError("lengths of queries and keys: give lengths_k as well where there are more keys than queries")
+        lengths_k = lengths
+    _check("lengths", lengths, (r.b,), torch.int32, dev)
+    _check("lengths_k", lengths_k, (r.b,), torch.int32, dev)
+    r.len_q, r.len_k = _at(lengths), _at(lengths_k)
+    return r
+
+
+def _attn_inputs(q, k, v):
+    """Checks q [..., H, D], k and v [..., G, D]. Returns (H, G, D, storage dtype code)."""
+    _on_gpu(q)
+    if q.dim() < 2 or not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+        raise ValueError("q and k must have the same number of axes")
+    H, D = q.shape[-2:]
+    G = k.shape[-2]
+    dev, st = q.device, q.dtype
+    code = _dtype_code(st)
+    _check_rows("q", q, q.shape, st, dev)
+    _check_rows("k", k, (q.shape[0], *k.shape[1:-1], D) if q.dim() == 4 else (k.shape[0], G, D), st, dev)
+    _check_rows("v", v, k.shape, st, dev)
+    return H, G, D, code
+
+
+def _attn_strides(q, k, v, do=None):
+    """As _linattn_strides, for [b, L, heads, D] or [T, heads, D]."""
+    if all(t is None or t.is_contiguous() for t in (q, k, v, do)):
+        return None
+    s = LinAttnStrides()
+    for name, t in (("q", q), ("k", k), ("v", v), ("do", do)):
+        if t is not None:
+            st = t.stride()
+            setattr(s, f"{name}_b", st[0] if len(st) == 4 else 0)
+            setattr(s, f"{name}_t", st[-3])
+            setattr(s, f"{name}_h", st[-2])
+    return ctypes.byref(s)
+
+
+def _scale(scale, D):
+    return D ** -0.5 if scale is None else float(scale)
+
+
+def ssm_attn_fwd(q, k, v, *, scale=None, causal=True, cu_seqlens=None, max_len=None, cu_seqlens_k=None, max_len_k=None,
+                 lengths=None, lengths_k=None, o=None, return_lse=False):
+    """Softmax attention over prompts: o_i = Σ_j p_ij v_j, p = softmax_j(scale·q_i·k_j) over the keys j <= i + nk − nq of
+    its sequence (causal; nq queries, nk keys) or over all of them. Head h of q reads head h·G/H of k and v; scale is
+    D^-1/2 unless given. float32 or bfloat16, G divides H, D <= 128; views whose last axis is contiguous (slices of a packed
+    projection) are read in place.
+
+    Rows: q [b, L, H, D], k and v [b, Lk, G, D]; lengths and lengths_k ([b] int32 on the GPU) say how many steps of each row
+    count (lengths alone: of both); outputs past them are 0. Packed: q [T, H, D], k and v [Tk, G, D] with cu_seqlens
+    ([b + 1] int32 on the GPU, rising offsets) and max_len, the longest sequence's length or more (a longer one is cut);
+    cu_seqlens_k and max_len_k where the keys' differ. Tokens of no sequence: 0, or as they were in an `o` that is given.
+
+    Returns o (q's shape), or (o, lse) with lse = log Σ_j e^(scale·q_i·k_j) float32 [..., H] when return_lse is set. A query
+    that sees no key has o = 0 and lse = −inf."""
+    H, G, D, code = _attn_inputs(q, k, v)
+    r = _attn_rows(q, k, cu_seqlens, max_len, cu_seqlens_k, max_len_k, lengths, lengths_k)
+    dev = q.device
+    with _on_device(dev):
+        lse = None
+        if return_lse:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if q.dim() == 4 else \
+                torch.full(q.shape[:-1], float("-inf"), dtype=torch.float32, device=dev)
+        if o is None:
+            o = (torch.empty if q.dim() == 4 else torch.zeros)(q.shape, dtype=q.dtype, device=dev)
+        else:
+            _check("o", o, q.shape, q.dtype, dev)
+        status = lib().ssm_attn_fwd(_at(q), _at(k), _at(v), _scale(scale, D), bool(causal), ctypes.byref(r), _at(o), _at(lse),
+                                    H, G, D, code, _attn_strides(q, k, v), _raw_stream(dev))
+    _raise(status, "ssm_attn_fwd")
+    return (o, lse) if return_lse else o
+
+
+def ssm_attn_bwd(q, k, v, *, o, lse, do, scale=None, causal=True, cu_seqlens=None, max_len=None, cu_seqlens_k=None,
+                 max_len_k=None, lengths=None, lengths_k=None) -> dict:
+    """Gradients of ssm_attn_fwd for an upstream gradient do on o, from the forward call's o and lse (contiguous; the other
+    arguments as in that call). Returns a dict: dq, dk, dv (the shapes and dtype of q, k, v; dk and dv summed over the heads
+    that share a key head)."""
+    H, G, D, code = _attn_inputs(q, k, v)
+    r = _attn_rows(q, k, cu_seqlens, max_len, cu_seqlens_k, max_len_k, lengths, lengths_k)
+    dev, st = q.device, q.dtype
+    for name, t, shape, dtype in (("o", o, q.shape, st), ("lse", lse, q.shape[:-1], torch.float32)):
+        if t is None:
+            raise TypeError(f"{name} must be a torch.Tensor")
+        _check(name, t, shape, dtype, dev)
+    _check_rows("do", do, q.shape, st, dev)
+    with _on_device(dev):
+        new = torch.empty if q.dim() == 4 else torch.zeros
+        out = {"dq": new(q.shape, dtype=st, device=dev), "dk": new(k.shape, dtype=st, device=dev),
+               "dv": new(k.shape, dtype=st, device=dev)}
+        n = ctypes.c_int64()
+        _raise(lib().ssm_attn_bwd_workspace(ctypes.byref(r), H, ctypes.byref(n)), "ssm_attn_bwd_workspace")
+        ws = _workspace(n.value, dev)
+        status = lib().ssm_attn_bwd(_at(q), _at(k), _at(v), _at(o), _at(lse), _at(do), _scale(scale, D), bool(causal),
+                                    ctypes.byref(r), _at(out["dq"]), _at(out["dk"]), _at(out["dv"]), H, G, D, code,
+                                    _attn_strides(q, k, v, do), _at(ws), n.value, _raw_stream(dev))
+    _raise(status, "ssm_attn_bwd")
+    return out
+
+
+def _pages(k_cache, v_cache, page_table, b, G, D, dtype, dev):
+    """The descriptor of a paged cache [pages, page_size, G, D] whose pages are dense."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name} must be a torch.Tensor [pages, page_size, G, D]")
+    shape = (*k_cache.shape[:2], G, D)
+    g = Pages()
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check_rows(name, t, shape, dtype, dev)
+        st = t.stride()
+        dense = all(n == 1 or s == want for n, s, want in zip(shape[1:], st[1:], (G * D, D, 1)))
+        if not dense or (shape[0] > 1 and st[0] < shape[1] * G * D):
+            raise ValueError(f"the pages of {name} must be contiguous")
+        setattr(g, name[0] + "_page", st[0] if shape[0] > 1 else 0)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a torch.Tensor [b, max_pages]")
+    _check("page_table", page_table, (b, page_table.shape[1]), torch.int32, dev)
+    g.page_table = page_table.data_ptr()
+    g.pages, g.page_size = shape[:2]
+    g.max_pages = page_table.shape[1]
+    return g
+
+
+def ssm_attn_step(q, k_cache, v_cache, page_table, lengths, *, scale=None, max_len=0, o=None, return_lse=False):
+    """Softmax attention of one new token a row over a paged cache (ssm_kv_append fills it): q [b, H, D]; k_cache and
+    v_cache [pages, page_size, G, D], contiguous or with pages further apart (halves of one pool); page_table [b,
+    max_pages] int32: token t of row i is in slot t mod page_size of page page_table[i, t // page_size]; lengths [b] int32:
+    tokens of each row in the cache, the new one among them (all on the GPU). Table entries that are no page count as
+    pages that are not there. max_len: the longest length that the call is planned for (0: what the table holds); rows may be
+    longer. Returns o [b, H, D], or (o, lse [b, H] float32) when return_lse is set; a row without tokens has o = 0."""
+    _on_gpu(q)
+    if q.dim() != 3 or not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("q must be [b, H, D] and k_cache [pages, page_size, G, D]")
+    b, H, D = q.shape
+    G, dev, st = k_cache.shape[2], q.device, q.dtype
+    code = _dtype_code(st)
+    _check_rows("q", q, (b, H, D), st, dev)
+    g = _pages(k_cache, v_cache, page_table, b, G, D, st, dev)
+    if lengths is None:
+        raise TypeError("lengths must be a torch.Tensor")
+    _check("lengths", lengths, (b,), torch.int32, dev)
+    with _on_device(dev):
+        if o is None:
+            o = torch.empty((b, H, D), dtype=st, device=dev)
+        else:
+            _check("o", o, (b, H, D), st, dev)
+        lse = torch.empty((b, H), dtype=torch.float32, device=dev) if return_lse else None
+        n = ctypes.c_int64()
+        _raise(lib().ssm_attn_step_workspace(b, H, G, D, ctypes.byref(g), max_len, ctypes.byref(n)),
+               "ssm_attn_step_workspace")
+        ws = _workspace(n.value, dev)
+        q_b, q_h = (0, 0) if q.is_contiguous() else q.stride()[:2]
+        if (q_b, q_h) == (0, 0) and not q.is_contiguous():  # one row and head for all: as a tensor of its own
+            q = q.contiguous()
+        status = lib().ssm_attn_step(_at(q), _at(k_cache), _at(v_cache), ctypes.byref(g), _at(lengths), _scale(scale, D),
+                                     _at(o), _at(lse), b, H, G, D, q_b, q_h, max_len, code, _at(ws), n.value,
+                                     _raw_stream(dev))
+    _raise(status, "ssm_attn_step")
+    return (o, lse) if return_lse else o
+
+
+def _new_tokens(x, cu_seqlens, new_lengths, b=None):
+    """The descriptor of new tokens x: [b, heads, D] one a row, [b, L, heads, D], or [T, heads, D] with cu_seqlens."""
+    t, dev = Tokens(), x.device
+    if x.dim() == 4:
+        if cu_seqlens is not None:
+            raise ValueError("cu_seqlens is for packed tokens [T, heads, D]")
+        t.b, t.L = x.shape[:2]
+        t.T = t.b * t.L
+        _check("new_lengths", new_lengths, (t.b,), torch.int32, dev)
+        t.new_lengths = _at(new_lengths)
+        return t
+    if x.dim() != 3:
+        raise ValueError("new tokens must be [b, heads, D], [b, L, heads, D], or [T, heads, D] with cu_seqlens")
+    if new_lengths is not None:
+        raise ValueError("new_lengths is for rows [b, L, heads, D]")
+    t.T = x.shape[0]
+    if cu_seqlens is None:
+        t.b, t.L = x.shape[0], 1
+        return t
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be [b + 1]")
+    t.b = cu_seqlens.shape[0] - 1
+    _check("cu_seqlens", cu_seqlens, (t.b + 1,), torch.int32, dev)
+    t.cu = cu_seqlens.data_ptr()
+    return t
+
+
+def _rotary(freq, D, dev) -> int:
+    if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
+        raise ValueError("freq must be a torch.Tensor [rotary / 2]")
+    _check("freq", freq, freq.shape, torch.float64, dev)
+    if not 1 <= freq.shape[0] <= D // 2:
+        raise ValueError("freq must have 1 to D / 2 entries")
+    return 2 * freq.shape[0]
+
+
+def ssm_kv_append(k, v, k_cache, v_cache, page_table, lengths, *, q=None, freq=None, cu_seqlens=None, new_lengths=None,
+                  interleaved=False, q_out=None, k_out=None, return_k=False):
+    """Appends the keys and values of new tokens to a paged cache (ssm_attn_step's), turning keys, and queries q if given,
+    by their positions on the way. k, v: [b, G, D] (one token a row), [b, L, G, D] (new_lengths [b] int32: how many of each
+    row count), or packed [T, G, D] with cu_seqlens [b + 1] int32; q likewise with H heads; views whose last axis is
+    contiguous are read in place. lengths [b] int32: tokens of each row in the cache with the new ones, which are its last.
+    freq [rotary/2] float64: radians a position of each coordinate pair (coordinates m and m + rotary/2, or 2m and 2m + 1 where
+    interleaved); None: no rotation. Tokens that the row's pages do not reach are not stored.
+
+    Returns (q_out, k_out): the turned queries (None without q) and, if return_k or k_out is given, the turned keys (else
+    None). q_out may be q, and k_out k, where they are contiguous. Tokens of no row are 0 there (in place: as they were)."""
+    _on_gpu(k)
+    t = _new_tokens(k, cu_seqlens, new_lengths)
+    G, D = k.shape[-2:]
+    dev, st = k.device, k.dtype
+    code = _dtype_code(st)
+    _check_rows("k", k, k.shape, st, dev)
+    _check_rows("v", v, k.shape, st, dev)
+    H = G
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != k.dim():
+            raise ValueError("q must be a torch.Tensor with as many axes as k")
+        H = q.shape[-2]
+        _check_rows("q", q, (*k.shape[:-2], H, D), st, dev)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    g = _pages(k_cache, v_cache, page_table, t.b, G, D, st, dev)
+    if lengths is None:
+        raise TypeError("lengths must be a torch.Tensor")
+    _check("lengths", lengths, (t.b,), torch.int32, dev)
+    rotary = 0 if freq is None else _rotary(freq, D, dev)
+    with _on_device(dev):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=st, device=dev)
+        if q is not None:
+            _check("q_out", q_out, q.shape, st, dev)
+        if return_k and k_out is None:
+            k_out = torch.empty(k.shape, dtype=st, device=dev)
+        _check("k_out", k_out, k.shape, st, dev)
+        status = lib().ssm_kv_append(_at(q), _at(k), _at(v), _at(q_out), _at(k_out), _at(k_cache), _at(v_cache),
+                                     ctypes.byref(g), _at(lengths), ctypes.byref(t), _at(freq), rotary, bool(interleaved), H, G,
+                                     D, code, _token_strides(q, k, v), _raw_stream(dev))
+    _raise(status, "ssm_kv_append")
+    return q_out, k_out
+
+
+def _token_strides(q, k, v):
+    """Strides of new tokens: a row's single token has those of its row."""
+    if all(t is None or t.is_contiguous() for t in (q, k, v)):
+        return None
+    s = LinAttnStrides()
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t is not None:
+            st = t.stride()
+            setattr(s, f"{name}_b", st[0])
+            setattr(s, f"{name}_t", st[-3])
+            setattr(s, f"{name}_h", st[-2])
+    return ctypes.byref(s)
+
+
+def ssm_rope(x, freq, *, lengths=None, cu_seqlens=None, new_lengths=None, interleaved=False, inverse=False, out=None):
+    """Turns the heads of tokens x by their positions, as ssm_kv_append does on the way to the cache. x: [b, heads, D],
+    [b, L, heads, D], or packed [T, heads, D] with cu_seqlens. The tokens of a row stand at its positions 0, 1, ..., or at the
+    last ones of lengths [b] int32. inverse: by the opposite angles (the gradient: the rotation of a gradient back). Returns out
+    (x's shape), which may be x itself where that is contiguous."""
+    _on_gpu(x)
+    t = _new_tokens(x, cu_seqlens, new_lengths)
+    H, D = x.shape[-2:]
+    dev, st = x.device, x.dtype
+    code = _dtype_code(st)
+    _check_rows("x", x, x.shape, st, dev)
+    _check("lengths", lengths, (t.b,), torch.int32, dev)
+    rotary = _rotary(freq, D, dev)
+    with _on_device(dev):
+        if out is None:
+            out = torch.empty(x.shape, dtype=st, device=dev)
+        _check("out", out, x.shape, st, dev)
+        s = (0, 0, 0) if x.is_contiguous() else (x.stride(0), x.stride(-3), x.stride(-2))
+        if s == (0, 0, 0) and not x.is_contiguous():
+            x = x.contiguous()
+        status = lib().ssm_rope(_at(x), _at(out), _at(lengths), ctypes.byref(t), _at(freq), rotary, bool(interleaved),
+                                bool(inverse), H, D, *s, code, _raw_stream(dev))
+    _raise(status, "ssm_rope")
     return out

@@ -13,8 +13,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libssmscan.so")
 SOURCES = ["scan_fwd.hip", "scan_small.hip", "agg_rev.hip", "scan_bwd.hip", "scan_step.hip", "conv1d.hip", "lti.hip", "ssd.hip",
-           "ssd_scan.hip", "linattn_fwd.hip", "linattn_bwd.hip", "linattn_step.hip", "layernorm.hip", "noalloc.hip",
-           "abi.cpp", "abi_attn.cpp"]
+           "ssd_scan.hip", "linattn_fwd.hip", "linattn_bwd.hip", "linattn_step.hip", "layernorm.hip", "softmax_fwd.hip",
+           "softmax_bwd.hip", "softmax_step.hip", "kv_append.hip", "noalloc.hip", "abi.cpp", "abi_attn.cpp", "abi_softmax.cpp"]
 ARCH = "gfx950"
 
 # Packed fp32 VALU forms are kept out of the generated code.
@@ -38,6 +38,9 @@ PROFILE_SOURCES = {
     "linattn": ("abi_attn.cpp", "device_common.h", "host_util.h", "launch_attn.h", "linattn_bwd.hip",
                 "linattn_common.h", "linattn_fwd.hip", "linattn_step.hip"),
     "layernorm": ("abi_attn.cpp", "device_common.h", "host_util.h", "launch_attn.h", "layernorm.hip"),
+    "softmax": ("abi_softmax.cpp", "device_common.h", "host_util.h", "kv_append.hip", "launch_softmax.h",
+                "linattn_common.h", "softmax_bwd.hip", "softmax_common.h", "softmax_fwd.hip", "softmax_index.h",
+                "softmax_step.hip"),
     "ssd": ("abi.cpp", "device_common.h", "launch.h", "ssd.hip", "ssd_common.h", "ssd_scan.hip"),
 }
 

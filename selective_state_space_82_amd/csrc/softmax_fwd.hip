@@ -1,0 +1,210 @@
+// softmax_fwd.hip — softmax attention over prompts: o_i = Σ_j p_ij v_j, p = softmax_j(scale·q_i·k_j) over the keys that query i
+// sees, with lse_i = log Σ_j e^(scale·q_i·k_j).
+//
+// One pass over the keys with the running maximum and sum of the softmax. A workgroup takes 32 queries a wavefront of one
+// head and walks the keys its queries see in tiles, which it fetches into registers during the tile before and then into one
+// of two LDS buffers. Scores stay in registers (softmax_common.h).
+#include "softmax_common.h"
+
+namespace ssm {
+namespace sm {
+namespace {
+
+// Keys of a tile.
+template <typename T> constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;
+// A running maximum is raised, and what was summed rescaled, once a score passes it by 2^8: weights are at most 2^8 then,
+// and nothing else changes, for fp32 and bf16 keep their relative precision there.
+constexpr float kSlack = 8.0f;
+
+template <typename T, int DP, bool VEC>
+__global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(SoftmaxLaunch a, int blocks) {
+    constexpr int KB = kKeys<T>, NT = KB / 32, NC = DP / kChunk<T>, ND = DP / 32, BQ = 32 * kSoftmaxThreads / 64;
+    constexpr int KS = kRowStride<T, DP>, VS = kColStride<T, DP>;
+    __shared__ __attribute__((aligned(16))) T kt[2][KB * KS], vt[2][KB * VS];
+    __shared__ int flag[2];
+
+    // work: sequence, then key head, then the heads that share it, then blocks of queries, the longest first
+    int64_t id = la::work_index(blockIdx.x, gridDim.x);
+    const int qb = blocks - 1 - (int)(id % blocks);
+    id /= blocks;
+    const int h = (int)(id % a.H);
+    const int64_t is = id / a.H;
+    const int g = h / (a.H / a.G);
+    const AttnSeq s = sequence(a.rows, is);
+    const bool packed = a.rows.cu_q != nullptr;
+    const int w = la::wave_id(), l = threadIdx.x & 63, col = l & 31, half = l >> 5;
+    const int q0 = qb * BQ, r0 = q0 + 32 * w;
+    const int to_write = packed ? s.nq : (int)a.rows.Lq;
+    if (q0 >= to_write) return;
+
+    const T *qp = static_cast<const T *>(a.q) + is * a.q_b + s.q0 * a.q_t + h * a.q_h + (int64_t)r0 * a.q_t;
+    const T *kp = static_cast<const T *>(a.k) + is * a.k_b + s.k0 * a.k_t + g * a.k_h;
+    const T *vp = static_cast<const T *>(a.v) + is * a.v_b + s.k0 * a.v_t + g * a.v_h;
+
+    // tiles up to the last key that the block's last query sees
+    const int last_q = (q0 + BQ < s.nq ? q0 + BQ : s.nq) - 1;
+    const int keys = last_q >= q0 ? last_key(s, a.causal, last_q) + 1 : 0;
+    const int tiles = (keys + KB - 1) / KB;
+    const int my_last = last_key(s, a.causal, r0 + col);                     // of the lane's query
+    const int first_seen = q0 < s.nq ? last_key(s, a.causal, q0) : -1;       // that every query of the block sees
+    const int wave_first = last_key(s, a.causal, r0);
+    const int wave_last = r0 < s.nq ? last_key(s, a.causal, (r0 + 32 < s.nq ? r0 + 32 : s.nq) - 1) : -1;
+
+    Frag<T> q[NC];
+    {
+        const int rows = s.nq - r0;
+        load_frags<T, DP, VEC>(q, la::rows_buffer(qp, (uint32_t)a.q_t, rows > 32 ? 32 : rows, a.D), (uint32_t)a.q_t, col,
+                               rows > 32 ? 32 : rows, a.D);
+        if (a.scale < 0.0f) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) negate<T>(q[c]);
+        }
+    }
+    const float sc = scale_of(a.scale);
+
+    f16 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[d] = f16(0.0f);
+    float m = -INFINITY, sum = 0.0f;  // sum: over the lane's half of the keys
+
+    Stage<T, KB, DP, VEC> ks, vs;
+    if (threadIdx.x < 2) flag[threadIdx.x] = 0;
+    if (tiles > 0) {
+        ks.load(kp, (uint32_t)a.k_t, s.nk, a.D);
+        vs.load(vp, (uint32_t)a.v_t, s.nk, a.D);
+        la::lds_barrier();
+        ks.store(kt[0], KS);
+        vs.store(vt[0], VS);
+        if (KB - 1 > first_seen && vs.bad()) flag[0] = 1;
+    }
+    for (int j = 0; j < tiles; ++j) {
+        const int j0 = j * KB;
+        la::lds_barrier();
+        if (j + 1 < tiles) {
+            ks.load(kp + (int64_t)(j0 + KB) * a.k_t, (uint32_t)a.k_t, s.nk - j0 - KB, a.D);
+            vs.load(vp + (int64_t)(j0 + KB) * a.v_t, (uint32_t)a.v_t, s.nk - j0 - KB, a.D);
+        }
+        const T *kb = kt[j & 1], *vb = vt[j & 1];
+        if (j0 <= wave_last) {
+            f16 p[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) p[t] = f16(0.0f);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma(p[t], row_frag(kb, KS, 32 * t, kChunk<T> * c), q[c]);
+            const bool masked = j0 + KB - 1 > wave_first;
+            if (masked) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (j0 + 32 * t + 8 * (i >> 2) + 4 * half + (i & 3) > my_last) p[t][i] = -INFINITY;
+            }
+            float top = p[0][0];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, p[t][i]);
+            top = __builtin_fmaxf(top, other_half(top)) * sc;
+            const bool raise = top > m + kSlack || (m == -INFINITY && top > m);  // each query by itself: its bits are its own
+            if (__any(raise)) {
+                const float f = raise ? exp2_fast(m - top) : 1.0f;
+                m = raise ? top : m;
+                sum *= f;
+#pragma unroll
+                for (int d = 0; d < ND; ++d) o[d] *= f;
+            }
+            const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    p[t][i] = exp2_fast(__builtin_fmaf(p[t][i], sc, -base));
+                    sum += p[t][i];
+                }
+            // A masked key's weight is 0, but 0 times a NaN or Inf is not: where a tile that not every query sees whole
+            // holds one, those values count as 0 here, and make the result NaN for the queries that do see them.
+            if (masked && flag[j & 1] == j + 1) {
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    f16 seen = f16(0.0f);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int c = 0; c < 32 / kChunk<T>; ++c) {
+                            Frag<T> v = col_frag(vb, VS, 32 * t + kChunk<T> * c, 32 * d), bad, see;
+#pragma unroll
+                            for (int e = 0; e < kE<T>; ++e) {
+                                const int i = kE<T> * c + e;
+                                const bool nf = !__builtin_isfinite((float)v[e]);
+                                bad[e] = nf ? 1.0f : 0.0f;
+                                if (nf) v[e] = 0.0f;
+                                see[e] = j0 + 32 * t + 8 * (i >> 2) + 4 * half + (i & 3) > my_last ? 0.0f : 1.0f;
+                            }
+                            mma(o[d], v, part_of<T>(p[t], c));
+                            mma(seen, bad, see);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (seen[i] > 0.0f) o[d][i] = NAN;
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int c = 0; c < 32 / kChunk<T>; ++c) {
+                        const Frag<T> pf = part_of<T>(p[t], c);
+#pragma unroll
+                        for (int d = 0; d < ND; ++d) mma(o[d], col_frag(vb, VS, 32 * t + kChunk<T> * c, 32 * d), pf);
+                    }
+            }
+        }
+        if (j + 1 < tiles) {
+            ks.store(kt[(j + 1) & 1], KS);
+            vs.store(vt[(j + 1) & 1], VS);
+            if (j0 + 2 * KB - 1 > first_seen && vs.bad()) flag[(j + 1) & 1] = j + 2;
+        }
+    }
+    sum += other_half(sum);
+
+    // rows past the sequence's queries (a padded batch): no keys, 0 and -inf
+    const bool live = r0 + col < s.nq && !(sum == 0.0f);
+    const float f = live ? 1.0f / sum : 0.0f;
+    const int64_t row = (packed ? s.q0 : is * a.rows.Lq) + r0;
+    int rows = to_write - r0;
+    rows = rows > 32 ? 32 : rows;
+    const uint32_t stride = (uint32_t)(a.H * a.D);
+    const Buffer out = la::rows_buffer(static_cast<T *>(a.o) + (row * a.H + h) * a.D, stride, rows, a.D);
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+        if (!live) o[d] = f16(0.0f);
+        store_tile<T, VEC>(out, stride, col, 32 * d, col < rows ? a.D : 0, o[d], f);
+    }
+    if (a.lse && half == 0 && col < rows)
+        a.lse[(row + col) * a.H + h] = live ? (m + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f : -INFINITY;
+}
+
+template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, hipStream_t stream) {
+    const int64_t blocks = (p.rows.Lq + softmax_fwd_block(p) - 1) / softmax_fwd_block(p);
+    softmax_fwd_kernel<T, DP, VEC><<<dim3((unsigned)(p.rows.b * p.H * blocks)), kSoftmaxThreads, 0, stream>>>(p, (int)blocks);
+    return hipGetLastError();
+}
+template <typename T> hipError_t by_width(const SoftmaxLaunch &p, hipStream_t stream) {
+    if (!p.vec) return p.D <= 64 ? run<T, 64, false>(p, stream) : run<T, 128, false>(p, stream);
+    if (p.D <= 32) return run<T, 32, true>(p, stream);
+    if (p.D <= 64) return run<T, 64, true>(p, stream);
+    if (p.D <= 96) return run<T, 96, true>(p, stream);
+    return run<T, 128, true>(p, stream);
+}
+
+}  // namespace
+}  // namespace sm
+
+int softmax_fwd_block(const SoftmaxLaunch &) { return 32 * kSoftmaxThreads / 64; }
+
+hipError_t launch_softmax_fwd(const SoftmaxLaunch &p, hipStream_t stream) {
+    return p.bf16 ? sm::by_width<uint16_t>(p, stream) : sm::by_width<float>(p, stream);
+}
+
+}  // namespace ssm
