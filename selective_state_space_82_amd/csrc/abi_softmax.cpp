@@ -89,10 +89,10 @@ struct View {
     Span span(const void *p, int64_t es) const {
         return {p, b < 1 || t < 1 ? 0 : ((b - 1) * sb + (t - 1) * st + (heads - 1) * sh + D) * es};
     }
-    // every row of D elements takes 16-byte accesses
+    // every row of D elements takes 16-byte accesses, and lies past the end of a buffer that ends with the row before
     bool vec(const void *p, int64_t es) const {
         const int64_t v = 16 / es;
-        return aligned16(p) && D % v == 0 && sb % v == 0 && st % v == 0 && sh % v == 0;
+        return aligned16(p) && D % v == 0 && st >= D && sb % v == 0 && st % v == 0 && sh % v == 0;
     }
 };
 

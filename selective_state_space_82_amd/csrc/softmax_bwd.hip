@@ -52,8 +52,8 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_stats_kernel(SoftmaxL
 // see them, head by head of the group, in tiles of 32.
 template <typename T, int DP, bool VEC>
 __global__ __launch_bounds__(kSoftmaxThreads) void softmax_dkv_kernel(SoftmaxLaunch a, int blocks, int64_t tokens) {
-    constexpr int QB = 32, NC = DP / kChunk<T>, ND = DP / 32, BK = 32 * kSoftmaxThreads / 64, S = kRowStride<T, DP>;
-    __shared__ __attribute__((aligned(16))) T qt[2][QB * S], dt[2][QB * S];
+    constexpr int QB = 32, NC = DP / kChunk<T>, ND = DP / 32, BK = 32 * kSoftmaxThreads / 64;
+    __shared__ __attribute__((aligned(1024))) char qt[2][QB * Tile<T, DP>::kRow], dt[2][QB * Tile<T, DP>::kRow];
     __shared__ __attribute__((aligned(16))) float lse_t[2][QB], delta_t[2][QB];
 
     int64_t id = la::work_index(blockIdx.x, gridDim.x);
@@ -85,48 +85,36 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_dkv_kernel(SoftmaxLau
 #pragma unroll
     for (int d = 0; d < ND; ++d) dk[d] = dv[d] = f16(0.0f);
 
-    Stage<T, QB, DP, VEC> qs, ds;
-    float stat[2];
-    const auto fetch = [&](int r, int tile) {
+    const Loader<T, QB, DP, VEC> qs((uint32_t)a.q_t, a.D), ds((uint32_t)a.do_t, a.D);
+    const auto fetch = [&](int r, int tile, int b) {
         const int h = g * R + r, i0 = (first + tile) * QB;
-        qs.load(static_cast<const T *>(a.q) + is * a.q_b + (s.q0 + i0) * a.q_t + h * a.q_h, (uint32_t)a.q_t, s.nq - i0, a.D);
-        ds.load(static_cast<const T *>(a.dout) + is * a.do_b + (s.q0 + i0) * a.do_t + h * a.do_h, (uint32_t)a.do_t, s.nq - i0,
-                a.D);
         if (threadIdx.x < QB) {
             const int i = i0 + (int)threadIdx.x;
             const int64_t t = (packed ? s.q0 : is * a.rows.Lq) + i;
             const float *p = a.stats + 2 * (h * tokens + t);
-            stat[0] = i < s.nq ? p[0] : 0.0f;
-            stat[1] = i < s.nq ? p[1] : 0.0f;
+            lse_t[b][threadIdx.x] = i < s.nq ? p[0] : 0.0f;
+            delta_t[b][threadIdx.x] = i < s.nq ? p[1] : 0.0f;
         }
-    };
-    const auto put = [&](int b) {
-        qs.store(qt[b], S);
-        ds.store(dt[b], S);
-        if (threadIdx.x < QB) {
-            lse_t[b][threadIdx.x] = stat[0];
-            delta_t[b][threadIdx.x] = stat[1];
-        }
+        qs(static_cast<const T *>(a.q) + is * a.q_b + (s.q0 + i0) * a.q_t + h * a.q_h, s.nq - i0, qt[b]);
+        ds(static_cast<const T *>(a.dout) + is * a.do_b + (s.q0 + i0) * a.do_t + h * a.do_h, s.nq - i0, dt[b]);
     };
     int r = 0, tile = 0;
-    if (tiles > 0) {
-        fetch(0, 0);
-        put(0);
-    }
+    if (tiles > 0) fetch(0, 0, 0);
     for (int n = 0; n < tiles * R; ++n) {
         const int i0 = (first + tile) * QB, b = n & 1;
+        landed();
         la::lds_barrier();
         if (++tile == tiles) {
             tile = 0;
             ++r;
         }
-        if (r < R) fetch(r, tile);
+        if (r < R) fetch(r, tile, b ^ 1);
         if (r0 < s.nk && (!a.causal || r0 <= i0 + QB - 1 + off)) {
             f16 p = f16(0.0f), dp = f16(0.0f);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                mma(p, row_frag(qt[b], S, 0, kChunk<T> * c), k[c]);
-                mma(dp, row_frag(dt[b], S, 0, kChunk<T> * c), v[c]);
+                mma(p, row_frag<T, DP>(qt[b], 0, c), k[c]);
+                mma(dp, row_frag<T, DP>(dt[b], 0, c), v[c]);
             }
             const bool masked = i0 + QB > s.nq || r0 + 32 > s.nk || (a.causal && r0 + 31 > i0 + off);
 #pragma unroll
@@ -151,12 +139,11 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_dkv_kernel(SoftmaxLau
                 const Frag<T> pf = part_of<T>(p, c), df = part_of<T>(dp, c);
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
-                    mma(dv[d], col_frag(dt[b], S, kChunk<T> * c, 32 * d), pf);
-                    mma(dk[d], col_frag(qt[b], S, kChunk<T> * c, 32 * d), df);
+                    mma(dv[d], col_frag<T, DP>(dt[b], kChunk<T> * c, 32 * d), pf);
+                    mma(dk[d], col_frag<T, DP>(qt[b], kChunk<T> * c, 32 * d), df);
                 }
             }
         }
-        if (r < R) put(b ^ 1);
     }
 
     const int64_t row = (packed ? s.k0 : is * a.rows.Lk) + r0;
@@ -177,8 +164,7 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_dkv_kernel(SoftmaxLau
 template <typename T, int DP, bool VEC>
 __global__ __launch_bounds__(kSoftmaxThreads) void softmax_dq_kernel(SoftmaxLaunch a, int blocks, int64_t tokens) {
     constexpr int KB = 32, NC = DP / kChunk<T>, ND = DP / 32, BQ = 32 * kSoftmaxThreads / 64;
-    constexpr int KS = kRowStride<T, DP>;
-    __shared__ __attribute__((aligned(16))) T kt[2][KB * KS], vt[2][KB * KS];
+    __shared__ __attribute__((aligned(1024))) char kt[2][KB * Tile<T, DP>::kRow], vt[2][KB * Tile<T, DP>::kRow];
 
     int64_t id = la::work_index(blockIdx.x, gridDim.x);
     const int qb = blocks - 1 - (int)(id % blocks);
@@ -221,26 +207,25 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_dq_kernel(SoftmaxLaun
 #pragma unroll
     for (int d = 0; d < ND; ++d) dq[d] = f16(0.0f);
 
-    Stage<T, KB, DP, VEC> ks, vs;
+    const Loader<T, KB, DP, VEC> ks((uint32_t)a.k_t, a.D), vs((uint32_t)a.v_t, a.D);
     if (tiles > 0) {
-        ks.load(kp, (uint32_t)a.k_t, s.nk, a.D);
-        vs.load(vp, (uint32_t)a.v_t, s.nk, a.D);
-        ks.store(kt[0], KS);
-        vs.store(vt[0], KS);
+        ks(kp, s.nk, kt[0]);
+        vs(vp, s.nk, vt[0]);
     }
     for (int j = 0; j < tiles; ++j) {
         const int j0 = j * KB, b = j & 1;
+        landed();
         la::lds_barrier();
         if (j + 1 < tiles) {
-            ks.load(kp + (int64_t)(j0 + KB) * a.k_t, (uint32_t)a.k_t, s.nk - j0 - KB, a.D);
-            vs.load(vp + (int64_t)(j0 + KB) * a.v_t, (uint32_t)a.v_t, s.nk - j0 - KB, a.D);
+            ks(kp + (int64_t)(j0 + KB) * a.k_t, s.nk - j0 - KB, kt[b ^ 1]);
+            vs(vp + (int64_t)(j0 + KB) * a.v_t, s.nk - j0 - KB, vt[b ^ 1]);
         }
         if (j0 <= wave_last) {
             f16 p = f16(0.0f), dp = f16(0.0f);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                mma(p, row_frag(kt[b], KS, 0, kChunk<T> * c), q[c]);
-                mma(dp, row_frag(vt[b], KS, 0, kChunk<T> * c), dout[c]);
+                mma(p, row_frag<T, DP>(kt[b], 0, c), q[c]);
+                mma(dp, row_frag<T, DP>(vt[b], 0, c), dout[c]);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -254,12 +239,8 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_dq_kernel(SoftmaxLaun
             for (int c = 0; c < 32 / kChunk<T>; ++c) {
                 const Frag<T> df = part_of<T>(dp, c);
 #pragma unroll
-                for (int d = 0; d < ND; ++d) mma(dq[d], col_frag(kt[b], KS, kChunk<T> * c, 32 * d), df);
+                for (int d = 0; d < ND; ++d) mma(dq[d], col_frag<T, DP>(kt[b], kChunk<T> * c, 32 * d), df);
             }
-        }
-        if (j + 1 < tiles) {
-            ks.store(kt[b ^ 1], KS);
-            vs.store(vt[b ^ 1], KS);
         }
     }
     const int rows = to_write - r0 > 32 ? 32 : to_write - r0;

@@ -43,31 +43,48 @@ __device__ __forceinline__ void mma(f16 &acc, const f4 &a, const f4 &b) {
     for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], acc, 0, 0, 0);
 }
 
-// Elements between the rows of an LDS tile of W columns. read_rows: 16-byte reads of 16 rows at once take all banks (rows 4
-// banks apart beyond whole turns). read_cols: the 4 rows of a transposing read lie 16 banks apart (bf16), the two of a
-// read by value 32 (fp32). A tile read both ways takes the first.
-template <typename T, int W> constexpr int kRowStride = W + 16 / sizeof(T);
-template <typename T, int W> constexpr int kColStride =
-    sizeof(T) == 2 ? (W % 64 == 32 ? W : W % 128 == 96 ? W : W + 32) : W + 8;
+// An LDS tile of rows of W columns, without padding between them, so that loads can go from memory straight into LDS, 64
+// pieces of 16 bytes at a time in the order of the lanes. Banks are spread by where a row's pieces stand: piece p of row r at place
+// p ^ turn(r). So 16 rows read 16 bytes each at one piece, the 4 rows × 64 bytes of a transposing read (bf16) and the two rows, 4
+// apart, of 128 bytes each of a read by value (fp32) lie in different banks.
+template <typename T, int W> struct Tile {
+    static constexpr int kPitch = W == 96 ? 128 : W;                    // columns between rows
+    static constexpr int kRow = kPitch * (int)sizeof(T), kPer = kRow / 16;  // bytes and pieces of a row
+    __device__ static __forceinline__ int turn(int r) {
+        if constexpr (kRow == 512) return (r & 3) | (r >> 3 & 1) << 2 | (r >> 2 & 1) << 3;
+        else if constexpr (kRow == 256) return (r & 3) << 2 | (r >> 2 & 3);
+        else if constexpr (kRow == 128) return (r >> 1 & 1) << 2 | (r >> 2 & 3);
+        else return r >> 2 & 3;
+    }
+    // byte offset of piece p of row r
+    __device__ static __forceinline__ int at(int r, int p) { return r * kRow + 16 * (p ^ turn(r)); }
+};
 
-// Row `row0 + col`, values n0 + E·half on, of a tile.
-template <typename T> __device__ __forceinline__ Frag<T> row_frag(const T *tile, int stride, int row0, int n0) {
+// Row `row0 + col` (row0 a multiple of 32), chunk c of a tile.
+template <typename T, int W> __device__ __forceinline__ Frag<T> row_frag(const char *tile, int row0, int c) {
     const int l = threadIdx.x & 63;
-    return *reinterpret_cast<const Frag<T> *>(tile + (row0 + (l & 31)) * stride + n0 + kE<T> * (l >> 5));
+    return *reinterpret_cast<const Frag<T> *>(tile + row0 * Tile<T, W>::kRow + Tile<T, W>::at(l & 31, 2 * c + (l >> 5)));
 }
-// Column `col0 + col`, rows s0 .. s0 + chunk − 1 in the order above, of a tile.
-__device__ __forceinline__ bf8 col_frag(const uint16_t *tile, int stride, int s0, int col0) {
-    typedef __attribute__((address_space(3))) s4 lds_s4;
-    const int l = threadIdx.x & 63, c = l & 15;
-    const uint16_t *p = tile + (s0 + 4 * (l >> 5) + (c >> 2)) * stride + col0 + (l & 16) + 4 * (c & 3);
-    const s4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)p);
-    const s4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p + 8 * stride));
-    return __builtin_bit_cast(bf8, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-__device__ __forceinline__ f4 col_frag(const float *tile, int stride, int s0, int col0) {
+// Column `col0 + col`, rows s0 .. s0 + chunk − 1 (s0 a multiple of the chunk) in the order above, of a tile.
+template <typename T, int W> __device__ __forceinline__ Frag<T> col_frag(const char *tile, int s0, int col0) {
     const int l = threadIdx.x & 63;
-    const float *p = tile + (s0 + 4 * (l >> 5)) * stride + col0 + (l & 31);
-    return f4{p[0], p[stride], p[2 * stride], p[3 * stride]};
+    using X = Tile<T, W>;
+    if constexpr (sizeof(T) == 2) {
+        typedef __attribute__((address_space(3))) s4 lds_s4;
+        const int c = l & 15, r = 4 * (l >> 5) + (c >> 2), p = col0 / 8 + (l >> 4 & 1) * 2 + (c >> 1 & 1), e = 8 * (c & 1);
+        const char *q = tile + s0 * X::kRow + e;
+        const s4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(q + X::at(r, p)));
+        const s4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(q + X::at(r + 8, p)));
+        return __builtin_bit_cast(bf8, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+        f4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = (s0 & 15) + 4 * (l >> 5) + e, p = col0 / 4 + (l >> 2 & 7);
+            x[e] = *reinterpret_cast<const float *>(tile + (s0 & ~15) * X::kRow + X::at(r, p) + 4 * (l & 3));
+        }
+        return x;
+    }
 }
 
 // Elements of chunk c of a lane's sixteen results as an operand in the order down a column. bf16: rounded to nearest, 2^-8.
@@ -110,59 +127,95 @@ __device__ __forceinline__ void load_frags(Frag<T> (&f)[DP / kChunk<T>], const B
     }
 }
 
-// Whether a 16-byte piece holds a NaN or Inf.
-template <typename T> __device__ __forceinline__ bool not_finite(const u4 &w) {
+// Whether ROWS rows of a tile hold a NaN or Inf in their first W columns; the same in every lane.
+template <typename T, int ROWS, int W> __device__ __forceinline__ bool not_finite(const char *tile) {
     bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 2) bad = bad || (~w[i] & 0x7f80u) == 0 || (~w[i] & 0x7f800000u) == 0;
-        else bad = bad || (~w[i] & 0x7f800000u) == 0;
-    }
-    return bad;
-}
-
-// ROWS rows × W columns on their way into an LDS tile, zeros past the rows and columns there are. A thread holds its pieces
-// between load and store, so that a tile is fetched while the one before is computed.
-template <typename T, int ROWS, int W, bool VEC> struct Stage {
-    static constexpr int E = kE<T>, PER = W / E, PIECES = ROWS * PER, N = (PIECES + kSoftmaxThreads - 1) / kSoftmaxThreads;
-    u4 w[N];
-    // first: row 0, column 0 of the tile, the same in every lane; rows: how many there are (0 and below: none)
-    __device__ __forceinline__ void load(const T *first, uint32_t stride, int rows, int cols) {
-        rows = rows > ROWS ? ROWS : rows;
-        const Buffer buf = la::rows_buffer(first, stride, rows, cols);
+    constexpr int N = ROWS * Tile<T, W>::kPer / 64;
+    static_assert(ROWS * Tile<T, W>::kPer % 64 == 0, "");
+    if constexpr (sizeof(T) == 2) {
+        typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+        us2 most = us2(0);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int id = (int)threadIdx.x + j * kSoftmaxThreads, r = id / PER, c = id % PER * E;
-            if constexpr (VEC) {
-                const uint32_t at = r < rows && c < cols ? (r * stride + c) * (uint32_t)sizeof(T) : kOutside;
-                w[j] = __builtin_amdgcn_raw_buffer_load_b128(buf, at, 0, 0);
-            } else {
-                T e[E];
+            const u4 w = *reinterpret_cast<const u4 *>(tile + 16 * (64 * j + (threadIdx.x & 63)));
 #pragma unroll
-                for (int k = 0; k < E; ++k) {
-                    const uint32_t at = r < rows && c + k < cols ? (r * stride + c + k) * (uint32_t)sizeof(T) : kOutside;
-                    if constexpr (sizeof(T) == 2) e[k] = (T)__builtin_amdgcn_raw_buffer_load_b16(buf, at, 0, 0);
-                    else e[k] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(buf, at, 0, 0));
-                }
-                __builtin_memcpy(&w[j], e, sizeof(w[j]));
+            for (int i = 0; i < 4; ++i)
+                most = __builtin_elementwise_max(most, __builtin_bit_cast(us2, w[i] & 0x7fff7fffu));
+        }
+        bad = most[0] >= 0x7f80 || most[1] >= 0x7f80;
+    } else {
+        uint32_t most = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const u4 w = *reinterpret_cast<const u4 *>(tile + 16 * (64 * j + (threadIdx.x & 63)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) most = most > (w[i] & 0x7fffffffu) ? most : (w[i] & 0x7fffffffu);
+        }
+        bad = most >= 0x7f800000u;
+    }
+    return __any(bad);
+}
+
+// ROWS rows × W columns of a strided matrix into an LDS tile, by a workgroup; zeros past the rows and columns there are.
+// VEC: straight into LDS, 16 bytes a lane, through a buffer that ends with the last row; the instructions are written out, for the
+// compiler would have every later read of LDS wait for a load that it knows to go there, also one from the other
+// buffer. A wavefront waits for its own with landed() before the barrier that hands the tile over. Otherwise element by
+// element through registers.
+template <typename T, int ROWS, int W, bool VEC> struct Loader {
+    using X = Tile<T, W>;
+    static constexpr int E = kE<T>, PIECES = ROWS * X::kPer, N = (PIECES + kSoftmaxThreads - 1) / kSoftmaxThreads;
+    static_assert(PIECES % kSoftmaxThreads == 0 || (PIECES < kSoftmaxThreads && PIECES % 64 == 0), "whole instructions");
+    uint32_t at[VEC ? N : 1];  // of the lane's pieces, in bytes from row 0
+    uint32_t stride;
+    int cols;
+    __device__ __forceinline__ Loader(uint32_t stride_, int cols_) : stride(stride_), cols(cols_) {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int id = (int)threadIdx.x + j * kSoftmaxThreads, r = id / X::kPer, c = (id % X::kPer ^ X::turn(r)) * E;
+                at[j] = c < cols ? (r * stride + c) * (uint32_t)sizeof(T) : kOutside;
             }
         }
     }
-    __device__ __forceinline__ void store(T *tile, int stride) const {
+    // first: row 0 of the tile, column 0, the same in every lane; rows: how many there are from it on
+    __device__ __forceinline__ void operator()(const T *first, int rows, char *tile) const {
+        rows = rows > ROWS ? ROWS : rows;
+        const uint32_t bytes = rows > 0 ? (uint32_t)((rows - 1) * stride + cols) * (uint32_t)sizeof(T) : 0u;
+        if constexpr (VEC) {
+            const uint64_t a = reinterpret_cast<uint64_t>(first);
+            const u4 buf = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                            (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
+                            (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00027000u};
+            if (PIECES < kSoftmaxThreads && la::wave_id() * 64 >= PIECES) return;
+            const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)tile + la::wave_id() * 1024;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int id = (int)threadIdx.x + j * kSoftmaxThreads;
-            if (PIECES % kSoftmaxThreads == 0 || id < PIECES)
-                *reinterpret_cast<u4 *>(tile + id / PER * stride + id % PER * E) = w[j];
+            for (int j = 0; j < N; ++j)
+                asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                             :
+                             : "s"(lds + j * kSoftmaxThreads * 16), "v"(at[j]), "s"(buf)
+                             : "memory");
+        } else {
+            const Buffer buf = la::buffer_of(first, bytes);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int id = (int)threadIdx.x + j * kSoftmaxThreads, r = id / X::kPer, c = (id % X::kPer ^ X::turn(r)) * E;
+                if (PIECES < kSoftmaxThreads && id >= PIECES) break;
+                T e[E];
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    const uint32_t off = r < rows && c + k < cols ? (r * stride + c + k) * (uint32_t)sizeof(T) : kOutside;
+                    if constexpr (sizeof(T) == 2) e[k] = (T)__builtin_amdgcn_raw_buffer_load_b16(buf, off, 0, 0);
+                    else e[k] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(buf, off, 0, 0));
+                }
+                u4 w;
+                __builtin_memcpy(&w, e, sizeof(w));
+                *reinterpret_cast<u4 *>(tile + 16 * id) = w;
+            }
         }
     }
-    __device__ __forceinline__ bool bad() const {
-        bool b = false;
-#pragma unroll
-        for (int j = 0; j < N; ++j) b = b || not_finite<T>(w[j]);
-        return b;
-    }
 };
+// The wavefront's loads into LDS are there.
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Of the lane's value and that of the lane 32 away.
 __device__ __forceinline__ float other_half(float v) {

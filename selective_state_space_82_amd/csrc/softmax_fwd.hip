@@ -19,9 +19,8 @@ constexpr float kSlack = 8.0f;
 template <typename T, int DP, bool VEC>
 __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(SoftmaxLaunch a, int blocks) {
     constexpr int KB = kKeys<T>, NT = KB / 32, NC = DP / kChunk<T>, ND = DP / 32, BQ = 32 * kSoftmaxThreads / 64;
-    constexpr int KS = kRowStride<T, DP>, VS = kColStride<T, DP>;
-    __shared__ __attribute__((aligned(16))) T kt[2][KB * KS], vt[2][KB * VS];
-    __shared__ int flag[2];
+    constexpr int kTileBytes = KB * Tile<T, DP>::kRow;
+    __shared__ __attribute__((aligned(1024))) char kt[2][kTileBytes], vt[2][kTileBytes];
 
     // work: sequence, then key head, then the heads that share it, then blocks of queries, the longest first
     int64_t id = la::work_index(blockIdx.x, gridDim.x);
@@ -46,7 +45,6 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
     const int keys = last_q >= q0 ? last_key(s, a.causal, last_q) + 1 : 0;
     const int tiles = (keys + KB - 1) / KB;
     const int my_last = last_key(s, a.causal, r0 + col);                     // of the lane's query
-    const int first_seen = q0 < s.nq ? last_key(s, a.causal, q0) : -1;       // that every query of the block sees
     const int wave_first = last_key(s, a.causal, r0);
     const int wave_last = r0 < s.nq ? last_key(s, a.causal, (r0 + 32 < s.nq ? r0 + 32 : s.nq) - 1) : -1;
 
@@ -67,24 +65,20 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
     for (int d = 0; d < ND; ++d) o[d] = f16(0.0f);
     float m = -INFINITY, sum = 0.0f;  // sum: over the lane's half of the keys
 
-    Stage<T, KB, DP, VEC> ks, vs;
-    if (threadIdx.x < 2) flag[threadIdx.x] = 0;
+    const Loader<T, KB, DP, VEC> ks((uint32_t)a.k_t, a.D), vs((uint32_t)a.v_t, a.D);
     if (tiles > 0) {
-        ks.load(kp, (uint32_t)a.k_t, s.nk, a.D);
-        vs.load(vp, (uint32_t)a.v_t, s.nk, a.D);
-        la::lds_barrier();
-        ks.store(kt[0], KS);
-        vs.store(vt[0], VS);
-        if (KB - 1 > first_seen && vs.bad()) flag[0] = 1;
+        ks(kp, s.nk, kt[0]);
+        vs(vp, s.nk, vt[0]);
     }
     for (int j = 0; j < tiles; ++j) {
         const int j0 = j * KB;
+        landed();
         la::lds_barrier();
         if (j + 1 < tiles) {
-            ks.load(kp + (int64_t)(j0 + KB) * a.k_t, (uint32_t)a.k_t, s.nk - j0 - KB, a.D);
-            vs.load(vp + (int64_t)(j0 + KB) * a.v_t, (uint32_t)a.v_t, s.nk - j0 - KB, a.D);
+            ks(kp + (int64_t)(j0 + KB) * a.k_t, s.nk - j0 - KB, kt[(j + 1) & 1]);
+            vs(vp + (int64_t)(j0 + KB) * a.v_t, s.nk - j0 - KB, vt[(j + 1) & 1]);
         }
-        const T *kb = kt[j & 1], *vb = vt[j & 1];
+        const char *kb = kt[j & 1], *vb = vt[j & 1];
         if (j0 <= wave_last) {
             f16 p[NT];
 #pragma unroll
@@ -92,7 +86,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma(p[t], row_frag(kb, KS, 32 * t, kChunk<T> * c), q[c]);
+                for (int t = 0; t < NT; ++t) mma(p[t], row_frag<T, DP>(kb, 32 * t, c), q[c]);
             const bool masked = j0 + KB - 1 > wave_first;
             if (masked) {
 #pragma unroll
@@ -125,7 +119,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
                 }
             // A masked key's weight is 0, but 0 times a NaN or Inf is not: where a tile that not every query sees whole
             // holds one, those values count as 0 here, and make the result NaN for the queries that do see them.
-            if (masked && flag[j & 1] == j + 1) {
+            if (masked && not_finite<T, KB, DP>(vb)) {
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
                     f16 seen = f16(0.0f);
@@ -133,7 +127,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int c = 0; c < 32 / kChunk<T>; ++c) {
-                            Frag<T> v = col_frag(vb, VS, 32 * t + kChunk<T> * c, 32 * d), bad, see;
+                            Frag<T> v = col_frag<T, DP>(vb, 32 * t + kChunk<T> * c, 32 * d), bad, see;
 #pragma unroll
                             for (int e = 0; e < kE<T>; ++e) {
                                 const int i = kE<T> * c + e;
@@ -156,14 +150,9 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
                     for (int c = 0; c < 32 / kChunk<T>; ++c) {
                         const Frag<T> pf = part_of<T>(p[t], c);
 #pragma unroll
-                        for (int d = 0; d < ND; ++d) mma(o[d], col_frag(vb, VS, 32 * t + kChunk<T> * c, 32 * d), pf);
+                        for (int d = 0; d < ND; ++d) mma(o[d], col_frag<T, DP>(vb, 32 * t + kChunk<T> * c, 32 * d), pf);
                     }
             }
-        }
-        if (j + 1 < tiles) {
-            ks.store(kt[(j + 1) & 1], KS);
-            vs.store(vt[(j + 1) & 1], VS);
-            if (j0 + 2 * KB - 1 > first_seen && vs.bad()) flag[(j + 1) & 1] = j + 2;
         }
     }
     sum += other_half(sum);
