@@ -118,12 +118,14 @@ ssm_status_t check_rows(const ssm_attn_rows_t *r, int64_t H, int64_t G, int64_t 
     } else if (!mul_ok(r->b, r->Lq, tokens_q) || !mul_ok(r->b, r->Lk, tokens_k)) {
         return SSM_ERR_SHAPE;
     }
-    int64_t nq = 0, nk = 0, wq = 0, wk = 0;
     if (*tokens_q > kMost / SSM_ATTN_MAX_D / H || *tokens_k > kMost / SSM_ATTN_MAX_D / G) return SSM_ERR_SHAPE;
-    if (!mul_ok(r->b, H, &nq) || !mul_ok(nq, ceil_div(r->Lq, 128), &wq) || !launchable(wq, ssm::kSoftmaxThreads))
-        return SSM_ERR_SHAPE;
-    if (!mul_ok(r->b, G, &nk) || !mul_ok(nk, ceil_div(r->Lk, 128), &wk) || !launchable(wk, ssm::kSoftmaxThreads))
-        return SSM_ERR_SHAPE;
+    if (r->b > kMost / H) return SSM_ERR_SHAPE;
+    const ssm::AttnRows z{nullptr, nullptr, nullptr, nullptr, r->b, r->Lq, r->Lk, 0, 0};
+    const ssm::SoftmaxWork q = ssm::softmax_fwd_work(z, H, G), k = ssm::softmax_dkv_work(z, G);
+    for (const ssm::SoftmaxWork &w : {q, k}) {
+        int64_t n = 0;
+        if (!mul_ok((w.units + 7) / 8 * 8, w.each, &n) || !launchable(n, ssm::kSoftmaxThreads)) return SSM_ERR_SHAPE;
+    }
     return SSM_OK;
 }
 

@@ -51,16 +51,15 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_stats_kernel(SoftmaxL
 // dk and dv: a workgroup takes 32 keys a wavefront of one key head, their keys and values in registers, and walks the queries that
 // see them, head by head of the group, in tiles of 32.
 template <typename T, int DP, bool VEC>
-__global__ __launch_bounds__(kSoftmaxThreads) void softmax_dkv_kernel(SoftmaxLaunch a, int blocks, int64_t tokens) {
+__global__ __launch_bounds__(kSoftmaxThreads) void softmax_dkv_kernel(SoftmaxLaunch a, SoftmaxWork work, int64_t tokens) {
     constexpr int QB = 32, NC = DP / kChunk<T>, ND = DP / 32, BK = 32 * kSoftmaxThreads / 64;
     __shared__ __attribute__((aligned(1024))) char qt[2][QB * Tile<T, DP>::kRow], dt[2][QB * Tile<T, DP>::kRow];
     __shared__ __attribute__((aligned(16))) float lse_t[2][QB], delta_t[2][QB];
 
-    int64_t id = la::work_index(blockIdx.x, gridDim.x);
-    const int kb = (int)(id % blocks);  // the first keys, which most queries see, go first
-    id /= blocks;
-    const int g = (int)(id % a.G), R = a.H / a.G;
-    const int64_t is = id / a.G;
+    SoftmaxPlace at;
+    if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
+    const int64_t is = at.seq;
+    const int g = at.g, R = a.H / a.G, kb = at.block;  // the first keys, which most queries see, first
     const AttnSeq s = sequence(a.rows, is);
     const bool packed = a.rows.cu_q != nullptr;
     const int w = la::wave_id(), l = threadIdx.x & 63, col = l & 31, half = l >> 5;
@@ -162,15 +161,14 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_dkv_kernel(SoftmaxLau
 // dq: a workgroup takes 32 queries a wavefront of one head, with their gradients in registers, and walks the keys that they
 // see in tiles of 32.
 template <typename T, int DP, bool VEC>
-__global__ __launch_bounds__(kSoftmaxThreads) void softmax_dq_kernel(SoftmaxLaunch a, int blocks, int64_t tokens) {
+__global__ __launch_bounds__(kSoftmaxThreads) void softmax_dq_kernel(SoftmaxLaunch a, SoftmaxWork work, int64_t tokens) {
     constexpr int KB = 32, NC = DP / kChunk<T>, ND = DP / 32, BQ = 32 * kSoftmaxThreads / 64;
     __shared__ __attribute__((aligned(1024))) char kt[2][KB * Tile<T, DP>::kRow], vt[2][KB * Tile<T, DP>::kRow];
 
-    int64_t id = la::work_index(blockIdx.x, gridDim.x);
-    const int qb = blocks - 1 - (int)(id % blocks);
-    id /= blocks;
-    const int h = (int)(id % a.H), g = h / (a.H / a.G);
-    const int64_t is = id / a.H;
+    SoftmaxPlace at;
+    if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
+    const int64_t is = at.seq;
+    const int g = at.g, h = g * work.per + at.which, qb = work.blocks - 1 - at.block;
     const AttnSeq s = sequence(a.rows, is);
     const bool packed = a.rows.cu_q != nullptr;
     const int w = la::wave_id(), l = threadIdx.x & 63, col = l & 31, half = l >> 5;
@@ -255,21 +253,20 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_dq_kernel(SoftmaxLaun
 
 template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, hipStream_t stream) {
     const int64_t tokens = p.rows.cu_q ? p.rows.Tq : p.rows.b * p.rows.Lq;
-    const int bk = softmax_dkv_block(p), bq = softmax_dq_block(p);
-    const int64_t kblocks = (p.rows.Lk + bk - 1) / bk, qblocks = (p.rows.Lq + bq - 1) / bq;
+    const SoftmaxWork kw = softmax_dkv_work(p.rows, p.G), qw = softmax_dq_work(p.rows, p.H, p.G);
     constexpr int64_t per = kSoftmaxThreads / kStatsLanes;
     if (tokens > 0) {
         softmax_stats_kernel<T, VEC><<<dim3((unsigned)((tokens * p.H + per - 1) / per)), kSoftmaxThreads, 0, stream>>>(p, tokens);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    if (kblocks > 0) {
+    if (kw.blocks > 0) {
         softmax_dkv_kernel<T, DP, VEC>
-            <<<dim3((unsigned)(p.rows.b * p.G * kblocks)), kSoftmaxThreads, 0, stream>>>(p, (int)kblocks, tokens);
+            <<<dim3((unsigned)softmax_groups(kw)), kSoftmaxThreads, 0, stream>>>(p, kw, tokens);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    if (qblocks > 0)
+    if (qw.blocks > 0)
         softmax_dq_kernel<T, DP, VEC>
-            <<<dim3((unsigned)(p.rows.b * p.H * qblocks)), kSoftmaxThreads, 0, stream>>>(p, (int)qblocks, tokens);
+            <<<dim3((unsigned)softmax_groups(qw)), kSoftmaxThreads, 0, stream>>>(p, qw, tokens);
     return hipGetLastError();
 }
 template <typename T> hipError_t by_width(const SoftmaxLaunch &p, hipStream_t stream) {
@@ -282,9 +279,6 @@ template <typename T> hipError_t by_width(const SoftmaxLaunch &p, hipStream_t st
 
 }  // namespace
 }  // namespace sm
-
-int softmax_dq_block(const SoftmaxLaunch &) { return 32 * kSoftmaxThreads / 64; }
-int softmax_dkv_block(const SoftmaxLaunch &) { return 32 * kSoftmaxThreads / 64; }
 
 hipError_t launch_softmax_bwd(const SoftmaxLaunch &p, hipStream_t stream) {
     return p.bf16 ? sm::by_width<uint16_t>(p, stream) : sm::by_width<float>(p, stream);

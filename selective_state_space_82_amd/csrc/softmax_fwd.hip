@@ -17,18 +17,15 @@ template <typename T> constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;
 constexpr float kSlack = 8.0f;
 
 template <typename T, int DP, bool VEC>
-__global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(SoftmaxLaunch a, int blocks) {
+__global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(SoftmaxLaunch a, SoftmaxWork work) {
     constexpr int KB = kKeys<T>, NT = KB / 32, NC = DP / kChunk<T>, ND = DP / 32, BQ = 32 * kSoftmaxThreads / 64;
     constexpr int kTileBytes = KB * Tile<T, DP>::kRow;
     __shared__ __attribute__((aligned(1024))) char kt[2][kTileBytes], vt[2][kTileBytes];
 
-    // work: sequence, then key head, then the heads that share it, then blocks of queries, the longest first
-    int64_t id = la::work_index(blockIdx.x, gridDim.x);
-    const int qb = blocks - 1 - (int)(id % blocks);
-    id /= blocks;
-    const int h = (int)(id % a.H);
-    const int64_t is = id / a.H;
-    const int g = h / (a.H / a.G);
+    SoftmaxPlace at;
+    if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
+    const int64_t is = at.seq;
+    const int g = at.g, h = g * work.per + at.which, qb = work.blocks - 1 - at.block;  // the last queries, which see most, first
     const AttnSeq s = sequence(a.rows, is);
     const bool packed = a.rows.cu_q != nullptr;
     const int w = la::wave_id(), l = threadIdx.x & 63, col = l & 31, half = l >> 5;
@@ -175,8 +172,8 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
 }
 
 template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, hipStream_t stream) {
-    const int64_t blocks = (p.rows.Lq + softmax_fwd_block(p) - 1) / softmax_fwd_block(p);
-    softmax_fwd_kernel<T, DP, VEC><<<dim3((unsigned)(p.rows.b * p.H * blocks)), kSoftmaxThreads, 0, stream>>>(p, (int)blocks);
+    const SoftmaxWork w = softmax_fwd_work(p.rows, p.H, p.G);
+    softmax_fwd_kernel<T, DP, VEC><<<dim3((unsigned)softmax_groups(w)), kSoftmaxThreads, 0, stream>>>(p, w);
     return hipGetLastError();
 }
 template <typename T> hipError_t by_width(const SoftmaxLaunch &p, hipStream_t stream) {
@@ -189,8 +186,6 @@ template <typename T> hipError_t by_width(const SoftmaxLaunch &p, hipStream_t st
 
 }  // namespace
 }  // namespace sm
-
-int softmax_fwd_block(const SoftmaxLaunch &) { return 32 * kSoftmaxThreads / 64; }
 
 hipError_t launch_softmax_fwd(const SoftmaxLaunch &p, hipStream_t stream) {
     return p.bf16 ? sm::by_width<uint16_t>(p, stream) : sm::by_width<float>(p, stream);

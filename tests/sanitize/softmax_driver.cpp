@@ -12,7 +12,6 @@ int g_launches = 0;
 SoftmaxLaunch g_last;
 SoftmaxStepLaunch g_step;
 KvAppendLaunch g_append;
-int softmax_fwd_block(const SoftmaxLaunch &) { return 128; }
 hipError_t launch_softmax_fwd(const SoftmaxLaunch &p, hipStream_t) { ++g_launches; g_last = p; return hipSuccess; }
 hipError_t launch_softmax_bwd(const SoftmaxLaunch &p, hipStream_t) { ++g_launches; g_last = p; return hipSuccess; }
 hipError_t launch_softmax_step(const SoftmaxStepLaunch &p, hipStream_t) { ++g_launches; g_step = p; return hipSuccess; }
@@ -100,6 +99,28 @@ static void tokens() {
     CHECK(locate({nullptr, nullptr, 9, 1, 9}, 7, &row, &index, &count) && row == 7 && index == 0 && count == 1);
 }
 
+// Every block of every sequence and head is some workgroup's, once, and a sequence's work is spread over the XCDs.
+static void places() {
+    using namespace ssm;
+    for (const int64_t b : {1, 2, 5})
+        for (const int64_t G : {1, 3, 7, 8, 12})
+            for (const int64_t per : {1, 4})
+                for (const int64_t blocks : {0, 1, 2, 5, 16, 33}) {
+                    const SoftmaxWork w = softmax_work(b, G, per, blocks);
+                    std::vector<int> seen((size_t)(b * G * per * blocks), 0), of(8, 0);
+                    for (int64_t id = 0; id < softmax_groups(w); ++id) {
+                        SoftmaxPlace p;
+                        if (!softmax_place(w, G, id, &p)) continue;
+                        CHECK(p.seq >= 0 && p.seq < b && p.g >= 0 && p.g < G && p.which < per && p.block >= 0 && p.block < blocks);
+                        ++seen[(size_t)(((p.seq * G + p.g) * per + p.which) * blocks + p.block)];
+                        if (p.seq == 0) ++of[(size_t)(id & 7)];
+                    }
+                    for (const int n : seen) CHECK(n == 1);
+                    if (blocks >= 8)
+                        for (const int n : of) CHECK(n > 0);
+                }
+}
+
 static void host_code() {
     using namespace ssm;
     alignas(16) static char mem[64][4096];
@@ -150,6 +171,7 @@ int main() {
     sequences();
     pages();
     tokens();
+    places();
     host_code();
     if (failures == 0) std::printf("all host paths behaved\n");
     return failures != 0;
