@@ -12,6 +12,8 @@ namespace ssm {
 namespace sm {
 namespace {
 
+// Tiles of 32 keys that a wavefront takes.
+template <typename T, int DP> constexpr int kKeyTiles = sizeof(T) == 2 ? 1 : 1;
 constexpr int kStatsLanes = 16;  // lanes to a query's row
 
 // stats[h][query] = {lse·log2 e, do·o}; a query that saw no key (lse = −inf) gets +inf, that is, weights of 0.
@@ -48,11 +50,11 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_stats_kernel(SoftmaxL
     }
 }
 
-// dk and dv: a workgroup takes 32 keys a wavefront of one key head, their keys and values in registers, and walks the queries that
-// see them, head by head of the group, in tiles of 32.
-template <typename T, int DP, bool VEC>
-__global__ __launch_bounds__(kSoftmaxThreads) void softmax_dkv_kernel(SoftmaxLaunch a, SoftmaxWork work, int64_t tokens) {
-    constexpr int QB = 32, NC = DP / kChunk<T>, ND = DP / 32, BK = 32 * kSoftmaxThreads / 64;
+// dk and dv: a workgroup takes KT·32 keys a wavefront of one key head, their keys and values in registers, and walks the queries
+// that see them, head by head of the group, in tiles of 32.
+template <typename T, int DP, int KT, bool VEC>
+__global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_dkv_kernel(SoftmaxLaunch a, SoftmaxWork work, int64_t tokens) {
+    constexpr int QB = 32, NC = DP / kChunk<T>, ND = DP / 32, KW = 32 * KT, BK = KW * kSoftmaxThreads / 64;
     __shared__ __attribute__((aligned(1024))) char qt[2][QB * Tile<T, DP>::kRow], dt[2][QB * Tile<T, DP>::kRow];
     __shared__ __attribute__((aligned(16))) float lse_t[2][QB], delta_t[2][QB];
 
@@ -63,26 +65,29 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_dkv_kernel(SoftmaxLau
     const AttnSeq s = sequence(a.rows, is);
     const bool packed = a.rows.cu_q != nullptr;
     const int w = la::wave_id(), l = threadIdx.x & 63, col = l & 31, half = l >> 5;
-    const int k0 = kb * BK, r0 = k0 + 32 * w, key = r0 + col;
+    const int k0 = kb * BK, r0 = k0 + KW * w;
     const int to_write = packed ? s.nk : (int)a.rows.Lk;
     if (k0 >= to_write) return;
 
-    const T *kp = static_cast<const T *>(a.k) + is * a.k_b + (s.k0 + r0) * a.k_t + g * a.k_h;
-    const T *vp = static_cast<const T *>(a.v) + is * a.v_b + (s.k0 + r0) * a.v_t + g * a.v_h;
-    Frag<T> k[NC], v[NC];
-    {
-        const int rows = s.nk - r0 > 32 ? 32 : s.nk - r0;
-        load_frags<T, DP, VEC>(k, la::rows_buffer(kp, (uint32_t)a.k_t, rows, a.D), (uint32_t)a.k_t, col, rows, a.D);
-        load_frags<T, DP, VEC>(v, la::rows_buffer(vp, (uint32_t)a.v_t, rows, a.D), (uint32_t)a.v_t, col, rows, a.D);
+    Frag<T> k[KT][NC], v[KT][NC];
+#pragma unroll
+    for (int u = 0; u < KT; ++u) {
+        const int r = r0 + 32 * u, rows = s.nk - r > 32 ? 32 : s.nk - r;
+        const T *kp = static_cast<const T *>(a.k) + is * a.k_b + (s.k0 + r) * a.k_t + g * a.k_h;
+        const T *vp = static_cast<const T *>(a.v) + is * a.v_b + (s.k0 + r) * a.v_t + g * a.v_h;
+        load_frags<T, DP, VEC>(k[u], la::rows_buffer(kp, (uint32_t)a.k_t, rows, a.D), (uint32_t)a.k_t, col, rows, a.D);
+        load_frags<T, DP, VEC>(v[u], la::rows_buffer(vp, (uint32_t)a.v_t, rows, a.D), (uint32_t)a.v_t, col, rows, a.D);
     }
     const int first = k0 < s.nk ? first_query(s, a.causal, k0) / QB : 0;
     const int tiles = k0 < s.nk ? (s.nq + QB - 1) / QB - first : 0;  // a head
     const int off = s.nk - s.nq;
     const float sc = a.scale * kLog2e;
 
-    f16 dk[ND], dv[ND];
+    f16 dk[KT][ND], dv[KT][ND];
 #pragma unroll
-    for (int d = 0; d < ND; ++d) dk[d] = dv[d] = f16(0.0f);
+    for (int u = 0; u < KT; ++u)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) dk[u][d] = dv[u][d] = f16(0.0f);
 
     const Loader<T, QB, DP, VEC> qs((uint32_t)a.q_t, a.D), ds((uint32_t)a.do_t, a.D);
     const auto fetch = [&](int r, int tile, int b) {
@@ -108,60 +113,83 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_dkv_kernel(SoftmaxLau
             ++r;
         }
         if (r < R) fetch(r, tile, b ^ 1);
-        if (r0 < s.nk && (!a.causal || r0 <= i0 + QB - 1 + off)) {
-            f16 p = f16(0.0f), dp = f16(0.0f);
+        if (r0 >= s.nk || (a.causal && r0 > i0 + QB - 1 + off)) continue;
+        f16 p[KT], dp[KT];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                mma(p, row_frag<T, DP>(qt[b], 0, c), k[c]);
-                mma(dp, row_frag<T, DP>(dt[b], 0, c), v[c]);
+        for (int u = 0; u < KT; ++u) p[u] = dp[u] = f16(0.0f);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const Frag<T> qf = row_frag<T, DP>(qt[b], 0, c), df = row_frag<T, DP>(dt[b], 0, c);
+#pragma unroll
+            for (int u = 0; u < KT; ++u) {
+                mma(p[u], qf, k[u][c]);
+                mma(dp[u], df, v[u][c]);
             }
-            const bool masked = i0 + QB > s.nq || r0 + 32 > s.nk || (a.causal && r0 + 31 > i0 + off);
+        }
+        const bool masked = i0 + QB > s.nq || r0 + KW > s.nk || (a.causal && r0 + KW - 1 > i0 + off);
+#pragma unroll
+        for (int u = 0; u < KT; ++u) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const f4 lse = *reinterpret_cast<const f4 *>(&lse_t[b][8 * j + 4 * half]);
                 const f4 delta = *reinterpret_cast<const f4 *>(&delta_t[b][8 * j + 4 * half]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    p[4 * j + e] = exp2_fast(__builtin_fmaf(p[4 * j + e], sc, -lse[e]));
-                    dp[4 * j + e] = p[4 * j + e] * (dp[4 * j + e] - delta[e]);
+                    p[u][4 * j + e] = exp2_fast(__builtin_fmaf(p[u][4 * j + e], sc, -lse[e]));
+                    dp[u][4 * j + e] = p[u][4 * j + e] * (dp[u][4 * j + e] - delta[e]);
                 }
             }
             if (masked) {
+                const int key = r0 + 32 * u + col;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int row = i0 + 8 * (i >> 2) + 4 * half + (i & 3);
-                    if (row >= s.nq || key >= s.nk || (a.causal && key > row + off)) p[i] = dp[i] = 0.0f;
+                    if (row >= s.nq || key >= s.nk || (a.causal && key > row + off)) p[u][i] = dp[u][i] = 0.0f;
                 }
             }
+        }
 #pragma unroll
-            for (int c = 0; c < 32 / kChunk<T>; ++c) {
-                const Frag<T> pf = part_of<T>(p, c), df = part_of<T>(dp, c);
+        for (int c = 0; c < 32 / kChunk<T>; ++c) {
+            Frag<T> pf[KT];
+            Split<T> df[KT];
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    mma(dv[d], col_frag<T, DP>(dt[b], kChunk<T> * c, 32 * d), pf);
-                    mma(dk[d], col_frag<T, DP>(qt[b], kChunk<T> * c, 32 * d), df);
+            for (int u = 0; u < KT; ++u) {
+                pf[u] = part_of<T>(p[u], c);
+                df[u] = Split<T>(dp[u], c);
+            }
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const Frag<T> of = col_frag<T, DP>(dt[b], kChunk<T> * c, 32 * d), qf = col_frag<T, DP>(qt[b], kChunk<T> * c, 32 * d);
+#pragma unroll
+                for (int u = 0; u < KT; ++u) {
+                    mma(dv[u][d], of, pf[u]);
+                    mma<T>(dk[u][d], qf, df[u]);
                 }
             }
         }
     }
 
     const int64_t row = (packed ? s.k0 : is * a.rows.Lk) + r0;
-    const int rows = to_write - r0 > 32 ? 32 : to_write - r0;
     const uint32_t stride = (uint32_t)(a.G * a.D);
-    const Buffer kout = la::rows_buffer(static_cast<T *>(a.dk) + (row * a.G + g) * a.D, stride, rows, a.D);
-    const Buffer vout = la::rows_buffer(static_cast<T *>(a.dv) + (row * a.G + g) * a.D, stride, rows, a.D);
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-        if (key >= s.nk) dk[d] = dv[d] = f16(0.0f);
-        store_tile<T, VEC>(kout, stride, col, 32 * d, col < rows ? a.D : 0, dk[d], a.scale);
-        store_tile<T, VEC>(vout, stride, col, 32 * d, col < rows ? a.D : 0, dv[d], 1.0f);
+    for (int u = 0; u < KT; ++u) {
+        const int r = r0 + 32 * u, rows = to_write - r > 32 ? 32 : to_write - r;
+        const int64_t first_out = ((row + 32 * u) * a.G + g) * a.D;
+        const Buffer kout = la::rows_buffer(static_cast<T *>(a.dk) + first_out, stride, rows, a.D);
+        const Buffer vout = la::rows_buffer(static_cast<T *>(a.dv) + first_out, stride, rows, a.D);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            if (r + col >= s.nk) dk[u][d] = dv[u][d] = f16(0.0f);
+            store_tile<T, VEC>(kout, stride, col, 32 * d, col < rows ? a.D : 0, dk[u][d], a.scale);
+            store_tile<T, VEC>(vout, stride, col, 32 * d, col < rows ? a.D : 0, dv[u][d], 1.0f);
+        }
     }
 }
 
 // dq: a workgroup takes 32 queries a wavefront of one head, with their gradients in registers, and walks the keys that they
 // see in tiles of 32.
 template <typename T, int DP, bool VEC>
-__global__ __launch_bounds__(kSoftmaxThreads) void softmax_dq_kernel(SoftmaxLaunch a, SoftmaxWork work, int64_t tokens) {
+__global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_dq_kernel(SoftmaxLaunch a, SoftmaxWork work, int64_t tokens) {
     constexpr int KB = 32, NC = DP / kChunk<T>, ND = DP / 32, BQ = 32 * kSoftmaxThreads / 64;
     __shared__ __attribute__((aligned(1024))) char kt[2][KB * Tile<T, DP>::kRow], vt[2][KB * Tile<T, DP>::kRow];
 
@@ -235,9 +263,9 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_dq_kernel(SoftmaxLaun
             }
 #pragma unroll
             for (int c = 0; c < 32 / kChunk<T>; ++c) {
-                const Frag<T> df = part_of<T>(dp, c);
+                const Split<T> df(dp, c);
 #pragma unroll
-                for (int d = 0; d < ND; ++d) mma(dq[d], col_frag<T, DP>(kt[b], kChunk<T> * c, 32 * d), df);
+                for (int d = 0; d < ND; ++d) mma<T>(dq[d], col_frag<T, DP>(kt[b], kChunk<T> * c, 32 * d), df);
             }
         }
     }
@@ -260,7 +288,7 @@ template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, h
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     if (kw.blocks > 0) {
-        softmax_dkv_kernel<T, DP, VEC>
+        softmax_dkv_kernel<T, DP, kKeyTiles<T, DP>, VEC>
             <<<dim3((unsigned)softmax_groups(kw)), kSoftmaxThreads, 0, stream>>>(p, kw, tokens);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }

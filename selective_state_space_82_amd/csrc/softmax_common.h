@@ -99,6 +99,24 @@ template <typename T> __device__ __forceinline__ Frag<T> part_of(const f16 &x, i
     }
 }
 
+// The same in two parts for bf16, the second the rounded remainder of the first: 2^-16.
+template <typename T> struct Split {
+    Frag<T> p, rest;
+    Split() = default;
+    __device__ __forceinline__ Split(const f16 &x, int c) : p(part_of<T>(x, c)) {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) rest[j] = (__bf16)(x[8 * c + j] - (float)p[j]);
+        }
+    }
+};
+template <typename T> __device__ __forceinline__ void mma(f16 &acc, const Frag<T> &a, const Split<T> &b);
+template <> __device__ __forceinline__ void mma<uint16_t>(f16 &acc, const bf8 &a, const Split<uint16_t> &b) {
+    mma(acc, a, b.p);
+    mma(acc, a, b.rest);
+}
+template <> __device__ __forceinline__ void mma<float>(f16 &acc, const f4 &a, const Split<float> &b) { mma(acc, a, b.p); }
+
 // A row of a strided matrix in memory as fragments in registers: row `row0 + col` (zeros from row `rows` on, columns from
 // `cols` on), all DP columns.
 template <typename T, int DP, bool VEC>
