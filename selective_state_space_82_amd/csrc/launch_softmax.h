@@ -33,7 +33,7 @@ constexpr int kSoftmaxThreads = 256;
 struct SoftmaxWork {
     int64_t units, each;  // each: workgroups of a unit
     int parts, per, blocks;
-};
+};  // workgroups number less than 2^24
 inline SoftmaxWork softmax_work(int64_t b, int64_t G, int64_t per, int64_t blocks) {
     const int64_t parts = G >= 8 || blocks < 2 ? 1 : ((8 + G - 1) / G < blocks ? (8 + G - 1) / G : blocks);
     return {b * G * parts, per * ((blocks + parts - 1) / parts), (int)parts, (int)per, (int)blocks};
@@ -44,15 +44,14 @@ struct SoftmaxPlace {
     int64_t seq;
     int g, which, block;
 };
-SSM_BOTH bool softmax_place(const SoftmaxWork &w, int64_t G, int64_t id, SoftmaxPlace *p) {
-    const int64_t turn = id >> 3, unit = turn / w.each * 8 + (id & 7);
-    const int at = (int)(turn % w.each), part = (int)(unit % w.parts);
-    const int64_t head = unit / w.parts;
-    p->seq = head / G;
-    p->g = (int)(head % G);
-    p->which = at % w.per;
-    p->block = at / w.per * w.parts + part;
-    return unit < w.units && p->block < w.blocks;
+SSM_BOTH bool softmax_place(const SoftmaxWork &w, int64_t G, uint32_t id, SoftmaxPlace *p) {
+    const uint32_t turn = id >> 3, each = (uint32_t)w.each, unit = turn / each * 8 + (id & 7), at = turn % each;
+    const uint32_t head = unit / (uint32_t)w.parts, part = unit % (uint32_t)w.parts;
+    p->seq = head / (uint32_t)G;
+    p->g = (int)(head % (uint32_t)G);
+    p->which = (int)(at % (uint32_t)w.per);
+    p->block = (int)(at / (uint32_t)w.per * (uint32_t)w.parts + part);
+    return unit < (uint32_t)w.units && p->block < w.blocks;
 }
 // The forward kernel and the gradient's for the queries take 128 queries to a workgroup, the gradient's for the keys 128 keys.
 constexpr int kSoftmaxBlock = 128;

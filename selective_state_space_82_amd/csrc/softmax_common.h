@@ -145,33 +145,21 @@ __device__ __forceinline__ void load_frags(Frag<T> (&f)[DP / kChunk<T>], const B
     }
 }
 
-// Whether ROWS rows of a tile hold a NaN or Inf in their first W columns; the same in every lane.
-template <typename T, int ROWS, int W> __device__ __forceinline__ bool not_finite(const char *tile) {
-    bool bad = false;
-    constexpr int N = ROWS * Tile<T, W>::kPer / 64;
-    static_assert(ROWS * Tile<T, W>::kPer % 64 == 0, "");
-    if constexpr (sizeof(T) == 2) {
-        typedef unsigned short us2 __attribute__((ext_vector_type(2)));
-        us2 most = us2(0);
+// Whether the thread's share of a tile of ROWS rows holds a NaN or Inf.
+template <typename T, int ROWS, int W> __device__ __forceinline__ bool share_not_finite(const char *tile) {
+    constexpr int PIECES = ROWS * Tile<T, W>::kPer;
+    typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+    us2 most = us2(0);  // the upper 16 bits say it for fp32 as well
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const u4 w = *reinterpret_cast<const u4 *>(tile + 16 * (64 * j + (threadIdx.x & 63)));
+    for (int j = 0; j < (PIECES + kSoftmaxThreads - 1) / kSoftmaxThreads; ++j) {
+        const int id = (int)threadIdx.x + j * kSoftmaxThreads;
+        if (PIECES < kSoftmaxThreads && id >= PIECES) break;
+        const u4 w = *reinterpret_cast<const u4 *>(tile + 16 * id);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                most = __builtin_elementwise_max(most, __builtin_bit_cast(us2, w[i] & 0x7fff7fffu));
-        }
-        bad = most[0] >= 0x7f80 || most[1] >= 0x7f80;
-    } else {
-        uint32_t most = 0;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const u4 w = *reinterpret_cast<const u4 *>(tile + 16 * (64 * j + (threadIdx.x & 63)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) most = most > (w[i] & 0x7fffffffu) ? most : (w[i] & 0x7fffffffu);
-        }
-        bad = most >= 0x7f800000u;
+        for (int i = 0; i < 4; ++i)
+            most = __builtin_elementwise_max(most, __builtin_bit_cast(us2, w[i] & (sizeof(T) == 2 ? 0x7fff7fffu : 0x7fff0000u)));
     }
-    return __any(bad);
+    return most[0] >= 0x7f80 || most[1] >= 0x7f80;
 }
 
 // ROWS rows × W columns of a strided matrix into an LDS tile, by a workgroup; zeros past the rows and columns there are.
@@ -183,13 +171,15 @@ template <typename T, int ROWS, int W, bool VEC> struct Loader {
     using X = Tile<T, W>;
     static constexpr int E = kE<T>, PIECES = ROWS * X::kPer, N = (PIECES + kSoftmaxThreads - 1) / kSoftmaxThreads;
     static_assert(PIECES % kSoftmaxThreads == 0 || (PIECES < kSoftmaxThreads && PIECES % 64 == 0), "whole instructions");
-    uint32_t at[VEC ? N : 1];  // of the lane's pieces, in bytes from row 0
+    // A workgroup's threads cover kStep rows at a time. Where a row's turn repeats after as many, one offset serves all pieces.
+    static constexpr int kStep = kSoftmaxThreads / X::kPer, kOffsets = kStep % 16 == 0 ? 1 : N;
+    uint32_t at[VEC ? kOffsets : 1];  // of the lane's pieces, in bytes from row 0
     uint32_t stride;
     int cols;
     __device__ __forceinline__ Loader(uint32_t stride_, int cols_) : stride(stride_), cols(cols_) {
         if constexpr (VEC) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
+            for (int j = 0; j < kOffsets; ++j) {
                 const int id = (int)threadIdx.x + j * kSoftmaxThreads, r = id / X::kPer, c = (id % X::kPer ^ X::turn(r)) * E;
                 at[j] = c < cols ? (r * stride + c) * (uint32_t)sizeof(T) : kOutside;
             }
@@ -208,9 +198,10 @@ template <typename T, int ROWS, int W, bool VEC> struct Loader {
             const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)tile + la::wave_id() * 1024;
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                              :
-                             : "s"(lds + j * kSoftmaxThreads * 16), "v"(at[j]), "s"(buf)
+                             : "s"(lds + j * kSoftmaxThreads * 16), "v"(at[kOffsets == 1 ? 0 : j]), "s"(buf),
+                               "s"(kOffsets == 1 ? j * kStep * stride * (uint32_t)sizeof(T) : 0u)
                              : "memory");
         } else {
             const Buffer buf = la::buffer_of(first, bytes);

@@ -21,6 +21,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
     constexpr int KB = kKeys<T>, NT = KB / 32, NC = DP / kChunk<T>, ND = DP / 32, BQ = 32 * kSoftmaxThreads / 64;
     constexpr int kTileBytes = KB * Tile<T, DP>::kRow;
     __shared__ __attribute__((aligned(1024))) char kt[2][kTileBytes], vt[2][kTileBytes];
+    __shared__ int found;  // a NaN or Inf among the values of a tile that not every query sees whole
 
     SoftmaxPlace at;
     if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
@@ -37,12 +38,11 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
     const T *kp = static_cast<const T *>(a.k) + is * a.k_b + s.k0 * a.k_t + g * a.k_h;
     const T *vp = static_cast<const T *>(a.v) + is * a.v_b + s.k0 * a.v_t + g * a.v_h;
 
-    // tiles up to the last key that the block's last query sees
+    // tiles up to the last key that the block's last query sees; of the first `full` every query sees every key
     const int last_q = (q0 + BQ < s.nq ? q0 + BQ : s.nq) - 1;
     const int keys = last_q >= q0 ? last_key(s, a.causal, last_q) + 1 : 0;
-    const int tiles = (keys + KB - 1) / KB;
-    const int my_last = last_key(s, a.causal, r0 + col);                     // of the lane's query
-    const int wave_first = last_key(s, a.causal, r0);
+    const int tiles = (keys + KB - 1) / KB, full = keys > 0 ? (last_key(s, a.causal, q0) + 1) / KB : 0;
+    const int my_last = last_key(s, a.causal, r0 + col);  // of the lane's query
     const int wave_last = r0 < s.nq ? last_key(s, a.causal, (r0 + 32 < s.nq ? r0 + 32 : s.nq) - 1) : -1;
 
     Frag<T> q[NC];
@@ -63,92 +63,138 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
     float m = -INFINITY, sum = 0.0f;  // sum: over the lane's half of the keys
 
     const Loader<T, KB, DP, VEC> ks((uint32_t)a.k_t, a.D), vs((uint32_t)a.v_t, a.D);
-    if (tiles > 0) {
-        ks(kp, s.nk, kt[0]);
-        vs(vp, s.nk, vt[0]);
-    }
-    for (int j = 0; j < tiles; ++j) {
-        const int j0 = j * KB;
+    // Past the last tile nothing is read: the buffer has no rows then, and zeros land in a place that nobody looks at.
+    const auto load_k = [&](int j, int b) { ks(kp + (int64_t)j * KB * a.k_t, s.nk - j * KB, kt[b]); };
+    const auto load_v = [&](int j, int b) { vs(vp + (int64_t)j * KB * a.v_t, s.nk - j * KB, vt[b]); };
+    const auto scores = [&](f16(&p)[NT], int b) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) p[t] = f16(0.0f);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma(p[t], row_frag<T, DP>(kt[b], 32 * t, c), q[c]);
+    };
+    // Hides the keys of tile j that a query does not see, and, if `now`, raises the maximum where tile j's scores ask for it.
+    const auto prepare = [&](f16(&p)[NT], int j, bool now, auto masked) {
+        if constexpr (masked) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (j * KB + 32 * t + 8 * (i >> 2) + 4 * half + (i & 3) > my_last) p[t][i] = -INFINITY;
+        }
+        float top = p[0][0];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, p[t][i]);
+        top = __builtin_fmaxf(top, other_half(top)) * sc;
+        const bool raise = now && (top > m + kSlack || (m == -INFINITY && top > m));  // each query by itself: its bits are its own
+        if (__any(raise)) {
+            const float f = raise ? exp2_fast(m - top) : 1.0f;
+            m = raise ? top : m;
+            sum *= f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[d] *= f;
+        }
+    };
+    const auto weigh = [&](f16(&p)[NT]) {
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                p[t][i] = exp2_fast(__builtin_fmaf(p[t][i], sc, -base));
+                sum += p[t][i];
+            }
+    };
+    // Adds what tile j's scores p say, with its values in buffer b, and forms tile j + 1's scores meanwhile.
+    const auto step = [&](int j, int b, f16(&p)[NT], f16(&next)[NT], auto masked) {
         landed();
         la::lds_barrier();
-        if (j + 1 < tiles) {
-            ks(kp + (int64_t)(j0 + KB) * a.k_t, s.nk - j0 - KB, kt[(j + 1) & 1]);
-            vs(vp + (int64_t)(j0 + KB) * a.v_t, s.nk - j0 - KB, vt[(j + 1) & 1]);
+        load_k(j + 2, b);
+        load_v(j + 1, b ^ 1);
+        const char *vb = vt[b];
+        if constexpr (masked) {
+            if (share_not_finite<T, KB, DP>(vb)) found = 1;
+            if (j * KB > wave_last) return;
         }
-        const char *kb = kt[j & 1], *vb = vt[j & 1];
-        if (j0 <= wave_last) {
+        scores(next, b ^ 1);
+        weigh(p);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c = 0; c < 32 / kChunk<T>; ++c) {
+                const Frag<T> pf = part_of<T>(p[t], c);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) mma(o[d], col_frag<T, DP>(vb, 32 * t + kChunk<T> * c, 32 * d), pf);
+            }
+    };
+    if (threadIdx.x == 0) found = 0;
+    if (tiles > 0) {
+        load_k(0, 0);
+        load_v(0, 0);
+        load_k(1, 1);
+        landed();
+        la::lds_barrier();
+        f16 p[NT], next[NT];
+        scores(p, 0);
+        int j = 0;
+        prepare(p, 0, full > 1, std::false_type());
+        for (; j + 1 < full; j += 2) {
+            step(j, 0, p, next, std::false_type());
+            prepare(next, j + 1, true, std::false_type());
+            step(j + 1, 1, next, p, std::false_type());
+            prepare(p, j + 2, j + 3 < full, std::false_type());  // the tiles from there on are prepared with their masks
+        }
+        for (; j < tiles; ++j) {
+            prepare(p, j, true, std::true_type());
+            step(j, j & 1, p, next, std::true_type());
+#pragma unroll
+            for (int t = 0; t < NT; ++t) p[t] = next[t];
+        }
+        landed();  // the loads past the last tile, before LDS is written again or given up
+        la::lds_barrier();
+    }
+    // A masked key's weight is 0, but 0 times a NaN or Inf is not. Where there is one the block is done again, one tile after
+    // the other, so that such values count as 0 in the product and make the result NaN for the queries that do see them.
+    if (found) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d] = f16(0.0f);
+        m = -INFINITY;
+        sum = 0.0f;
+        for (int j = 0; j < tiles; ++j) {
+            la::lds_barrier();
+            load_k(j, 0);
+            load_v(j, 0);
+            landed();
+            la::lds_barrier();
             f16 p[NT];
+            scores(p, 0);
+            prepare(p, j, true, std::true_type());
+            weigh(p);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) p[t] = f16(0.0f);
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                for (int t = 0; t < NT; ++t) mma(p[t], row_frag<T, DP>(kb, 32 * t, c), q[c]);
-            const bool masked = j0 + KB - 1 > wave_first;
-            if (masked) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (j0 + 32 * t + 8 * (i >> 2) + 4 * half + (i & 3) > my_last) p[t][i] = -INFINITY;
-            }
-            float top = p[0][0];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, p[t][i]);
-            top = __builtin_fmaxf(top, other_half(top)) * sc;
-            const bool raise = top > m + kSlack || (m == -INFINITY && top > m);  // each query by itself: its bits are its own
-            if (__any(raise)) {
-                const float f = raise ? exp2_fast(m - top) : 1.0f;
-                m = raise ? top : m;
-                sum *= f;
-#pragma unroll
-                for (int d = 0; d < ND; ++d) o[d] *= f;
-            }
-            const float base = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    p[t][i] = exp2_fast(__builtin_fmaf(p[t][i], sc, -base));
-                    sum += p[t][i];
-                }
-            // A masked key's weight is 0, but 0 times a NaN or Inf is not: where a tile that not every query sees whole
-            // holds one, those values count as 0 here, and make the result NaN for the queries that do see them.
-            if (masked && not_finite<T, KB, DP>(vb)) {
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    f16 seen = f16(0.0f);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int c = 0; c < 32 / kChunk<T>; ++c) {
-                            Frag<T> v = col_frag<T, DP>(vb, 32 * t + kChunk<T> * c, 32 * d), bad, see;
-#pragma unroll
-                            for (int e = 0; e < kE<T>; ++e) {
-                                const int i = kE<T> * c + e;
-                                const bool nf = !__builtin_isfinite((float)v[e]);
-                                bad[e] = nf ? 1.0f : 0.0f;
-                                if (nf) v[e] = 0.0f;
-                                see[e] = j0 + 32 * t + 8 * (i >> 2) + 4 * half + (i & 3) > my_last ? 0.0f : 1.0f;
-                            }
-                            mma(o[d], v, part_of<T>(p[t], c));
-                            mma(seen, bad, see);
-                        }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (seen[i] > 0.0f) o[d][i] = NAN;
-                }
-            } else {
+            for (int d = 0; d < ND; ++d) {
+                f16 seen = f16(0.0f);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int c = 0; c < 32 / kChunk<T>; ++c) {
-                        const Frag<T> pf = part_of<T>(p[t], c);
+                        Frag<T> v = col_frag<T, DP>(vt[0], 32 * t + kChunk<T> * c, 32 * d), bad, see;
 #pragma unroll
-                        for (int d = 0; d < ND; ++d) mma(o[d], col_frag<T, DP>(vb, 32 * t + kChunk<T> * c, 32 * d), pf);
+                        for (int e = 0; e < kE<T>; ++e) {
+                            const int i = kE<T> * c + e;
+                            const bool nf = !__builtin_isfinite((float)v[e]);
+                            bad[e] = nf ? 1.0f : 0.0f;
+                            if (nf) v[e] = 0.0f;
+                            see[e] = j * KB + 32 * t + 8 * (i >> 2) + 4 * half + (i & 3) > my_last ? 0.0f : 1.0f;
+                        }
+                        mma(o[d], v, part_of<T>(p[t], c));
+                        mma(seen, bad, see);
                     }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (seen[i] > 0.0f) o[d][i] = NAN;
             }
         }
     }

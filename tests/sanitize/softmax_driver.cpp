@@ -110,7 +110,7 @@ static void places() {
                     std::vector<int> seen((size_t)(b * G * per * blocks), 0), of(8, 0);
                     for (int64_t id = 0; id < softmax_groups(w); ++id) {
                         SoftmaxPlace p;
-                        if (!softmax_place(w, G, id, &p)) continue;
+                        if (!softmax_place(w, G, (uint32_t)id, &p)) continue;
                         CHECK(p.seq >= 0 && p.seq < b && p.g >= 0 && p.g < G && p.which < per && p.block >= 0 && p.block < blocks);
                         ++seen[(size_t)(((p.seq * G + p.g) * per + p.which) * blocks + p.block)];
                         if (p.seq == 0) ++of[(size_t)(id & 7)];
