@@ -21,7 +21,7 @@ struct SoftmaxLaunch {
     int64_t q_b, q_t, q_h, k_b, k_t, k_h, v_b, v_t, v_h, do_b, do_t, do_h;  // elements
     void *o, *dq, *dk, *dv;
     float *lse;
-    float *stats;  // gradient: per head and query, [H][tokens][2]: lse·log2 e and scale·delta
+    float *stats;  // gradient: [2][H][tokens]: lse·log2 e and −delta of each head and query
     bool vec;      // every row takes 16-byte accesses
 };
 constexpr int kSoftmaxThreads = 256;

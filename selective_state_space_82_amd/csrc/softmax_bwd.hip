@@ -12,11 +12,9 @@ namespace ssm {
 namespace sm {
 namespace {
 
-// Tiles of 32 keys that a wavefront takes.
-template <typename T, int DP> constexpr int kKeyTiles = sizeof(T) == 2 ? 1 : 1;
 constexpr int kStatsLanes = 16;  // lanes to a query's row
 
-// stats[h][query] = {lse·log2 e, do·o}; a query that saw no key (lse = −inf) gets +inf, that is, weights of 0.
+// stats[0][h][query] = lse·log2 e, +inf for a query that saw no key (lse = −inf), that is, weights of 0; stats[1][h][query] = −do·o.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(kSoftmaxThreads) void softmax_stats_kernel(SoftmaxLaunch a, int64_t tokens) {
     const int64_t id = (int64_t)blockIdx.x * (kSoftmaxThreads / kStatsLanes) + threadIdx.x / kStatsLanes;
@@ -44,19 +42,23 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_stats_kernel(SoftmaxL
     for (int d = 1; d < kStatsLanes; d <<= 1) sum += __shfl_xor(sum, d);
     if (lane == 0) {
         const float lse = a.lse_in[id];
-        float *out = a.stats + 2 * (h * tokens + t);
+        float *out = a.stats + h * tokens + t;
         out[0] = lse == -INFINITY ? INFINITY : lse * kLog2e;
-        out[1] = sum;
+        out[tokens * a.H] = -sum;
     }
 }
 
-// dk and dv: a workgroup takes KT·32 keys a wavefront of one key head, their keys and values in registers, and walks the queries
-// that see them, head by head of the group, in tiles of 32.
-template <typename T, int DP, int KT, bool VEC>
-__global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_dkv_kernel(SoftmaxLaunch a, SoftmaxWork work, int64_t tokens) {
-    constexpr int QB = 32, NC = DP / kChunk<T>, ND = DP / 32, KW = 32 * KT, BK = KW * kSoftmaxThreads / 64;
-    __shared__ __attribute__((aligned(1024))) char qt[2][QB * Tile<T, DP>::kRow], dt[2][QB * Tile<T, DP>::kRow];
-    __shared__ __attribute__((aligned(16))) float lse_t[2][QB], delta_t[2][QB];
+// dk and dv: a workgroup takes 32 keys a wavefront of one key head, their keys and values in registers, and walks the queries
+// that see them, head by head of the group, in tiles of 32. While a tile's weights are formed and enter their products, so are the
+// next tile's scores, and the one after is on its way into the third of three LDS buffers.
+template <typename T, int DP, bool VEC>
+__global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void softmax_dkv_kernel(SoftmaxLaunch a,
+                                                                                                    SoftmaxWork work,
+                                                                                                    int64_t tokens) {
+    constexpr int QB = 32, NC = DP / kChunk<T>, ND = DP / 32, BK = 32 * kSoftmaxThreads / 64;
+    constexpr int kTileBytes = QB * Tile<T, DP>::kRow, kStats = 2 * QB * 4;
+    __shared__ __attribute__((aligned(1024))) char qt[4 * kTileBytes], dt[4 * kTileBytes];
+    __shared__ __attribute__((aligned(16))) char stat_t[4 * kStats];  // lse, then −delta, of a tile's queries
 
     SoftmaxPlace at;
     if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
@@ -65,133 +67,175 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_dkv_kernel(Softmax
     const AttnSeq s = sequence(a.rows, is);
     const bool packed = a.rows.cu_q != nullptr;
     const int w = la::wave_id(), l = threadIdx.x & 63, col = l & 31, half = l >> 5;
-    const int k0 = kb * BK, r0 = k0 + KW * w;
+    const int k0 = kb * BK, r0 = k0 + 32 * w, key = r0 + col;
     const int to_write = packed ? s.nk : (int)a.rows.Lk;
     if (k0 >= to_write) return;
 
-    Frag<T> k[KT][NC], v[KT][NC];
+    Frag<T> k[NC], v[NC];
+    {
+        const int rows = s.nk - r0 > 32 ? 32 : s.nk - r0;
+        const T *kp = static_cast<const T *>(a.k) + is * a.k_b + (s.k0 + r0) * a.k_t + g * a.k_h;
+        const T *vp = static_cast<const T *>(a.v) + is * a.v_b + (s.k0 + r0) * a.v_t + g * a.v_h;
+        load_frags<T, DP, VEC>(k, la::rows_buffer(kp, (uint32_t)a.k_t, rows, a.D), (uint32_t)a.k_t, col, rows, a.D);
+        load_frags<T, DP, VEC>(v, la::rows_buffer(vp, (uint32_t)a.v_t, rows, a.D), (uint32_t)a.v_t, col, rows, a.D);
+        if (a.scale < 0.0f) {
 #pragma unroll
-    for (int u = 0; u < KT; ++u) {
-        const int r = r0 + 32 * u, rows = s.nk - r > 32 ? 32 : s.nk - r;
-        const T *kp = static_cast<const T *>(a.k) + is * a.k_b + (s.k0 + r) * a.k_t + g * a.k_h;
-        const T *vp = static_cast<const T *>(a.v) + is * a.v_b + (s.k0 + r) * a.v_t + g * a.v_h;
-        load_frags<T, DP, VEC>(k[u], la::rows_buffer(kp, (uint32_t)a.k_t, rows, a.D), (uint32_t)a.k_t, col, rows, a.D);
-        load_frags<T, DP, VEC>(v[u], la::rows_buffer(vp, (uint32_t)a.v_t, rows, a.D), (uint32_t)a.v_t, col, rows, a.D);
+            for (int c = 0; c < NC; ++c) negate<T>(k[c]);
+        }
     }
     const int first = k0 < s.nk ? first_query(s, a.causal, k0) / QB : 0;
     const int tiles = k0 < s.nk ? (s.nq + QB - 1) / QB - first : 0;  // a head
-    const int off = s.nk - s.nq;
-    const float sc = a.scale * kLog2e;
+    const float sc = scale_of(a.scale);
+    // the lane's key is seen by queries lo .. nq - 1, and all of the wavefront's keys by those from all_lo on
+    const int lo = key < s.nk ? first_query(s, a.causal, key) : s.nq;
+    const int all_lo = r0 + 32 <= s.nk ? first_query(s, a.causal, r0 + 31) : s.nq;
 
-    f16 dk[KT][ND], dv[KT][ND];
+    f16 dk[ND], dv[ND];
 #pragma unroll
-    for (int u = 0; u < KT; ++u)
-#pragma unroll
-        for (int d = 0; d < ND; ++d) dk[u][d] = dv[u][d] = f16(0.0f);
+    for (int d = 0; d < ND; ++d) dk[d] = dv[d] = f16(0.0f);
 
+    // Tiles in order: head r of the group, tile t of a head's. Past the last nothing is read.
     const Loader<T, QB, DP, VEC> qs((uint32_t)a.q_t, a.D), ds((uint32_t)a.do_t, a.D);
-    const auto fetch = [&](int r, int tile, int b) {
-        const int h = g * R + r, i0 = (first + tile) * QB;
-        if (threadIdx.x < QB) {
-            const int i = i0 + (int)threadIdx.x;
-            const int64_t t = (packed ? s.q0 : is * a.rows.Lq) + i;
-            const float *p = a.stats + 2 * (h * tokens + t);
-            lse_t[b][threadIdx.x] = i < s.nq ? p[0] : 0.0f;
-            delta_t[b][threadIdx.x] = i < s.nq ? p[1] : 0.0f;
-        }
-        qs(static_cast<const T *>(a.q) + is * a.q_b + (s.q0 + i0) * a.q_t + h * a.q_h, s.nq - i0, qt[b]);
-        ds(static_cast<const T *>(a.dout) + is * a.do_b + (s.q0 + i0) * a.do_t + h * a.do_h, s.nq - i0, dt[b]);
-    };
-    int r = 0, tile = 0;
-    if (tiles > 0) fetch(0, 0, 0);
-    for (int n = 0; n < tiles * R; ++n) {
-        const int i0 = (first + tile) * QB, b = n & 1;
-        landed();
-        la::lds_barrier();
-        if (++tile == tiles) {
-            tile = 0;
+    int r = 0, t = 0, into = 0;  // of the next one to load, and its buffer
+    const auto fetch = [&] {
+        const int h = g * R + r, i0 = (first + t) * QB, rows = r < R ? s.nq - i0 : 0;
+        const T *qp = static_cast<const T *>(a.q) + is * a.q_b + (s.q0 + i0) * a.q_t + h * a.q_h;
+        const T *dp = static_cast<const T *>(a.dout) + is * a.do_b + (s.q0 + i0) * a.do_t + h * a.do_h;
+        const int64_t token = (packed ? s.q0 : is * a.rows.Lq) + i0;
+        qs(qp, rows, qt + into * kTileBytes);
+        ds(dp, rows, dt + into * kTileBytes);
+        load_stats(a.stats + h * tokens + token, tokens * a.H, rows, stat_t + into * kStats);
+        if (++t == tiles) {
+            t = 0;
             ++r;
         }
-        if (r < R) fetch(r, tile, b ^ 1);
-        if (r0 >= s.nk || (a.causal && r0 > i0 + QB - 1 + off)) continue;
-        f16 p[KT], dp[KT];
+        into = into + 1 & 3;
+    };
+    // scores, and do·v − delta: the sums start at −delta
+    const auto start = [&](f16 &p, f16 &dp, int b) {
+        p = f16(0.0f);
 #pragma unroll
-        for (int u = 0; u < KT; ++u) p[u] = dp[u] = f16(0.0f);
+        for (int j = 0; j < 4; ++j) {
+            const f4 x = *reinterpret_cast<const f4 *>(stat_t + b * kStats + QB * 4 + (8 * j + 4 * half) * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dp[4 * j + e] = x[e];
+        }
+    };
+    const auto scores = [&](f16 &p, f16 &dp, int b) {
+        start(p, dp, b);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const Frag<T> qf = row_frag<T, DP>(qt[b], 0, c), df = row_frag<T, DP>(dt[b], 0, c);
-#pragma unroll
-            for (int u = 0; u < KT; ++u) {
-                mma(p[u], qf, k[u][c]);
-                mma(dp[u], df, v[u][c]);
-            }
+            mma(p, row_frag<T, DP>(qt + b * kTileBytes, 0, c), k[c]);
+            mma(dp, row_frag<T, DP>(dt + b * kTileBytes, 0, c), v[c]);
         }
-        const bool masked = i0 + QB > s.nq || r0 + KW > s.nk || (a.causal && r0 + KW - 1 > i0 + off);
-#pragma unroll
-        for (int u = 0; u < KT; ++u) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f4 lse = *reinterpret_cast<const f4 *>(&lse_t[b][8 * j + 4 * half]);
-                const f4 delta = *reinterpret_cast<const f4 *>(&delta_t[b][8 * j + 4 * half]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[u][4 * j + e] = exp2_fast(__builtin_fmaf(p[u][4 * j + e], sc, -lse[e]));
-                    dp[u][4 * j + e] = p[u][4 * j + e] * (dp[u][4 * j + e] - delta[e]);
-                }
-            }
-            if (masked) {
-                const int key = r0 + 32 * u + col;
+    };
+    if (tiles > 0) {
+        // a fetch's instructions, which may still be on their way when the fetch before has to be there
+        constexpr int FETCH = 2 * Loader<T, QB, DP, VEC>::N;
+        const auto before_last = [&] {
+            if (w == 0) landed_but<FETCH + 2>();
+            else landed_but<FETCH>();
+        };
+        fetch();
+        fetch();
+        before_last();
+        la::lds_barrier();
+        f16 p, dp, next_p, next_dp;
+        scores(p, dp, 0);
+        int b = 0, tile = 0;
+        for (int n = 0; n < tiles * R; ++n) {
+            fetch();
+            before_last();
+            la::lds_barrier();
+            const int i0 = (first + tile) * QB, ahead = b + 1 & 3;
+            if (i0 < all_lo || i0 + QB > s.nq) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int row = i0 + 8 * (i >> 2) + 4 * half + (i & 3);
-                    if (row >= s.nq || key >= s.nk || (a.causal && key > row + off)) p[u][i] = dp[u][i] = 0.0f;
+                    if (row < lo || row >= s.nq) p[i] = -INFINITY;
                 }
             }
-        }
-#pragma unroll
-        for (int c = 0; c < 32 / kChunk<T>; ++c) {
-            Frag<T> pf[KT];
-            Split<T> df[KT];
-#pragma unroll
-            for (int u = 0; u < KT; ++u) {
-                pf[u] = part_of<T>(p[u], c);
-                df[u] = Split<T>(dp[u], c);
-            }
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const Frag<T> of = col_frag<T, DP>(dt[b], kChunk<T> * c, 32 * d), qf = col_frag<T, DP>(qt[b], kChunk<T> * c, 32 * d);
-#pragma unroll
-                for (int u = 0; u < KT; ++u) {
-                    mma(dv[u][d], of, pf[u]);
-                    mma<T>(dk[u][d], qf, df[u]);
+            // 2·NC products for the next tile's scores, then 2·UNITS with this one's weights, in steps of two: a step reads the
+            // fragments of the next but one, and forms a share of the weights.
+            constexpr int CH = 32 / kChunk<T>, UNITS = CH * ND;
+            const char *qn = qt + ahead * kTileBytes, *dn = dt + ahead * kTileBytes;
+            const char *qc = qt + b * kTileBytes, *dc = dt + b * kTileBytes;
+            Frag<T> qr[NC], dr[NC], qu[UNITS], du[UNITS], pf[CH], df[CH];
+            const auto read = [&](int i) {  // for step i
+                if (i < NC) {
+                    qr[i] = row_frag<T, DP>(qn, 0, i);
+                    dr[i] = row_frag<T, DP>(dn, 0, i);
+                } else if (i < NC + UNITS) {
+                    const int u = i - NC;
+                    du[u] = col_frag<T, DP>(dc, kChunk<T> * (u / ND), 32 * (u % ND));
+                    qu[u] = col_frag<T, DP>(qc, kChunk<T> * (u / ND), 32 * (u % ND));
                 }
+            };
+            f4 lse[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) lse[j] = *reinterpret_cast<const f4 *>(stat_t + b * kStats + (8 * j + 4 * half) * 4);
+            start(next_p, next_dp, ahead);
+            read(0);
+            read(1);
+            step_end();
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                read(i + 2);
+                mma(next_p, qr[i], k[i]);
+                mma(next_dp, dr[i], v[i]);
+#pragma unroll
+                for (int e = 16 * i / NC; e < 16 * (i + 1) / NC; ++e) {
+                    p[e] = exp2_fast(__builtin_fmaf(p[e], sc, -lse[e / 4][e % 4]));
+                    dp[e] *= p[e];
+                }
+                if (i == NC - 1) {
+                    pf[0] = part_of<T>(p, 0);
+                    df[0] = part_of<T>(dp, 0);
+                }
+                step_end();
             }
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) {
+                const int c = u / ND, d = u % ND;
+                read(NC + u + 2);
+                mma(dv[d], du[u], pf[c]);
+                mma(dk[d], qu[u], df[c]);
+                if (d == ND - 1 && c + 1 < CH) {
+                    pf[c + 1] = part_of<T>(p, c + 1);
+                    df[c + 1] = part_of<T>(dp, c + 1);
+                }
+                step_end();
+            }
+            p = next_p;
+            dp = next_dp;
+            b = ahead;
+            tile = tile + 1 == tiles ? 0 : tile + 1;
         }
+        landed_but<0>();
     }
 
     const int64_t row = (packed ? s.k0 : is * a.rows.Lk) + r0;
+    const int rows = to_write - r0 > 32 ? 32 : to_write - r0;
     const uint32_t stride = (uint32_t)(a.G * a.D);
+    const Buffer kout = la::rows_buffer(static_cast<T *>(a.dk) + (row * a.G + g) * a.D, stride, rows, a.D);
+    const Buffer vout = la::rows_buffer(static_cast<T *>(a.dv) + (row * a.G + g) * a.D, stride, rows, a.D);
 #pragma unroll
-    for (int u = 0; u < KT; ++u) {
-        const int r = r0 + 32 * u, rows = to_write - r > 32 ? 32 : to_write - r;
-        const int64_t first_out = ((row + 32 * u) * a.G + g) * a.D;
-        const Buffer kout = la::rows_buffer(static_cast<T *>(a.dk) + first_out, stride, rows, a.D);
-        const Buffer vout = la::rows_buffer(static_cast<T *>(a.dv) + first_out, stride, rows, a.D);
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            if (r + col >= s.nk) dk[u][d] = dv[u][d] = f16(0.0f);
-            store_tile<T, VEC>(kout, stride, col, 32 * d, col < rows ? a.D : 0, dk[u][d], a.scale);
-            store_tile<T, VEC>(vout, stride, col, 32 * d, col < rows ? a.D : 0, dv[u][d], 1.0f);
-        }
+    for (int d = 0; d < ND; ++d) {
+        if (key >= s.nk) dk[d] = dv[d] = f16(0.0f);
+        store_tile<T, VEC>(kout, stride, col, 32 * d, col < rows ? a.D : 0, dk[d], a.scale);
+        store_tile<T, VEC>(vout, stride, col, 32 * d, col < rows ? a.D : 0, dv[d], 1.0f);
     }
 }
 
 // dq: a workgroup takes 32 queries a wavefront of one head, with their gradients in registers, and walks the keys that they
-// see in tiles of 32.
+// see in tiles of 32, pipelined as above: three LDS buffers for keys, which are read one tile longer, and two for values.
 template <typename T, int DP, bool VEC>
-__global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_dq_kernel(SoftmaxLaunch a, SoftmaxWork work, int64_t tokens) {
+__global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void softmax_dq_kernel(SoftmaxLaunch a,
+                                                                                                        SoftmaxWork work,
+                                                                                                        int64_t tokens) {
     constexpr int KB = 32, NC = DP / kChunk<T>, ND = DP / 32, BQ = 32 * kSoftmaxThreads / 64;
-    __shared__ __attribute__((aligned(1024))) char kt[2][KB * Tile<T, DP>::kRow], vt[2][KB * Tile<T, DP>::kRow];
+    constexpr int kTileBytes = KB * Tile<T, DP>::kRow;
+    __shared__ __attribute__((aligned(1024))) char kt[3 * kTileBytes], vt[2 * kTileBytes];
 
     SoftmaxPlace at;
     if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
@@ -211,64 +255,86 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_dq_kernel(SoftmaxL
     const int tiles = (keys + KB - 1) / KB;
     const int my_last = last_key(s, a.causal, r0 + col);
     const int wave_first = last_key(s, a.causal, r0);
-    const int wave_last = r0 < s.nq ? last_key(s, a.causal, (r0 + 32 < s.nq ? r0 + 32 : s.nq) - 1) : -1;
     const int64_t row = (packed ? s.q0 : is * a.rows.Lq) + r0;
 
     Frag<T> q[NC], dout[NC];
-    float lse = 0.0f, delta = 0.0f;
+    float lse = 0.0f, less = 0.0f, exact = 0.0f;  // less: −do·o, exact: the lane's half of Σ p (do·v)
+    float *stat = a.stats + h * tokens + row + col;
     {
         const int rows = s.nq - r0 > 32 ? 32 : s.nq - r0;
         const T *qp = static_cast<const T *>(a.q) + is * a.q_b + (s.q0 + r0) * a.q_t + h * a.q_h;
         const T *dp = static_cast<const T *>(a.dout) + is * a.do_b + (s.q0 + r0) * a.do_t + h * a.do_h;
         load_frags<T, DP, VEC>(q, la::rows_buffer(qp, (uint32_t)a.q_t, rows, a.D), (uint32_t)a.q_t, col, rows, a.D);
         load_frags<T, DP, VEC>(dout, la::rows_buffer(dp, (uint32_t)a.do_t, rows, a.D), (uint32_t)a.do_t, col, rows, a.D);
+        if (a.scale < 0.0f) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) negate<T>(q[c]);
+        }
         if (col < rows) {
-            const float *p = a.stats + 2 * (h * tokens + row + col);
-            lse = p[0];
-            delta = p[1];
+            lse = stat[0];
+            less = stat[tokens * a.H];
         }
     }
-    const float sc = a.scale * kLog2e;
+    const float sc = scale_of(a.scale);
     f16 dq[ND];
 #pragma unroll
     for (int d = 0; d < ND; ++d) dq[d] = f16(0.0f);
 
     const Loader<T, KB, DP, VEC> ks((uint32_t)a.k_t, a.D), vs((uint32_t)a.v_t, a.D);
-    if (tiles > 0) {
-        ks(kp, s.nk, kt[0]);
-        vs(vp, s.nk, vt[0]);
-    }
-    for (int j = 0; j < tiles; ++j) {
-        const int j0 = j * KB, b = j & 1;
-        landed();
-        la::lds_barrier();
-        if (j + 1 < tiles) {
-            ks(kp + (int64_t)(j0 + KB) * a.k_t, s.nk - j0 - KB, kt[b ^ 1]);
-            vs(vp + (int64_t)(j0 + KB) * a.v_t, s.nk - j0 - KB, vt[b ^ 1]);
+    const auto load_k = [&](int j, int b) { ks(kp + (int64_t)j * KB * a.k_t, s.nk - j * KB, kt + b * kTileBytes); };
+    const auto load_v = [&](int j) { vs(vp + (int64_t)j * KB * a.v_t, s.nk - j * KB, vt + (j & 1) * kTileBytes); };
+    const auto scores = [&](f16 &p, f16 &dp, int j, int b) {
+        p = dp = f16(0.0f);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            mma(p, row_frag<T, DP>(kt + b * kTileBytes, 0, c), q[c]);
+            mma(dp, row_frag<T, DP>(vt + (j & 1) * kTileBytes, 0, c), dout[c]);
         }
-        if (j0 <= wave_last) {
-            f16 p = f16(0.0f), dp = f16(0.0f);
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                mma(p, row_frag<T, DP>(kt[b], 0, c), q[c]);
-                mma(dp, row_frag<T, DP>(vt[b], 0, c), dout[c]);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                dp[i] = exp2_fast(__builtin_fmaf(p[i], sc, -lse)) * (dp[i] - delta);
+    };
+    if (tiles > 0) {
+        load_k(0, 0);
+        load_v(0);
+        load_k(1, 1);
+        load_v(1);
+        landed_but<0>();
+        la::lds_barrier();
+        f16 p, dp, next_p, next_dp;
+        scores(p, dp, 0, 0);
+        int b = 0;
+        for (int j = 0; j < tiles; ++j) {
+            landed_but<0>();
+            la::lds_barrier();
+            const int ahead = b == 2 ? 0 : b + 1, into = ahead == 2 ? 0 : ahead + 1;
+            load_k(j + 2, into);
+            load_v(j + 2);
+            const int j0 = j * KB;
             if (j0 + KB - 1 > wave_first) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (j0 + 8 * (i >> 2) + 4 * half + (i & 3) > my_last) dp[i] = 0.0f;
+                    if (j0 + 8 * (i >> 2) + 4 * half + (i & 3) > my_last) p[i] = -INFINITY;
+            }
+            scores(next_p, next_dp, j + 1, ahead);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float weight = exp2_fast(__builtin_fmaf(p[i], sc, -lse));
+                exact = __builtin_fmaf(weight, dp[i], exact);
+                dp[i] = weight * (dp[i] + less);
             }
 #pragma unroll
             for (int c = 0; c < 32 / kChunk<T>; ++c) {
                 const Split<T> df(dp, c);
 #pragma unroll
-                for (int d = 0; d < ND; ++d) mma<T>(dq[d], col_frag<T, DP>(kt[b], kChunk<T> * c, 32 * d), df);
+                for (int d = 0; d < ND; ++d)
+                    mma<T>(dq[d], col_frag<T, DP>(kt + b * kTileBytes, kChunk<T> * c, 32 * d), df);
             }
+            p = next_p;
+            dp = next_dp;
+            b = ahead;
         }
+        landed_but<0>();
     }
+    exact += other_half(exact);
+    if (half == 0 && r0 + col < s.nq) stat[tokens * a.H] = -exact;
     const int rows = to_write - r0 > 32 ? 32 : to_write - r0;
     const uint32_t stride = (uint32_t)(a.H * a.D);
     const Buffer out = la::rows_buffer(static_cast<T *>(a.dq) + (row * a.H + h) * a.D, stride, rows, a.D);
@@ -287,14 +353,14 @@ template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, h
         softmax_stats_kernel<T, VEC><<<dim3((unsigned)((tokens * p.H + per - 1) / per)), kSoftmaxThreads, 0, stream>>>(p, tokens);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    if (kw.blocks > 0) {
-        softmax_dkv_kernel<T, DP, kKeyTiles<T, DP>, VEC>
-            <<<dim3((unsigned)softmax_groups(kw)), kSoftmaxThreads, 0, stream>>>(p, kw, tokens);
-        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    }
-    if (qw.blocks > 0)
+    if (qw.blocks > 0) {
         softmax_dq_kernel<T, DP, VEC>
             <<<dim3((unsigned)softmax_groups(qw)), kSoftmaxThreads, 0, stream>>>(p, qw, tokens);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    if (kw.blocks > 0)
+        softmax_dkv_kernel<T, DP, VEC>
+            <<<dim3((unsigned)softmax_groups(kw)), kSoftmaxThreads, 0, stream>>>(p, kw, tokens);
     return hipGetLastError();
 }
 template <typename T> hipError_t by_width(const SoftmaxLaunch &p, hipStream_t stream) {

@@ -90,32 +90,33 @@ template <typename T, int W> __device__ __forceinline__ Frag<T> col_frag(const c
 // Elements of chunk c of a lane's sixteen results as an operand in the order down a column. bf16: rounded to nearest, 2^-8.
 template <typename T> __device__ __forceinline__ Frag<T> part_of(const f16 &x, int c) {
     if constexpr (sizeof(T) == 2) {
-        bf8 r;
+        la::f8 y;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = (__bf16)x[8 * c + j];
-        return r;
+        for (int j = 0; j < 8; ++j) y[j] = x[8 * c + j];
+        return __builtin_convertvector(y, bf8);
     } else {
         return f4{x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]};
     }
 }
-
 // The same in two parts for bf16, the second the rounded remainder of the first: 2^-16.
 template <typename T> struct Split {
     Frag<T> p, rest;
     Split() = default;
     __device__ __forceinline__ Split(const f16 &x, int c) : p(part_of<T>(x, c)) {
         if constexpr (sizeof(T) == 2) {
+            const u4 w = __builtin_bit_cast(u4, p);
+            la::f8 y;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) rest[j] = (__bf16)(x[8 * c + j] - (float)p[j]);
+            for (int j = 0; j < 8; ++j)
+                y[j] = x[8 * c + j] - __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+            rest = __builtin_convertvector(y, bf8);
         }
     }
 };
-template <typename T> __device__ __forceinline__ void mma(f16 &acc, const Frag<T> &a, const Split<T> &b);
-template <> __device__ __forceinline__ void mma<uint16_t>(f16 &acc, const bf8 &a, const Split<uint16_t> &b) {
+template <typename T> __device__ __forceinline__ void mma(f16 &acc, const Frag<T> &a, const Split<T> &b) {
     mma(acc, a, b.p);
-    mma(acc, a, b.rest);
+    if constexpr (sizeof(T) == 2) mma(acc, a, b.rest);
 }
-template <> __device__ __forceinline__ void mma<float>(f16 &acc, const f4 &a, const Split<float> &b) { mma(acc, a, b.p); }
 
 // A row of a strided matrix in memory as fragments in registers: row `row0 + col` (zeros from row `rows` on, columns from
 // `cols` on), all DP columns.
@@ -223,10 +224,33 @@ template <typename T, int ROWS, int W, bool VEC> struct Loader {
         }
     }
 };
-// The wavefront's loads into LDS are there.
+// 32 values from `first` on and 32 from `apart` further on into LDS, one a lane of the first wavefront, zeros past `rows` of each.
+__device__ __forceinline__ void load_stats(const float *first, int64_t apart, int rows, char *lds) {
+    if (la::wave_id() != 0) return;
+    const int l = threadIdx.x & 63;
+    const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint64_t a = reinterpret_cast<uint64_t>(first + i * apart);
+        const u4 buf = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                        (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
+                        (uint32_t)__builtin_amdgcn_readfirstlane(rows > 32 ? 128 : rows > 0 ? rows * 4 : 0), 0x00027000u};
+        if (l < 32)
+            asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                         :
+                         : "s"(m0 + i * 128), "v"(l * 4u), "s"(buf)
+                         : "memory");
+    }
+}
+// The wavefront's loads into LDS are there, all but the last N.
+template <int N> __device__ __forceinline__ void landed_but() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// Of the lane's value and that of the lane 32 away.
+// Ends a step of a sequence written out by hand: the compiler moves nothing across. Left alone, it puts LDS reads right before the
+// matrix instructions that wait for them.
+__device__ __forceinline__ void step_end() { __builtin_amdgcn_sched_barrier(0); }
+
+// The value of the lane 32 away.
 __device__ __forceinline__ float other_half(float v) {
     const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return __uint_as_float((threadIdx.x & 32) ? a[0] : a[1]);
