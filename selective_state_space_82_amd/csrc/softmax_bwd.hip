@@ -50,7 +50,7 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_stats_kernel(SoftmaxL
 
 // dk and dv: a workgroup takes 32 keys a wavefront of one key head, their keys and values in registers, and walks the queries
 // that see them, head by head of the group, in tiles of 32. While a tile's weights are formed and enter their products, so are the
-// next tile's scores, and the one after is on its way into the third of three LDS buffers.
+// next tile's scores, and the two after are on their way into LDS.
 template <typename T, int DP, bool VEC>
 __global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void softmax_dkv_kernel(SoftmaxLaunch a,
                                                                                                     SoftmaxWork work,
@@ -94,22 +94,26 @@ __global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void
 #pragma unroll
     for (int d = 0; d < ND; ++d) dk[d] = dv[d] = f16(0.0f);
 
-    // Tiles in order: head r of the group, tile t of a head's. Past the last nothing is read.
+    // Tiles in order, head by head of the group. Past the last nothing is read.
     const Loader<T, QB, DP, VEC> qs((uint32_t)a.q_t, a.D), ds((uint32_t)a.do_t, a.D);
-    int r = 0, t = 0, into = 0;  // of the next one to load, and its buffer
-    const auto fetch = [&] {
-        const int h = g * R + r, i0 = (first + t) * QB, rows = r < R ? s.nq - i0 : 0;
-        const T *qp = static_cast<const T *>(a.q) + is * a.q_b + (s.q0 + i0) * a.q_t + h * a.q_h;
-        const T *dp = static_cast<const T *>(a.dout) + is * a.do_b + (s.q0 + i0) * a.do_t + h * a.do_h;
-        const int64_t token = (packed ? s.q0 : is * a.rows.Lq) + i0;
-        qs(qp, rows, qt + into * kTileBytes);
-        ds(dp, rows, dt + into * kTileBytes);
-        load_stats(a.stats + h * tokens + token, tokens * a.H, rows, stat_t + into * kStats);
-        if (++t == tiles) {
-            t = 0;
-            ++r;
-        }
-        into = into + 1 & 3;
+    const int64_t token = (packed ? s.q0 : is * a.rows.Lq) + first * QB;
+    const T *qp = static_cast<const T *>(a.q) + is * a.q_b + (s.q0 + first * QB) * a.q_t + (int64_t)g * R * a.q_h;
+    const T *dop = static_cast<const T *>(a.dout) + is * a.do_b + (s.q0 + first * QB) * a.do_t + (int64_t)g * R * a.do_h;
+    const float *sp = a.stats + (int64_t)g * R * tokens + token;
+    const int64_t q_step = QB * a.q_t, do_step = QB * a.do_t;
+    const int64_t q_turn = a.q_h - (tiles - 1) * q_step, do_turn = a.do_h - (tiles - 1) * do_step;
+    int left = tiles * R, t = 0;  // tiles still to load; the next one's place among its head's
+    const auto fetch = [&](int b) {
+        const int rows = left > 0 ? s.nq - (first + t) * QB : 0;
+        qs(qp, rows, qt + b * kTileBytes);
+        ds(dop, rows, dt + b * kTileBytes);
+        load_stats(sp, tokens * a.H, rows, stat_t + b * kStats);
+        const bool turn = ++t == tiles;
+        qp += turn ? q_turn : q_step;
+        dop += turn ? do_turn : do_step;
+        sp += turn ? tokens - (tiles - 1) * QB : QB;
+        if (turn) t = 0;
+        --left;
     };
     // scores, and do·v − delta: the sums start at −delta
     const auto start = [&](f16 &p, f16 &dp, int b) {
@@ -136,18 +140,17 @@ __global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void
             if (w == 0) landed_but<FETCH + 2>();
             else landed_but<FETCH>();
         };
-        fetch();
-        fetch();
+        fetch(0);
+        fetch(1);
         before_last();
         la::lds_barrier();
-        f16 p, dp, next_p, next_dp;
-        scores(p, dp, 0);
-        int b = 0, tile = 0;
-        for (int n = 0; n < tiles * R; ++n) {
-            fetch();
+        int tile = 0;
+        const auto step = [&](auto B, f16 &p, f16 &dp, f16 &next_p, f16 &next_dp) {
+            fetch(B + 2 & 3);
             before_last();
             la::lds_barrier();
-            const int i0 = (first + tile) * QB, ahead = b + 1 & 3;
+            const int i0 = (first + tile) * QB;
+            tile = tile + 1 == tiles ? 0 : tile + 1;
             if (i0 < all_lo || i0 + QB > s.nq) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -157,7 +160,8 @@ __global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void
             }
             // 2·NC products for the next tile's scores, then 2·UNITS with this one's weights, in steps of two: a step reads the
             // fragments of the next but one, and forms a share of the weights.
-            constexpr int CH = 32 / kChunk<T>, UNITS = CH * ND;
+            constexpr int b = B, ahead = b + 1 & 3;
+            constexpr int CH = 32 / kChunk<T>, UNITS = CH * ND, AHEAD = 2;
             const char *qn = qt + ahead * kTileBytes, *dn = dt + ahead * kTileBytes;
             const char *qc = qt + b * kTileBytes, *dc = dt + b * kTileBytes;
             Frag<T> qr[NC], dr[NC], qu[UNITS], du[UNITS], pf[CH], df[CH];
@@ -175,12 +179,12 @@ __global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void
 #pragma unroll
             for (int j = 0; j < 4; ++j) lse[j] = *reinterpret_cast<const f4 *>(stat_t + b * kStats + (8 * j + 4 * half) * 4);
             start(next_p, next_dp, ahead);
-            read(0);
-            read(1);
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) read(i);
             step_end();
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                read(i + 2);
+                read(i + AHEAD);
                 mma(next_p, qr[i], k[i]);
                 mma(next_dp, dr[i], v[i]);
 #pragma unroll
@@ -197,7 +201,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void
 #pragma unroll
             for (int u = 0; u < UNITS; ++u) {
                 const int c = u / ND, d = u % ND;
-                read(NC + u + 2);
+                read(NC + u + AHEAD);
                 mma(dv[d], du[u], pf[c]);
                 mma(dk[d], qu[u], df[c]);
                 if (d == ND - 1 && c + 1 < CH) {
@@ -206,10 +210,19 @@ __global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void
                 }
                 step_end();
             }
-            p = next_p;
-            dp = next_dp;
-            b = ahead;
-            tile = tile + 1 == tiles ? 0 : tile + 1;
+        };
+        // the buffers in turn, so that their places are constants
+        f16 p, dp, next_p, next_dp;
+        scores(p, dp, 0);
+        for (int n = tiles * R;;) {
+            step(std::integral_constant<int, 0>(), p, dp, next_p, next_dp);
+            if (--n == 0) break;
+            step(std::integral_constant<int, 1>(), next_p, next_dp, p, dp);
+            if (--n == 0) break;
+            step(std::integral_constant<int, 2>(), p, dp, next_p, next_dp);
+            if (--n == 0) break;
+            step(std::integral_constant<int, 3>(), next_p, next_dp, p, dp);
+            if (--n == 0) break;
         }
         landed_but<0>();
     }
@@ -228,14 +241,14 @@ __global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void
 }
 
 // dq: a workgroup takes 32 queries a wavefront of one head, with their gradients in registers, and walks the keys that they
-// see in tiles of 32, pipelined as above: three LDS buffers for keys, which are read one tile longer, and two for values.
+// see in tiles of 32, pipelined as above: four LDS buffers for keys, which are read one tile longer, and two for values.
 template <typename T, int DP, bool VEC>
 __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void softmax_dq_kernel(SoftmaxLaunch a,
                                                                                                         SoftmaxWork work,
                                                                                                         int64_t tokens) {
     constexpr int KB = 32, NC = DP / kChunk<T>, ND = DP / 32, BQ = 32 * kSoftmaxThreads / 64;
     constexpr int kTileBytes = KB * Tile<T, DP>::kRow;
-    __shared__ __attribute__((aligned(1024))) char kt[3 * kTileBytes], vt[2 * kTileBytes];
+    __shared__ __attribute__((aligned(1024))) char kt[4 * kTileBytes], vt[2 * kTileBytes];
 
     SoftmaxPlace at;
     if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
@@ -258,7 +271,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
     const int64_t row = (packed ? s.q0 : is * a.rows.Lq) + r0;
 
     Frag<T> q[NC], dout[NC];
-    float lse = 0.0f, less = 0.0f, exact = 0.0f;  // less: −do·o, exact: the lane's half of Σ p (do·v)
+    float lse = 0.0f, less = 0.0f, rest = 0.0f;  // less: −delta; rest: the lane's half of Σ ds
     float *stat = a.stats + h * tokens + row + col;
     {
         const int rows = s.nq - r0 > 32 ? 32 : s.nq - r0;
@@ -281,60 +294,72 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
     for (int d = 0; d < ND; ++d) dq[d] = f16(0.0f);
 
     const Loader<T, KB, DP, VEC> ks((uint32_t)a.k_t, a.D), vs((uint32_t)a.v_t, a.D);
-    const auto load_k = [&](int j, int b) { ks(kp + (int64_t)j * KB * a.k_t, s.nk - j * KB, kt + b * kTileBytes); };
-    const auto load_v = [&](int j) { vs(vp + (int64_t)j * KB * a.v_t, s.nk - j * KB, vt + (j & 1) * kTileBytes); };
-    const auto scores = [&](f16 &p, f16 &dp, int j, int b) {
-        p = dp = f16(0.0f);
+    const int64_t k_step = KB * a.k_t, v_step = KB * a.v_t;
+    int left = s.nk;  // keys from the next tile to load on
+    const auto fetch = [&](int b) {
+        ks(kp, left, kt + b * kTileBytes);
+        vs(vp, left, vt + (b & 1) * kTileBytes);
+        kp += k_step;
+        vp += v_step;
+        left -= KB;
+    };
+    // scores, and do·v − delta: the sums start at −delta
+    const auto scores = [&](f16 &p, f16 &dp, int b) {
+        p = f16(0.0f);
+        dp = f16(less);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             mma(p, row_frag<T, DP>(kt + b * kTileBytes, 0, c), q[c]);
-            mma(dp, row_frag<T, DP>(vt + (j & 1) * kTileBytes, 0, c), dout[c]);
+            mma(dp, row_frag<T, DP>(vt + (b & 1) * kTileBytes, 0, c), dout[c]);
         }
     };
     if (tiles > 0) {
-        load_k(0, 0);
-        load_v(0);
-        load_k(1, 1);
-        load_v(1);
+        fetch(0);
+        fetch(1);
         landed_but<0>();
         la::lds_barrier();
-        f16 p, dp, next_p, next_dp;
-        scores(p, dp, 0, 0);
-        int b = 0;
-        for (int j = 0; j < tiles; ++j) {
+        int j0 = 0;
+        const auto step = [&](auto B, f16 &p, f16 &dp, f16 &next_p, f16 &next_dp) {
             landed_but<0>();
             la::lds_barrier();
-            const int ahead = b == 2 ? 0 : b + 1, into = ahead == 2 ? 0 : ahead + 1;
-            load_k(j + 2, into);
-            load_v(j + 2);
-            const int j0 = j * KB;
+            fetch(B + 2 & 3);
             if (j0 + KB - 1 > wave_first) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (j0 + 8 * (i >> 2) + 4 * half + (i & 3) > my_last) p[i] = -INFINITY;
             }
-            scores(next_p, next_dp, j + 1, ahead);
+            j0 += KB;
+            scores(next_p, next_dp, B + 1 & 3);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float weight = exp2_fast(__builtin_fmaf(p[i], sc, -lse));
-                exact = __builtin_fmaf(weight, dp[i], exact);
-                dp[i] = weight * (dp[i] + less);
+                dp[i] *= exp2_fast(__builtin_fmaf(p[i], sc, -lse));
+                rest += dp[i];
             }
 #pragma unroll
             for (int c = 0; c < 32 / kChunk<T>; ++c) {
                 const Split<T> df(dp, c);
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
-                    mma<T>(dq[d], col_frag<T, DP>(kt + b * kTileBytes, kChunk<T> * c, 32 * d), df);
+                    mma<T>(dq[d], col_frag<T, DP>(kt + B * kTileBytes, kChunk<T> * c, 32 * d), df);
             }
-            p = next_p;
-            dp = next_dp;
-            b = ahead;
+        };
+        f16 p, dp, next_p, next_dp;
+        scores(p, dp, 0);
+        for (int n = tiles;;) {
+            step(std::integral_constant<int, 0>(), p, dp, next_p, next_dp);
+            if (--n == 0) break;
+            step(std::integral_constant<int, 1>(), next_p, next_dp, p, dp);
+            if (--n == 0) break;
+            step(std::integral_constant<int, 2>(), p, dp, next_p, next_dp);
+            if (--n == 0) break;
+            step(std::integral_constant<int, 3>(), next_p, next_dp, p, dp);
+            if (--n == 0) break;
         }
         landed_but<0>();
     }
-    exact += other_half(exact);
-    if (half == 0 && r0 + col < s.nq) stat[tokens * a.H] = -exact;
+    // Σ_j ds_ij is 0 but for the rounding of o, from which delta was formed: what is left corrects delta for dk.
+    rest += other_half(rest);
+    if (half == 0 && r0 + col < s.nq) stat[tokens * a.H] = less - rest;
     const int rows = to_write - r0 > 32 ? 32 : to_write - r0;
     const uint32_t stride = (uint32_t)(a.H * a.D);
     const Buffer out = la::rows_buffer(static_cast<T *>(a.dq) + (row * a.H + h) * a.D, stride, rows, a.D);
