@@ -124,7 +124,7 @@ ssm_status_t check_rows(const ssm_attn_rows_t *r, int64_t H, int64_t G, int64_t 
     const ssm::SoftmaxWork q = ssm::softmax_fwd_work(z, H, G), k = ssm::softmax_dkv_work(z, G);
     for (const ssm::SoftmaxWork &w : {q, k}) {
         int64_t n = 0;
-        if (!mul_ok((w.units + 7) / 8 * 8, w.each, &n) || !launchable(n, ssm::kSoftmaxThreads)) return SSM_ERR_SHAPE;
+        if (!mul_ok((w.units + 7) / 8 * 8, w.each, &n) || !launchable(n, 2 * ssm::kSoftmaxThreads)) return SSM_ERR_SHAPE;
     }
     return SSM_OK;
 }

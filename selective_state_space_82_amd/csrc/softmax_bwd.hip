@@ -48,17 +48,19 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_stats_kernel(SoftmaxL
     }
 }
 
-// dk and dv: a workgroup takes 32 keys a wavefront of one key head, their keys and values in registers, and walks the queries
-// that see them, head by head of the group, in tiles of 32. While a tile's weights are formed and enter their products, so are the
-// next tile's scores, and the two after are on their way into LDS.
+// dk and dv: a workgroup takes 128 keys of one key head and walks the queries that see them, head by head of the group, in
+// tiles of 32. Two wavefronts share 32 keys: the first forms their scores and weights and adds to dv, the second forms do·v and, from
+// the weights that the first left in LDS in the round before, ds, and adds to dk. Each so holds one operand and one sum (one
+// wavefront with both of each takes the registers of two: 36 % of the matrix instructions' rate, for want of a second
+// wavefront to issue while one waits).
 template <typename T, int DP, bool VEC>
-__global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void softmax_dkv_kernel(SoftmaxLaunch a,
-                                                                                                    SoftmaxWork work,
-                                                                                                    int64_t tokens) {
+__global__ __launch_bounds__(2 * kSoftmaxThreads, DP * sizeof(T) > 128 ? 2 : 4) void softmax_dkv_kernel(SoftmaxLaunch a,
+                                                                                                        SoftmaxWork work,
+                                                                                                        int64_t tokens) {
     constexpr int QB = 32, NC = DP / kChunk<T>, ND = DP / 32, BK = 32 * kSoftmaxThreads / 64;
-    constexpr int kTileBytes = QB * Tile<T, DP>::kRow, kStats = 2 * QB * 4;
-    __shared__ __attribute__((aligned(1024))) char qt[4 * kTileBytes], dt[4 * kTileBytes];
-    __shared__ __attribute__((aligned(16))) char stat_t[4 * kStats];  // lse, then −delta, of a tile's queries
+    constexpr int kTileBytes = QB * Tile<T, DP>::kRow, kStats = QB * 4, kWeights = 32 * 32 * 4;
+    __shared__ __attribute__((aligned(1024))) char qt[4 * kTileBytes], dt[2 * kTileBytes], weights[2][4][kWeights];
+    __shared__ __attribute__((aligned(16))) char lse_t[2 * kStats], less_t[2 * kStats];  // lse, −delta of a tile's queries
 
     SoftmaxPlace at;
     if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
@@ -66,21 +68,23 @@ __global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void
     const int g = at.g, R = a.H / a.G, kb = at.block;  // the first keys, which most queries see, first
     const AttnSeq s = sequence(a.rows, is);
     const bool packed = a.rows.cu_q != nullptr;
-    const int w = la::wave_id(), l = threadIdx.x & 63, col = l & 31, half = l >> 5;
+    const int w = la::wave_id() & 3, l = threadIdx.x & 63, col = l & 31, half = l >> 5;
+    const bool second = la::wave_id() >= 4;
     const int k0 = kb * BK, r0 = k0 + 32 * w, key = r0 + col;
     const int to_write = packed ? s.nk : (int)a.rows.Lk;
     if (k0 >= to_write) return;
 
-    Frag<T> k[NC], v[NC];
+    // the wavefront's operand, keys or values
+    Frag<T> kv[NC];
     {
         const int rows = s.nk - r0 > 32 ? 32 : s.nk - r0;
-        const T *kp = static_cast<const T *>(a.k) + is * a.k_b + (s.k0 + r0) * a.k_t + g * a.k_h;
-        const T *vp = static_cast<const T *>(a.v) + is * a.v_b + (s.k0 + r0) * a.v_t + g * a.v_h;
-        load_frags<T, DP, VEC>(k, la::rows_buffer(kp, (uint32_t)a.k_t, rows, a.D), (uint32_t)a.k_t, col, rows, a.D);
-        load_frags<T, DP, VEC>(v, la::rows_buffer(vp, (uint32_t)a.v_t, rows, a.D), (uint32_t)a.v_t, col, rows, a.D);
-        if (a.scale < 0.0f) {
+        const T *p = second ? static_cast<const T *>(a.v) + is * a.v_b + (s.k0 + r0) * a.v_t + g * a.v_h
+                            : static_cast<const T *>(a.k) + is * a.k_b + (s.k0 + r0) * a.k_t + g * a.k_h;
+        const uint32_t step = (uint32_t)(second ? a.v_t : a.k_t);
+        load_frags<T, DP, VEC>(kv, la::rows_buffer(p, step, rows, a.D), step, col, rows, a.D);
+        if (a.scale < 0.0f && !second) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) negate<T>(k[c]);
+            for (int c = 0; c < NC; ++c) negate<T>(kv[c]);
         }
     }
     const int first = k0 < s.nk ? first_query(s, a.causal, k0) / QB : 0;
@@ -90,65 +94,57 @@ __global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void
     const int lo = key < s.nk ? first_query(s, a.causal, key) : s.nq;
     const int all_lo = r0 + 32 <= s.nk ? first_query(s, a.causal, r0 + 31) : s.nq;
 
-    f16 dk[ND], dv[ND];
+    f16 sum[ND];  // dv, or dk
 #pragma unroll
-    for (int d = 0; d < ND; ++d) dk[d] = dv[d] = f16(0.0f);
+    for (int d = 0; d < ND; ++d) sum[d] = f16(0.0f);
 
-    // Tiles in order, head by head of the group. Past the last nothing is read.
-    const Loader<T, QB, DP, VEC> qs((uint32_t)a.q_t, a.D), ds((uint32_t)a.do_t, a.D);
+    // Tiles in order, head by head of the group; past the last nothing is read. The first half of the workgroup loads queries, the
+    // second their gradients; the first wavefront of each a tile's lse or −delta.
+    const Loader<T, QB, DP, VEC> load((uint32_t)(second ? a.do_t : a.q_t), a.D);
     const int64_t token = (packed ? s.q0 : is * a.rows.Lq) + first * QB;
-    const T *qp = static_cast<const T *>(a.q) + is * a.q_b + (s.q0 + first * QB) * a.q_t + (int64_t)g * R * a.q_h;
-    const T *dop = static_cast<const T *>(a.dout) + is * a.do_b + (s.q0 + first * QB) * a.do_t + (int64_t)g * R * a.do_h;
-    const float *sp = a.stats + (int64_t)g * R * tokens + token;
-    const int64_t q_step = QB * a.q_t, do_step = QB * a.do_t;
-    const int64_t q_turn = a.q_h - (tiles - 1) * q_step, do_turn = a.do_h - (tiles - 1) * do_step;
-    int left = tiles * R, t = 0;  // tiles still to load; the next one's place among its head's
-    const auto fetch = [&](int b) {
-        const int rows = left > 0 ? s.nq - (first + t) * QB : 0;
-        qs(qp, rows, qt + b * kTileBytes);
-        ds(dop, rows, dt + b * kTileBytes);
-        load_stats(sp, tokens * a.H, rows, stat_t + b * kStats);
+    const int64_t step_t = second ? a.do_t : a.q_t, step_h = second ? a.do_h : a.q_h, batch = second ? a.do_b : a.q_b;
+    const T *rp = static_cast<const T *>(second ? a.dout : a.q) + is * batch + (s.q0 + first * QB) * step_t +
+                  (int64_t)g * R * step_h;
+    const float *sp = a.stats + (second ? tokens * a.H : 0) + (int64_t)g * R * tokens + token;
+    const int64_t tile_step = QB * step_t, turn_step = step_h - (tiles - 1) * tile_step;
+    int left = tiles * R, t = 0, stats_left = tiles * R, st = 0;  // still to load, and the next one's place among its head's
+    const auto fetch_rows = [&](char *tile) {
+        load(rp, left > 0 ? s.nq - (first + t) * QB : 0, tile);
         const bool turn = ++t == tiles;
-        qp += turn ? q_turn : q_step;
-        dop += turn ? do_turn : do_step;
-        sp += turn ? tokens - (tiles - 1) * QB : QB;
+        rp += turn ? turn_step : tile_step;
         if (turn) t = 0;
         --left;
     };
-    // scores, and do·v − delta: the sums start at −delta
-    const auto start = [&](f16 &p, f16 &dp, int b) {
-        p = f16(0.0f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f4 x = *reinterpret_cast<const f4 *>(stat_t + b * kStats + QB * 4 + (8 * j + 4 * half) * 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dp[4 * j + e] = x[e];
-        }
+    const auto fetch_stats = [&](char *to) {
+        if (w == 0) load_stats(sp, stats_left > 0 ? s.nq - (first + st) * QB : 0, to);
+        const bool turn = ++st == tiles;
+        sp += turn ? tokens - (tiles - 1) * QB : QB;
+        if (turn) st = 0;
+        --stats_left;
     };
-    const auto scores = [&](f16 &p, f16 &dp, int b) {
-        start(p, dp, b);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            mma(p, row_frag<T, DP>(qt + b * kTileBytes, 0, c), k[c]);
-            mma(dp, row_frag<T, DP>(dt + b * kTileBytes, 0, c), v[c]);
-        }
-    };
-    if (tiles > 0) {
-        // a fetch's instructions, which may still be on their way when the fetch before has to be there
-        constexpr int FETCH = 2 * Loader<T, QB, DP, VEC>::N;
-        const auto before_last = [&] {
-            if (w == 0) landed_but<FETCH + 2>();
-            else landed_but<FETCH>();
-        };
-        fetch(0);
-        fetch(1);
-        before_last();
+    const int rounds = tiles * R;  // the second wavefronts take one more, the first of which only starts
+
+    // In round n the first wavefronts use tile n's gradients' columns and tile n + 1's queries' rows, the second tile n's gradients'
+    // rows and tile n − 1's queries' columns. Queries are loaded two rounds ahead into one of four buffers, the rest one
+    // round ahead into one of two.
+    if (tiles > 0 && !second) {
+        fetch_rows(qt);
+        fetch_rows(qt + kTileBytes);
+        fetch_stats(lse_t);
+        landed();
         la::lds_barrier();
+        const auto scores = [&](f16 &p, int b) {
+            p = f16(0.0f);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) mma(p, row_frag<T, DP>(qt + b * kTileBytes, 0, c), kv[c]);
+        };
         int tile = 0;
-        const auto step = [&](auto B, f16 &p, f16 &dp, f16 &next_p, f16 &next_dp) {
-            fetch(B + 2 & 3);
-            before_last();
+        const auto round = [&](auto B, f16 &p, f16 &next) {
+            constexpr int b = B, odd = b & 1;
+            landed();
             la::lds_barrier();
+            fetch_rows(qt + (b + 2 & 3) * kTileBytes);
+            fetch_stats(lse_t + (odd ^ 1) * kStats);
             const int i0 = (first + tile) * QB;
             tile = tile + 1 == tiles ? 0 : tile + 1;
             if (i0 < all_lo || i0 + QB > s.nq) {
@@ -158,85 +154,99 @@ __global__ __launch_bounds__(kSoftmaxThreads, DP * sizeof(T) > 128 ? 1 : 2) void
                     if (row < lo || row >= s.nq) p[i] = -INFINITY;
                 }
             }
-            // 2·NC products for the next tile's scores, then 2·UNITS with this one's weights, in steps of two: a step reads the
-            // fragments of the next but one, and forms a share of the weights.
-            constexpr int b = B, ahead = b + 1 & 3;
-            constexpr int CH = 32 / kChunk<T>, UNITS = CH * ND, AHEAD = 2;
-            const char *qn = qt + ahead * kTileBytes, *dn = dt + ahead * kTileBytes;
-            const char *qc = qt + b * kTileBytes, *dc = dt + b * kTileBytes;
-            Frag<T> qr[NC], dr[NC], qu[UNITS], du[UNITS], pf[CH], df[CH];
-            const auto read = [&](int i) {  // for step i
-                if (i < NC) {
-                    qr[i] = row_frag<T, DP>(qn, 0, i);
-                    dr[i] = row_frag<T, DP>(dn, 0, i);
-                } else if (i < NC + UNITS) {
-                    const int u = i - NC;
-                    du[u] = col_frag<T, DP>(dc, kChunk<T> * (u / ND), 32 * (u % ND));
-                    qu[u] = col_frag<T, DP>(qc, kChunk<T> * (u / ND), 32 * (u % ND));
-                }
-            };
-            f4 lse[4];
+            scores(next, b + 1 & 3);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) lse[j] = *reinterpret_cast<const f4 *>(stat_t + b * kStats + (8 * j + 4 * half) * 4);
-            start(next_p, next_dp, ahead);
+            for (int j = 0; j < 4; ++j) {
+                const f4 lse = *reinterpret_cast<const f4 *>(lse_t + odd * kStats + (8 * j + 4 * half) * 4);
+                f4 x;
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) read(i);
-            step_end();
-#pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                read(i + AHEAD);
-                mma(next_p, qr[i], k[i]);
-                mma(next_dp, dr[i], v[i]);
-#pragma unroll
-                for (int e = 16 * i / NC; e < 16 * (i + 1) / NC; ++e) {
-                    p[e] = exp2_fast(__builtin_fmaf(p[e], sc, -lse[e / 4][e % 4]));
-                    dp[e] *= p[e];
-                }
-                if (i == NC - 1) {
-                    pf[0] = part_of<T>(p, 0);
-                    df[0] = part_of<T>(dp, 0);
-                }
-                step_end();
+                for (int e = 0; e < 4; ++e) x[e] = p[4 * j + e] = exp2_fast(__builtin_fmaf(p[4 * j + e], sc, -lse[e]));
+                *reinterpret_cast<f4 *>(weights[odd][w] + (64 * j + l) * 16) = x;
             }
 #pragma unroll
-            for (int u = 0; u < UNITS; ++u) {
-                const int c = u / ND, d = u % ND;
-                read(NC + u + AHEAD);
-                mma(dv[d], du[u], pf[c]);
-                mma(dk[d], qu[u], df[c]);
-                if (d == ND - 1 && c + 1 < CH) {
-                    pf[c + 1] = part_of<T>(p, c + 1);
-                    df[c + 1] = part_of<T>(dp, c + 1);
-                }
-                step_end();
+            for (int c = 0; c < 32 / kChunk<T>; ++c) {
+                const Frag<T> pf = part_of<T>(p, c);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) mma(sum[d], col_frag<T, DP>(dt + odd * kTileBytes, kChunk<T> * c, 32 * d), pf);
             }
         };
-        // the buffers in turn, so that their places are constants
-        f16 p, dp, next_p, next_dp;
-        scores(p, dp, 0);
-        for (int n = tiles * R;;) {
-            step(std::integral_constant<int, 0>(), p, dp, next_p, next_dp);
+        f16 p, next;
+        scores(p, 0);
+        for (int n = rounds;;) {
+            round(std::integral_constant<int, 0>(), p, next);
             if (--n == 0) break;
-            step(std::integral_constant<int, 1>(), next_p, next_dp, p, dp);
+            round(std::integral_constant<int, 1>(), next, p);
             if (--n == 0) break;
-            step(std::integral_constant<int, 2>(), p, dp, next_p, next_dp);
+            round(std::integral_constant<int, 2>(), p, next);
             if (--n == 0) break;
-            step(std::integral_constant<int, 3>(), next_p, next_dp, p, dp);
+            round(std::integral_constant<int, 3>(), next, p);
             if (--n == 0) break;
         }
-        landed_but<0>();
+        landed();
+        la::lds_barrier();
+    } else if (tiles > 0) {
+        fetch_rows(dt);
+        fetch_stats(less_t);
+        landed();
+        la::lds_barrier();
+        // do·v − delta: the sums start at −delta
+        const auto products = [&](f16 &dp, int odd) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f4 x = *reinterpret_cast<const f4 *>(less_t + odd * kStats + (8 * j + 4 * half) * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dp[4 * j + e] = x[e];
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c) mma(dp, row_frag<T, DP>(dt + odd * kTileBytes, 0, c), kv[c]);
+        };
+        const auto open = [&](int odd) {
+            landed();
+            la::lds_barrier();
+            fetch_rows(dt + (odd ^ 1) * kTileBytes);
+            fetch_stats(less_t + (odd ^ 1) * kStats);
+        };
+        const auto round = [&](auto B, f16 &dp, f16 &next) {  // B: of tile n − 1
+            constexpr int b = B, odd = b & 1;
+            open(odd ^ 1);
+            products(next, odd ^ 1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f4 x = *reinterpret_cast<const f4 *>(weights[odd][w] + (64 * j + l) * 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dp[4 * j + e] *= x[e];
+            }
+#pragma unroll
+            for (int c = 0; c < 32 / kChunk<T>; ++c) {
+                const Frag<T> df = part_of<T>(dp, c);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) mma(sum[d], col_frag<T, DP>(qt + b * kTileBytes, kChunk<T> * c, 32 * d), df);
+            }
+        };
+        f16 dp, next;
+        open(0);
+        products(dp, 0);
+        for (int n = rounds;;) {
+            round(std::integral_constant<int, 0>(), dp, next);
+            if (--n == 0) break;
+            round(std::integral_constant<int, 1>(), next, dp);
+            if (--n == 0) break;
+            round(std::integral_constant<int, 2>(), dp, next);
+            if (--n == 0) break;
+            round(std::integral_constant<int, 3>(), next, dp);
+            if (--n == 0) break;
+        }
+        landed();
     }
 
     const int64_t row = (packed ? s.k0 : is * a.rows.Lk) + r0;
     const int rows = to_write - r0 > 32 ? 32 : to_write - r0;
     const uint32_t stride = (uint32_t)(a.G * a.D);
-    const Buffer kout = la::rows_buffer(static_cast<T *>(a.dk) + (row * a.G + g) * a.D, stride, rows, a.D);
-    const Buffer vout = la::rows_buffer(static_cast<T *>(a.dv) + (row * a.G + g) * a.D, stride, rows, a.D);
+    const Buffer out = la::rows_buffer(static_cast<T *>(second ? a.dk : a.dv) + (row * a.G + g) * a.D, stride, rows, a.D);
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
-        if (key >= s.nk) dk[d] = dv[d] = f16(0.0f);
-        store_tile<T, VEC>(kout, stride, col, 32 * d, col < rows ? a.D : 0, dk[d], a.scale);
-        store_tile<T, VEC>(vout, stride, col, 32 * d, col < rows ? a.D : 0, dv[d], 1.0f);
+        if (key >= s.nk) sum[d] = f16(0.0f);
+        store_tile<T, VEC>(out, stride, col, 32 * d, col < rows ? a.D : 0, sum[d], second ? a.scale : 1.0f);
     }
 }
 
@@ -316,11 +326,11 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
     if (tiles > 0) {
         fetch(0);
         fetch(1);
-        landed_but<0>();
+        landed();
         la::lds_barrier();
         int j0 = 0;
         const auto step = [&](auto B, f16 &p, f16 &dp, f16 &next_p, f16 &next_dp) {
-            landed_but<0>();
+            landed();
             la::lds_barrier();
             fetch(B + 2 & 3);
             if (j0 + KB - 1 > wave_first) {
@@ -355,7 +365,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
             step(std::integral_constant<int, 3>(), next_p, next_dp, p, dp);
             if (--n == 0) break;
         }
-        landed_but<0>();
+        landed();
     }
     // Σ_j ds_ij is 0 but for the rounding of o, from which delta was formed: what is left corrects delta for dk.
     rest += other_half(rest);
@@ -385,7 +395,7 @@ template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, h
     }
     if (kw.blocks > 0)
         softmax_dkv_kernel<T, DP, VEC>
-            <<<dim3((unsigned)softmax_groups(kw)), kSoftmaxThreads, 0, stream>>>(p, kw, tokens);
+            <<<dim3((unsigned)softmax_groups(kw)), 2 * kSoftmaxThreads, 0, stream>>>(p, kw, tokens);
     return hipGetLastError();
 }
 template <typename T> hipError_t by_width(const SoftmaxLaunch &p, hipStream_t stream) {

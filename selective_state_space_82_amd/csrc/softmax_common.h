@@ -163,7 +163,7 @@ template <typename T, int ROWS, int W> __device__ __forceinline__ bool share_not
     return most[0] >= 0x7f80 || most[1] >= 0x7f80;
 }
 
-// ROWS rows × W columns of a strided matrix into an LDS tile, by a workgroup; zeros past the rows and columns there are.
+// ROWS rows × W columns of a strided matrix into an LDS tile, by four wavefronts; zeros past the rows and columns there are.
 // VEC: straight into LDS, 16 bytes a lane, through a buffer that ends with the last row; the instructions are written out, for the
 // compiler would have every later read of LDS wait for a load that it knows to go there, also one from the other
 // buffer. A wavefront waits for its own with landed() before the barrier that hands the tile over. Otherwise element by
@@ -177,11 +177,13 @@ template <typename T, int ROWS, int W, bool VEC> struct Loader {
     uint32_t at[VEC ? kOffsets : 1];  // of the lane's pieces, in bytes from row 0
     uint32_t stride;
     int cols;
+    // a tile is loaded by 256 threads; of a workgroup of 512, each half loads its own
+    __device__ static __forceinline__ int thread() { return (int)threadIdx.x % kSoftmaxThreads; }
     __device__ __forceinline__ Loader(uint32_t stride_, int cols_) : stride(stride_), cols(cols_) {
         if constexpr (VEC) {
 #pragma unroll
             for (int j = 0; j < kOffsets; ++j) {
-                const int id = (int)threadIdx.x + j * kSoftmaxThreads, r = id / X::kPer, c = (id % X::kPer ^ X::turn(r)) * E;
+                const int id = thread() + j * kSoftmaxThreads, r = id / X::kPer, c = (id % X::kPer ^ X::turn(r)) * E;
                 at[j] = c < cols ? (r * stride + c) * (uint32_t)sizeof(T) : kOutside;
             }
         }
@@ -195,8 +197,9 @@ template <typename T, int ROWS, int W, bool VEC> struct Loader {
             const u4 buf = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
                             (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
                             (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00027000u};
-            if (PIECES < kSoftmaxThreads && la::wave_id() * 64 >= PIECES) return;
-            const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)tile + la::wave_id() * 1024;
+            const int w = la::wave_id() % (kSoftmaxThreads / 64);
+            if (PIECES < kSoftmaxThreads && w * 64 >= PIECES) return;
+            const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)tile + w * 1024;
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
@@ -208,7 +211,7 @@ template <typename T, int ROWS, int W, bool VEC> struct Loader {
             const Buffer buf = la::buffer_of(first, bytes);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const int id = (int)threadIdx.x + j * kSoftmaxThreads, r = id / X::kPer, c = (id % X::kPer ^ X::turn(r)) * E;
+                const int id = thread() + j * kSoftmaxThreads, r = id / X::kPer, c = (id % X::kPer ^ X::turn(r)) * E;
                 if (PIECES < kSoftmaxThreads && id >= PIECES) break;
                 T e[E];
 #pragma unroll
@@ -224,31 +227,21 @@ template <typename T, int ROWS, int W, bool VEC> struct Loader {
         }
     }
 };
-// 32 values from `first` on and 32 from `apart` further on into LDS, one a lane of the first wavefront, zeros past `rows` of each.
-__device__ __forceinline__ void load_stats(const float *first, int64_t apart, int rows, char *lds) {
-    if (la::wave_id() != 0) return;
+// 32 values from `first` on into LDS, one a lane, by one wavefront; zeros past the first `rows`.
+__device__ __forceinline__ void load_stats(const float *first, int rows, char *lds) {
     const int l = threadIdx.x & 63;
-    const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint64_t a = reinterpret_cast<uint64_t>(first + i * apart);
-        const u4 buf = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
-                        (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
-                        (uint32_t)__builtin_amdgcn_readfirstlane(rows > 32 ? 128 : rows > 0 ? rows * 4 : 0), 0x00027000u};
-        if (l < 32)
-            asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                         :
-                         : "s"(m0 + i * 128), "v"(l * 4u), "s"(buf)
-                         : "memory");
-    }
+    const uint64_t a = reinterpret_cast<uint64_t>(first);
+    const u4 buf = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                    (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
+                    (uint32_t)__builtin_amdgcn_readfirstlane(rows > 32 ? 128 : rows > 0 ? rows * 4 : 0), 0x00027000u};
+    if (l < 32)
+        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                     :
+                     : "s"((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds), "v"(l * 4u), "s"(buf)
+                     : "memory");
 }
-// The wavefront's loads into LDS are there, all but the last N.
-template <int N> __device__ __forceinline__ void landed_but() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+// The wavefront's loads into LDS are there.
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-// Ends a step of a sequence written out by hand: the compiler moves nothing across. Left alone, it puts LDS reads right before the
-// matrix instructions that wait for them.
-__device__ __forceinline__ void step_end() { __builtin_amdgcn_sched_barrier(0); }
 
 // The value of the lane 32 away.
 __device__ __forceinline__ float other_half(float v) {

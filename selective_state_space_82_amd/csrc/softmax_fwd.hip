@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
     };
     // Adds what tile j's scores p say, with its values in buffer b, and forms tile j + 1's scores meanwhile.
     const auto step = [&](int j, int b, f16(&p)[NT], f16(&next)[NT], auto masked) {
-        landed_but<0>();
+        landed();
         la::lds_barrier();
         load_k(j + 2, b);
         load_v(j + 1, b ^ 1);
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
         load_k(0, 0);
         load_v(0, 0);
         load_k(1, 1);
-        landed_but<0>();
+        landed();
         la::lds_barrier();
         f16 p[NT], next[NT];
         scores(p, 0);
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
 #pragma unroll
             for (int t = 0; t < NT; ++t) p[t] = next[t];
         }
-        landed_but<0>();  // the loads past the last tile, before LDS is written again or given up
+        landed();  // the loads past the last tile, before LDS is written again or given up
         la::lds_barrier();
     }
     // A masked key's weight is 0, but 0 times a NaN or Inf is not. Where there is one the block is done again, one tile after
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
             la::lds_barrier();
             load_k(j, 0);
             load_v(j, 0);
-            landed_but<0>();
+            landed();
             la::lds_barrier();
             f16 p[NT];
             scores(p, 0);
