@@ -33,10 +33,15 @@ constexpr int kSoftmaxThreads = 256;
 struct SoftmaxWork {
     int64_t units, each;  // each: workgroups of a unit
     int parts, per, blocks;
+    bool across;  // an XCD takes the first block of each of its units, then the second of each, ...; otherwise unit by unit
 };  // workgroups number less than 2^24
 inline SoftmaxWork softmax_work(int64_t b, int64_t G, int64_t per, int64_t blocks) {
     const int64_t parts = G >= 8 || blocks < 2 ? 1 : ((8 + G - 1) / G < blocks ? (8 + G - 1) / G : blocks);
-    return {b * G * parts, per * ((blocks + parts - 1) / parts), (int)parts, (int)per, (int)blocks};
+    const int64_t units = b * G * parts, each = per * ((blocks + parts - 1) / parts);
+    // The last unit's longest blocks should not start when all else is done: where a unit does not fill an XCD (32 compute units,
+    // two workgroups each) and there are rounds enough for that to matter. (4 sequences of 2048, 24 heads, gradient: 314 us unit
+    // by unit, 264 across; 8 of 4096, 32 heads on 8 key heads, forward: 1091 and 1139.)
+    return {units, each, (int)parts, (int)per, (int)blocks, each < 64 && (units + 7) / 8 * each >= 128};
 }
 inline int64_t softmax_groups(const SoftmaxWork &w) { return (w.units + 7) / 8 * 8 * w.each; }
 // Of a workgroup: sequence, key head, which of the `per`, and which block counted from the first to be taken; false: none.
@@ -45,7 +50,8 @@ struct SoftmaxPlace {
     int g, which, block;
 };
 SSM_BOTH bool softmax_place(const SoftmaxWork &w, int64_t G, uint32_t id, SoftmaxPlace *p) {
-    const uint32_t turn = id >> 3, each = (uint32_t)w.each, unit = turn / each * 8 + (id & 7), at = turn % each;
+    const uint32_t turn = id >> 3, each = (uint32_t)w.each, mine = ((uint32_t)w.units + 7) / 8;  // an XCD's units
+    const uint32_t unit = (w.across ? turn % mine : turn / each) * 8 + (id & 7), at = w.across ? turn / mine : turn % each;
     const uint32_t head = unit / (uint32_t)w.parts, part = unit % (uint32_t)w.parts;
     p->seq = head / (uint32_t)G;
     p->g = (int)(head % (uint32_t)G);

@@ -277,13 +277,26 @@ template <typename T> __global__ __launch_bounds__(kSoftmaxThreads) void softmax
     for (int u = 0; u < WAVES; ++u) most = __builtin_fmaxf(most, most_of[u]);
     const float base = most == -INFINITY ? 0.0f : most;
     float x[2] = {0.0f, 0.0f}, total = 0.0f;
-    for (int i = w; i < pieces; i += WAVES) {
-        const float *p = part + (int64_t)i * (a.D + 2);
-        const float f = exp2_fast(p[0] - base);
-        total = __builtin_fmaf(f, p[1], total);
+    constexpr int AT_ONCE = 8;  // pieces whose loads are on their way together
+    for (int i0 = w; i0 < pieces; i0 += WAVES * AT_ONCE) {
+        float f[AT_ONCE], n[AT_ONCE], y[AT_ONCE][2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-            if (l + 64 * u < a.D) x[u] = __builtin_fmaf(f, p[2 + l + 64 * u], x[u]);
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const int i = i0 + WAVES * k;
+            const float *p = part + (int64_t)(i < pieces ? i : 0) * (a.D + 2);
+            f[k] = p[0];
+            n[k] = p[1];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) y[k][u] = l + 64 * u < a.D ? p[2 + l + 64 * u] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            if (i0 + WAVES * k >= pieces) break;
+            const float e = exp2_fast(f[k] - base);
+            total = __builtin_fmaf(e, n[k], total);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) x[u] = __builtin_fmaf(e, y[k][u], x[u]);
+        }
     }
     acc[w][l] = x[0];
     acc[w][l + 64] = x[1];
