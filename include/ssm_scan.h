@@ -403,6 +403,7 @@ SSM_API ssm_status_t ssm_layernorm_bwd(const void *x, const float *w, const void
  *                       them (o, dq, dk, dv) are 0, lse −inf.
  *   strides           NULL: dense. Otherwise as ssm_linattn_strides_t's for q, k, v, do_ (b unused where packed). Outputs, and
  *                     o and lse as inputs, are always dense.
+ *   workspace         as for ssm_linattn_fwd, of the bytes the call's _workspace function gives (may be 0)
  * Products are exact bf16 products summed in fp32 (bf16) or fp32 products (f32); the softmax' statistics and all sums are
  * fp32. With bf16, weights and their gradients enter products rounded to bf16, 2^-8 each (a second part for each would add half
  * again to the forward call's products). Results are deterministic. A NaN or Inf reaches the
@@ -419,14 +420,17 @@ typedef struct {
     int64_t b, Lq, Lk, tokens_q, tokens_k;
 } ssm_attn_rows_t;
 
+SSM_API ssm_status_t ssm_attn_fwd_workspace(const ssm_attn_rows_t *rows, int64_t H, int64_t G, int64_t D, ssm_dtype_t dtype,
+                                            int64_t *bytes);
 SSM_API ssm_status_t ssm_attn_fwd(const void *q, const void *k, const void *v, float scale, int32_t causal,
                                   const ssm_attn_rows_t *rows, void *o, float *lse, int64_t H, int64_t G, int64_t D,
-                                  ssm_dtype_t dtype, const ssm_attn_strides_t *strides, hipStream_t stream);
+                                  ssm_dtype_t dtype, const ssm_attn_strides_t *strides, void *workspace,
+                                  int64_t workspace_bytes, hipStream_t stream);
 
 /* Gradients for an upstream gradient do_ on o, from the forward call's o and lse. dq [tokens][H][D], dk and dv
  * [tokens][G][D] (summed over the heads that share a key head, in fp32) dtype, all required. workspace as for
  * ssm_linattn_bwd, of the bytes ssm_attn_bwd_workspace gives. */
-SSM_API ssm_status_t ssm_attn_bwd_workspace(const ssm_attn_rows_t *rows, int64_t H, int64_t *bytes);
+SSM_API ssm_status_t ssm_attn_bwd_workspace(const ssm_attn_rows_t *rows, int64_t H, int64_t G, int64_t D, int64_t *bytes);
 SSM_API ssm_status_t ssm_attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
                                   const void *do_, float scale, int32_t causal, const ssm_attn_rows_t *rows, void *dq,
                                   void *dk, void *dv, int64_t H, int64_t G, int64_t D, ssm_dtype_t dtype,

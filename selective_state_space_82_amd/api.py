@@ -131,9 +131,11 @@ def lib() -> ctypes.CDLL:
     L.ssm_layernorm_bwd.argtypes = [vp] * 8 + [i64] * 5 + [i32, vp, i64, vp]
     L.ssm_layernorm_bwd.restype = i32
     rows, pages, tokens = ctypes.POINTER(AttnRows), ctypes.POINTER(Pages), ctypes.POINTER(Tokens)
-    L.ssm_attn_fwd.argtypes = [vp] * 3 + [f32, i32, rows, vp, vp] + [i64] * 3 + [i32, strides, vp]
+    L.ssm_attn_fwd_workspace.argtypes = [rows, i64, i64, i64, i32, ctypes.POINTER(i64)]
+    L.ssm_attn_fwd_workspace.restype = i32
+    L.ssm_attn_fwd.argtypes = [vp] * 3 + [f32, i32, rows, vp, vp] + [i64] * 3 + [i32, strides, vp, i64, vp]
     L.ssm_attn_fwd.restype = i32
-    L.ssm_attn_bwd_workspace.argtypes = [rows, i64, ctypes.POINTER(i64)]
+    L.ssm_attn_bwd_workspace.argtypes = [rows, i64, i64, i64, ctypes.POINTER(i64)]
     L.ssm_attn_bwd_workspace.restype = i32
     L.ssm_attn_bwd.argtypes = [vp] * 6 + [f32, i32, rows] + [vp] * 3 + [i64] * 3 + [i32, strides, vp, i64, vp]
     L.ssm_attn_bwd.restype = i32
@@ -883,8 +885,11 @@ def ssm_attn_fwd(q, k, v, *, scale=None, causal=True, cu_seqlens=None, max_len=N
             o = (torch.empty if q.dim() == 4 else torch.zeros)(q.shape, dtype=q.dtype, device=dev)
         else:
             _check("o", o, q.shape, q.dtype, dev)
+        n = ctypes.c_int64()
+        _raise(lib().ssm_attn_fwd_workspace(ctypes.byref(r), H, G, D, code, ctypes.byref(n)), "ssm_attn_fwd_workspace")
+        ws = _workspace(n.value, dev)
         status = lib().ssm_attn_fwd(_at(q), _at(k), _at(v), _scale(scale, D), bool(causal), ctypes.byref(r), _at(o), _at(lse),
-                                    H, G, D, code, _attn_strides(q, k, v), _raw_stream(dev))
+                                    H, G, D, code, _attn_strides(q, k, v), _at(ws), n.value, _raw_stream(dev))
     _raise(status, "ssm_attn_fwd")
     return (o, lse) if return_lse else o
 
@@ -907,7 +912,7 @@ def ssm_attn_bwd(q, k, v, *, o, lse, do, scale=None, causal=True, cu_seqlens=Non
         out = {"dq": new(q.shape, dtype=st, device=dev), "dk": new(k.shape, dtype=st, device=dev),
                "dv": new(k.shape, dtype=st, device=dev)}
         n = ctypes.c_int64()
-        _raise(lib().ssm_attn_bwd_workspace(ctypes.byref(r), H, ctypes.byref(n)), "ssm_attn_bwd_workspace")
+        _raise(lib().ssm_attn_bwd_workspace(ctypes.byref(r), H, G, D, ctypes.byref(n)), "ssm_attn_bwd_workspace")
         ws = _workspace(n.value, dev)
         status = lib().ssm_attn_bwd(_at(q), _at(k), _at(v), _at(o), _at(lse), _at(do), _scale(scale, D), bool(causal),
                                     ctypes.byref(r), _at(out["dq"]), _at(out["dk"]), _at(out["dv"]), H, G, D, code,

@@ -104,6 +104,10 @@ ssm_status_t check_heads(int64_t H, int64_t G, int64_t D, ssm_dtype_t dtype, flo
     return SSM_OK;
 }
 
+ssm::AttnRows attn_rows(const ssm_attn_rows_t &r) {
+    return {r.cu_q, r.cu_k, r.len_q, r.len_k, r.b, r.Lq, r.Lk, r.tokens_q, r.tokens_k};
+}
+
 // Tokens of queries and keys; checks the rows.
 ssm_status_t check_rows(const ssm_attn_rows_t *r, int64_t H, int64_t G, int64_t *tokens_q, int64_t *tokens_k) {
     if (!r) return SSM_ERR_NULL;
@@ -120,9 +124,9 @@ ssm_status_t check_rows(const ssm_attn_rows_t *r, int64_t H, int64_t G, int64_t 
     }
     if (*tokens_q > kMost / SSM_ATTN_MAX_D / H || *tokens_k > kMost / SSM_ATTN_MAX_D / G) return SSM_ERR_SHAPE;
     if (r->b > kMost / H) return SSM_ERR_SHAPE;
-    const ssm::AttnRows z{nullptr, nullptr, nullptr, nullptr, r->b, r->Lq, r->Lk, 0, 0};
-    const ssm::SoftmaxWork q = ssm::softmax_fwd_work(z, H, G), k = ssm::softmax_dkv_work(z, G);
-    for (const ssm::SoftmaxWork &w : {q, k}) {
+    const ssm::AttnRows z = attn_rows(*r);
+    for (const ssm::SoftmaxWork &w : {ssm::softmax_fwd_work(z, H, G, true), ssm::softmax_fwd_work(z, H, G, false),
+                                      ssm::softmax_dq_work(z, H, G), ssm::softmax_dkv_work(z, H, G)}) {
         int64_t n = 0;
         if (!mul_ok((w.units + 7) / 8 * 8, w.each, &n) || !launchable(n, 2 * ssm::kSoftmaxThreads)) return SSM_ERR_SHAPE;
     }
@@ -143,7 +147,7 @@ struct Prompt {
         if (!q.set(s, u.q_b, u.q_t, u.q_h) || !k.set(s, u.k_b, u.k_t, u.k_h) || !v.set(s, u.v_b, u.v_t, u.v_h) ||
             !dout.set(s, u.do_b, u.do_t, u.do_h))
             return SSM_ERR_SHAPE;
-        p.rows = {r.cu_q, r.cu_k, r.len_q, r.len_k, r.b, r.Lq, r.Lk, r.tokens_q, r.tokens_k};
+        p.rows = attn_rows(r);
         p.H = (int)H; p.G = (int)G; p.D = (int)D;
         p.bf16 = dtype == SSM_BF16;
         p.q_b = packed ? 0 : q.sb; p.q_t = q.st; p.q_h = q.sh;
@@ -156,7 +160,18 @@ struct Prompt {
 
 int64_t offsets_bytes(const ssm_attn_rows_t &r, const int32_t *p) { return p ? (r.b + (r.cu_q ? 1 : 0)) * 4 : 0; }
 
-int64_t stats_bytes(int64_t tokens_q, int64_t H) { return 2 * tokens_q * H * 4; }
+// Bytes of the pieces of a forward call's walks; of a gradient's stats and pieces, which the queries' gradient and the keys' hold
+// one after the other.
+int64_t fwd_bytes(const ssm_attn_rows_t &r, int64_t tq, int64_t H, int64_t G, int64_t D, ssm_dtype_t dtype) {
+    const int64_t n = ssm::softmax_fwd_work(attn_rows(r), H, G, dtype == SSM_BF16).splits;
+    return n > 1 ? n * tq * H * (D + 2) * 4 : 0;
+}
+int64_t stats_bytes(int64_t tq, int64_t H) { return ceil_div(2 * tq * H * 4, 256) * 256; }
+int64_t bwd_bytes(const ssm_attn_rows_t &r, int64_t tq, int64_t tk, int64_t H, int64_t G, int64_t D) {
+    const int64_t nq = ssm::softmax_dq_work(attn_rows(r), H, G).splits, nk = ssm::softmax_dkv_work(attn_rows(r), H, G).splits;
+    const int64_t q = nq > 1 ? nq * tq * H * (D + 1) * 4 : 0, k = nk > 1 ? 2 * nk * tk * G * D * 4 : 0;
+    return stats_bytes(tq, H) + (q > k ? q : k);
+}
 bool stats_launch(int64_t tokens_q, int64_t H) { return launchable(ceil_div(tokens_q * H, 16), ssm::kSoftmaxThreads); }
 
 // ---- the paged cache ---------------------------------------------------------------------------------------------
@@ -249,9 +264,20 @@ bool vec_rotation(const KvAppendLaunch &p, int64_t es) { return p.rotary % (2 * 
 
 extern "C" {
 
+ssm_status_t ssm_attn_fwd_workspace(const ssm_attn_rows_t *rows, int64_t H, int64_t G, int64_t D, ssm_dtype_t dtype,
+                                    int64_t *bytes) {
+    if (!bytes) return SSM_ERR_NULL;
+    ssm_status_t st = check_heads(H, G, D, dtype, 1.0f);
+    if (st != SSM_OK) return st;
+    int64_t tq = 0, tk = 0;
+    if ((st = check_rows(rows, H, G, &tq, &tk)) != SSM_OK) return st;
+    *bytes = fwd_bytes(*rows, tq, H, G, D, dtype);
+    return SSM_OK;
+}
+
 ssm_status_t ssm_attn_fwd(const void *q, const void *k, const void *v, float scale, int32_t causal, const ssm_attn_rows_t *rows,
                           void *o, float *lse, int64_t H, int64_t G, int64_t D, ssm_dtype_t dtype,
-                          const ssm_attn_strides_t *strides, hipStream_t stream) {
+                          const ssm_attn_strides_t *strides, void *workspace, int64_t workspace_bytes, hipStream_t stream) {
     ssm_status_t st = check_heads(H, G, D, dtype, scale);
     if (st != SSM_OK) return st;
     int64_t tq = 0, tk = 0;
@@ -259,29 +285,32 @@ ssm_status_t ssm_attn_fwd(const void *q, const void *k, const void *v, float sca
     Prompt c;
     if ((st = c.set(*rows, tq, tk, H, G, D, dtype, strides)) != SSM_OK) return st;
     if ((tq > 0 && (!q || !o)) || (tk > 0 && (!k || !v))) return SSM_ERR_NULL;
-    const int64_t es = dtype == SSM_BF16 ? 2 : 4;
-    const Span outs[] = {{o, tq * H * D * es}, {lse, tq * H * 4}};
+    const int64_t es = dtype == SSM_BF16 ? 2 : 4, need = fwd_bytes(*rows, tq, H, G, D, dtype);
+    const Span outs[] = {{o, tq * H * D * es}, {lse, tq * H * 4}, {workspace, need}};
     const Span ins[] = {c.q.span(q, es), c.k.span(k, es), c.v.span(v, es), {rows->cu_q, offsets_bytes(*rows, rows->cu_q)},
                         {rows->cu_k, offsets_bytes(*rows, rows->cu_k)}, {rows->len_q, offsets_bytes(*rows, rows->len_q)},
                         {rows->len_k, offsets_bytes(*rows, rows->len_k)}};
     if (any_overlap(outs, ins)) return SSM_ERR_ALIAS;
     if (tq == 0 || rows->Lq == 0) return SSM_OK;
+    Scratch scratch;
+    if ((st = scratch.take(workspace, workspace_bytes, need, stream)) != SSM_OK) return st;
     SoftmaxLaunch &p = c.p;
+    p.part = static_cast<float *>(scratch.p);
     p.q = q; p.k = k; p.v = v; p.o = o; p.lse = lse;
     p.scale = scale;
     p.causal = causal != 0;
     p.vec = c.q.vec(q, es) && c.k.vec(k, es) && c.v.vec(v, es) && aligned16(o);
-    return ssm::launch_softmax_fwd(p, stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+    return scratch.done(ssm::launch_softmax_fwd(p, stream), stream);
 }
 
-ssm_status_t ssm_attn_bwd_workspace(const ssm_attn_rows_t *rows, int64_t H, int64_t *bytes) {
+ssm_status_t ssm_attn_bwd_workspace(const ssm_attn_rows_t *rows, int64_t H, int64_t G, int64_t D, int64_t *bytes) {
     if (!bytes) return SSM_ERR_NULL;
-    if (H < 1 || H > kMostStep) return SSM_ERR_SHAPE;
-    int64_t tq = 0, tk = 0;
-    const ssm_status_t st = check_rows(rows, H, 1, &tq, &tk);
+    ssm_status_t st = check_heads(H, G, D, SSM_F32, 1.0f);
     if (st != SSM_OK) return st;
+    int64_t tq = 0, tk = 0;
+    if ((st = check_rows(rows, H, G, &tq, &tk)) != SSM_OK) return st;
     if (!stats_launch(tq, H)) return SSM_ERR_SHAPE;
-    *bytes = stats_bytes(tq, H);
+    *bytes = bwd_bytes(*rows, tq, tk, H, G, D);
     return SSM_OK;
 }
 
@@ -297,7 +326,7 @@ ssm_status_t ssm_attn_bwd(const void *q, const void *k, const void *v, const voi
     Prompt c;
     if ((st = c.set(*rows, tq, tk, H, G, D, dtype, strides)) != SSM_OK) return st;
     if ((tq > 0 && (!q || !o || !lse || !do_ || !dq)) || (tk > 0 && (!k || !v || !dk || !dv))) return SSM_ERR_NULL;
-    const int64_t es = dtype == SSM_BF16 ? 2 : 4, need = stats_bytes(tq, H);
+    const int64_t es = dtype == SSM_BF16 ? 2 : 4, need = bwd_bytes(*rows, tq, tk, H, G, D);
     const Span outs[] = {{dq, tq * H * D * es}, {dk, tk * G * D * es}, {dv, tk * G * D * es}, {workspace, need}};
     const Span ins[] = {c.q.span(q, es), c.k.span(k, es), c.v.span(v, es), c.dout.span(do_, es), {o, tq * H * D * es},
                         {lse, tq * H * 4}, {rows->cu_q, offsets_bytes(*rows, rows->cu_q)},
@@ -310,6 +339,7 @@ ssm_status_t ssm_attn_bwd(const void *q, const void *k, const void *v, const voi
     p.q = q; p.k = k; p.v = v; p.o_in = o; p.lse_in = lse; p.dout = do_;
     p.dq = dq; p.dk = dk; p.dv = dv;
     p.stats = static_cast<float *>(scratch.p);
+    p.part = p.stats + stats_bytes(tq, H) / 4;
     p.scale = scale;
     p.causal = causal != 0;
     p.vec = c.q.vec(q, es) && c.k.vec(k, es) && c.v.vec(v, es) && c.dout.vec(do_, es) && aligned16(o) && aligned16(dq) &&

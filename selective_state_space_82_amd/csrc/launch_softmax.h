@@ -22,6 +22,9 @@ struct SoftmaxLaunch {
     void *o, *dq, *dk, *dv;
     float *lse;
     float *stats;  // gradient: [2][H][tokens]: lse·log2 e and −delta of each head and query
+    float *part;   // results of pieces, where a walk is cut (SoftmaxWork): the forward call's [splits][tokens][H][D], then
+                   // maximum and sum [splits][tokens][H][2]; dq's [splits][tokens][H][D], then sums of ds
+                   // [splits][H][tokens]; dk's [splits][tokens][G][D], then dv's
     bool vec;      // every row takes 16-byte accesses
 };
 constexpr int kSoftmaxThreads = 256;
@@ -30,43 +33,76 @@ constexpr int kSoftmaxThreads = 256;
 // should be in one; but sequences may differ in length, so that each should be spread over all. Units are therefore key heads, or,
 // where a sequence has fewer than 8, every `parts`-th block of one, and dealt to the XCDs in turn; an XCD takes its units one
 // after the other. (Units as runs of neighbours: 9 sequences of 100 to 4096 tokens, 8 key heads, gradient 6.5 ms.)
+// Where there are too few of these to fill the device, the tiles that a block walks are cut into up to `splits` pieces of at
+// least `least` tiles, a workgroup each, and a second launch joins them.
 struct SoftmaxWork {
     int64_t units, each;  // each: workgroups of a unit
-    int parts, per, blocks;
+    int parts, per, blocks, splits, least;
     bool across;  // an XCD takes the first block of each of its units, then the second of each, ...; otherwise unit by unit
 };  // workgroups number less than 2^24
-inline SoftmaxWork softmax_work(int64_t b, int64_t G, int64_t per, int64_t blocks) {
+inline SoftmaxWork softmax_work(int64_t b, int64_t G, int64_t per, int64_t blocks, int64_t splits, int64_t least) {
     const int64_t parts = G >= 8 || blocks < 2 ? 1 : ((8 + G - 1) / G < blocks ? (8 + G - 1) / G : blocks);
-    const int64_t units = b * G * parts, each = per * ((blocks + parts - 1) / parts);
+    const int64_t units = b * G * parts, each = per * splits * ((blocks + parts - 1) / parts);
     // The last unit's longest blocks should not start when all else is done: where a unit does not fill an XCD (32 compute units,
     // two workgroups each) and there are rounds enough for that to matter. (4 sequences of 2048, 24 heads, gradient: 314 us unit
     // by unit, 264 across; 8 of 4096, 32 heads on 8 key heads, forward: 1091 and 1139.)
-    return {units, each, (int)parts, (int)per, (int)blocks, each < 64 && (units + 7) / 8 * each >= 128};
+    return {units, each, (int)parts, (int)per, (int)blocks, (int)splits, (int)least,
+            each < 64 && (units + 7) / 8 * each >= 128};
 }
 inline int64_t softmax_groups(const SoftmaxWork &w) { return (w.units + 7) / 8 * 8 * w.each; }
-// Of a workgroup: sequence, key head, which of the `per`, and which block counted from the first to be taken; false: none.
+// Of a workgroup: sequence, key head, which of the `per`, which block counted from the first to be taken, which piece of it;
+// false: none.
 struct SoftmaxPlace {
     int64_t seq;
-    int g, which, block;
+    int g, which, block, piece;
 };
 SSM_BOTH bool softmax_place(const SoftmaxWork &w, int64_t G, uint32_t id, SoftmaxPlace *p) {
     const uint32_t turn = id >> 3, each = (uint32_t)w.each, mine = ((uint32_t)w.units + 7) / 8;  // an XCD's units
     const uint32_t unit = (w.across ? turn % mine : turn / each) * 8 + (id & 7), at = w.across ? turn / mine : turn % each;
-    const uint32_t head = unit / (uint32_t)w.parts, part = unit % (uint32_t)w.parts;
+    const uint32_t head = unit / (uint32_t)w.parts, part = unit % (uint32_t)w.parts, row = at / (uint32_t)w.splits;
     p->seq = head / (uint32_t)G;
     p->g = (int)(head % (uint32_t)G);
-    p->which = (int)(at % (uint32_t)w.per);
-    p->block = (int)(at / (uint32_t)w.per * (uint32_t)w.parts + part);
+    p->piece = (int)(at % (uint32_t)w.splits);
+    p->which = (int)(row % (uint32_t)w.per);
+    p->block = (int)(row / (uint32_t)w.per * (uint32_t)w.parts + part);
     return unit < (uint32_t)w.units && p->block < w.blocks;
 }
+// Tiles of each piece of a walk of `tiles`, and how many pieces it has.
+SSM_BOTH int softmax_piece(const SoftmaxWork &w, int tiles, int *pieces) {
+    int per = (tiles + w.splits - 1) / w.splits;
+    per = per < w.least ? w.least : per;
+    *pieces = tiles > per ? (tiles + per - 1) / per : 1;
+    return per;
+}
+
 // The forward kernel and the gradient's for the queries take 128 queries to a workgroup, the gradient's for the keys 128 keys.
 constexpr int kSoftmaxBlock = 128;
-inline SoftmaxWork softmax_fwd_work(const AttnRows &r, int64_t H, int64_t G) {
-    return softmax_work(r.b, G, H / G, (r.Lq + kSoftmaxBlock - 1) / kSoftmaxBlock);
+constexpr int64_t kSoftmaxLeast = 256;  // keys or queries of a piece
+// Blocks that there are, of b sequences of at most L tokens: packed sequences have as many as their tokens say, or b more.
+inline int64_t softmax_blocks(const AttnRows &r, int64_t L, int64_t tokens) {
+    const int64_t all = r.b * ((L + kSoftmaxBlock - 1) / kSoftmaxBlock), some = tokens / kSoftmaxBlock + (r.b < tokens ? r.b : tokens);
+    return r.cu_q && some < all ? some : all;
 }
-inline SoftmaxWork softmax_dq_work(const AttnRows &r, int64_t H, int64_t G) { return softmax_fwd_work(r, H, G); }
-inline SoftmaxWork softmax_dkv_work(const AttnRows &r, int64_t G) {
-    return softmax_work(r.b, G, 1, (r.Lk + kSoftmaxBlock - 1) / kSoftmaxBlock);
+// Pieces for `groups` blocks of walks of up to `tiles` tiles where `fill` workgroups fill the device.
+inline int64_t softmax_splits(int64_t groups, int64_t tiles, int64_t least, int64_t fill) {
+    int64_t n = groups > 0 ? (fill + groups - 1) / groups : 1;
+    const int64_t most = (tiles + least - 1) / least;
+    n = n < 16 ? n : 16;
+    return n < most ? n : (most > 1 ? most : 1);
+}
+inline SoftmaxWork softmax_query_work(const AttnRows &r, int64_t H, int64_t G, int64_t keys) {
+    const int64_t least = kSoftmaxLeast / keys;
+    const int64_t splits = softmax_splits(softmax_blocks(r, r.Lq, r.Tq) * H, (r.Lk + keys - 1) / keys, least, 512);
+    return softmax_work(r.b, G, H / G, (r.Lq + kSoftmaxBlock - 1) / kSoftmaxBlock, splits, least);
+}
+inline SoftmaxWork softmax_fwd_work(const AttnRows &r, int64_t H, int64_t G, bool bf16) {
+    return softmax_query_work(r, H, G, bf16 ? 64 : 32);  // keys of a tile
+}
+inline SoftmaxWork softmax_dq_work(const AttnRows &r, int64_t H, int64_t G) { return softmax_query_work(r, H, G, 32); }
+inline SoftmaxWork softmax_dkv_work(const AttnRows &r, int64_t H, int64_t G) {
+    const int64_t splits =
+        softmax_splits(softmax_blocks(r, r.Lk, r.Tk) * G, (r.Lq + 31) / 32 * (H / G), kSoftmaxLeast / 32, 256);
+    return softmax_work(r.b, G, 1, (r.Lk + kSoftmaxBlock - 1) / kSoftmaxBlock, splits, kSoftmaxLeast / 32);
 }
 hipError_t launch_softmax_fwd(const SoftmaxLaunch &p, hipStream_t stream);
 hipError_t launch_softmax_bwd(const SoftmaxLaunch &p, hipStream_t stream);

@@ -89,6 +89,13 @@ __global__ __launch_bounds__(2 * kSoftmaxThreads, DP * sizeof(T) > 128 ? 2 : 4) 
     }
     const int first = k0 < s.nk ? first_query(s, a.causal, k0) / QB : 0;
     const int tiles = k0 < s.nk ? (s.nq + QB - 1) / QB - first : 0;  // a head
+    // The piece's rounds, a tile each, from tile t0 of head h0 of the group on; the second wavefronts take one more, the first of
+    // which only starts.
+    int pieces;
+    const int per = softmax_piece(work, tiles * R, &pieces), begin = at.piece * per;
+    if (at.piece >= pieces) return;
+    const int rounds = pieces > 1 && tiles * R - begin > per ? per : tiles * R - begin;
+    const int h0 = tiles > 0 ? begin / tiles : 0, t0 = tiles > 0 ? begin % tiles : 0;
     const float sc = scale_of(a.scale);
     // the lane's key is seen by queries lo .. nq - 1, and all of the wavefront's keys by those from all_lo on
     const int lo = key < s.nk ? first_query(s, a.causal, key) : s.nq;
@@ -104,10 +111,10 @@ __global__ __launch_bounds__(2 * kSoftmaxThreads, DP * sizeof(T) > 128 ? 2 : 4) 
     const int64_t token = (packed ? s.q0 : is * a.rows.Lq) + first * QB;
     const int64_t step_t = second ? a.do_t : a.q_t, step_h = second ? a.do_h : a.q_h, batch = second ? a.do_b : a.q_b;
     const T *rp = static_cast<const T *>(second ? a.dout : a.q) + is * batch + (s.q0 + first * QB) * step_t +
-                  (int64_t)g * R * step_h;
-    const float *sp = a.stats + (second ? tokens * a.H : 0) + (int64_t)g * R * tokens + token;
+                  (int64_t)(g * R + h0) * step_h + t0 * QB * step_t;
+    const float *sp = a.stats + (second ? tokens * a.H : 0) + (int64_t)(g * R + h0) * tokens + token + t0 * QB;
     const int64_t tile_step = QB * step_t, turn_step = step_h - (tiles - 1) * tile_step;
-    int left = tiles * R, t = 0, stats_left = tiles * R, st = 0;  // still to load, and the next one's place among its head's
+    int left = rounds, t = t0, stats_left = rounds, st = t0;  // still to load, and the next one's place among its head's
     const auto fetch_rows = [&](char *tile) {
         load(rp, left > 0 ? s.nq - (first + t) * QB : 0, tile);
         const bool turn = ++t == tiles;
@@ -122,7 +129,6 @@ __global__ __launch_bounds__(2 * kSoftmaxThreads, DP * sizeof(T) > 128 ? 2 : 4) 
         if (turn) st = 0;
         --stats_left;
     };
-    const int rounds = tiles * R;  // the second wavefronts take one more, the first of which only starts
 
     // In round n the first wavefronts use tile n's gradients' columns and tile n + 1's queries' rows, the second tile n's gradients'
     // rows and tile n − 1's queries' columns. Queries are loaded two rounds ahead into one of four buffers, the rest one
@@ -138,7 +144,7 @@ __global__ __launch_bounds__(2 * kSoftmaxThreads, DP * sizeof(T) > 128 ? 2 : 4) 
 #pragma unroll
             for (int c = 0; c < NC; ++c) mma(p, row_frag<T, DP>(qt + b * kTileBytes, 0, c), kv[c]);
         };
-        int tile = 0;
+        int tile = t0;
         const auto round = [&](auto B, f16 &p, f16 &next) {
             constexpr int b = B, odd = b & 1;
             landed();
@@ -240,8 +246,17 @@ __global__ __launch_bounds__(2 * kSoftmaxThreads, DP * sizeof(T) > 128 ? 2 : 4) 
     }
 
     const int64_t row = (packed ? s.k0 : is * a.rows.Lk) + r0;
-    const int rows = to_write - r0 > 32 ? 32 : to_write - r0;
     const uint32_t stride = (uint32_t)(a.G * a.D);
+    if (pieces > 1) {
+        const int64_t tokens_k = packed ? a.rows.Tk : a.rows.b * a.rows.Lk;
+        const int rows = s.nk - r0 > 32 ? 32 : s.nk - r0;
+        float *to = a.part + (((second ? 0 : work.splits) + at.piece) * tokens_k + row) * a.G * a.D + g * a.D;
+        const Buffer out = la::rows_buffer(to, stride, rows, a.D);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) store_tile<float, VEC>(out, stride, col, 32 * d, col < rows ? a.D : 0, sum[d], 1.0f);
+        return;
+    }
+    const int rows = to_write - r0 > 32 ? 32 : to_write - r0;
     const Buffer out = la::rows_buffer(static_cast<T *>(second ? a.dk : a.dv) + (row * a.G + g) * a.D, stride, rows, a.D);
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
@@ -275,9 +290,16 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
     const T *vp = static_cast<const T *>(a.v) + is * a.v_b + s.k0 * a.v_t + g * a.v_h;
     const int last_q = (q0 + BQ < s.nq ? q0 + BQ : s.nq) - 1;
     const int keys = last_q >= q0 ? last_key(s, a.causal, last_q) + 1 : 0;
-    const int tiles = (keys + KB - 1) / KB;
-    const int my_last = last_key(s, a.causal, r0 + col);
-    const int wave_first = last_key(s, a.causal, r0);
+    int pieces;
+    const int per = softmax_piece(work, (keys + KB - 1) / KB, &pieces);
+    if (at.piece >= pieces) return;
+    // all counted from the piece's first key
+    const int begin = at.piece * per * KB, n_keys = pieces > 1 && keys - begin > per * KB ? per * KB : keys - begin;
+    const int tiles = (n_keys + KB - 1) / KB;
+    const int my_last = last_key(s, a.causal, r0 + col) - begin;
+    const int wave_first = last_key(s, a.causal, r0) - begin;
+    kp += begin * a.k_t;
+    vp += begin * a.v_t;
     const int64_t row = (packed ? s.q0 : is * a.rows.Lq) + r0;
 
     Frag<T> q[NC], dout[NC];
@@ -305,7 +327,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
 
     const Loader<T, KB, DP, VEC> ks((uint32_t)a.k_t, a.D), vs((uint32_t)a.v_t, a.D);
     const int64_t k_step = KB * a.k_t, v_step = KB * a.v_t;
-    int left = s.nk;  // keys from the next tile to load on
+    int left = s.nk - begin;  // keys from the next tile to load on
     const auto fetch = [&](int b) {
         ks(kp, left, kt + b * kTileBytes);
         vs(vp, left, vt + (b & 1) * kTileBytes);
@@ -369,6 +391,16 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
     }
     // Σ_j ds_ij is 0 but for the rounding of o, from which delta was formed: what is left corrects delta for dk.
     rest += other_half(rest);
+    if (pieces > 1) {
+        const int rows = s.nq - r0 > 32 ? 32 : s.nq - r0;
+        const uint32_t stride = (uint32_t)(a.H * a.D);
+        const Buffer out = la::rows_buffer(a.part + ((at.piece * tokens + row) * a.H + h) * a.D, stride, rows, a.D);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) store_tile<float, VEC>(out, stride, col, 32 * d, col < rows ? a.D : 0, dq[d], 1.0f);
+        if (half == 0 && col < rows)
+            a.part[work.splits * tokens * a.H * a.D + (at.piece * a.H + h) * tokens + row + col] = rest;
+        return;
+    }
     if (half == 0 && r0 + col < s.nq) stat[tokens * a.H] = less - rest;
     const int rows = to_write - r0 > 32 ? 32 : to_write - r0;
     const uint32_t stride = (uint32_t)(a.H * a.D);
@@ -380,23 +412,76 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
     }
 }
 
+// Sums of pieces, in their order: of a block of queries' dq, with delta's correction, or of a block of keys' dk and dv.
+template <typename T, bool KEYS>
+__global__ __launch_bounds__(kSoftmaxThreads) void softmax_bwd_join_kernel(SoftmaxLaunch a, SoftmaxWork work) {
+    SoftmaxPlace at;
+    if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
+    const AttnSeq s = sequence(a.rows, at.seq);
+    const bool packed = a.rows.cu_q != nullptr;
+    const int n = KEYS ? s.nk : s.nq, first = (KEYS ? at.block : work.blocks - 1 - at.block) * kSoftmaxBlock;
+    const int rows = n - first > kSoftmaxBlock ? kSoftmaxBlock : n - first;
+    if (rows <= 0) return;  // one piece
+    const int tiles = KEYS ? ((s.nq + 31) / 32 - first_query(s, a.causal, first) / 32) * (a.H / a.G)
+                           : (last_key(s, a.causal, first + rows - 1) + 32) / 32;
+    int pieces;
+    softmax_piece(work, tiles, &pieces);
+    if (pieces < 2) return;
+    const int64_t L = KEYS ? a.rows.Lk : a.rows.Lq, tokens = packed ? (KEYS ? a.rows.Tk : a.rows.Tq) : a.rows.b * L;
+    // rows past the sequence's (a padded batch) are 0
+    const int past = packed ? rows : (int)(L - first > kSoftmaxBlock ? kSoftmaxBlock : L - first);
+    const int64_t row0 = (packed ? (KEYS ? s.k0 : s.q0) : at.seq * L) + first;
+    const int heads = KEYS ? a.G : a.H, h = KEYS ? at.g : at.g * work.per + at.which;
+    const int64_t apart = tokens * heads * a.D;  // floats of a piece
+    const int w = la::wave_id(), l = threadIdx.x & 63;
+    // a workgroup takes every splits-th group of four rows
+    for (int r = at.piece * 4 + w; r < past; r += 4 * work.splits) {
+        const int64_t to = ((row0 + r) * heads + h) * a.D;
+        const int m = r < rows ? pieces : 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int d = l + 64 * u;
+            if (d >= a.D) continue;
+            float x = 0.0f, y = 0.0f;
+            for (int i = 0; i < m; ++i) {
+                x += a.part[i * apart + to + d];
+                if (KEYS) y += a.part[(work.splits + i) * apart + to + d];
+            }
+            static_cast<T *>(KEYS ? a.dk : a.dq)[to + d] = narrow<T>(x * a.scale);
+            if (KEYS) static_cast<T *>(a.dv)[to + d] = narrow<T>(y);
+        }
+        if (!KEYS && l == 0 && m > 0) {
+            float rest = 0.0f;
+            for (int i = 0; i < pieces; ++i) rest += a.part[work.splits * apart + (i * a.H + h) * tokens + row0 + r];
+            a.stats[(a.H + h) * tokens + row0 + r] -= rest;
+        }
+    }
+}
+
 template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, hipStream_t stream) {
     const int64_t tokens = p.rows.cu_q ? p.rows.Tq : p.rows.b * p.rows.Lq;
-    const SoftmaxWork kw = softmax_dkv_work(p.rows, p.G), qw = softmax_dq_work(p.rows, p.H, p.G);
+    const SoftmaxWork kw = softmax_dkv_work(p.rows, p.H, p.G), qw = softmax_dq_work(p.rows, p.H, p.G);
     constexpr int64_t per = kSoftmaxThreads / kStatsLanes;
+    hipError_t e = hipSuccess;
     if (tokens > 0) {
         softmax_stats_kernel<T, VEC><<<dim3((unsigned)((tokens * p.H + per - 1) / per)), kSoftmaxThreads, 0, stream>>>(p, tokens);
-        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (qw.blocks > 0) {
-        softmax_dq_kernel<T, DP, VEC>
-            <<<dim3((unsigned)softmax_groups(qw)), kSoftmaxThreads, 0, stream>>>(p, qw, tokens);
-        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        const dim3 grid((unsigned)softmax_groups(qw));
+        softmax_dq_kernel<T, DP, VEC><<<grid, kSoftmaxThreads, 0, stream>>>(p, qw, tokens);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (qw.splits > 1) softmax_bwd_join_kernel<T, false><<<grid, kSoftmaxThreads, 0, stream>>>(p, qw);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    if (kw.blocks > 0)
-        softmax_dkv_kernel<T, DP, VEC>
-            <<<dim3((unsigned)softmax_groups(kw)), 2 * kSoftmaxThreads, 0, stream>>>(p, kw, tokens);
-    return hipGetLastError();
+    if (kw.blocks > 0) {
+        const dim3 grid((unsigned)softmax_groups(kw));
+        softmax_dkv_kernel<T, DP, VEC><<<grid, 2 * kSoftmaxThreads, 0, stream>>>(p, kw, tokens);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (kw.splits > 1) softmax_bwd_join_kernel<T, true><<<grid, kSoftmaxThreads, 0, stream>>>(p, kw);
+        e = hipGetLastError();
+    }
+    return e;
 }
 template <typename T> hipError_t by_width(const SoftmaxLaunch &p, hipStream_t stream) {
     if (!p.vec) return p.D <= 64 ? run<T, 64, false>(p, stream) : run<T, 128, false>(p, stream);

@@ -41,9 +41,19 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
     // tiles up to the last key that the block's last query sees; of the first `full` every query sees every key
     const int last_q = (q0 + BQ < s.nq ? q0 + BQ : s.nq) - 1;
     const int keys = last_q >= q0 ? last_key(s, a.causal, last_q) + 1 : 0;
-    const int tiles = (keys + KB - 1) / KB, full = keys > 0 ? (last_key(s, a.causal, q0) + 1) / KB : 0;
-    const int my_last = last_key(s, a.causal, r0 + col);  // of the lane's query
-    const int wave_last = r0 < s.nq ? last_key(s, a.causal, (r0 + 32 < s.nq ? r0 + 32 : s.nq) - 1) : -1;
+    int pieces;
+    const int per = softmax_piece(work, (keys + KB - 1) / KB, &pieces);
+    if (at.piece >= pieces) return;
+    // all counted from the piece's first key
+    const int begin = at.piece * per * KB, n_keys = pieces > 1 && keys - begin > per * KB ? per * KB : keys - begin;
+    const int tiles = (n_keys + KB - 1) / KB;
+    int full = keys > 0 ? (last_key(s, a.causal, q0) + 1 - begin) / KB : 0;
+    full = full < 0 ? 0 : full > tiles ? tiles : full;
+    const int my_last = last_key(s, a.causal, r0 + col) - begin;  // of the lane's query
+    const int wave_last = r0 < s.nq ? last_key(s, a.causal, (r0 + 32 < s.nq ? r0 + 32 : s.nq) - 1) - begin : -1;
+    const int there = s.nk - begin;
+    kp += begin * a.k_t;
+    vp += begin * a.v_t;
 
     Frag<T> q[NC];
     {
@@ -64,8 +74,8 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
 
     const Loader<T, KB, DP, VEC> ks((uint32_t)a.k_t, a.D), vs((uint32_t)a.v_t, a.D);
     // Past the last tile nothing is read: the buffer has no rows then, and zeros land in a place that nobody looks at.
-    const auto load_k = [&](int j, int b) { ks(kp + (int64_t)j * KB * a.k_t, s.nk - j * KB, kt[b]); };
-    const auto load_v = [&](int j, int b) { vs(vp + (int64_t)j * KB * a.v_t, s.nk - j * KB, vt[b]); };
+    const auto load_k = [&](int j, int b) { ks(kp + (int64_t)j * KB * a.k_t, there - j * KB, kt[b]); };
+    const auto load_v = [&](int j, int b) { vs(vp + (int64_t)j * KB * a.v_t, there - j * KB, vt[b]); };
     const auto scores = [&](f16(&p)[NT], int b) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) p[t] = f16(0.0f);
@@ -200,10 +210,25 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
     }
     sum += other_half(sum);
 
+    const int64_t row = (packed ? s.q0 : is * a.rows.Lq) + r0;
+    if (pieces > 1) {
+        const int64_t tokens = packed ? a.rows.Tq : a.rows.b * a.rows.Lq;
+        const int64_t first = (at.piece * tokens + row) * a.H + h;
+        const int rows = s.nq - r0 > 32 ? 32 : s.nq - r0;
+        const Buffer out = la::rows_buffer(a.part + first * a.D, (uint32_t)(a.H * a.D), rows, a.D);
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+            store_tile<float, VEC>(out, (uint32_t)(a.H * a.D), col, 32 * d, col < rows ? a.D : 0, o[d], 1.0f);
+        if (half == 0 && col < rows) {
+            float *ms = a.part + work.splits * tokens * a.H * a.D + 2 * (first + (int64_t)col * a.H);
+            ms[0] = m;
+            ms[1] = sum;
+        }
+        return;
+    }
     // rows past the sequence's queries (a padded batch): no keys, 0 and -inf
     const bool live = r0 + col < s.nq && !(sum == 0.0f);
     const float f = live ? 1.0f / sum : 0.0f;
-    const int64_t row = (packed ? s.q0 : is * a.rows.Lq) + r0;
     int rows = to_write - r0;
     rows = rows > 32 ? 32 : rows;
     const uint32_t stride = (uint32_t)(a.H * a.D);
@@ -217,9 +242,53 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
         a.lse[(row + col) * a.H + h] = live ? (m + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 
+// The pieces of a block of queries, in their order. (Blocks with one piece are written already.)
+template <typename T> __global__ __launch_bounds__(kSoftmaxThreads) void softmax_fwd_join_kernel(SoftmaxLaunch a, SoftmaxWork work) {
+    constexpr int KB = kKeys<T>;
+    SoftmaxPlace at;
+    if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
+    const int h = at.g * work.per + at.which, q0 = (work.blocks - 1 - at.block) * kSoftmaxBlock;
+    const AttnSeq s = sequence(a.rows, at.seq);
+    const bool packed = a.rows.cu_q != nullptr;
+    const int rows = s.nq - q0 > kSoftmaxBlock ? kSoftmaxBlock : s.nq - q0;
+    if (rows <= 0) return;  // one piece
+    // rows past the sequence's queries (a padded batch) are 0, -inf
+    const int past = packed ? rows : (int)(a.rows.Lq - q0 > kSoftmaxBlock ? kSoftmaxBlock : a.rows.Lq - q0);
+    int pieces;
+    softmax_piece(work, (last_key(s, a.causal, q0 + rows - 1) + KB) / KB, &pieces);
+    if (pieces < 2) return;
+    const int64_t tokens = packed ? a.rows.Tq : a.rows.b * a.rows.Lq, row0 = (packed ? s.q0 : at.seq * a.rows.Lq) + q0;
+    const float *ms = a.part + work.splits * tokens * a.H * a.D;
+    const int w = la::wave_id(), l = threadIdx.x & 63;
+    // a workgroup takes every splits-th group of four rows
+    for (int r = at.piece * 4 + w; r < past; r += 4 * work.splits) {
+        const int64_t to = (row0 + r) * a.H + h;
+        float most = -INFINITY, total = 0.0f, x[2] = {0.0f, 0.0f};
+        const int n = r < rows ? pieces : 0;
+        for (int i = 0; i < n; ++i) most = __builtin_fmaxf(most, ms[2 * (i * tokens * a.H + to)]);
+        const float base = most == -INFINITY ? 0.0f : most;
+        for (int i = 0; i < n; ++i) {
+            const int64_t from = i * tokens * a.H + to;
+            const float f = exp2_fast(ms[2 * from] - base);
+            total = __builtin_fmaf(f, ms[2 * from + 1], total);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (l + 64 * u < a.D) x[u] = __builtin_fmaf(f, a.part[from * a.D + l + 64 * u], x[u]);
+        }
+        const bool live = !(total == 0.0f);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (l + 64 * u < a.D) static_cast<T *>(a.o)[to * a.D + l + 64 * u] = narrow<T>(live ? x[u] / total : 0.0f);
+        if (a.lse && l == 0) a.lse[to] = live ? (base + __builtin_amdgcn_logf(total)) * 0.69314718055994530942f : -INFINITY;
+    }
+}
+
 template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, hipStream_t stream) {
-    const SoftmaxWork w = softmax_fwd_work(p.rows, p.H, p.G);
-    softmax_fwd_kernel<T, DP, VEC><<<dim3((unsigned)softmax_groups(w)), kSoftmaxThreads, 0, stream>>>(p, w);
+    const SoftmaxWork w = softmax_fwd_work(p.rows, p.H, p.G, p.bf16);
+    const dim3 grid((unsigned)softmax_groups(w));
+    softmax_fwd_kernel<T, DP, VEC><<<grid, kSoftmaxThreads, 0, stream>>>(p, w);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (w.splits > 1) softmax_fwd_join_kernel<T><<<grid, kSoftmaxThreads, 0, stream>>>(p, w);
     return hipGetLastError();
 }
 template <typename T> hipError_t by_width(const SoftmaxLaunch &p, hipStream_t stream) {

@@ -105,20 +105,41 @@ static void places() {
     for (const int64_t b : {1, 2, 5})
         for (const int64_t G : {1, 3, 7, 8, 12})
             for (const int64_t per : {1, 4})
-                for (const int64_t blocks : {0, 1, 2, 5, 16, 33}) {
-                    const SoftmaxWork w = softmax_work(b, G, per, blocks);
-                    std::vector<int> seen((size_t)(b * G * per * blocks), 0), of(8, 0);
-                    for (int64_t id = 0; id < softmax_groups(w); ++id) {
-                        SoftmaxPlace p;
-                        if (!softmax_place(w, G, (uint32_t)id, &p)) continue;
-                        CHECK(p.seq >= 0 && p.seq < b && p.g >= 0 && p.g < G && p.which < per && p.block >= 0 && p.block < blocks);
-                        ++seen[(size_t)(((p.seq * G + p.g) * per + p.which) * blocks + p.block)];
-                        if (p.seq == 0) ++of[(size_t)(id & 7)];
+                for (const int64_t splits : {1, 3})
+                    for (const int64_t blocks : {0, 1, 2, 5, 16, 33}) {
+                        const SoftmaxWork w = softmax_work(b, G, per, blocks, splits, 8);
+                        std::vector<int> seen((size_t)(b * G * per * blocks * splits), 0), of(8, 0);
+                        for (int64_t id = 0; id < softmax_groups(w); ++id) {
+                            SoftmaxPlace p;
+                            if (!softmax_place(w, G, (uint32_t)id, &p)) continue;
+                            CHECK(p.seq >= 0 && p.seq < b && p.g >= 0 && p.g < G && p.which < per && p.block >= 0 &&
+                                  p.block < blocks && p.piece >= 0 && p.piece < splits);
+                            ++seen[(size_t)((((p.seq * G + p.g) * per + p.which) * blocks + p.block) * splits + p.piece)];
+                            if (p.seq == 0) ++of[(size_t)(id & 7)];
+                        }
+                        for (const int n : seen) CHECK(n == 1);
+                        if (blocks >= 8)
+                            for (const int n : of) CHECK(n > 0);
                     }
-                    for (const int n : seen) CHECK(n == 1);
-                    if (blocks >= 8)
-                        for (const int n : of) CHECK(n > 0);
-                }
+    // pieces cover a walk, none of them empty
+    for (int splits = 1; splits < 17; ++splits)
+        for (const int least : {4, 8})
+            for (int tiles = 0; tiles < 200; ++tiles) {
+                SoftmaxWork w{};
+                w.splits = splits;
+                w.least = least;
+                int pieces = 0;
+                const int per = softmax_piece(w, tiles, &pieces);
+                CHECK(pieces >= 1 && pieces <= splits && (int64_t)per * pieces >= tiles);
+                CHECK(pieces == 1 || (pieces - 1) * per < tiles);
+                CHECK(pieces == 1 || per >= least);
+            }
+    const AttnRows one{nullptr, nullptr, nullptr, nullptr, 1, 4096, 4096, 0, 0};
+    CHECK(softmax_fwd_work(one, 2, 1, true).splits == 8 && softmax_fwd_work(one, 16, 1, true).splits == 1);
+    CHECK(softmax_dkv_work(one, 2, 1).splits == 8);
+    const int32_t cu[2] = {0, 0};
+    const AttnRows packed{cu, cu, nullptr, nullptr, 64, 4096, 4096, 1280, 1280};  // few tokens of many short sequences
+    CHECK(softmax_blocks(packed, 4096, 1280) == 74);
 }
 
 static void host_code() {
@@ -129,16 +150,19 @@ static void host_code() {
     const auto in = [&](int i) { return (const int32_t *)at(i); };
     ssm_attn_rows_t rows{nullptr, nullptr, nullptr, nullptr, 2, 3, 3, 0, 0};
     int launches = g_launches;
-    CHECK(ssm_attn_fwd(at(0), at(1), at(2), 1.0f, 1, &rows, at(3), fl(4), 2, 1, 8, SSM_F32, nullptr, nullptr) == SSM_OK);
+    CHECK(ssm_attn_fwd(at(0), at(1), at(2), 1.0f, 1, &rows, at(3), fl(4), 2, 1, 8, SSM_F32, nullptr, nullptr, 0, nullptr) == SSM_OK);
     CHECK(g_launches == ++launches && g_last.vec && g_last.q_t == 16 && g_last.q_b == 48 && g_last.k_t == 8);
-    CHECK(ssm_attn_fwd((char *)at(0) + 4, at(1), at(2), 1.0f, 1, &rows, at(3), nullptr, 2, 1, 8, SSM_F32, nullptr, nullptr) == SSM_OK);
+    CHECK(ssm_attn_fwd((char *)at(0) + 4, at(1), at(2), 1.0f, 1, &rows, at(3), nullptr, 2, 1, 8, SSM_F32, nullptr, nullptr, 0,
+                       nullptr) == SSM_OK);
     CHECK(g_launches == ++launches && !g_last.vec);
     rows.Lq = 0;
-    CHECK(ssm_attn_fwd(nullptr, at(1), at(2), 1.0f, 1, &rows, nullptr, nullptr, 2, 1, 8, SSM_F32, nullptr, nullptr) == SSM_OK);
+    CHECK(ssm_attn_fwd(nullptr, at(1), at(2), 1.0f, 1, &rows, nullptr, nullptr, 2, 1, 8, SSM_F32, nullptr, nullptr, 0,
+                       nullptr) == SSM_OK);
     CHECK(g_launches == launches);
     rows = {in(10), in(11), nullptr, nullptr, 2, 5, 5, 7, 7};
     int64_t need = 0;
-    CHECK(ssm_attn_bwd_workspace(&rows, 2, &need) == SSM_OK && need == 7 * 2 * 2 * 4);
+    CHECK(ssm_attn_fwd_workspace(&rows, 2, 1, 8, SSM_BF16, &need) == SSM_OK && need == 0);
+    CHECK(ssm_attn_bwd_workspace(&rows, 2, 1, 8, &need) == SSM_OK && need == 256);
     CHECK(ssm_attn_bwd(at(0), at(1), at(2), at(3), fl(4), at(5), 1.0f, 0, &rows, at(6), at(7), at(8), 2, 1, 8, SSM_BF16, nullptr,
                        at(9), need, nullptr) == SSM_OK);
     CHECK(g_launches == ++launches && g_last.bf16 && !g_last.causal && g_last.q_b == 0 && g_last.stats == at(9));

@@ -129,6 +129,16 @@ def test_more_keys_or_queries(layout, causal, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("layout", ["packed", "padded"])
+@pytest.mark.parametrize("lens,lens_k,H,G,D", [([1000, 300, 40], None, 2, 1, 64), ([700], [1500], 4, 1, 20),
+                                               ([5, 900], [600, 300], 3, 3, 128), ([1, 2], [513, 1100], 1, 1, 33)])
+def test_cut_walks(lens, lens_k, H, G, D, layout, causal, dtype):
+    """Few blocks and long walks: cut into pieces that a second launch joins; pieces that some queries see nothing of."""
+    check(make(lens, H, G, D, dtype, lens_k, layout, seed=D), causal)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.0, 3.0])
 def test_scales(scale, dtype):
     check(make([100], 2, 2, 32, dtype, layout="rows", seed=3), scale=scale)
@@ -186,6 +196,19 @@ def test_not_finite_where_masked(name, bad, D, dtype):
         assert hit[..., 3].all() and not hit[..., :3].any() and not hit[..., 4:].any()
     elif not math.isinf(bad):
         assert torch.isnan(o[70:150]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("at", [3, 700, 895])
+def test_not_finite_in_a_cut_walk(at, dtype):
+    x = make([900], 2, 1, 64, dtype, seed=1)
+    run = lambda: api.ssm_attn_fwd(x["q"].cuda(), x["k"].cuda(), x["v"].cuda(), **where(x)).cpu()  # noqa: E731
+    clean = run()
+    x["v"] = x["v"].clone()
+    x["v"][at, 0, 5] = math.nan
+    o = run()
+    assert torch.equal(o[:at], clean[:at]) and torch.isnan(o[at:900, :, 5]).all()
+    assert torch.isfinite(o[..., :5]).all() and torch.isfinite(o[..., 6:]).all()
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
