@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -786,65 +787,91 @@ def ssm_layernorm_bwd(x, w=None, *, dy, mean, rstd, want_dw=True, want_dbias=Tru
 def _on_gpu(t):
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("tensors must live on a ROCm GPU")
+
+
+def _alike(*tensors):
+    """Whether all are contiguous tensors of one type on one device: nothing else is left to check but shapes."""
+    a = tensors[0]
+    dtype, device = a.dtype, a.device
+    return all(isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_contiguous() and t.device == device
+               for t in tensors)
+
+
+@functools.lru_cache(maxsize=1024)
+def _attn_bytes(gradient, packed, b, Lq, Lk, tokens_q, tokens_k, H, G, D, code) -> int:
+    """Workspace bytes of ssm_attn_fwd or ssm_attn_bwd, which go by sizes alone."""
+    one = 16 if packed else None  # any address: only whether there is one matters here
+    r, n = AttnRows(one, one, None, None, b, Lq, Lk, tokens_q, tokens_k), ctypes.c_int64()
+    if gradient:
+        _raise(lib().ssm_attn_bwd_workspace(ctypes.byref(r), H, G, D, ctypes.byref(n)), "ssm_attn_bwd_workspace")
+    else:
+        _raise(lib().ssm_attn_fwd_workspace(ctypes.byref(r), H, G, D, code, ctypes.byref(n)), "ssm_attn_fwd_workspace")
+    return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _step_bytes(b, H, G, D, pages, page_size, max_pages, k_page, v_page, max_len) -> int:
+    """Workspace bytes of ssm_attn_step, which go by sizes alone."""
+    g, n = Pages(None, pages, page_size, max_pages, k_page, v_page), ctypes.c_int64()
+    _raise(lib().ssm_attn_step_workspace(b, H, G, D, ctypes.byref(g), max_len, ctypes.byref(n)), "ssm_attn_step_workspace")
+    return n.value
 
 
 def _attn_rows(q, k, cu_seqlens, max_len, cu_seqlens_k, max_len_k, lengths, lengths_k):
     """Where the sequences of q and k lie: the descriptor of a packed batch [T, heads, D] or of rows [b, L, heads, D]."""
-    r, dev = AttnRows(), q.device
-    if q.dim() != k.dim() or q.dim() not in (3, 4):
+    dev = q.device
+    if q.dim() == 4 and k.dim() == 4:
+        if cu_seqlens is not None or cu_seqlens_k is not None or max_len is not None or max_len_k is not None:
+            raise ValueError("cu_seqlens and max_len are for packed sequences [T, heads, D]")
+        b, Lq = q.shape[:2]
+        Lk = k.shape[1]
+        if lengths is not None and lengths_k is None:
+            if Lk != Lq:
+                raise ValueError("lengths of queries and keys: give lengths_k as well where there are more keys than queries")
+            lengths_k = lengths
+        _check("lengths", lengths, (b,), torch.int32, dev)
+        _check("lengths_k", lengths_k, (b,), torch.int32, dev)
+        return AttnRows(None, None, _at(lengths), _at(lengths_k), b, Lq, Lk, 0, 0)
+    if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be [b, L, heads, D], or [T, heads, D] with cu_seqlens")
-    if q.dim() == 3:
-        if cu_seqlens is None or max_len is None:
-            raise ValueError("packed sequences [T, heads, D] need cu_seqlens and max_len")
-        if lengths is not None or lengths_k is not None:
-            raise ValueError("lengths are for rows [b, L, heads, D]")
-        if (cu_seqlens_k is None) != (max_len_k is None):
-            raise ValueError("cu_seqlens_k and max_len_k go together")
-        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
-            raise ValueError("cu_seqlens must be [b + 1]")
-        r.b = cu_seqlens.shape[0] - 1
-        _check("cu_seqlens", cu_seqlens, (r.b + 1,), torch.int32, dev)
-        _check("cu_seqlens_k", cu_seqlens_k, (r.b + 1,), torch.int32, dev)
-        r.cu_q = cu_seqlens.data_ptr()
-        r.cu_k = r.cu_q if cu_seqlens_k is None else cu_seqlens_k.data_ptr()
-        r.Lq, r.Lk = max_len, max_len if max_len_k is None else max_len_k
-        r.tokens_q, r.tokens_k = q.shape[0], k.shape[0]
-        return r
-    if cu_seqlens is not None or cu_seqlens_k is not None or max_len is not None or max_len_k is not None:
-        raise ValueError("cu_seqlens and max_len are for packed sequences [T, heads, D]")
-    r.b, r.Lq = q.shape[:2]
-    r.Lk = k.shape[1]
-    if lengths is not None and lengths_k is None:
-        if r.Lk != r.Lq:
-            raise ValueError("lengths of queries and keys: give lengths_k as well where there are more keys than queries")
-        lengths_k = lengths
-    _check("lengths", lengths, (r.b,), torch.int32, dev)
-    _check("lengths_k", lengths_k, (r.b,), torch.int32, dev)
-    r.len_q, r.len_k = _at(lengths), _at(lengths_k)
-    return r
+    if cu_seqlens is None or max_len is None:
+        raise ValueError("packed sequences [T, heads, D] need cu_seqlens and max_len")
+    if lengths is not None or lengths_k is not None:
+        raise ValueError("lengths are for rows [b, L, heads, D]")
+    if (cu_seqlens_k is None) != (max_len_k is None):
+        raise ValueError("cu_seqlens_k and max_len_k go together")
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be a torch.Tensor [b + 1]")
+    b = cu_seqlens.shape[0] - 1
+    _check("cu_seqlens", cu_seqlens, (b + 1,), torch.int32, dev)
+    _check("cu_seqlens_k", cu_seqlens_k, (b + 1,), torch.int32, dev)
+    cu_q = cu_seqlens.data_ptr()
+    cu_k = cu_q if cu_seqlens_k is None else cu_seqlens_k.data_ptr()
+    return AttnRows(cu_q, cu_k, None, None, b, max_len, max_len if max_len_k is None else max_len_k, q.shape[0], k.shape[0])
 
 
 def _attn_inputs(q, k, v):
-    """Checks q [..., H, D], k and v [..., G, D]. Returns (H, G, D, storage dtype code)."""
+    """Checks q [..., H, D], k and v [..., G, D]. Returns (H, G, D, storage dtype code, whether all are dense)."""
     _on_gpu(q)
     if q.dim() < 2 or not isinstance(k, torch.Tensor) or k.dim() != q.dim():
         raise ValueError("q and k must have the same number of axes")
     H, D = q.shape[-2:]
     G = k.shape[-2]
+    code = _dtype_code(q.dtype)
+    dense = _alike(q, k, v)
+    if dense and v.shape == k.shape and k.shape[-1] == D and (q.dim() == 3 or k.shape[0] == q.shape[0]):
+        return H, G, D, code, True
     dev, st = q.device, q.dtype
-    code = _dtype_code(st)
     _check_rows("q", q, q.shape, st, dev)
     _check_rows("k", k, (q.shape[0], *k.shape[1:-1], D) if q.dim() == 4 else (k.shape[0], G, D), st, dev)
     _check_rows("v", v, k.shape, st, dev)
-    return H, G, D, code
+    return H, G, D, code, dense
 
 
 def _attn_strides(q, k, v, do=None):
-    """As _linattn_strides, for [b, L, heads, D] or [T, heads, D]."""
-    if all(t is None or t.is_contiguous() for t in (q, k, v, do)):
-        return None
+    """As _linattn_strides, for [b, L, heads, D] or [T, heads, D] of which not all are dense."""
     s = LinAttnStrides()
     for name, t in (("q", q), ("k", k), ("v", v), ("do", do)):
         if t is not None:
@@ -873,23 +900,23 @@ def ssm_attn_fwd(q, k, v, *, scale=None, causal=True, cu_seqlens=None, max_len=N
 
     Returns o (q's shape), or (o, lse) with lse = log Σ_j e^(scale·q_i·k_j) float32 [..., H] when return_lse is set. A query
     that sees no key has o = 0 and lse = −inf."""
-    H, G, D, code = _attn_inputs(q, k, v)
+    H, G, D, code, dense = _attn_inputs(q, k, v)
     r = _attn_rows(q, k, cu_seqlens, max_len, cu_seqlens_k, max_len_k, lengths, lengths_k)
-    dev = q.device
+    dev, packed = q.device, q.dim() == 3
     with _on_device(dev):
         lse = None
         if return_lse:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if q.dim() == 4 else \
-                torch.full(q.shape[:-1], float("-inf"), dtype=torch.float32, device=dev)
+            lse = torch.full(q.shape[:-1], float("-inf"), dtype=torch.float32, device=dev) if packed else \
+                torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
         if o is None:
-            o = (torch.empty if q.dim() == 4 else torch.zeros)(q.shape, dtype=q.dtype, device=dev)
+            o = torch.zeros(q.shape, dtype=q.dtype, device=dev) if packed else torch.empty(q.shape, dtype=q.dtype, device=dev)
         else:
             _check("o", o, q.shape, q.dtype, dev)
-        n = ctypes.c_int64()
-        _raise(lib().ssm_attn_fwd_workspace(ctypes.byref(r), H, G, D, code, ctypes.byref(n)), "ssm_attn_fwd_workspace")
-        ws = _workspace(n.value, dev)
-        status = lib().ssm_attn_fwd(_at(q), _at(k), _at(v), _scale(scale, D), bool(causal), ctypes.byref(r), _at(o), _at(lse),
-                                    H, G, D, code, _attn_strides(q, k, v), _at(ws), n.value, _raw_stream(dev))
+        need = _attn_bytes(False, packed, r.b, r.Lq, r.Lk, r.tokens_q, r.tokens_k, H, G, D, code)
+        ws = _workspace(need, dev)
+        status = lib().ssm_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _scale(scale, D), bool(causal), ctypes.byref(r),
+                                    o.data_ptr(), _at(lse), H, G, D, code, None if dense else _attn_strides(q, k, v), _at(ws),
+                                    need, _raw_stream(dev))
     _raise(status, "ssm_attn_fwd")
     return (o, lse) if return_lse else o
 
@@ -899,49 +926,51 @@ def ssm_attn_bwd(q, k, v, *, o, lse, do, scale=None, causal=True, cu_seqlens=Non
     """Gradients of ssm_attn_fwd for an upstream gradient do on o, from the forward call's o and lse (contiguous; the other
     arguments as in that call). Returns a dict: dq, dk, dv (the shapes and dtype of q, k, v; dk and dv summed over the heads
     that share a key head)."""
-    H, G, D, code = _attn_inputs(q, k, v)
+    H, G, D, code, dense = _attn_inputs(q, k, v)
     r = _attn_rows(q, k, cu_seqlens, max_len, cu_seqlens_k, max_len_k, lengths, lengths_k)
-    dev, st = q.device, q.dtype
+    dev, st, packed = q.device, q.dtype, q.dim() == 3
     for name, t, shape, dtype in (("o", o, q.shape, st), ("lse", lse, q.shape[:-1], torch.float32)):
         if t is None:
             raise TypeError(f"{name} must be a torch.Tensor")
         _check(name, t, shape, dtype, dev)
     _check_rows("do", do, q.shape, st, dev)
+    dense = dense and do.is_contiguous()
     with _on_device(dev):
-        new = torch.empty if q.dim() == 4 else torch.zeros
+        new = torch.zeros if packed else torch.empty
         out = {"dq": new(q.shape, dtype=st, device=dev), "dk": new(k.shape, dtype=st, device=dev),
                "dv": new(k.shape, dtype=st, device=dev)}
-        n = ctypes.c_int64()
-        _raise(lib().ssm_attn_bwd_workspace(ctypes.byref(r), H, G, D, ctypes.byref(n)), "ssm_attn_bwd_workspace")
-        ws = _workspace(n.value, dev)
+        need = _attn_bytes(True, packed, r.b, r.Lq, r.Lk, r.tokens_q, r.tokens_k, H, G, D, code)
+        ws = _workspace(need, dev)
         status = lib().ssm_attn_bwd(_at(q), _at(k), _at(v), _at(o), _at(lse), _at(do), _scale(scale, D), bool(causal),
                                     ctypes.byref(r), _at(out["dq"]), _at(out["dk"]), _at(out["dv"]), H, G, D, code,
-                                    _attn_strides(q, k, v, do), _at(ws), n.value, _raw_stream(dev))
+                                    None if dense else _attn_strides(q, k, v, do), _at(ws), need, _raw_stream(dev))
     _raise(status, "ssm_attn_bwd")
     return out
 
 
 def _pages(k_cache, v_cache, page_table, b, G, D, dtype, dev):
     """The descriptor of a paged cache [pages, page_size, G, D] whose pages are dense."""
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a torch.Tensor [b, max_pages]")
+    most = page_table.shape[1]
+    _check("page_table", page_table, (b, most), torch.int32, dev)
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{name} must be a torch.Tensor [pages, page_size, G, D]")
-    shape = (*k_cache.shape[:2], G, D)
-    g = Pages()
+    shape = k_cache.shape
+    n, size = shape[:2]
+    if _alike(k_cache, v_cache) and v_cache.shape == shape and shape[2] == G and shape[3] == D and \
+            k_cache.dtype == dtype and k_cache.device == dev:
+        return Pages(page_table.data_ptr(), n, size, most, 0, 0)
+    apart = []
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check_rows(name, t, shape, dtype, dev)
+        _check_rows(name, t, (n, size, G, D), dtype, dev)
         st = t.stride()
-        dense = all(n == 1 or s == want for n, s, want in zip(shape[1:], st[1:], (G * D, D, 1)))
-        if not dense or (shape[0] > 1 and st[0] < shape[1] * G * D):
+        dense = all(m == 1 or s == want for m, s, want in zip(shape[1:], st[1:], (G * D, D, 1)))
+        if not dense or (n > 1 and st[0] < size * G * D):
             raise ValueError(f"the pages of {name} must be contiguous")
-        setattr(g, name[0] + "_page", st[0] if shape[0] > 1 else 0)
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-        raise ValueError("page_table must be a torch.Tensor [b, max_pages]")
-    _check("page_table", page_table, (b, page_table.shape[1]), torch.int32, dev)
-    g.page_table = page_table.data_ptr()
-    g.pages, g.page_size = shape[:2]
-    g.max_pages = page_table.shape[1]
-    return g
+        apart.append(st[0] if n > 1 else 0)
+    return Pages(page_table.data_ptr(), n, size, most, *apart)
 
 
 def ssm_attn_step(q, k_cache, v_cache, page_table, lengths, *, scale=None, max_len=0, o=None, return_lse=False):
@@ -968,45 +997,39 @@ def ssm_attn_step(q, k_cache, v_cache, page_table, lengths, *, scale=None, max_l
         else:
             _check("o", o, (b, H, D), st, dev)
         lse = torch.empty((b, H), dtype=torch.float32, device=dev) if return_lse else None
-        n = ctypes.c_int64()
-        _raise(lib().ssm_attn_step_workspace(b, H, G, D, ctypes.byref(g), max_len, ctypes.byref(n)),
-               "ssm_attn_step_workspace")
-        ws = _workspace(n.value, dev)
+        need = _step_bytes(b, H, G, D, g.pages, g.page_size, g.max_pages, g.k_page, g.v_page, max_len)
+        ws = _workspace(need, dev)
         q_b, q_h = (0, 0) if q.is_contiguous() else q.stride()[:2]
         if (q_b, q_h) == (0, 0) and not q.is_contiguous():  # one row and head for all: as a tensor of its own
             q = q.contiguous()
         status = lib().ssm_attn_step(_at(q), _at(k_cache), _at(v_cache), ctypes.byref(g), _at(lengths), _scale(scale, D),
-                                     _at(o), _at(lse), b, H, G, D, q_b, q_h, max_len, code, _at(ws), n.value,
+                                     _at(o), _at(lse), b, H, G, D, q_b, q_h, max_len, code, _at(ws), need,
                                      _raw_stream(dev))
     _raise(status, "ssm_attn_step")
     return (o, lse) if return_lse else o
 
 
-def _new_tokens(x, cu_seqlens, new_lengths, b=None):
+def _new_tokens(x, cu_seqlens, new_lengths):
     """The descriptor of new tokens x: [b, heads, D] one a row, [b, L, heads, D], or [T, heads, D] with cu_seqlens."""
-    t, dev = Tokens(), x.device
+    dev = x.device
     if x.dim() == 4:
         if cu_seqlens is not None:
             raise ValueError("cu_seqlens is for packed tokens [T, heads, D]")
-        t.b, t.L = x.shape[:2]
-        t.T = t.b * t.L
-        _check("new_lengths", new_lengths, (t.b,), torch.int32, dev)
-        t.new_lengths = _at(new_lengths)
-        return t
+        b, L = x.shape[:2]
+        _check("new_lengths", new_lengths, (b,), torch.int32, dev)
+        return Tokens(None, _at(new_lengths), b, L, b * L)
     if x.dim() != 3:
         raise ValueError("new tokens must be [b, heads, D], [b, L, heads, D], or [T, heads, D] with cu_seqlens")
     if new_lengths is not None:
         raise ValueError("new_lengths is for rows [b, L, heads, D]")
-    t.T = x.shape[0]
+    T = x.shape[0]
     if cu_seqlens is None:
-        t.b, t.L = x.shape[0], 1
-        return t
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
-        raise ValueError("cu_seqlens must be [b + 1]")
-    t.b = cu_seqlens.shape[0] - 1
-    _check("cu_seqlens", cu_seqlens, (t.b + 1,), torch.int32, dev)
-    t.cu = cu_seqlens.data_ptr()
-    return t
+        return Tokens(None, None, T, 1, T)
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be a torch.Tensor [b + 1]")
+    b = cu_seqlens.shape[0] - 1
+    _check("cu_seqlens", cu_seqlens, (b + 1,), torch.int32, dev)
+    return Tokens(cu_seqlens.data_ptr(), None, b, 0, T)
 
 
 def _rotary(freq, D, dev) -> int:
@@ -1065,17 +1088,11 @@ def ssm_kv_append(k, v, k_cache, v_cache, page_table, lengths, *, q=None, freq=N
 
 
 def _token_strides(q, k, v):
-    """Strides of new tokens: a row's single token has those of its row."""
-    if all(t is None or t.is_contiguous() for t in (q, k, v)):
+    """Strides of new tokens; a single token of a row has those of its row."""
+    if k.is_contiguous() and v.is_contiguous() and (q is None or q.is_contiguous()):
         return None
-    s = LinAttnStrides()
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t is not None:
-            st = t.stride()
-            setattr(s, f"{name}_b", st[0])
-            setattr(s, f"{name}_t", st[-3])
-            setattr(s, f"{name}_h", st[-2])
-    return ctypes.byref(s)
+    ks, vs, qs = k.stride(), v.stride(), (0, 0, 0) if q is None else q.stride()
+    return ctypes.byref(LinAttnStrides(qs[0], qs[-3], qs[-2], ks[0], ks[-3], ks[-2], vs[0], vs[-3], vs[-2]))
 
 
 def ssm_rope(x, freq, *, lengths=None, cu_seqlens=None, new_lengths=None, interleaved=False, inverse=False, out=None):

@@ -129,6 +129,7 @@ ssm_status_t check_rows(const ssm_attn_rows_t *r, int64_t H, int64_t G, int64_t 
                                       ssm::softmax_dq_work(z, H, G), ssm::softmax_dkv_work(z, H, G)}) {
         int64_t n = 0;
         if (!mul_ok((w.units + 7) / 8 * 8, w.each, &n) || !launchable(n, 2 * ssm::kSoftmaxThreads)) return SSM_ERR_SHAPE;
+        if (w.splits > 1 && !launchable(ssm::softmax_groups(ssm::softmax_join_work(w)), ssm::kSoftmaxThreads)) return SSM_ERR_SHAPE;
     }
     return SSM_OK;
 }

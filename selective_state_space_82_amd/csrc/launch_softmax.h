@@ -75,6 +75,14 @@ SSM_BOTH int softmax_piece(const SoftmaxWork &w, int tiles, int *pieces) {
     return per;
 }
 
+// The work of joining a block's pieces: 16 workgroups to a block, 32 lanes to each of its 128 rows.
+inline SoftmaxWork softmax_join_work(SoftmaxWork w) {
+    w.each = w.each / w.splits * 16;
+    w.splits = 16;
+    w.across = false;
+    return w;
+}
+
 // The forward kernel and the gradient's for the queries take 128 queries to a workgroup, the gradient's for the keys 128 keys.
 constexpr int kSoftmaxBlock = 128;
 constexpr int64_t kSoftmaxLeast = 256;  // keys or queries of a piece
@@ -92,7 +100,7 @@ inline int64_t softmax_splits(int64_t groups, int64_t tiles, int64_t least, int6
 }
 inline SoftmaxWork softmax_query_work(const AttnRows &r, int64_t H, int64_t G, int64_t keys) {
     const int64_t least = kSoftmaxLeast / keys;
-    const int64_t splits = softmax_splits(softmax_blocks(r, r.Lq, r.Tq) * H, (r.Lk + keys - 1) / keys, least, 512);
+    const int64_t splits = softmax_splits(softmax_blocks(r, r.Lq, r.Tq) * H, (r.Lk + keys - 1) / keys, least, 1024);
     return softmax_work(r.b, G, H / G, (r.Lq + kSoftmaxBlock - 1) / kSoftmaxBlock, splits, least);
 }
 inline SoftmaxWork softmax_fwd_work(const AttnRows &r, int64_t H, int64_t G, bool bf16) {
@@ -101,7 +109,7 @@ inline SoftmaxWork softmax_fwd_work(const AttnRows &r, int64_t H, int64_t G, boo
 inline SoftmaxWork softmax_dq_work(const AttnRows &r, int64_t H, int64_t G) { return softmax_query_work(r, H, G, 32); }
 inline SoftmaxWork softmax_dkv_work(const AttnRows &r, int64_t H, int64_t G) {
     const int64_t splits =
-        softmax_splits(softmax_blocks(r, r.Lk, r.Tk) * G, (r.Lq + 31) / 32 * (H / G), kSoftmaxLeast / 32, 256);
+        softmax_splits(softmax_blocks(r, r.Lk, r.Tk) * G, (r.Lq + 31) / 32 * (H / G), kSoftmaxLeast / 32, 512);
     return softmax_work(r.b, G, 1, (r.Lk + kSoftmaxBlock - 1) / kSoftmaxBlock, splits, kSoftmaxLeast / 32);
 }
 hipError_t launch_softmax_fwd(const SoftmaxLaunch &p, hipStream_t stream);

@@ -414,9 +414,9 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
 
 // Sums of pieces, in their order: of a block of queries' dq, with delta's correction, or of a block of keys' dk and dv.
 template <typename T, bool KEYS>
-__global__ __launch_bounds__(kSoftmaxThreads) void softmax_bwd_join_kernel(SoftmaxLaunch a, SoftmaxWork work) {
+__global__ __launch_bounds__(kSoftmaxThreads) void softmax_bwd_join_kernel(SoftmaxLaunch a, SoftmaxWork work, SoftmaxWork join) {
     SoftmaxPlace at;
-    if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
+    if (!softmax_place(join, a.G, blockIdx.x, &at)) return;
     const AttnSeq s = sequence(a.rows, at.seq);
     const bool packed = a.rows.cu_q != nullptr;
     const int n = KEYS ? s.nk : s.nq, first = (KEYS ? at.block : work.blocks - 1 - at.block) * kSoftmaxBlock;
@@ -428,33 +428,34 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_bwd_join_kernel(Softm
     softmax_piece(work, tiles, &pieces);
     if (pieces < 2) return;
     const int64_t L = KEYS ? a.rows.Lk : a.rows.Lq, tokens = packed ? (KEYS ? a.rows.Tk : a.rows.Tq) : a.rows.b * L;
+    const int l = threadIdx.x & 31, r = at.piece * 8 + (int)threadIdx.x / 32;
     // rows past the sequence's (a padded batch) are 0
-    const int past = packed ? rows : (int)(L - first > kSoftmaxBlock ? kSoftmaxBlock : L - first);
-    const int64_t row0 = (packed ? (KEYS ? s.k0 : s.q0) : at.seq * L) + first;
+    if (first + r >= (packed ? n : L)) return;
+    const int m = r < rows ? pieces : 0;
+    const int64_t row = (packed ? (KEYS ? s.k0 : s.q0) : at.seq * L) + first + r;
     const int heads = KEYS ? a.G : a.H, h = KEYS ? at.g : at.g * work.per + at.which;
-    const int64_t apart = tokens * heads * a.D;  // floats of a piece
-    const int w = la::wave_id(), l = threadIdx.x & 63;
-    // a workgroup takes every splits-th group of four rows
-    for (int r = at.piece * 4 + w; r < past; r += 4 * work.splits) {
-        const int64_t to = ((row0 + r) * heads + h) * a.D;
-        const int m = r < rows ? pieces : 0;
+    const int64_t apart = tokens * heads * a.D, to = (row * heads + h) * a.D;  // apart: floats of a piece
+    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < m; ++i) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int d = l + 64 * u;
+        for (int u = 0; u < 4; ++u) {
+            const int d = l + 32 * u;
             if (d >= a.D) continue;
-            float x = 0.0f, y = 0.0f;
-            for (int i = 0; i < m; ++i) {
-                x += a.part[i * apart + to + d];
-                if (KEYS) y += a.part[(work.splits + i) * apart + to + d];
-            }
-            static_cast<T *>(KEYS ? a.dk : a.dq)[to + d] = narrow<T>(x * a.scale);
-            if (KEYS) static_cast<T *>(a.dv)[to + d] = narrow<T>(y);
+            x[u] += a.part[i * apart + to + d];
+            if (KEYS) y[u] += a.part[(work.splits + i) * apart + to + d];
         }
-        if (!KEYS && l == 0 && m > 0) {
-            float rest = 0.0f;
-            for (int i = 0; i < pieces; ++i) rest += a.part[work.splits * apart + (i * a.H + h) * tokens + row0 + r];
-            a.stats[(a.H + h) * tokens + row0 + r] -= rest;
-        }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int d = l + 32 * u;
+        if (d >= a.D) continue;
+        static_cast<T *>(KEYS ? a.dk : a.dq)[to + d] = narrow<T>(x[u] * a.scale);
+        if (KEYS) static_cast<T *>(a.dv)[to + d] = narrow<T>(y[u]);
+    }
+    if (!KEYS && l == 0 && m > 0) {
+        float rest = 0.0f;
+        for (int i = 0; i < m; ++i) rest += a.part[work.splits * apart + (i * a.H + h) * tokens + row];
+        a.stats[(a.H + h) * tokens + row] -= rest;
     }
 }
 
@@ -471,14 +472,20 @@ template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, h
         const dim3 grid((unsigned)softmax_groups(qw));
         softmax_dq_kernel<T, DP, VEC><<<grid, kSoftmaxThreads, 0, stream>>>(p, qw, tokens);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        if (qw.splits > 1) softmax_bwd_join_kernel<T, false><<<grid, kSoftmaxThreads, 0, stream>>>(p, qw);
+        if (qw.splits > 1) {
+            const SoftmaxWork j = softmax_join_work(qw);
+            softmax_bwd_join_kernel<T, false><<<dim3((unsigned)softmax_groups(j)), kSoftmaxThreads, 0, stream>>>(p, qw, j);
+        }
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (kw.blocks > 0) {
         const dim3 grid((unsigned)softmax_groups(kw));
         softmax_dkv_kernel<T, DP, VEC><<<grid, 2 * kSoftmaxThreads, 0, stream>>>(p, kw, tokens);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        if (kw.splits > 1) softmax_bwd_join_kernel<T, true><<<grid, kSoftmaxThreads, 0, stream>>>(p, kw);
+        if (kw.splits > 1) {
+            const SoftmaxWork j = softmax_join_work(kw);
+            softmax_bwd_join_kernel<T, true><<<dim3((unsigned)softmax_groups(j)), kSoftmaxThreads, 0, stream>>>(p, kw, j);
+        }
         e = hipGetLastError();
     }
     return e;

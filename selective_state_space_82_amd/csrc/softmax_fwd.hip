@@ -243,44 +243,42 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
 }
 
 // The pieces of a block of queries, in their order. (Blocks with one piece are written already.)
-template <typename T> __global__ __launch_bounds__(kSoftmaxThreads) void softmax_fwd_join_kernel(SoftmaxLaunch a, SoftmaxWork work) {
+template <typename T>
+__global__ __launch_bounds__(kSoftmaxThreads) void softmax_fwd_join_kernel(SoftmaxLaunch a, SoftmaxWork work, SoftmaxWork join) {
     constexpr int KB = kKeys<T>;
     SoftmaxPlace at;
-    if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
+    if (!softmax_place(join, a.G, blockIdx.x, &at)) return;
     const int h = at.g * work.per + at.which, q0 = (work.blocks - 1 - at.block) * kSoftmaxBlock;
     const AttnSeq s = sequence(a.rows, at.seq);
     const bool packed = a.rows.cu_q != nullptr;
     const int rows = s.nq - q0 > kSoftmaxBlock ? kSoftmaxBlock : s.nq - q0;
     if (rows <= 0) return;  // one piece
-    // rows past the sequence's queries (a padded batch) are 0, -inf
-    const int past = packed ? rows : (int)(a.rows.Lq - q0 > kSoftmaxBlock ? kSoftmaxBlock : a.rows.Lq - q0);
     int pieces;
     softmax_piece(work, (last_key(s, a.causal, q0 + rows - 1) + KB) / KB, &pieces);
     if (pieces < 2) return;
-    const int64_t tokens = packed ? a.rows.Tq : a.rows.b * a.rows.Lq, row0 = (packed ? s.q0 : at.seq * a.rows.Lq) + q0;
+    const int l = threadIdx.x & 31, r = at.piece * 8 + (int)threadIdx.x / 32;
+    // rows past the sequence's queries (a padded batch) are 0, -inf
+    if (q0 + r >= (packed ? s.nq : a.rows.Lq)) return;
+    const int n = r < rows ? pieces : 0;
+    const int64_t tokens = packed ? a.rows.Tq : a.rows.b * a.rows.Lq, row = (packed ? s.q0 : at.seq * a.rows.Lq) + q0 + r;
+    const int64_t to = row * a.H + h;
     const float *ms = a.part + work.splits * tokens * a.H * a.D;
-    const int w = la::wave_id(), l = threadIdx.x & 63;
-    // a workgroup takes every splits-th group of four rows
-    for (int r = at.piece * 4 + w; r < past; r += 4 * work.splits) {
-        const int64_t to = (row0 + r) * a.H + h;
-        float most = -INFINITY, total = 0.0f, x[2] = {0.0f, 0.0f};
-        const int n = r < rows ? pieces : 0;
-        for (int i = 0; i < n; ++i) most = __builtin_fmaxf(most, ms[2 * (i * tokens * a.H + to)]);
-        const float base = most == -INFINITY ? 0.0f : most;
-        for (int i = 0; i < n; ++i) {
-            const int64_t from = i * tokens * a.H + to;
-            const float f = exp2_fast(ms[2 * from] - base);
-            total = __builtin_fmaf(f, ms[2 * from + 1], total);
+    float most = -INFINITY, total = 0.0f, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < n; ++i) most = __builtin_fmaxf(most, ms[2 * (i * tokens * a.H + to)]);
+    const float base = most == -INFINITY ? 0.0f : most;
+    for (int i = 0; i < n; ++i) {
+        const int64_t from = i * tokens * a.H + to;
+        const float f = exp2_fast(ms[2 * from] - base);
+        total = __builtin_fmaf(f, ms[2 * from + 1], total);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                if (l + 64 * u < a.D) x[u] = __builtin_fmaf(f, a.part[from * a.D + l + 64 * u], x[u]);
-        }
-        const bool live = !(total == 0.0f);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            if (l + 64 * u < a.D) static_cast<T *>(a.o)[to * a.D + l + 64 * u] = narrow<T>(live ? x[u] / total : 0.0f);
-        if (a.lse && l == 0) a.lse[to] = live ? (base + __builtin_amdgcn_logf(total)) * 0.69314718055994530942f : -INFINITY;
+        for (int u = 0; u < 4; ++u)
+            if (l + 32 * u < a.D) x[u] = __builtin_fmaf(f, a.part[from * a.D + l + 32 * u], x[u]);
     }
+    const bool live = !(total == 0.0f);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (l + 32 * u < a.D) static_cast<T *>(a.o)[to * a.D + l + 32 * u] = narrow<T>(live ? x[u] / total : 0.0f);
+    if (a.lse && l == 0) a.lse[to] = live ? (base + __builtin_amdgcn_logf(total)) * 0.69314718055994530942f : -INFINITY;
 }
 
 template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, hipStream_t stream) {
@@ -288,7 +286,10 @@ template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, h
     const dim3 grid((unsigned)softmax_groups(w));
     softmax_fwd_kernel<T, DP, VEC><<<grid, kSoftmaxThreads, 0, stream>>>(p, w);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    if (w.splits > 1) softmax_fwd_join_kernel<T><<<grid, kSoftmaxThreads, 0, stream>>>(p, w);
+    if (w.splits > 1) {
+        const SoftmaxWork j = softmax_join_work(w);
+        softmax_fwd_join_kernel<T><<<dim3((unsigned)softmax_groups(j)), kSoftmaxThreads, 0, stream>>>(p, w, j);
+    }
     return hipGetLastError();
 }
 template <typename T> hipError_t by_width(const SoftmaxLaunch &p, hipStream_t stream) {

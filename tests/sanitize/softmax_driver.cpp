@@ -135,8 +135,8 @@ static void places() {
                 CHECK(pieces == 1 || per >= least);
             }
     const AttnRows one{nullptr, nullptr, nullptr, nullptr, 1, 4096, 4096, 0, 0};
-    CHECK(softmax_fwd_work(one, 2, 1, true).splits == 8 && softmax_fwd_work(one, 16, 1, true).splits == 1);
-    CHECK(softmax_dkv_work(one, 2, 1).splits == 8);
+    CHECK(softmax_fwd_work(one, 2, 1, true).splits == 16 && softmax_fwd_work(one, 32, 1, true).splits == 1);
+    CHECK(softmax_dkv_work(one, 2, 1).splits == 16);
     const int32_t cu[2] = {0, 0};
     const AttnRows packed{cu, cu, nullptr, nullptr, 64, 4096, 4096, 1280, 1280};  // few tokens of many short sequences
     CHECK(softmax_blocks(packed, 4096, 1280) == 74);
