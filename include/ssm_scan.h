@@ -406,12 +406,15 @@ SSM_API ssm_status_t ssm_layernorm_bwd(const void *x, const float *w, const void
  *   workspace         as for ssm_linattn_fwd, of the bytes the call's _workspace function gives (may be 0)
  * Products are exact bf16 products summed in fp32 (bf16) or fp32 products (f32); the softmax' statistics and all sums are
  * fp32. With bf16, weights and their gradients enter products rounded to bf16, 2^-8 each (a second part for each would add half
- * again to the forward call's products). Results are deterministic. A NaN or Inf reaches the
+ * again to the forward call's products), but that ds, the scores' gradients, enter dq's in two parts, 2^-16. Results are
+ * deterministic. A NaN or Inf reaches the
  * queries that see its key and no others (an Inf in v may come out as NaN); gradients may become NaN for the 32 tokens of
  * the same sequence around it.
  * b, H, G, D >= 1; G divides H; D <= SSM_ATTN_MAX_D and scale finite (SSM_ERR_UNSUPPORTED otherwise); Lq, Lk <= 2^30; H·D and
- * strides between tokens at most 2^24; a launch takes fewer than 2^32 threads (b·H·⌈Lq/128⌉ and b·G·⌈Lk/128⌉ below 2^24,
- * queries times H in the gradient below 2^28). No output may overlap an input, the workspace or another output.
+ * strides between tokens at most 2^24; a launch takes fewer than 2^32 threads: SSM_ERR_SHAPE where b·H·⌈Lq/128⌉ or
+ * b·G·⌈Lk/128⌉ (b·G rounded up to a multiple of 8, and ⌈./128⌉ to one of ⌈8/G⌉) reaches 2^23. No output may overlap an
+ * input, the workspace or another output. Where few blocks of 128 queries (keys, in the gradient for k and v) leave the device idle,
+ * the keys (queries) are summed in up to 16 pieces: then fp32 sums, and so the last bits, depend on b, H, G, the lengths' bounds and tokens.
  */
 #define SSM_ATTN_MAX_D 128
 typedef ssm_linattn_strides_t ssm_attn_strides_t;

@@ -173,7 +173,6 @@ int64_t bwd_bytes(const ssm_attn_rows_t &r, int64_t tq, int64_t tk, int64_t H, i
     const int64_t q = nq > 1 ? nq * tq * H * (D + 1) * 4 : 0, k = nk > 1 ? 2 * nk * tk * G * D * 4 : 0;
     return stats_bytes(tq, H) + (q > k ? q : k);
 }
-bool stats_launch(int64_t tokens_q, int64_t H) { return launchable(ceil_div(tokens_q * H, 16), ssm::kSoftmaxThreads); }
 
 // ---- the paged cache ---------------------------------------------------------------------------------------------
 
@@ -310,7 +309,6 @@ ssm_status_t ssm_attn_bwd_workspace(const ssm_attn_rows_t *rows, int64_t H, int6
     if (st != SSM_OK) return st;
     int64_t tq = 0, tk = 0;
     if ((st = check_rows(rows, H, G, &tq, &tk)) != SSM_OK) return st;
-    if (!stats_launch(tq, H)) return SSM_ERR_SHAPE;
     *bytes = bwd_bytes(*rows, tq, tk, H, G, D);
     return SSM_OK;
 }
@@ -323,7 +321,6 @@ ssm_status_t ssm_attn_bwd(const void *q, const void *k, const void *v, const voi
     if (st != SSM_OK) return st;
     int64_t tq = 0, tk = 0;
     if ((st = check_rows(rows, H, G, &tq, &tk)) != SSM_OK) return st;
-    if (!stats_launch(tq, H)) return SSM_ERR_SHAPE;
     Prompt c;
     if ((st = c.set(*rows, tq, tk, H, G, D, dtype, strides)) != SSM_OK) return st;
     if ((tq > 0 && (!q || !o || !lse || !do_ || !dq)) || (tk > 0 && (!k || !v || !dk || !dv))) return SSM_ERR_NULL;

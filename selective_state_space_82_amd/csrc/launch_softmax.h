@@ -91,26 +91,31 @@ inline int64_t softmax_blocks(const AttnRows &r, int64_t L, int64_t tokens) {
     const int64_t all = r.b * ((L + kSoftmaxBlock - 1) / kSoftmaxBlock), some = tokens / kSoftmaxBlock + (r.b < tokens ? r.b : tokens);
     return r.cu_q && some < all ? some : all;
 }
-// Pieces for `groups` blocks of walks of up to `tiles` tiles where `fill` workgroups fill the device.
-inline int64_t softmax_splits(int64_t groups, int64_t tiles, int64_t least, int64_t fill) {
+// Pieces for `groups` blocks of walks of up to `tiles` tiles where `fill` workgroups fill the device; `launched`: blocks that
+// a launch has workgroups for, which many packed sequences of different lengths leave mostly empty (2^16 of them start in 30 us).
+inline int64_t softmax_splits(int64_t groups, int64_t launched, int64_t tiles, int64_t least, int64_t fill) {
     int64_t n = groups > 0 ? (fill + groups - 1) / groups : 1;
+    if (n > 1 && n * launched > (INT64_C(1) << 16)) n = (INT64_C(1) << 16) / launched;
     const int64_t most = (tiles + least - 1) / least;
     n = n < 16 ? n : 16;
-    return n < most ? n : (most > 1 ? most : 1);
+    n = n < most ? n : most;
+    return n > 1 ? n : 1;
 }
 inline SoftmaxWork softmax_query_work(const AttnRows &r, int64_t H, int64_t G, int64_t keys) {
     const int64_t least = kSoftmaxLeast / keys;
-    const int64_t splits = softmax_splits(softmax_blocks(r, r.Lq, r.Tq) * H, (r.Lk + keys - 1) / keys, least, 1024);
-    return softmax_work(r.b, G, H / G, (r.Lq + kSoftmaxBlock - 1) / kSoftmaxBlock, splits, least);
+    const int64_t blocks = (r.Lq + kSoftmaxBlock - 1) / kSoftmaxBlock;
+    const int64_t splits =
+        softmax_splits(softmax_blocks(r, r.Lq, r.Tq) * H, r.b * blocks * H, (r.Lk + keys - 1) / keys, least, 1024);
+    return softmax_work(r.b, G, H / G, blocks, splits, least);
 }
 inline SoftmaxWork softmax_fwd_work(const AttnRows &r, int64_t H, int64_t G, bool bf16) {
     return softmax_query_work(r, H, G, bf16 ? 64 : 32);  // keys of a tile
 }
 inline SoftmaxWork softmax_dq_work(const AttnRows &r, int64_t H, int64_t G) { return softmax_query_work(r, H, G, 32); }
 inline SoftmaxWork softmax_dkv_work(const AttnRows &r, int64_t H, int64_t G) {
-    const int64_t splits =
-        softmax_splits(softmax_blocks(r, r.Lk, r.Tk) * G, (r.Lq + 31) / 32 * (H / G), kSoftmaxLeast / 32, 512);
-    return softmax_work(r.b, G, 1, (r.Lk + kSoftmaxBlock - 1) / kSoftmaxBlock, splits, kSoftmaxLeast / 32);
+    const int64_t blocks = (r.Lk + kSoftmaxBlock - 1) / kSoftmaxBlock, least = kSoftmaxLeast / 32;
+    const int64_t splits = softmax_splits(softmax_blocks(r, r.Lk, r.Tk) * G, r.b * blocks * G, (r.Lq + 31) / 32 * (H / G), least, 512);
+    return softmax_work(r.b, G, 1, blocks, splits, least);
 }
 hipError_t launch_softmax_fwd(const SoftmaxLaunch &p, hipStream_t stream);
 hipError_t launch_softmax_bwd(const SoftmaxLaunch &p, hipStream_t stream);

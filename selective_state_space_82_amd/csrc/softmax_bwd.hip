@@ -3,50 +3,14 @@
 //     dv_j = Σ_i p_ij do_i,   ds_ij = p_ij (do_i·v_j − delta_i),   dq_i = scale Σ_j ds_ij k_j,   dk_j = scale Σ_i ds_ij q_i,
 // sums over i taken over all heads that share the key head.
 //
-// Three launches: delta; dk and dv by workgroups of keys that walk the queries; dq by workgroups of queries that walk the
-// keys. The scores and do·v are so formed twice (7 products of queries × keys × width instead of 5), and in turn no sum is
+// Two launches: delta and dq by workgroups of queries that walk the keys; dk and dv by workgroups of keys that walk the
+// queries. The scores and do·v are so formed twice (7 products of queries × keys × width instead of 5), and in turn no sum is
 // taken by atomics: results do not depend on the order in which workgroups run.
 #include "softmax_common.h"
 
 namespace ssm {
 namespace sm {
 namespace {
-
-constexpr int kStatsLanes = 16;  // lanes to a query's row
-
-// stats[0][h][query] = lse·log2 e, +inf for a query that saw no key (lse = −inf), that is, weights of 0; stats[1][h][query] = −do·o.
-template <typename T, bool VEC>
-__global__ __launch_bounds__(kSoftmaxThreads) void softmax_stats_kernel(SoftmaxLaunch a, int64_t tokens) {
-    const int64_t id = (int64_t)blockIdx.x * (kSoftmaxThreads / kStatsLanes) + threadIdx.x / kStatsLanes;
-    const int lane = threadIdx.x % kStatsLanes;
-    if (id >= tokens * a.H) return;
-    const int64_t t = id / a.H;
-    const int h = (int)(id % a.H);
-    const int64_t is = a.rows.cu_q ? 0 : t / a.rows.Lq, it = a.rows.cu_q ? t : t % a.rows.Lq;
-    const T *dp = static_cast<const T *>(a.dout) + is * a.do_b + it * a.do_t + h * a.do_h;
-    const T *op = static_cast<const T *>(a.o_in) + id * a.D;
-    float sum = 0.0f;
-    if constexpr (VEC) {
-        for (int c = lane * kE<T>; c < a.D; c += kStatsLanes * kE<T>) {
-            const u4 u = *reinterpret_cast<const u4 *>(dp + c), v = *reinterpret_cast<const u4 *>(op + c);
-            T x[kE<T>], y[kE<T>];
-            __builtin_memcpy(x, &u, 16);
-            __builtin_memcpy(y, &v, 16);
-#pragma unroll
-            for (int k = 0; k < kE<T>; ++k) sum = __builtin_fmaf(widen(x[k]), widen(y[k]), sum);
-        }
-    } else {
-        for (int c = lane; c < a.D; c += kStatsLanes) sum = __builtin_fmaf(widen(dp[c]), widen(op[c]), sum);
-    }
-#pragma unroll
-    for (int d = 1; d < kStatsLanes; d <<= 1) sum += __shfl_xor(sum, d);
-    if (lane == 0) {
-        const float lse = a.lse_in[id];
-        float *out = a.stats + h * tokens + t;
-        out[0] = lse == -INFINITY ? INFINITY : lse * kLog2e;
-        out[tokens * a.H] = -sum;
-    }
-}
 
 // dk and dv: a workgroup takes 128 keys of one key head and walks the queries that see them, head by head of the group, in
 // tiles of 32. Two wavefronts share 32 keys: the first forms their scores and weights and adds to dv, the second forms do·v and, from
@@ -303,21 +267,35 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
     const int64_t row = (packed ? s.q0 : is * a.rows.Lq) + r0;
 
     Frag<T> q[NC], dout[NC];
-    float lse = 0.0f, less = 0.0f, rest = 0.0f;  // less: −delta; rest: the lane's half of Σ ds
+    float lse = INFINITY, less = 0.0f, rest = 0.0f;  // less: −delta; rest: the lane's half of Σ ds
     float *stat = a.stats + h * tokens + row + col;
     {
         const int rows = s.nq - r0 > 32 ? 32 : s.nq - r0;
         const T *qp = static_cast<const T *>(a.q) + is * a.q_b + (s.q0 + r0) * a.q_t + h * a.q_h;
         const T *dp = static_cast<const T *>(a.dout) + is * a.do_b + (s.q0 + r0) * a.do_t + h * a.do_h;
-        load_frags<T, DP, VEC>(q, la::rows_buffer(qp, (uint32_t)a.q_t, rows, a.D), (uint32_t)a.q_t, col, rows, a.D);
+        const uint32_t o_t = (uint32_t)(a.H * a.D);
+        Frag<T> o[NC];
+        load_frags<T, DP, VEC>(o, la::rows_buffer(static_cast<const T *>(a.o_in) + (row * a.H + h) * a.D, o_t, rows, a.D), o_t,
+                               col, rows, a.D);
         load_frags<T, DP, VEC>(dout, la::rows_buffer(dp, (uint32_t)a.do_t, rows, a.D), (uint32_t)a.do_t, col, rows, a.D);
+        load_frags<T, DP, VEC>(q, la::rows_buffer(qp, (uint32_t)a.q_t, rows, a.D), (uint32_t)a.q_t, col, rows, a.D);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < kE<T>; ++e) less = __builtin_fmaf(-(float)dout[c][e], (float)o[c][e], less);
+        less += other_half(less);
         if (a.scale < 0.0f) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) negate<T>(q[c]);
         }
         if (col < rows) {
-            lse = stat[0];
-            less = stat[tokens * a.H];
+            const float given = a.lse_in[(row + col) * a.H + h];
+            // a query that saw no key (lse = −inf): weights of 0
+            lse = given == -INFINITY ? INFINITY : given * kLog2e;
+        }
+        if (half == 0 && col < rows && at.piece == 0) {
+            stat[0] = lse;
+            stat[tokens * a.H] = less;
         }
     }
     const float sc = scale_of(a.scale);
@@ -462,12 +440,7 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_bwd_join_kernel(Softm
 template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, hipStream_t stream) {
     const int64_t tokens = p.rows.cu_q ? p.rows.Tq : p.rows.b * p.rows.Lq;
     const SoftmaxWork kw = softmax_dkv_work(p.rows, p.H, p.G), qw = softmax_dq_work(p.rows, p.H, p.G);
-    constexpr int64_t per = kSoftmaxThreads / kStatsLanes;
     hipError_t e = hipSuccess;
-    if (tokens > 0) {
-        softmax_stats_kernel<T, VEC><<<dim3((unsigned)((tokens * p.H + per - 1) / per)), kSoftmaxThreads, 0, stream>>>(p, tokens);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
     if (qw.blocks > 0) {
         const dim3 grid((unsigned)softmax_groups(qw));
         softmax_dq_kernel<T, DP, VEC><<<grid, kSoftmaxThreads, 0, stream>>>(p, qw, tokens);
