@@ -407,9 +407,9 @@ SSM_API ssm_status_t ssm_layernorm_bwd(const void *x, const float *w, const void
  * Products are exact bf16 products summed in fp32 (bf16) or fp32 products (f32); the softmax' statistics and all sums are
  * fp32. With bf16, weights and their gradients enter products rounded to bf16, 2^-8 each (a second part for each would add half
  * again to the forward call's products), but that ds, the scores' gradients, enter dq's in two parts, 2^-16. Results are
- * deterministic. A NaN or Inf reaches the
- * queries that see its key and no others (an Inf in v may come out as NaN); gradients may become NaN for the 32 tokens of
- * the same sequence around it.
+ * deterministic. A NaN or Inf reaches the queries that see its key and no others (an Inf in v may come out as NaN); in
+ * gradients it may also reach queries and keys of the same sequence less than 128 from it. A query all of whose scores are
+ * −Inf counts as one that sees no key.
  * b, H, G, D >= 1; G divides H; D <= SSM_ATTN_MAX_D and scale finite (SSM_ERR_UNSUPPORTED otherwise); Lq, Lk <= 2^30; H·D and
  * strides between tokens at most 2^24; a launch takes fewer than 2^32 threads: SSM_ERR_SHAPE where b·H·⌈Lq/128⌉ or
  * b·G·⌈Lk/128⌉ (b·G rounded up to a multiple of 8, and ⌈./128⌉ to one of ⌈8/G⌉) reaches 2^23. No output may overlap an
@@ -483,8 +483,8 @@ SSM_API ssm_status_t ssm_attn_step(const void *q, const void *k_cache, const voi
  *   freq              [rotary/2] fp64 on the device, radians a position, or NULL: no rotation. rotary even, 2 .. D
  *   strides           as for ssm_attn_fwd (do_'s are not used)
  * Tokens whose position the row's pages do not reach are not stored. Two new tokens on the same slot (rows that share a page)
- * leave either's values there. Outputs q_out and k_out of tokens that belong to no row are 0 (left as they are in place). T and T·H·D
- * within ssm_attn_fwd's limits, T below 2^26. Errors as for ssm_attn_fwd.
+ * leave either's values there. Outputs q_out and k_out of tokens that belong to no row are 0 (left as they are in place). T below
+ * 2^24, H, G, D and strides as for ssm_attn_fwd, errors too.
  */
 typedef struct {
     const int32_t *cu, *new_lengths;

@@ -236,7 +236,7 @@ ssm_status_t plan_step(int64_t b, int64_t H, int64_t G, int64_t D, const ssm_pag
 ssm_status_t check_tokens(const ssm_tokens_t *t) {
     if (!t) return SSM_ERR_NULL;
     int64_t n = 0;
-    if (t->b < 1 || t->b >= INT32_MAX || t->T < 0 || !launchable(ceil_div(t->T, 4), ssm::kAppendThreads)) return SSM_ERR_SHAPE;
+    if (t->b < 1 || t->b >= INT32_MAX || t->T < 0 || !launchable(t->T, ssm::kAppendThreads)) return SSM_ERR_SHAPE;
     if (!t->cu && (t->L < 0 || !mul_ok(t->b, t->L, &n) || n != t->T)) return SSM_ERR_SHAPE;
     return SSM_OK;
 }

@@ -235,6 +235,28 @@ def test_tokens_that_do_not_count(dtype):
             R.assert_within(g[n], ref[n], tol[n], f"{layout} {n}")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("name", ["q", "k", "v", "do"])
+def test_not_finite_in_gradients(name, dtype):
+    """A NaN in one token's inputs leaves the gradients of other sequences, and of tokens 128 away that do not see it, as
+    they are."""
+    x = make([700, 90], 2, 1, 64, dtype, seed=1)
+    t = {n: x[n].cuda() for n in ("q", "k", "v", "do")}
+    o, lse = api.ssm_attn_fwd(t["q"], t["k"], t["v"], return_lse=True, **where(x))
+    run = lambda: api.ssm_attn_bwd(t["q"], t["k"], t["v"], o=o, lse=lse, do=t["do"], **where(x))  # noqa: E731
+    clean = run()
+    t[name] = t[name].clone()
+    t[name][300, 0, 7] = math.nan
+    got = run()
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(got[n][700:], clean[n][700:]), n
+    if name in ("q", "do"):  # query 300: keys after it do not enter
+        assert torch.equal(got["dq"][:300 - 127], clean["dq"][:300 - 127]) and torch.equal(got["dq"][428:700], clean["dq"][428:700])
+        assert all(torch.equal(got[n][428:700], clean[n][428:700]) for n in ("dk", "dv"))
+    else:  # key 300: queries before it do not see it
+        assert torch.equal(got["dq"][:300 - 127], clean["dq"][:300 - 127])
+
+
 def test_gradient_against_differences():
     """(f(x + h d) − f(x − h d)) / 2h in 64 bits of the forward's definition, against the kernel's gradient along d."""
     x = make([37, 20], 4, 2, 16, F32, seed=4)
