@@ -6,6 +6,15 @@
 // Two launches: delta and dq by workgroups of queries that walk the keys; dk and dv by workgroups of keys that walk the
 // queries. The scores and do·v are so formed twice (7 products of queries × keys × width instead of 5), and in turn no sum is
 // taken by atomics: results do not depend on the order in which workgroups run.
+//
+// Rounding with bf16. delta comes from an o rounded to bf16, 2^-8, which shows in ds where a query sees few keys; ds and p enter
+// products rounded, 2^-8 each. dq takes ds in two parts; its sum over the keys, 0 for an exact delta, is what delta lacks, and
+// the keys' kernel is given the corrected one. So dq, dk and dv are 2.0e-3, 2.3e-3 and 2.3e-3 of their norm off where their own
+// rounding is 1.7e-3 (without both, dq and dk 2.5e-3 to 2.9e-3).
+//
+// 130M-like layer (4 rows of 2048, 24 heads of 64, causal): 0.26 ms, 0.49 PFLOP/s counting five products; 9 packed documents of 463
+// to 4096 tokens, 32 heads on 8 key heads of 128: 1.55 ms, 0.56 PFLOP/s: 0.62 ms for dq at 55 % of the matrix units' time,
+// 0.85 for dk and dv at 39 %, of which a fifth is the last workgroups' and a third of the rest waits at the round's barrier.
 #include "softmax_common.h"
 
 namespace ssm {

@@ -2,8 +2,17 @@
 // sees, with lse_i = log Σ_j e^(scale·q_i·k_j).
 //
 // One pass over the keys with the running maximum and sum of the softmax. A workgroup takes 32 queries a wavefront of one
-// head and walks the keys its queries see in tiles, which it fetches into registers during the tile before and then into one
-// of two LDS buffers. Scores stay in registers (softmax_common.h).
+// head and walks the keys that its queries see in tiles of 64 (fp32: 32), which go from memory straight into one of two LDS
+// buffers each for keys and values while the tile before is computed. Scores and weights stay in registers (softmax_common.h).
+//
+// What carries it: the next tile's scores are formed in the same stretch of code, without branches, as this tile's weights and
+// products, so that matrix and vector instructions of one wavefront overlap; tiles that every query sees whole take no mask; the
+// maximum is raised only where it has to be. 1.4B-like layer (8 rows of 4096, 32 heads on 8 key heads of 128, bf16, causal):
+// 1.10 ms, 1.0 PFLOP/s; one row of 16384, 16 heads of 128: 1.01 ms, 1.09 PFLOP/s, where a library product of 8192³ runs at 1.18.
+// The matrix units are busy 52 % of the time, vector instructions take 26 % of the wavefronts' and LDS 26 % of the compute
+// units'; one exponential, at a quarter of the vector rate, is half of what a score costs there. Steps measured on the way
+// (1.4B-like, ms): tiles through registers 5.59; straight into LDS without bank conflicts 1.46; key heads kept to an XCD
+// 1.43; scores ahead 1.29; no masks and no path for NaN in the loop over whole tiles 1.10.
 #include "softmax_common.h"
 
 namespace ssm {
