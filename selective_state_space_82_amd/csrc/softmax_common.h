@@ -166,7 +166,10 @@ template <typename T, int ROWS, int W> __device__ __forceinline__ bool share_not
 // ROWS rows × W columns of a strided matrix into an LDS tile, by four wavefronts; zeros past the rows and columns there are.
 // VEC: straight into LDS, 16 bytes a lane, through a buffer that ends with the last row; the instructions are written out, for the
 // compiler would have every later read of LDS wait for a load that it knows to go there, also one from the other
-// buffer. A wavefront waits for its own with landed() before the barrier that hands the tile over. Otherwise element by
+// buffer. A wavefront waits for its own with landed() before the barrier that hands the tile over. The compiler puts no wait states
+// into written-out code: one has to lie between a scalar write of m0 and the load that goes to LDS by it, five between a vector
+// instruction's write of a scalar register (readfirstlane, a spilled one's readlane) and a load that reads it. m0 is a reserved
+// register that the compiler writes right before each use of its own, so none of its values can be lost here. Otherwise element by
 // element through registers.
 template <typename T, int ROWS, int W, bool VEC> struct Loader {
     using X = Tile<T, W>;
@@ -202,7 +205,7 @@ template <typename T, int ROWS, int W, bool VEC> struct Loader {
             const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)tile + w * 1024;
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                              :
                              : "s"(lds + j * kSoftmaxThreads * 16), "v"(at[kOffsets == 1 ? 0 : j]), "s"(buf),
                                "s"(kOffsets == 1 ? j * kStep * stride * (uint32_t)sizeof(T) : 0u)
@@ -235,7 +238,7 @@ __device__ __forceinline__ void load_stats(const float *first, int rows, char *l
                     (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
                     (uint32_t)__builtin_amdgcn_readfirstlane(rows > 32 ? 128 : rows > 0 ? rows * 4 : 0), 0x00027000u};
     if (l < 32)
-        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
                      :
                      : "s"((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds), "v"(l * 4u), "s"(buf)
                      : "memory");
