@@ -5,14 +5,17 @@
 // head and walks the keys that its queries see in tiles of 64 (fp32: 32), which go from memory straight into one of two LDS
 // buffers each for keys and values while the tile before is computed. Scores and weights stay in registers (softmax_common.h).
 //
+// With bf16 a weight enters its product with the values in two parts, its value rounded and what that leaves, rounded: 2^-16. One part
+// alone (2^-8 of every weight, each on its own) is two thirds of the result's own rounding, of 1.6e-3 of its norm: 2.06e-3 in all.
+//
 // What carries it: the next tile's scores are formed in the same stretch of code, without branches, as this tile's weights and
 // products, so that matrix and vector instructions of one wavefront overlap; tiles that every query sees whole take no mask; the
 // maximum is raised only where it has to be. 1.4B-like layer (8 rows of 4096, 32 heads on 8 key heads of 128, bf16, causal):
-// 1.10 ms, 1.0 PFLOP/s; one row of 16384, 16 heads of 128: 1.01 ms, 1.09 PFLOP/s, where a library product of 8192³ runs at 1.18.
-// The matrix units are busy 52 % of the time, vector instructions take 26 % of the wavefronts' and LDS 26 % of the compute
-// units'; one exponential, at a quarter of the vector rate, is half of what a score costs there. Steps measured on the way
-// (1.4B-like, ms): tiles through registers 5.59; straight into LDS without bank conflicts 1.46; key heads kept to an XCD
-// 1.43; scores ahead 1.29; no masks and no path for NaN in the loop over whole tiles 1.10.
+// 1.42 ms; one row of 16384, 16 heads of 128: 1.35 ms: three products of 0.55 TFLOP for two, 1.16 and 1.22 PFLOP/s of matrix
+// instructions, where a library product of 8192³ runs at 1.18 to 1.20: they bound it. Weights in one part take 1.11 and 1.03 ms.
+// Steps measured on the way with one part (1.4B-like, ms): tiles through registers 5.59; straight into LDS without bank
+// conflicts 1.46; key heads kept to an XCD 1.43; scores ahead 1.29; no masks and no path for NaN in the loop over whole
+// tiles 1.10.
 #include "softmax_common.h"
 
 namespace ssm {
@@ -144,9 +147,9 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int c = 0; c < 32 / kChunk<T>; ++c) {
-                const Frag<T> pf = part_of<T>(p[t], c);
+                const Split<T> pf(p[t], c);
 #pragma unroll
-                for (int d = 0; d < ND; ++d) mma(o[d], col_frag<T, DP>(vb, 32 * t + kChunk<T> * c, 32 * d), pf);
+                for (int d = 0; d < ND; ++d) mma<T>(o[d], col_frag<T, DP>(vb, 32 * t + kChunk<T> * c, 32 * d), pf);
             }
     };
     if (threadIdx.x == 0) found = 0;
@@ -208,7 +211,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
                             if (nf) v[e] = 0.0f;
                             see[e] = j * KB + 32 * t + 8 * (i >> 2) + 4 * half + (i & 3) > my_last ? 0.0f : 1.0f;
                         }
-                        mma(o[d], v, part_of<T>(p[t], c));
+                        mma<T>(o[d], v, Split<T>(p[t], c));
                         mma(seen, bad, see);
                     }
 #pragma unroll
