@@ -71,3 +71,18 @@ def test_prompt_with_a_nan_behind_it(lib):
     v[290, 0, 3] = math.nan
     o = api.ssm_attn_fwd(*(x.bfloat16()[None].cuda() for x in (q, k, v)))[0]
     R.assert_within(o[:290], ref[:290], tol[:290], "o")
+
+
+@gpu
+@pytest.mark.parametrize("H,G,D,page,lens", [(4, 2, 64, 16, [200, 1, 63]), (40, 2, 128, 64, [250]), (2, 1, 96, 7, [3000, 40]),
+                                             (3, 3, 30, 5, [90])])
+def test_one_token(lib, H, G, D, page, lens):
+    b, most = len(lens), -(-max(lens) // page)
+    q, kc, vc = normal(D, (b, H, D), (b * most, page, G, D), (b * most, page, G, D))
+    table = torch.arange(b * most).flip(0).view(b, most)
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    o = api.ssm_attn_step(*(x.bfloat16().cuda() for x in (q, kc, vc)), table.int().cuda(), n)
+    for i, m in enumerate(lens):
+        k, v = (c[table[i]].flatten(0, 1)[:m] for c in (kc, vc))
+        ref, _, tol, _ = R.bounds(q[i:i + 1], k, v, D ** -0.5, True, BF16)
+        R.assert_within(o[i:i + 1], ref, tol, f"row {i}")
