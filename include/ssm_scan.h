@@ -406,8 +406,7 @@ SSM_API ssm_status_t ssm_layernorm_bwd(const void *x, const float *w, const void
  *   workspace         as for ssm_linattn_fwd, of the bytes the call's _workspace function gives (may be 0)
  * Products are exact bf16 products summed in fp32 (bf16) or fp32 products (f32); the softmax' statistics and all sums are
  * fp32. With bf16, weights enter the product with v in two bf16 parts, 2^-16 of each, so that o is its own rounding off; in
- * gradients ds, those of the scores, enter dq's in two parts, and weights and ds enter those of dv and dk in one, 2^-8. Results
- * are deterministic. A NaN or Inf reaches the queries that see its key and no others (an Inf in v may come out as NaN); in
+ * gradients weights and ds, those of the scores, enter theirs so as well. Results are deterministic. A NaN or Inf reaches the queries that see its key and no others (an Inf in v may come out as NaN); in
  * gradients it may also reach queries and keys of the same sequence less than 128 from it. A query all of whose scores are
  * −Inf counts as one that sees no key.
  * b, H, G, D >= 1; G divides H; D <= SSM_ATTN_MAX_D and scale finite (SSM_ERR_UNSUPPORTED otherwise); Lq, Lk <= 2^30; H·D and

@@ -7,14 +7,13 @@
 // queries. The scores and do·v are so formed twice (7 products of queries × keys × width instead of 5), and in turn no sum is
 // taken by atomics: results do not depend on the order in which workgroups run.
 //
-// Rounding with bf16. delta comes from an o rounded to bf16, 2^-8, which shows in ds where a query sees few keys; ds and p enter
-// products rounded, 2^-8 each. dq takes ds in two parts; its sum over the keys, 0 for an exact delta, is what delta lacks, and
-// the keys' kernel is given the corrected one. So dq, dk and dv are 2.0e-3, 2.3e-3 and 2.3e-3 of their norm off where their own
-// rounding is 1.7e-3 (without both, dq and dk 2.5e-3 to 2.9e-3).
+// Rounding with bf16. delta comes from an o rounded to bf16, 2^-8, which shows in ds where a query sees few keys. ds and p enter
+// products in two parts, 2^-16 (one part each for dv and dk: 2.3e-3 of their norm off where their own rounding is 1.7e-3, and
+// 0.26 and 1.54 ms for the cases below). The sum of ds over the keys, 0 for an exact delta, is what delta lacks, and the keys' kernel
+// is given the corrected one. dq is 2.0e-3 off where keys have no mean, and more where they share an offset.
 //
-// 130M-like layer (4 rows of 2048, 24 heads of 64, causal): 0.26 ms, 0.49 PFLOP/s counting five products; 9 packed documents of 463
-// to 4096 tokens, 32 heads on 8 key heads of 128: 1.55 ms, 0.56 PFLOP/s: 0.62 ms for dq at 55 % of the matrix units' time,
-// 0.85 for dk and dv at 39 %, of which a fifth is the last workgroups' and a third of the rest waits at the round's barrier.
+// 130M-like layer (4 rows of 2048, 24 heads of 64, causal): 0.30 ms, 0.43 PFLOP/s counting five products; 9 packed documents of 463
+// to 4096 tokens, 32 heads on 8 key heads of 128: 1.76 ms, 0.49 PFLOP/s.
 #include "softmax_common.h"
 
 namespace ssm {
@@ -144,9 +143,10 @@ __global__ __launch_bounds__(2 * kSoftmaxThreads, DP * sizeof(T) > 128 ? 2 : 4) 
             }
 #pragma unroll
             for (int c = 0; c < 32 / kChunk<T>; ++c) {
-                const Frag<T> pf = part_of<T>(p, c);
+                const Split<T> pf(p, c);
 #pragma unroll
-                for (int d = 0; d < ND; ++d) mma(sum[d], col_frag<T, DP>(dt + odd * kTileBytes, kChunk<T> * c, 32 * d), pf);
+                for (int d = 0; d < ND; ++d)
+                    mma<T>(sum[d], col_frag<T, DP>(dt + odd * kTileBytes, kChunk<T> * c, 32 * d), pf);
             }
         };
         f16 p, next;
@@ -197,9 +197,10 @@ __global__ __launch_bounds__(2 * kSoftmaxThreads, DP * sizeof(T) > 128 ? 2 : 4) 
             }
 #pragma unroll
             for (int c = 0; c < 32 / kChunk<T>; ++c) {
-                const Frag<T> df = part_of<T>(dp, c);
+                const Split<T> df(dp, c);
 #pragma unroll
-                for (int d = 0; d < ND; ++d) mma(sum[d], col_frag<T, DP>(qt + b * kTileBytes, kChunk<T> * c, 32 * d), df);
+                for (int d = 0; d < ND; ++d)
+                    mma<T>(sum[d], col_frag<T, DP>(qt + b * kTileBytes, kChunk<T> * c, 32 * d), df);
             }
         };
         f16 dp, next;

@@ -86,3 +86,25 @@ def test_one_token(lib, H, G, D, page, lens):
         k, v = (c[table[i]].flatten(0, 1)[:m] for c in (kc, vc))
         ref, _, tol, _ = R.bounds(q[i:i + 1], k, v, D ** -0.5, True, BF16)
         R.assert_within(o[i:i + 1], ref, tol, f"row {i}")
+
+
+# whole walks; walks cut into pieces; 96 columns; rows without 16-byte accesses; more keys than queries
+GRADIENT = [(2000, 2000, 24, 24, 64), (300, 300, 4, 2, 128), (1500, 1500, 2, 1, 64), (133, 133, 6, 2, 96), (130, 300, 2, 2, 30)]
+
+
+def gradients(nq, nk, H, G, D, causal, shift=0.0):
+    q, k, v, do = normal(D + nq, (nq, H, D), (nk, G, D), (nk, G, D), (nq, H, D), shift=shift)
+    t = [x.bfloat16()[None].cuda() for x in (q, k, v, do)]
+    o, lse = api.ssm_attn_fwd(*t[:3], causal=causal, return_lse=True)
+    g = api.ssm_attn_bwd(*t[:3], o=o, lse=lse, do=t[3], causal=causal)
+    return (q, k, v, do), {n: x[0] for n, x in g.items()}
+
+
+@gpu
+@pytest.mark.parametrize("nq,nk,H,G,D", GRADIENT)
+@pytest.mark.parametrize("causal", [True, False])
+def test_gradient_of_values(lib, nq, nk, H, G, D, causal):
+    x, g = gradients(nq, nk, H, G, D, causal)
+    q, k, v, do = (t[:, : t.shape[1] // G] for t in x)  # the first key head and its queries' heads
+    (_, _, dv), (_, _, tol) = R.grad_bounds(q, k, v, do, D ** -0.5, causal, BF16)
+    R.assert_within(g["dv"][:, :1], dv, tol, "dv")
