@@ -431,7 +431,10 @@ SSM_API ssm_status_t ssm_attn_fwd(const void *q, const void *k, const void *v, f
 
 /* Gradients for an upstream gradient do_ on o, from the forward call's o and lse. dq [tokens][H][D], dk and dv
  * [tokens][G][D] (summed over the heads that share a key head, in fp32) dtype, all required. workspace as for
- * ssm_linattn_bwd, of the bytes ssm_attn_bwd_workspace gives. */
+ * ssm_linattn_bwd, of the bytes ssm_attn_bwd_workspace gives. delta_i = do_i·o_i; with bf16, where o is rounded, it is
+ * Σ_j p_ij do_i·v_j wherever that is within twice that rounding (2^-7 Σ_d |do_id o_id|) of do_i·o_i. So results are their own
+ * rounding off, and o and lse may also be those of more keys than the call is given: with keys in shards, each call's dk and dv are
+ * its keys', and dq is the sum of the calls' (with bf16 as exact as do_i·o_i of the rounded o). */
 SSM_API ssm_status_t ssm_attn_bwd_workspace(const ssm_attn_rows_t *rows, int64_t H, int64_t G, int64_t D, int64_t *bytes);
 SSM_API ssm_status_t ssm_attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
                                   const void *do_, float scale, int32_t causal, const ssm_attn_rows_t *rows, void *dq,

@@ -925,7 +925,8 @@ def ssm_attn_bwd(q, k, v, *, o, lse, do, scale=None, causal=True, cu_seqlens=Non
                  max_len_k=None, lengths=None, lengths_k=None) -> dict:
     """Gradients of ssm_attn_fwd for an upstream gradient do on o, from the forward call's o and lse (contiguous; the other
     arguments as in that call). Returns a dict: dq, dk, dv (the shapes and dtype of q, k, v; dk and dv summed over the heads
-    that share a key head)."""
+    that share a key head). o and lse may be those of more keys than are given here (keys in shards): dk and dv are then those
+    of the given keys, and dq is the sum over the calls."""
     H, G, D, code, dense = _attn_inputs(q, k, v)
     r = _attn_rows(q, k, cu_seqlens, max_len, cu_seqlens_k, max_len_k, lengths, lengths_k)
     dev, st, packed = q.device, q.dtype, q.dim() == 3

@@ -167,11 +167,13 @@ int64_t fwd_bytes(const ssm_attn_rows_t &r, int64_t tq, int64_t H, int64_t G, in
     const int64_t n = ssm::softmax_fwd_work(attn_rows(r), H, G, dtype == SSM_BF16).splits;
     return n > 1 ? n * tq * H * (D + 2) * 4 : 0;
 }
-int64_t stats_bytes(int64_t tq, int64_t H) { return ceil_div(2 * tq * H * 4, 256) * 256; }
+int64_t stats_bytes(const ssm_attn_rows_t &r, int64_t tq, int64_t H, int64_t G) {
+    return ceil_div((2 + ssm::softmax_dq_work(attn_rows(r), H, G).splits) * tq * H * 4, 256) * 256;
+}
 int64_t bwd_bytes(const ssm_attn_rows_t &r, int64_t tq, int64_t tk, int64_t H, int64_t G, int64_t D) {
     const int64_t nq = ssm::softmax_dq_work(attn_rows(r), H, G).splits, nk = ssm::softmax_dkv_work(attn_rows(r), H, G).splits;
-    const int64_t q = nq > 1 ? nq * tq * H * (D + 1) * 4 : 0, k = nk > 1 ? 2 * nk * tk * G * D * 4 : 0;
-    return stats_bytes(tq, H) + (q > k ? q : k);
+    const int64_t q = nq > 1 ? nq * tq * H * D * 4 : 0, k = nk > 1 ? 2 * nk * tk * G * D * 4 : 0;
+    return stats_bytes(r, tq, H, G) + (q > k ? q : k);
 }
 
 // ---- the paged cache ---------------------------------------------------------------------------------------------
@@ -337,7 +339,8 @@ ssm_status_t ssm_attn_bwd(const void *q, const void *k, const void *v, const voi
     p.q = q; p.k = k; p.v = v; p.o_in = o; p.lse_in = lse; p.dout = do_;
     p.dq = dq; p.dk = dk; p.dv = dv;
     p.stats = static_cast<float *>(scratch.p);
-    p.part = p.stats + stats_bytes(tq, H) / 4;
+    p.rest = p.stats + 2 * tq * H;
+    p.part = p.stats + stats_bytes(*rows, tq, H, G) / 4;
     p.scale = scale;
     p.causal = causal != 0;
     p.vec = c.q.vec(q, es) && c.k.vec(k, es) && c.v.vec(v, es) && c.dout.vec(do_, es) && aligned16(o) && aligned16(dq) &&

@@ -22,9 +22,9 @@ struct SoftmaxLaunch {
     void *o, *dq, *dk, *dv;
     float *lse;
     float *stats;  // gradient: [2][H][tokens]: lse·log2 e and −delta of each head and query
+    float *rest;   // gradient with bf16: [splits][H][tokens]: what do·o lacks as delta, of each piece
     float *part;   // results of pieces, where a walk is cut (SoftmaxWork): the forward call's [splits][tokens][H][D], then
-                   // maximum and sum [splits][tokens][H][2]; dq's [splits][tokens][H][D], then sums of ds
-                   // [splits][H][tokens]; dk's [splits][tokens][G][D], then dv's
+                   // maximum and sum [splits][tokens][H][2]; dq's [splits][tokens][H][D]; dk's [splits][tokens][G][D], then dv's
     bool vec;      // every row takes 16-byte accesses
 };
 constexpr int kSoftmaxThreads = 256;

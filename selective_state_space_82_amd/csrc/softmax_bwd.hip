@@ -3,17 +3,17 @@
 //     dv_j = Σ_i p_ij do_i,   ds_ij = p_ij (do_i·v_j − delta_i),   dq_i = scale Σ_j ds_ij k_j,   dk_j = scale Σ_i ds_ij q_i,
 // sums over i taken over all heads that share the key head.
 //
-// Two launches: delta and dq by workgroups of queries that walk the keys; dk and dv by workgroups of keys that walk the
-// queries. The scores and do·v are so formed twice (7 products of queries × keys × width instead of 5), and in turn no sum is
-// taken by atomics: results do not depend on the order in which workgroups run.
+// Launches: with bf16 what do·o lacks as delta, and dq, each by workgroups of queries that walk the keys; dk and dv by workgroups of
+// keys that walk the queries. Scores and do·v are so formed twice, with bf16 three times (7 or 9 products of queries × keys × width
+// instead of 5), and in turn no sum is taken by atomics: results do not depend on the order in which workgroups run.
 //
-// Rounding with bf16. delta comes from an o rounded to bf16, 2^-8, which shows in ds where a query sees few keys. ds and p enter
-// products in two parts, 2^-16 (one part each for dv and dk: 2.3e-3 of their norm off where their own rounding is 1.7e-3, and
-// 0.26 and 1.54 ms for the cases below). The sum of ds over the keys, 0 for an exact delta, is what delta lacks, and the keys' kernel
-// is given the corrected one. dq is 2.0e-3 off where keys have no mean, and more where they share an offset.
+// Rounding with bf16. ds and p enter products in two parts, 2^-16. do·o is off by what o is rounded, 2^-8 of each of its values, so
+// delta is summed over the keys; dq, dk and dv are then their own rounding off, 1.7e-3 of their norm, whatever keys and queries
+// have in common.
 //
-// 130M-like layer (4 rows of 2048, 24 heads of 64, causal): 0.30 ms, 0.43 PFLOP/s counting five products; 9 packed documents of 463
-// to 4096 tokens, 32 heads on 8 key heads of 128: 1.76 ms, 0.49 PFLOP/s.
+// 130M-like layer (4 rows of 2048, 24 heads of 64, causal): 0.36 ms, 0.36 PFLOP/s counting five products (0.26 with one part each
+// and delta from o alone, 0.30 with two parts); 9 packed documents of 463 to 4096 tokens, 32 heads on 8 key heads of 128: 2.10 ms,
+// 0.41 PFLOP/s (1.54, 1.76): 0.43 for what delta lacks, 0.70 for dq, 1.1 for dk and dv.
 #include "softmax_common.h"
 
 namespace ssm {
@@ -239,73 +239,196 @@ __global__ __launch_bounds__(2 * kSoftmaxThreads, DP * sizeof(T) > 128 ? 2 : 4) 
     }
 }
 
+// The queries of a workgroup, 32 a wavefront, of one head, and the piece of the keys that they see, which it walks in tiles of 32.
+struct QueryWalk {
+    static constexpr int KB = 32, BQ = 32 * kSoftmaxThreads / 64;
+    AttnSeq s;
+    int64_t is, row;  // row: of the wavefront's first query among the call's tokens
+    int g, h, r0, to_write, piece, pieces, begin, tiles;
+    // false: nothing to do
+    __device__ __forceinline__ bool set(const SoftmaxLaunch &a, const SoftmaxWork &work) {
+        SoftmaxPlace at;
+        if (!softmax_place(work, a.G, blockIdx.x, &at)) return false;
+        is = at.seq;
+        g = at.g;
+        h = g * work.per + at.which;
+        s = sequence(a.rows, is);
+        const bool packed = a.rows.cu_q != nullptr;
+        const int q0 = (work.blocks - 1 - at.block) * BQ;
+        r0 = q0 + 32 * la::wave_id();
+        to_write = packed ? s.nq : (int)a.rows.Lq;
+        if (q0 >= to_write) return false;
+        const int last_q = (q0 + BQ < s.nq ? q0 + BQ : s.nq) - 1;
+        const int keys = last_q >= q0 ? last_key(s, a.causal, last_q) + 1 : 0;
+        const int per = softmax_piece(work, (keys + KB - 1) / KB, &pieces);
+        piece = at.piece;
+        if (piece >= pieces) return false;
+        begin = piece * per * KB;
+        tiles = ((pieces > 1 && keys - begin > per * KB ? per * KB : keys - begin) + KB - 1) / KB;
+        row = (packed ? s.q0 : is * a.rows.Lq) + r0;
+        return true;
+    }
+    __device__ __forceinline__ int rows() const { return s.nq - r0 > 32 ? 32 : s.nq - r0; }
+    // the last key that query r0 + col sees, counted from the piece's first
+    __device__ __forceinline__ int last(const SoftmaxLaunch &a, int col) const { return last_key(s, a.causal, r0 + col) - begin; }
+    template <typename T> __device__ __forceinline__ const T *keys(const SoftmaxLaunch &a) const {
+        return static_cast<const T *>(a.k) + is * a.k_b + (s.k0 + begin) * a.k_t + g * a.k_h;
+    }
+    template <typename T> __device__ __forceinline__ const T *values(const SoftmaxLaunch &a) const {
+        return static_cast<const T *>(a.v) + is * a.v_b + (s.k0 + begin) * a.v_t + g * a.v_h;
+    }
+};
+
+// The wavefront's queries and their gradients, and of the lane's query lse·log2 e, −do·o and Σ_d |do_d o_d|.
+template <typename T, int DP, bool VEC>
+__device__ __forceinline__ void load_queries(const SoftmaxLaunch &a, const QueryWalk &x, Frag<T> (&q)[DP / kChunk<T>],
+                                             Frag<T> (&dout)[DP / kChunk<T>], float &lse, float &less, float &size) {
+    constexpr int NC = DP / kChunk<T>;
+    const int col = threadIdx.x & 31, rows = x.rows();
+    const T *qp = static_cast<const T *>(a.q) + x.is * a.q_b + (x.s.q0 + x.r0) * a.q_t + x.h * a.q_h;
+    const T *dp = static_cast<const T *>(a.dout) + x.is * a.do_b + (x.s.q0 + x.r0) * a.do_t + x.h * a.do_h;
+    const uint32_t o_t = (uint32_t)(a.H * a.D);
+    Frag<T> o[NC];
+    load_frags<T, DP, VEC>(o, la::rows_buffer(static_cast<const T *>(a.o_in) + (x.row * a.H + x.h) * a.D, o_t, rows, a.D), o_t, col,
+                           rows, a.D);
+    load_frags<T, DP, VEC>(dout, la::rows_buffer(dp, (uint32_t)a.do_t, rows, a.D), (uint32_t)a.do_t, col, rows, a.D);
+    load_frags<T, DP, VEC>(q, la::rows_buffer(qp, (uint32_t)a.q_t, rows, a.D), (uint32_t)a.q_t, col, rows, a.D);
+    less = size = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < kE<T>; ++e) {
+            const float x = (float)dout[c][e], y = (float)o[c][e];
+            less = __builtin_fmaf(-x, y, less);
+            size = __builtin_fmaf(__builtin_fabsf(x), __builtin_fabsf(y), size);
+        }
+    less += other_half(less);
+    size += other_half(size);
+    if (a.scale < 0.0f) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) negate<T>(q[c]);
+    }
+    lse = INFINITY;
+    if (col < rows) {
+        const float given = a.lse_in[(x.row + col) * a.H + x.h];
+        // a query that saw no key (lse = −inf): weights of 0
+        lse = given == -INFINITY ? INFINITY : given * kLog2e;
+    }
+}
+
+// What do·o lacks as delta where o is rounded to bf16: rest_i = Σ_j p_ij (do_i·v_j − do_i·o_i) over the keys of each piece. delta's
+// error enters dq times Σ_j p_ij k_j: with keys that share an offset of four deviations, dq would be 8e-3 of its norm off. Two
+// products are formed once more for it, by rows of tiles alone. Tiles are on their way three rounds ahead: a round of two products is
+// shorter than a load takes (packed documents: 0.43 ms; 0.47 one round ahead; 0.50 with 64 queries to a wavefront, which
+// halves what is read from LDS, or 256 to a workgroup, which halves what is read from the L2).
+template <int DP, bool VEC>
+__global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_rest_kernel(SoftmaxLaunch a, SoftmaxWork work, int64_t tokens) {
+    using T = uint16_t;
+    constexpr int KB = QueryWalk::KB, NC = DP / kChunk<T>, kTileBytes = KB * Tile<T, DP>::kRow;
+    constexpr int kLoads = VEC ? 2 * Loader<T, KB, DP, VEC>::N : 0;  // of a tile of keys and one of values, by a wavefront
+    __shared__ __attribute__((aligned(1024))) char kt[4 * kTileBytes], vt[4 * kTileBytes];
+
+    QueryWalk x;
+    if (!x.set(a, work)) return;
+    const int l = threadIdx.x & 63, col = l & 31, half = l >> 5;
+    const int my_last = x.last(a, col), wave_first = x.last(a, 0);
+    Frag<T> q[NC], dout[NC];
+    float lse, less, size, rest[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    load_queries<T, DP, VEC>(a, x, q, dout, lse, less, size);
+    const float sc = scale_of(a.scale);
+
+    const Loader<T, KB, DP, VEC> ks((uint32_t)a.k_t, a.D), vs((uint32_t)a.v_t, a.D);
+    const T *kp = x.keys<T>(a), *vp = x.values<T>(a);
+    const int64_t k_step = KB * a.k_t, v_step = KB * a.v_t;
+    int left = x.s.nk - x.begin;  // keys from the next tile to load on
+    const auto fetch = [&](int b) {
+        ks(kp, left, kt + b * kTileBytes);
+        vs(vp, left, vt + b * kTileBytes);
+        kp += k_step;
+        vp += v_step;
+        left -= KB;
+    };
+    const auto scores = [&](f16 &p, f16 &dp, int b) {
+        p = f16(0.0f);
+        dp = f16(less);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            mma(p, row_frag<T, DP>(kt + b * kTileBytes, 0, c), q[c]);
+            mma(dp, row_frag<T, DP>(vt + b * kTileBytes, 0, c), dout[c]);
+        }
+    };
+    if (x.tiles > 0) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) fetch(b);
+        landed<3 * kLoads>();
+        la::lds_barrier();
+        int j0 = 0;
+        // tile n's sum, tile n + 1's scores, and tile n + 4 into the buffer of tile n, which all have read
+        const auto step = [&](auto B, f16 &p, f16 &dp, f16 &next_p, f16 &next_dp) {
+            landed<2 * kLoads>();
+            la::lds_barrier();
+            fetch(B);
+            if (j0 + KB - 1 > wave_first) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (j0 + 8 * (i >> 2) + 4 * half + (i & 3) > my_last) {
+                        p[i] = -INFINITY;
+                        dp[i] = 0.0f;  // a NaN or Inf there
+                    }
+            }
+            j0 += KB;
+            scores(next_p, next_dp, B + 1 & 3);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) rest[i & 3] = __builtin_fmaf(dp[i], exp2_fast(__builtin_fmaf(p[i], sc, -lse)), rest[i & 3]);
+        };
+        f16 p, dp, next_p, next_dp;
+        scores(p, dp, 0);
+        for (int n = x.tiles;;) {
+            step(std::integral_constant<int, 0>(), p, dp, next_p, next_dp);
+            if (--n == 0) break;
+            step(std::integral_constant<int, 1>(), next_p, next_dp, p, dp);
+            if (--n == 0) break;
+            step(std::integral_constant<int, 2>(), p, dp, next_p, next_dp);
+            if (--n == 0) break;
+            step(std::integral_constant<int, 3>(), next_p, next_dp, p, dp);
+            if (--n == 0) break;
+        }
+        landed();
+    }
+    float sum = (rest[0] + rest[1]) + (rest[2] + rest[3]);
+    sum += other_half(sum);
+    if (half == 0 && col < x.rows()) a.rest[(x.piece * a.H + x.h) * tokens + x.row + col] = sum;
+}
+
 // dq: a workgroup takes 32 queries a wavefront of one head, with their gradients in registers, and walks the keys that they
 // see in tiles of 32, pipelined as above: four LDS buffers for keys, which are read one tile longer, and two for values.
 template <typename T, int DP, bool VEC>
 __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void softmax_dq_kernel(SoftmaxLaunch a,
                                                                                                         SoftmaxWork work,
                                                                                                         int64_t tokens) {
-    constexpr int KB = 32, NC = DP / kChunk<T>, ND = DP / 32, BQ = 32 * kSoftmaxThreads / 64;
+    constexpr int KB = QueryWalk::KB, NC = DP / kChunk<T>, ND = DP / 32;
     constexpr int kTileBytes = KB * Tile<T, DP>::kRow;
     __shared__ __attribute__((aligned(1024))) char kt[4 * kTileBytes], vt[2 * kTileBytes];
 
-    SoftmaxPlace at;
-    if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
-    const int64_t is = at.seq;
-    const int g = at.g, h = g * work.per + at.which, qb = work.blocks - 1 - at.block;
-    const AttnSeq s = sequence(a.rows, is);
-    const bool packed = a.rows.cu_q != nullptr;
-    const int w = la::wave_id(), l = threadIdx.x & 63, col = l & 31, half = l >> 5;
-    const int q0 = qb * BQ, r0 = q0 + 32 * w;
-    const int to_write = packed ? s.nq : (int)a.rows.Lq;
-    if (q0 >= to_write) return;
-
-    const T *kp = static_cast<const T *>(a.k) + is * a.k_b + s.k0 * a.k_t + g * a.k_h;
-    const T *vp = static_cast<const T *>(a.v) + is * a.v_b + s.k0 * a.v_t + g * a.v_h;
-    const int last_q = (q0 + BQ < s.nq ? q0 + BQ : s.nq) - 1;
-    const int keys = last_q >= q0 ? last_key(s, a.causal, last_q) + 1 : 0;
-    int pieces;
-    const int per = softmax_piece(work, (keys + KB - 1) / KB, &pieces);
-    if (at.piece >= pieces) return;
-    // all counted from the piece's first key
-    const int begin = at.piece * per * KB, n_keys = pieces > 1 && keys - begin > per * KB ? per * KB : keys - begin;
-    const int tiles = (n_keys + KB - 1) / KB;
-    const int my_last = last_key(s, a.causal, r0 + col) - begin;
-    const int wave_first = last_key(s, a.causal, r0) - begin;
-    kp += begin * a.k_t;
-    vp += begin * a.v_t;
-    const int64_t row = (packed ? s.q0 : is * a.rows.Lq) + r0;
+    QueryWalk x;
+    if (!x.set(a, work)) return;
+    const int l = threadIdx.x & 63, col = l & 31, half = l >> 5;
+    const int my_last = x.last(a, col), wave_first = x.last(a, 0);
 
     Frag<T> q[NC], dout[NC];
-    float lse = INFINITY, less = 0.0f, rest = 0.0f;  // less: −delta; rest: the lane's half of Σ ds
-    float *stat = a.stats + h * tokens + row + col;
-    {
-        const int rows = s.nq - r0 > 32 ? 32 : s.nq - r0;
-        const T *qp = static_cast<const T *>(a.q) + is * a.q_b + (s.q0 + r0) * a.q_t + h * a.q_h;
-        const T *dp = static_cast<const T *>(a.dout) + is * a.do_b + (s.q0 + r0) * a.do_t + h * a.do_h;
-        const uint32_t o_t = (uint32_t)(a.H * a.D);
-        Frag<T> o[NC];
-        load_frags<T, DP, VEC>(o, la::rows_buffer(static_cast<const T *>(a.o_in) + (row * a.H + h) * a.D, o_t, rows, a.D), o_t,
-                               col, rows, a.D);
-        load_frags<T, DP, VEC>(dout, la::rows_buffer(dp, (uint32_t)a.do_t, rows, a.D), (uint32_t)a.do_t, col, rows, a.D);
-        load_frags<T, DP, VEC>(q, la::rows_buffer(qp, (uint32_t)a.q_t, rows, a.D), (uint32_t)a.q_t, col, rows, a.D);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int e = 0; e < kE<T>; ++e) less = __builtin_fmaf(-(float)dout[c][e], (float)o[c][e], less);
-        less += other_half(less);
-        if (a.scale < 0.0f) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) negate<T>(q[c]);
+    float lse, less, size;  // less: −delta
+    load_queries<T, DP, VEC>(a, x, q, dout, lse, less, size);
+    if (col < x.rows()) {
+        const int64_t at = x.h * tokens + x.row + col;
+        if constexpr (sizeof(T) == 2) {
+            float rest = 0.0f;
+            for (int i = 0; i < x.pieces; ++i) rest += a.rest[i * a.H * tokens + at];
+            // more than twice the rounding of o: o and lse are of more keys than these, whose part of delta is not here
+            if (__builtin_fabsf(rest) <= 0x1p-7f * size) less -= rest;
         }
-        if (col < rows) {
-            const float given = a.lse_in[(row + col) * a.H + h];
-            // a query that saw no key (lse = −inf): weights of 0
-            lse = given == -INFINITY ? INFINITY : given * kLog2e;
-        }
-        if (half == 0 && col < rows && at.piece == 0) {
-            stat[0] = lse;
-            stat[tokens * a.H] = less;
+        if (half == 0 && x.piece == 0) {
+            a.stats[at] = lse;
+            a.stats[a.H * tokens + at] = less;
         }
     }
     const float sc = scale_of(a.scale);
@@ -314,8 +437,9 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
     for (int d = 0; d < ND; ++d) dq[d] = f16(0.0f);
 
     const Loader<T, KB, DP, VEC> ks((uint32_t)a.k_t, a.D), vs((uint32_t)a.v_t, a.D);
+    const T *kp = x.keys<T>(a), *vp = x.values<T>(a);
     const int64_t k_step = KB * a.k_t, v_step = KB * a.v_t;
-    int left = s.nk - begin;  // keys from the next tile to load on
+    int left = x.s.nk - x.begin;  // keys from the next tile to load on
     const auto fetch = [&](int b) {
         ks(kp, left, kt + b * kTileBytes);
         vs(vp, left, vt + (b & 1) * kTileBytes);
@@ -333,7 +457,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
             mma(dp, row_frag<T, DP>(vt + (b & 1) * kTileBytes, 0, c), dout[c]);
         }
     };
-    if (tiles > 0) {
+    if (x.tiles > 0) {
         fetch(0);
         fetch(1);
         landed();
@@ -351,10 +475,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
             j0 += KB;
             scores(next_p, next_dp, B + 1 & 3);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                dp[i] *= exp2_fast(__builtin_fmaf(p[i], sc, -lse));
-                rest += dp[i];
-            }
+            for (int i = 0; i < 16; ++i) dp[i] *= exp2_fast(__builtin_fmaf(p[i], sc, -lse));
 #pragma unroll
             for (int c = 0; c < 32 / kChunk<T>; ++c) {
                 const Split<T> df(dp, c);
@@ -365,7 +486,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
         };
         f16 p, dp, next_p, next_dp;
         scores(p, dp, 0);
-        for (int n = tiles;;) {
+        for (int n = x.tiles;;) {
             step(std::integral_constant<int, 0>(), p, dp, next_p, next_dp);
             if (--n == 0) break;
             step(std::integral_constant<int, 1>(), next_p, next_dp, p, dp);
@@ -377,30 +498,24 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
         }
         landed();
     }
-    // Σ_j ds_ij is 0 but for the rounding of o, from which delta was formed: what is left corrects delta for dk.
-    rest += other_half(rest);
-    if (pieces > 1) {
-        const int rows = s.nq - r0 > 32 ? 32 : s.nq - r0;
-        const uint32_t stride = (uint32_t)(a.H * a.D);
-        const Buffer out = la::rows_buffer(a.part + ((at.piece * tokens + row) * a.H + h) * a.D, stride, rows, a.D);
+    const uint32_t stride = (uint32_t)(a.H * a.D);
+    if (x.pieces > 1) {
+        const int rows = x.rows();
+        const Buffer out = la::rows_buffer(a.part + ((x.piece * tokens + x.row) * a.H + x.h) * a.D, stride, rows, a.D);
 #pragma unroll
         for (int d = 0; d < ND; ++d) store_tile<float, VEC>(out, stride, col, 32 * d, col < rows ? a.D : 0, dq[d], 1.0f);
-        if (half == 0 && col < rows)
-            a.part[work.splits * tokens * a.H * a.D + (at.piece * a.H + h) * tokens + row + col] = rest;
         return;
     }
-    if (half == 0 && r0 + col < s.nq) stat[tokens * a.H] = less - rest;
-    const int rows = to_write - r0 > 32 ? 32 : to_write - r0;
-    const uint32_t stride = (uint32_t)(a.H * a.D);
-    const Buffer out = la::rows_buffer(static_cast<T *>(a.dq) + (row * a.H + h) * a.D, stride, rows, a.D);
+    const int rows = x.to_write - x.r0 > 32 ? 32 : x.to_write - x.r0;
+    const Buffer out = la::rows_buffer(static_cast<T *>(a.dq) + (x.row * a.H + x.h) * a.D, stride, rows, a.D);
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
-        if (r0 + col >= s.nq) dq[d] = f16(0.0f);
+        if (x.r0 + col >= x.s.nq) dq[d] = f16(0.0f);
         store_tile<T, VEC>(out, stride, col, 32 * d, col < rows ? a.D : 0, dq[d], a.scale);
     }
 }
 
-// Sums of pieces, in their order: of a block of queries' dq, with delta's correction, or of a block of keys' dk and dv.
+// Sums of pieces, in their order: of a block of queries' dq, or of a block of keys' dk and dv.
 template <typename T, bool KEYS>
 __global__ __launch_bounds__(kSoftmaxThreads) void softmax_bwd_join_kernel(SoftmaxLaunch a, SoftmaxWork work, SoftmaxWork join) {
     SoftmaxPlace at;
@@ -440,11 +555,6 @@ __global__ __launch_bounds__(kSoftmaxThreads) void softmax_bwd_join_kernel(Softm
         static_cast<T *>(KEYS ? a.dk : a.dq)[to + d] = narrow<T>(x[u] * a.scale);
         if (KEYS) static_cast<T *>(a.dv)[to + d] = narrow<T>(y[u]);
     }
-    if (!KEYS && l == 0 && m > 0) {
-        float rest = 0.0f;
-        for (int i = 0; i < m; ++i) rest += a.part[work.splits * apart + (i * a.H + h) * tokens + row];
-        a.stats[(a.H + h) * tokens + row] -= rest;
-    }
 }
 
 template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, hipStream_t stream) {
@@ -453,6 +563,10 @@ template <typename T, int DP, bool VEC> hipError_t run(const SoftmaxLaunch &p, h
     hipError_t e = hipSuccess;
     if (qw.blocks > 0) {
         const dim3 grid((unsigned)softmax_groups(qw));
+        if constexpr (sizeof(T) == 2) {
+            softmax_rest_kernel<DP, VEC><<<grid, kSoftmaxThreads, 0, stream>>>(p, qw, tokens);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
         softmax_dq_kernel<T, DP, VEC><<<grid, kSoftmaxThreads, 0, stream>>>(p, qw, tokens);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (qw.splits > 1) {

@@ -243,8 +243,8 @@ __device__ __forceinline__ void load_stats(const float *first, int rows, char *l
                      : "s"((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds), "v"(l * 4u), "s"(buf)
                      : "memory");
 }
-// The wavefront's loads into LDS are there.
-__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// The wavefront's loads into LDS are there, but for the last `left`.
+template <int left = 0> __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(%0)" ::"i"(left) : "memory"); }
 
 // The value of the lane 32 away.
 __device__ __forceinline__ float other_half(float v) {

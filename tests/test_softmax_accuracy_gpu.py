@@ -2,7 +2,17 @@
 
 The bounds are those of softmax_ref.py but that weights enter products in two bf16 parts, the second of which is what the first
 leaves, rounded: (2^-8)^2 = 2^-16 of each instead of 2^-8. Results of one part are outside of them wherever a sum's terms cancel
-(test_one_part_is_outside shows it on the CPU)."""
+(test_one_part_is_outside shows it on the CPU).
+
+delta, as the gradient's kernels form it with D' = do·o of a rounded o: D' + Σ_j p_j (do·v_j − D'). Weights off by e of their value
+(their sum so off 1 by e), products by (D + 1)·u·(Σ|do||v_j| + |D'|), and a sum of nk terms make of that
+Σ_j p_j ((e + (nk + 4)·u)(|do·v_j| + |D'|) + (D + 1)·u·(Σ|do||v_j| + |D'|)) + 4u·|D'|, where |D'| <= |delta| + Σ|do|·(what o is off by).
+Where what is left could be more than 2^-7·Σ|do o|, the kernels take D' itself (grad_bounds).
+
+Norms: rounding alone puts a result ‖x − bf16(x)‖ off, 1.6e-3 of its norm. 1.1 of that leaves 0.45 of it, 7e-4, to all else, which is
+independent of it: two parts (2^-16 = 1.5e-5 of each weight) and fp32 products (below 1e-4 for these sizes, keys of 4 deviations'
+offset among them). One part of ds or of the weights (1.2 to 1.4 of that) or a delta from the rounded o (1.2, with
+offsets of the keys up to 6) does not fit in."""
 import math
 
 import pytest
@@ -100,11 +110,98 @@ def gradients(nq, nk, H, G, D, causal, shift=0.0):
     return (q, k, v, do), {n: x[0] for n, x in g.items()}
 
 
+def grad_bounds(q, k, v, do, scale, causal, given=None):
+    """dq, dk, dv of one sequence and how far results may be from them. given: (o, lse) of more keys than these, whose delta do·o
+    is then taken as it is."""
+    nq, H, D = q.shape
+    nk, G = k.shape[:2]
+    see = R.visible(nq, nk, causal)
+    o, lse, tol_o, _ = R.bounds(q, k, v, scale, causal, BF16)
+    if given is not None:
+        o, lse, tol_o = given
+    p, a, head = R._weights(q, k, scale, lse, see)
+    first = lambda t: t.transpose(0, 1)  # noqa: E731  heads first
+    e = R.relative(a, lse, D, nk) + 2 * R.U * lse.t()[..., None].abs().nan_to_num(0, 0, 0)
+    dp = torch.matmul(first(do), v[:, head].permute(1, 2, 0))
+    size_dp = torch.matmul(first(do).abs(), v[:, head].abs().permute(1, 2, 0))
+    delta = (do * o).sum(-1).t()[..., None]
+    of_o = (do.abs() * tol_o).sum(-1).t()[..., None]
+    rough = of_o + D * R.U * (do.abs() * o.abs()).sum(-1).t()[..., None]
+    d0 = delta.abs() + rough
+    off_dp = (D + 1) * R.U * (size_dp + d0)
+    fine = (p * ((e + (nk + 4) * R.U) * (dp.abs() + d0) + off_dp)).sum(-1, keepdim=True) + 4 * R.U * d0
+    surely = rough + fine < 2.0 ** -7 * (1 - 2.0 ** -7) * (do.abs() * o.abs()).sum(-1).t()[..., None]
+    off_delta = torch.where(surely, fine, torch.maximum(fine, rough)) if given is None else rough
+    ds = p * (dp - delta)
+    off = p * (e * (dp.abs() + delta.abs()) + off_dp + off_delta + 2 * R.U * (dp.abs() + delta.abs()))
+    size = lambda n: R.PART[BF16] * 1.01 + (n + 4) * R.U  # noqa: E731
+    dq = scale * torch.matmul(ds, first(k[:, head])).transpose(0, 1)
+    dk = scale * torch.matmul(ds.transpose(1, 2), first(q))
+    dv = torch.matmul(p.transpose(1, 2), first(do))
+    t_q = abs(scale) * torch.matmul(off + size(nk) * (ds.abs() + off), first(k[:, head]).abs()).transpose(0, 1)
+    t_k = abs(scale) * torch.matmul((off + size(nq * H // G) * (ds.abs() + off)).transpose(1, 2), first(q).abs())
+    t_v = torch.matmul((p * (e + size(nq * H // G))).transpose(1, 2), first(do).abs())
+    fold = lambda t: t.reshape(G, H // G, nk, D).sum(1).transpose(0, 1)  # noqa: E731
+    end = lambda t, ref: t + R.HALF[BF16] * (ref.abs() + t) + 2.0 ** -110  # noqa: E731
+    dk, dv = fold(dk), fold(dv)
+    return (dq, dk, dv), (end(t_q, dq), end(fold(t_k), dk), end(fold(t_v), dv))
+
+
+def test_the_bounds_are_of_the_same_gradient():
+    x = normal(0, (40, 4, 16), (60, 2, 16), (60, 2, 16), (40, 4, 16))
+    for a, b in zip(grad_bounds(*x, 0.25, True)[0], R.grads(*x, 0.25, True)):
+        assert (a - b).abs().max() <= 1e-12 * b.abs().max()
+
+
+def norms(g, ref):
+    for n, want in zip(("dq", "dk", "dv"), ref):
+        own = (want - want.bfloat16().double()).norm()
+        off = (g[n].double().cpu() - want).norm()
+        assert off <= 1.1 * own, f"{n}: {off / own:.3f} of its own rounding ({own / want.norm():.2e})"
+
+
 @gpu
 @pytest.mark.parametrize("nq,nk,H,G,D", GRADIENT)
 @pytest.mark.parametrize("causal", [True, False])
-def test_gradient_of_values(lib, nq, nk, H, G, D, causal):
+def test_gradient(lib, nq, nk, H, G, D, causal):
     x, g = gradients(nq, nk, H, G, D, causal)
-    q, k, v, do = (t[:, : t.shape[1] // G] for t in x)  # the first key head and its queries' heads
-    (_, _, dv), (_, _, tol) = R.grad_bounds(q, k, v, do, D ** -0.5, causal, BF16)
-    R.assert_within(g["dv"][:, :1], dv, tol, "dv")
+    few = [t[:, : t.shape[1] // G] for t in x]  # the first key head and its queries' heads
+    got = {n: t[:, : t.shape[1] // G] for n, t in g.items()}
+    ref, tol = grad_bounds(*few, D ** -0.5, causal)
+    for n, r, t in zip(("dv", "dk", "dq"), ref[::-1], tol[::-1]):
+        R.assert_within(got[n], r, t, n)
+    norms(got, ref)
+
+
+@gpu
+@pytest.mark.parametrize("shift", [1.0, 4.0])
+@pytest.mark.parametrize("L,H,G,D", [(64, 2, 2, 64), (512, 4, 2, 64), (1500, 2, 1, 128), (2000, 24, 24, 64)])
+def test_keys_that_share_an_offset(lib, L, H, G, D, shift):
+    """dq does not change with what all keys have in common, and its error does not grow with it."""
+    x, g = gradients(L, L, H, G, D, True, shift)
+    ref, _ = grad_bounds(*(t[:, : t.shape[1] // G] for t in x), D ** -0.5, True)
+    norms({n: t[:, : t.shape[1] // G] for n, t in g.items()}, ref)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("L,cut", [(300, 170), (1500, 64)])
+def test_keys_in_shards(lib, L, cut, dtype):
+    """o and lse of all keys, the gradient of some of them in each call: dk and dv are theirs, and dq adds up."""
+    q, k, v, do = normal(L, (L, 2, 64), (L, 1, 64), (L, 1, 64), (L, 2, 64))
+    t = [x.to(dtype)[None].cuda() for x in (q, k, v, do)]
+    o, lse = api.ssm_attn_fwd(*t[:3], causal=False, return_lse=True)
+    whole = R.bounds(q, k, v, 0.125, False, BF16)
+    dq, tol_q = 0.0, 0.0
+    got_q = torch.zeros(L, 2, 64, dtype=torch.float64)
+    for part in (slice(0, cut), slice(cut, L)):
+        g = api.ssm_attn_bwd(t[0], t[1][:, part], t[2][:, part], o=o, lse=lse, do=t[3], causal=False)
+        ref, tol = grad_bounds(q, k[part], v[part], do, 0.125, False, given=whole[:3])
+        for n, r, e in zip(("dv", "dk"), ref[:0:-1], tol[:0:-1]):
+            R.assert_within(g[n][0], r, e, n)
+        R.assert_within(g["dq"][0], ref[0], tol[0], "dq")
+        got_q += g["dq"][0].double().cpu()
+        dq, tol_q = dq + ref[0], tol_q + tol[0]
+    assert ((got_q - dq).abs() <= tol_q).all()
+    full = R.grads(q, k, v, do, 0.125, False)[0]
+    assert (dq - full).abs().max() <= 1e-12 * full.abs().max()
