@@ -411,7 +411,9 @@ SSM_API ssm_status_t ssm_layernorm_bwd(const void *x, const float *w, const void
  * −Inf counts as one that sees no key.
  * b, H, G, D >= 1; G divides H; D <= SSM_ATTN_MAX_D and scale finite (SSM_ERR_UNSUPPORTED otherwise); Lq, Lk <= 2^30; H·D and
  * strides between tokens at most 2^24; a launch takes fewer than 2^32 threads: SSM_ERR_SHAPE where b·H·⌈Lq/128⌉ or
- * b·G·⌈Lk/128⌉ (b·G rounded up to a multiple of 8, and ⌈./128⌉ to one of ⌈8/G⌉) reaches 2^23. No output may overlap an
+ * b·G·⌈Lk/128⌉ (b·G rounded up to a multiple of 8, and ⌈./128⌉ to one of ⌈8/G⌉) reaches 2^23. Packed sequences count as
+ * ⌊tokens/128⌋ + b blocks in place of b·⌈L/128⌉ (rounded up to a multiple of 8) where that is less and b·⌈L/128⌉ times the heads
+ * passes 2^16. No output may overlap an
  * input, the workspace or another output. Where few blocks of 128 queries (keys, in the gradient for k and v) leave the device idle,
  * the keys (queries) are summed in up to 16 pieces: then fp32 sums, and so the last bits, depend on b, H, G, the lengths' bounds and tokens.
  */

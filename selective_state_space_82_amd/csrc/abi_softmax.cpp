@@ -6,7 +6,7 @@
 
 #include <cmath>
 #include <cstdint>
-#include <utility>
+#include <tuple>
 
 #include "host_util.h"
 #include "launch_attn.h"
@@ -126,10 +126,11 @@ ssm_status_t check_rows(const ssm_attn_rows_t *r, int64_t H, int64_t G, int64_t 
     if (*tokens_q > kMost / SSM_ATTN_MAX_D / H || *tokens_k > kMost / SSM_ATTN_MAX_D / G) return SSM_ERR_SHAPE;
     if (r->b > kMost / H) return SSM_ERR_SHAPE;
     // No plan is made of sizes whose blocks alone are more than a launch takes.
-    for (const auto &[L, heads] : {std::pair(r->Lq, H), std::pair(r->Lk, G)}) {
+    for (const auto &[L, tokens, heads] : {std::tuple(r->Lq, *tokens_q, H), std::tuple(r->Lk, *tokens_k, G)}) {
         int64_t n = 0;
-        if (!mul_ok(r->b, ceil_div(L, ssm::kSoftmaxBlock), &n) || !mul_ok(n, heads, &n) || !launchable(n, 2 * ssm::kSoftmaxThreads))
-            return SSM_ERR_SHAPE;
+        if (!mul_ok(r->b, ceil_div(L, ssm::kSoftmaxBlock), &n)) return SSM_ERR_SHAPE;
+        const int64_t slots = tokens / ssm::kSoftmaxBlock + r->b;
+        if (!mul_ok(r->cu_q && slots < n ? slots : n, heads, &n) || !launchable(n, 2 * ssm::kSoftmaxThreads)) return SSM_ERR_SHAPE;
     }
     const ssm::AttnRows z = attn_rows(*r);
     for (const ssm::SoftmaxWork &w : {ssm::softmax_fwd_work(z, H, G, true), ssm::softmax_fwd_work(z, H, G, false),

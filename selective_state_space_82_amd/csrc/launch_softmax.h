@@ -35,10 +35,19 @@ constexpr int kSoftmaxThreads = 256;
 // after the other. (Units as runs of neighbours: 9 sequences of 100 to 4096 tokens, 8 key heads, gradient 6.5 ms.)
 // Where there are too few of these to fill the device, the tiles that a block walks are cut into up to `splits` pieces of at
 // least `least` tiles, a workgroup each, and a second launch joins them.
+//
+// Packed sequences may be many and most of them far shorter than the longest. Where workgroups for the longest's blocks of each
+// would be more than 2^16 (which start in 30 us), a launch has them for slots of a block instead: sequence i has those from
+// ⌊cu_i/128⌋ + i on, of which there are enough whatever its length, ⌊tokens/128⌋ + b in all, and a workgroup finds its sequence in
+// the offsets (softmax_find). (Lengths of exponential spread, bf16, forward and gradient, by sequences and by slots: 2^21 workgroups for
+// 1024 sequences of up to 8192, 138726 tokens, 32 heads on 8 key heads of 128: 5.4 and 2.3 ms, 18.5 and 8.3 ms; 1.1·2^16 for 96 of
+// up to 4096, 24 heads of 64: 3.7 and 2.9, 13.9 and 11.0; 2^17 for 128 of up to 4096, 32 heads on 8 of 128: 8.2 and 8.2, 36.7 and
+// 36.8. Below 2^16 calls are as they were.)
 struct SoftmaxWork {
     int64_t units, each;  // each: workgroups of a unit
     int parts, per, blocks, splits, least;
     bool across;  // an XCD takes the first block of each of its units, then the second of each, ...; otherwise unit by unit
+    int block = 0, most = 0;  // by slots: tokens of a block (0: by sequences), and blocks of the longest sequence
 };  // workgroups number less than 2^24
 inline SoftmaxWork softmax_work(int64_t b, int64_t G, int64_t per, int64_t blocks, int64_t splits, int64_t least) {
     const int64_t parts = G >= 8 || blocks < 2 ? 1 : ((8 + G - 1) / G < blocks ? (8 + G - 1) / G : blocks);
@@ -48,6 +57,13 @@ inline SoftmaxWork softmax_work(int64_t b, int64_t G, int64_t per, int64_t block
     // by unit, 264 across; 8 of 4096, 32 heads on 8 key heads, forward: 1091 and 1139.)
     return {units, each, (int)parts, (int)per, (int)blocks, (int)splits, (int)least,
             each < 64 && (units + 7) / 8 * each >= 128};
+}
+// By slots: all sequences' blocks of a key head as if they were one sequence's, spread so that each XCD has as many units.
+inline SoftmaxWork softmax_slot_work(int64_t G, int64_t per, int64_t slots, int64_t splits, int64_t least, int64_t block, int64_t most) {
+    int64_t parts = G % 8 == 0 ? 1 : G % 4 == 0 ? 2 : G % 2 == 0 ? 4 : 8;
+    parts = parts < slots ? parts : slots;
+    return {G * parts, per * splits * ((slots + parts - 1) / parts), (int)parts, (int)per, (int)slots, (int)splits, (int)least, false,
+            (int)block, (int)most};
 }
 inline int64_t softmax_groups(const SoftmaxWork &w) { return (w.units + 7) / 8 * 8 * w.each; }
 // Of a workgroup: sequence, key head, which of the `per`, which block counted from the first to be taken, which piece of it;
@@ -66,6 +82,28 @@ SSM_BOTH bool softmax_place(const SoftmaxWork &w, int64_t G, uint32_t id, Softma
     p->which = (int)(row % (uint32_t)w.per);
     p->block = (int)(row / (uint32_t)w.per * (uint32_t)w.parts + part);
     return unit < (uint32_t)w.units && p->block < w.blocks;
+}
+// The same with the block's place in its sequence, of queries (the last first) or of keys (the first first).
+SSM_BOTH bool softmax_find(const SoftmaxWork &w, const AttnRows &r, int64_t G, uint32_t id, bool keys, SoftmaxPlace *p) {
+    if (!softmax_place(w, G, id, p)) return false;
+    const int at = keys ? p->block : w.blocks - 1 - p->block;
+    p->block = at;
+    if (w.block == 0) return true;
+    const int32_t *cu = keys ? r.cu_k : r.cu_q;
+    const int64_t tokens = keys ? r.Tk : r.Tq;
+    int64_t lo = 0, hi = r.b, first = clamp_to(cu[0], 0, tokens) / w.block;  // lo's first slot <= at, where offsets rise
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) / 2, from = clamp_to(cu[mid], 0, tokens) / w.block + mid;
+        if (from <= at) {
+            lo = mid;
+            first = from;
+        } else {
+            hi = mid;
+        }
+    }
+    p->seq = lo;
+    p->block = (int)(at - first);
+    return at >= first && at - first < w.most;
 }
 // Tiles of each piece of a walk of `tiles`, and how many pieces it has.
 SSM_BOTH int softmax_piece(const SoftmaxWork &w, int tiles, int *pieces) {
@@ -92,7 +130,7 @@ inline int64_t softmax_blocks(const AttnRows &r, int64_t L, int64_t tokens) {
     return r.cu_q && some < all ? some : all;
 }
 // Pieces for `groups` blocks of walks of up to `tiles` tiles where `fill` workgroups fill the device; `launched`: blocks that
-// a launch has workgroups for, which many packed sequences of different lengths leave mostly empty (2^16 of them start in 30 us).
+// a launch has workgroups for, of which packed sequences of different lengths leave some empty (2^16 of them start in 30 us).
 inline int64_t softmax_splits(int64_t groups, int64_t launched, int64_t tiles, int64_t least, int64_t fill) {
     int64_t n = groups > 0 ? (fill + groups - 1) / groups : 1;
     if (n > 1 && n * launched > (INT64_C(1) << 16)) n = (INT64_C(1) << 16) / launched;
@@ -101,12 +139,18 @@ inline int64_t softmax_splits(int64_t groups, int64_t launched, int64_t tiles, i
     n = n < most ? n : most;
     return n > 1 ? n : 1;
 }
+// Slots of packed sequences of at most L tokens for `heads` workgroups a block, or 0: by sequences.
+inline int64_t softmax_slots(const AttnRows &r, int64_t L, int64_t tokens, int64_t heads) {
+    const int64_t all = r.b * ((L + kSoftmaxBlock - 1) / kSoftmaxBlock), slots = tokens / kSoftmaxBlock + r.b;
+    return r.cu_q && slots < all && all * heads > (INT64_C(1) << 16) ? slots : 0;
+}
 inline SoftmaxWork softmax_query_work(const AttnRows &r, int64_t H, int64_t G, int64_t keys) {
     const int64_t least = kSoftmaxLeast / keys;
-    const int64_t blocks = (r.Lq + kSoftmaxBlock - 1) / kSoftmaxBlock;
-    const int64_t splits =
-        softmax_splits(softmax_blocks(r, r.Lq, r.Tq) * H, r.b * blocks * H, (r.Lk + keys - 1) / keys, least, 1024);
-    return softmax_work(r.b, G, H / G, blocks, splits, least);
+    const int64_t blocks = (r.Lq + kSoftmaxBlock - 1) / kSoftmaxBlock, slots = softmax_slots(r, r.Lq, r.Tq, H);
+    const int64_t splits = softmax_splits(softmax_blocks(r, r.Lq, r.Tq) * H, (slots > 0 ? slots : r.b * blocks) * H,
+                                          (r.Lk + keys - 1) / keys, least, 1024);
+    return slots > 0 ? softmax_slot_work(G, H / G, slots, splits, least, kSoftmaxBlock, blocks)
+                     : softmax_work(r.b, G, H / G, blocks, splits, least);
 }
 inline SoftmaxWork softmax_fwd_work(const AttnRows &r, int64_t H, int64_t G, bool bf16) {
     return softmax_query_work(r, H, G, bf16 ? 64 : 32);  // keys of a tile
@@ -114,8 +158,11 @@ inline SoftmaxWork softmax_fwd_work(const AttnRows &r, int64_t H, int64_t G, boo
 inline SoftmaxWork softmax_dq_work(const AttnRows &r, int64_t H, int64_t G) { return softmax_query_work(r, H, G, 32); }
 inline SoftmaxWork softmax_dkv_work(const AttnRows &r, int64_t H, int64_t G) {
     const int64_t blocks = (r.Lk + kSoftmaxBlock - 1) / kSoftmaxBlock, least = kSoftmaxLeast / 32;
-    const int64_t splits = softmax_splits(softmax_blocks(r, r.Lk, r.Tk) * G, r.b * blocks * G, (r.Lq + 31) / 32 * (H / G), least, 512);
-    return softmax_work(r.b, G, 1, blocks, splits, least);
+    const int64_t slots = softmax_slots(r, r.Lk, r.Tk, G);
+    const int64_t splits = softmax_splits(softmax_blocks(r, r.Lk, r.Tk) * G, (slots > 0 ? slots : r.b * blocks) * G,
+                                          (r.Lq + 31) / 32 * (H / G), least, 512);
+    return slots > 0 ? softmax_slot_work(G, 1, slots, splits, least, kSoftmaxBlock, blocks)
+                     : softmax_work(r.b, G, 1, blocks, splits, least);
 }
 hipError_t launch_softmax_fwd(const SoftmaxLaunch &p, hipStream_t stream);
 hipError_t launch_softmax_bwd(const SoftmaxLaunch &p, hipStream_t stream);

@@ -35,9 +35,9 @@ __global__ __launch_bounds__(2 * kSoftmaxThreads, DP * sizeof(T) > 128 ? 2 : 4) 
     __shared__ __attribute__((aligned(16))) char lse_t[2 * kStats], less_t[2 * kStats];  // lse, −delta of a tile's queries
 
     SoftmaxPlace at;
-    if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
+    if (!softmax_find(work, a.rows, a.G, blockIdx.x, true, &at)) return;  // the first keys, which most queries see, first
     const int64_t is = at.seq;
-    const int g = at.g, R = a.H / a.G, kb = at.block;  // the first keys, which most queries see, first
+    const int g = at.g, R = a.H / a.G, kb = at.block;
     const AttnSeq s = sequence(a.rows, is);
     const bool packed = a.rows.cu_q != nullptr;
     const int w = la::wave_id() & 3, l = threadIdx.x & 63, col = l & 31, half = l >> 5;
@@ -248,13 +248,13 @@ struct QueryWalk {
     // false: nothing to do
     __device__ __forceinline__ bool set(const SoftmaxLaunch &a, const SoftmaxWork &work) {
         SoftmaxPlace at;
-        if (!softmax_place(work, a.G, blockIdx.x, &at)) return false;
+        if (!softmax_find(work, a.rows, a.G, blockIdx.x, false, &at)) return false;
         is = at.seq;
         g = at.g;
         h = g * work.per + at.which;
         s = sequence(a.rows, is);
         const bool packed = a.rows.cu_q != nullptr;
-        const int q0 = (work.blocks - 1 - at.block) * BQ;
+        const int q0 = at.block * BQ;
         r0 = q0 + 32 * la::wave_id();
         to_write = packed ? s.nq : (int)a.rows.Lq;
         if (q0 >= to_write) return false;
@@ -519,10 +519,10 @@ __global__ __launch_bounds__(kSoftmaxThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2)
 template <typename T, bool KEYS>
 __global__ __launch_bounds__(kSoftmaxThreads) void softmax_bwd_join_kernel(SoftmaxLaunch a, SoftmaxWork work, SoftmaxWork join) {
     SoftmaxPlace at;
-    if (!softmax_place(join, a.G, blockIdx.x, &at)) return;
+    if (!softmax_find(join, a.rows, a.G, blockIdx.x, KEYS, &at)) return;
     const AttnSeq s = sequence(a.rows, at.seq);
     const bool packed = a.rows.cu_q != nullptr;
-    const int n = KEYS ? s.nk : s.nq, first = (KEYS ? at.block : work.blocks - 1 - at.block) * kSoftmaxBlock;
+    const int n = KEYS ? s.nk : s.nq, first = at.block * kSoftmaxBlock;
     const int rows = n - first > kSoftmaxBlock ? kSoftmaxBlock : n - first;
     if (rows <= 0) return;  // one piece
     const int tiles = KEYS ? ((s.nq + 31) / 32 - first_query(s, a.causal, first) / 32) * (a.H / a.G)

@@ -36,9 +36,9 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
     __shared__ int found;  // a NaN or Inf among the values of a tile that not every query sees whole
 
     SoftmaxPlace at;
-    if (!softmax_place(work, a.G, blockIdx.x, &at)) return;
+    if (!softmax_find(work, a.rows, a.G, blockIdx.x, false, &at)) return;  // the last queries, which see most, first
     const int64_t is = at.seq;
-    const int g = at.g, h = g * work.per + at.which, qb = work.blocks - 1 - at.block;  // the last queries, which see most, first
+    const int g = at.g, h = g * work.per + at.which, qb = at.block;
     const AttnSeq s = sequence(a.rows, is);
     const bool packed = a.rows.cu_q != nullptr;
     const int w = la::wave_id(), l = threadIdx.x & 63, col = l & 31, half = l >> 5;
@@ -259,8 +259,8 @@ template <typename T>
 __global__ __launch_bounds__(kSoftmaxThreads) void softmax_fwd_join_kernel(SoftmaxLaunch a, SoftmaxWork work, SoftmaxWork join) {
     constexpr int KB = kKeys<T>;
     SoftmaxPlace at;
-    if (!softmax_place(join, a.G, blockIdx.x, &at)) return;
-    const int h = at.g * work.per + at.which, q0 = (work.blocks - 1 - at.block) * kSoftmaxBlock;
+    if (!softmax_find(join, a.rows, a.G, blockIdx.x, false, &at)) return;
+    const int h = at.g * work.per + at.which, q0 = at.block * kSoftmaxBlock;
     const AttnSeq s = sequence(a.rows, at.seq);
     const bool packed = a.rows.cu_q != nullptr;
     const int rows = s.nq - q0 > kSoftmaxBlock ? kSoftmaxBlock : s.nq - q0;
