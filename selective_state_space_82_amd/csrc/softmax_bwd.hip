@@ -54,10 +54,7 @@ __global__ __launch_bounds__(2 * kSoftmaxThreads, DP * sizeof(T) > 128 ? 2 : 4) 
                             : static_cast<const T *>(a.k) + is * a.k_b + (s.k0 + r0) * a.k_t + g * a.k_h;
         const uint32_t step = (uint32_t)(second ? a.v_t : a.k_t);
         load_frags<T, DP, VEC>(kv, la::rows_buffer(p, step, rows, a.D), step, col, rows, a.D);
-        if (a.scale < 0.0f && !second) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) negate<T>(kv[c]);
-        }
+        if (!second) for_scale(kv, a.scale);
     }
     const int first = k0 < s.nk ? first_query(s, a.causal, k0) / QB : 0;
     const int tiles = k0 < s.nk ? (s.nq + QB - 1) / QB - first : 0;  // a head
@@ -304,10 +301,7 @@ __device__ __forceinline__ void load_queries(const SoftmaxLaunch &a, const Query
         }
     less += other_half(less);
     size += other_half(size);
-    if (a.scale < 0.0f) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c) negate<T>(q[c]);
-    }
+    for_scale(q, a.scale);
     lse = INFINITY;
     if (col < rows) {
         const float given = a.lse_in[(x.row + col) * a.H + x.h];

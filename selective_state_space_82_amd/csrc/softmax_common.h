@@ -252,13 +252,17 @@ __device__ __forceinline__ float other_half(float v) {
     return __uint_as_float((threadIdx.x & 32) ? a[0] : a[1]);
 }
 
-// The scale times log2 e, and whether the queries change sign for it: weights are then 2^(|scale|·log2 e·s − maximum). A scale of 0
-// counts as 2^-126 (scores below 2^-100 of any input that fp32 products can hold: the same weights), so that masked
+// Weights are 2^(scale_of(scale)·s − maximum) of scores s of a product's one operand as for_scale() leaves it: negated for a negative
+// scale, zeros for a scale of 0. So the factor is above 0 and finite (a scale of more than 2^128 / log2 e counts as that), and masked
 // scores of −inf stay what they are.
 __device__ __forceinline__ float scale_of(float scale) {
-    return __builtin_fmaxf(__builtin_fabsf(scale) * kLog2e, 1.17549435e-38f);
+    return scale == 0.0f ? 1.0f : __builtin_fminf(__builtin_fabsf(scale) * kLog2e, 3.40282347e38f);
 }
-template <typename T> __device__ __forceinline__ void negate(Frag<T> &f) { f = -f; }
+template <typename F, int N> __device__ __forceinline__ void for_scale(F (&f)[N], float scale) {
+    if (scale > 0.0f) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = scale < 0.0f ? -f[i] : F(0.0f);
+}
 
 // Results [8j + 4·half + r][col] as rows of a matrix: row `row` (the lane's), columns n0 + 8j + 4·half + r.
 template <typename T, bool VEC>

@@ -72,10 +72,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
         const int rows = s.nq - r0;
         load_frags<T, DP, VEC>(q, la::rows_buffer(qp, (uint32_t)a.q_t, rows > 32 ? 32 : rows, a.D), (uint32_t)a.q_t, col,
                                rows > 32 ? 32 : rows, a.D);
-        if (a.scale < 0.0f) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) negate<T>(q[c]);
-        }
+        for_scale(q, a.scale);
     }
     const float sc = scale_of(a.scale);
 

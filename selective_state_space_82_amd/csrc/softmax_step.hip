@@ -123,7 +123,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_step_kernel(Softma
         const T *qp = static_cast<const T *>(a.q) + is * a.q_b + (h0 + (col < heads ? col : 0)) * a.q_h;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            q[c] = load8<T, VEC>(qp, 32 * c + 8 * grp, col < heads ? a.D : 0);
+            q[c] = load8<T, VEC>(qp, 32 * c + 8 * grp, col < heads && a.scale != 0.0f ? a.D : 0);  // as for_scale() leaves it
             if (a.scale < 0.0f) q[c] = -q[c];
         }
     }
