@@ -108,7 +108,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, p[t][i]);
         top = __builtin_fmaxf(top, other_half(top)) * sc;
-        const bool raise = now && (top > m + kSlack || (m == -INFINITY && top > m));  // each query by itself: its bits are its own
+        const bool raise = now && top > m + kSlack;  // each query by itself: its bits are its own
         if (__any(raise)) {
             const float f = raise ? exp2_fast(m - top) : 1.0f;
             m = raise ? top : m;
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(kSoftmaxThreads, 2) void softmax_fwd_kernel(Softmax
     }
     // A masked key's weight is 0, but 0 times a NaN or Inf is not. Where there is one the block is done again, one tile after
     // the other, so that such values count as 0 in the product and make the result NaN for the queries that do see them.
-    if (found) {
+    if (tiles > 0 && found) {
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[d] = f16(0.0f);
         m = -INFINITY;
