@@ -217,7 +217,10 @@ bool caches_apart(const ssm_pages_t &g, const Span &k, const Span &v, int64_t ks
 
 constexpr int kLeast = 256;         // tokens of a piece: one tile for each wavefront
 constexpr int64_t kGroups = 512;    // workgroups that fill the device (two on each of 256 compute units)
-constexpr int64_t kLongest = 4096;  // tokens of a piece, so that one long row among short ones is spread too
+// Tokens of a piece, so that one long row among short ones is spread too. Pieces of 2048, 4096 and 8192, us (bf16, 32 heads on 8 key
+// heads of 128): 64 rows of up to 8192: 237, 260, 293; one of 8192 among 63 short ones 70, 79, 124; 64 of up to 16384 437, 437,
+// 488, one among short ones 103, 96, 137; 256 of up to 8192 790, 807, 846, one among short ones 176, 115, 146.
+constexpr int64_t kLongest = 4096;
 
 // Pieces that the longest row is cut into.
 int64_t step_splits(int64_t b, int64_t H, int64_t G, int64_t max_len) {

@@ -53,8 +53,12 @@ inline SoftmaxWork softmax_work(int64_t b, int64_t G, int64_t per, int64_t block
     const int64_t parts = G >= 8 || blocks < 2 ? 1 : ((8 + G - 1) / G < blocks ? (8 + G - 1) / G : blocks);
     const int64_t units = b * G * parts, each = per * splits * ((blocks + parts - 1) / parts);
     // The last unit's longest blocks should not start when all else is done: where a unit does not fill an XCD (32 compute units,
-    // two workgroups each) and there are rounds enough for that to matter. (4 sequences of 2048, 24 heads, gradient: 314 us unit
-    // by unit, 264 across; 8 of 4096, 32 heads on 8 key heads, forward: 1091 and 1139.)
+    // two workgroups each) and there are rounds enough for that to matter. Measured on both sides, unit by unit and across, us
+    // (bf16, causal; workgroups of a unit; of an XCD): 16; 192: forward 116 and 100, gradient 427 and 366. 32; 128: 147 and 131,
+    // 531 and 477. 48; 192: 438 and 407, 1725 and 1636. 64; 256: 731 and 694, 2915 and 2874. 96; 192: 812 and 786, 3190 and 3136.
+    // With four heads to a key head, whose tiles a unit shares: 32; 256: 134 and 126. 32; 512: 247 and 268. 32; 1024: 510 and
+    // 563. 64; 512: 413 and 424. Below the second border: 32; 64: 103 and 96. So the rule is right where it matters most and within
+    // 10 % elsewhere.
     return {units, each, (int)parts, (int)per, (int)blocks, (int)splits, (int)least,
             each < 64 && (units + 7) / 8 * each >= 128};
 }
