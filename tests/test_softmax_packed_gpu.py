@@ -87,6 +87,57 @@ def test_many_short_sequences(b, longest, most, total, H, G, D, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H,G", [(1, 1), (6, 3)])
+def test_cut_walks(H, G, dtype):
+    """Few tokens under a bound of 2^20: by slots, and walks cut into pieces that are joined."""
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm GPU visible")
+    lens = [300, 0, 1500, 1, 0, 130, 700, 128, 40]
+    more = [0, 50, 400, 900, 0, 3, 0, 127, 1]
+    x, cu, cu_k = case(lens, H, G, 64, dtype, more, before=5, behind=200, seed=H)
+    g = call(x, cu, 1 << 20, cu_k)
+    for i, n in enumerate(lens):
+        rows, keys, h = slice(cu[i], cu[i + 1]), slice(cu_k[i], cu_k[i + 1]), H // G
+        q, do = x["q"][rows, -h:].double(), x["do"][rows, -h:].double()
+        k, v = x["k"][keys, -1:].double(), x["v"][keys, -1:].double()
+        o, lse, tol_o, tol_lse = R.bounds(q, k, v, 0.125, True, dtype)
+        R.assert_within(g["o"][rows, -h:], o, tol_o, f"o of {i}")
+        R.assert_within(g["lse"][rows, -h:], lse, tol_lse, f"lse of {i}")
+        ref, tol = R.grad_bounds(q, k, v, do, 0.125, True, dtype)
+        for name, at, heads, want, t in zip(("dq", "dk", "dv"), (rows, keys, keys), (h, 1, 1), ref, tol):
+            R.assert_within(g[name][at, -heads:], want, t, f"{name} of {i}")
+
+
+@gpu
+def test_replayed_with_other_lengths():
+    """A captured call finds the sequences in the offsets that there are when it is replayed."""
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm GPU visible")
+    x, cu, _ = case(lengths(500, 700, 9000, 2), 12, 4, 32, BF16, behind=2000, seed=3)
+    T = x["q"].shape[0]
+    t = {n: v.cuda() for n, v in x.items()}
+    at = torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+    def step():
+        o, lse = api.ssm_attn_fwd(t["q"], t["k"], t["v"], return_lse=True, cu_seqlens=at, max_len=4096)
+        return [o, lse, *api.ssm_attn_bwd(t["q"], t["k"], t["v"], o=o, lse=lse, do=t["do"], cu_seqlens=at, max_len=4096).values()]
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in range(3):
+        lens = lengths(500, 900, 8000, 10 + seed)
+        new = torch.tensor([0] + lens).cumsum(0)
+        at.copy_(new.clamp(max=T).to(torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [a.clone() for a in out]
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+@gpu
 def test_wrong_offsets_stay_inside():
     if not torch.cuda.is_available():
         pytest.skip("no ROCm GPU visible")
