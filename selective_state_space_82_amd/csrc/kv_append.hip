@@ -4,8 +4,9 @@
 // A token's coordinate pair m turns by the angle t·freq_m at position t. The angle is formed in turns in fp64 and reduced to
 // a fraction of one before its sine and cosine are taken in fp32, so far positions lose nothing (a rounding of t·freq to
 // fp32 would be 2^-8 of a turn at t = 2^17). A workgroup takes one token: its first lanes form the angles, and all go through the
-// token's heads with them. Reading and writing every value once is the cost: 32 heads on 8 key heads of 128, bf16, 32768
-// packed tokens (0.8 GB) take 139 us, 5.8 TB/s (with a wavefront to a token 153), 512 tokens 5.4 us (6.7), one 4.1 (5.3).
+// token's heads with them. Reading and writing every value once is the cost: 32 heads on 8 key heads of 128, bf16, 8 packed prompts
+// of 17000 tokens in all (0.45 GB) take 87 us, 5.2 TB/s, 512 tokens 5.8 us. With a wavefront to a token both took longer (32768
+// packed tokens 153 us for 139, 512 tokens 6.7 for 5.4, one 5.3 for 4.1).
 #include "softmax_common.h"
 
 namespace ssm {

@@ -11,9 +11,10 @@
 // delta is summed over the keys; dq, dk and dv are then their own rounding off, 1.7e-3 of their norm, whatever keys and queries
 // have in common.
 //
-// 130M-like layer (4 rows of 2048, 24 heads of 64, causal): 0.36 ms, 0.36 PFLOP/s counting five products (0.26 with one part each
-// and delta from o alone, 0.30 with two parts); 9 packed documents of 463 to 4096 tokens, 32 heads on 8 key heads of 128: 2.10 ms,
-// 0.41 PFLOP/s (1.54, 1.76): 0.43 for what delta lacks, 0.70 for dq, 1.1 for dk and dv.
+// 130M-like layer (4 rows of 2048, 24 heads of 64, causal): 0.36 to 0.37 ms, 0.35 PFLOP/s counting five products (0.26 with one part
+// each and delta from o alone, 0.30 with two parts); 9 packed documents of 463 to 4096 tokens, 32 heads on 8 key heads of 128: 2.10
+// to 2.27 ms, 0.40 PFLOP/s (1.54, 1.76): 0.43 for what delta lacks at 44 % of the matrix units' time, 0.70 for dq at 56 %, 1.10 for
+// dk and dv at 46 %.
 #include "softmax_common.h"
 
 namespace ssm {

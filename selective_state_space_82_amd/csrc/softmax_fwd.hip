@@ -11,8 +11,9 @@
 // What carries it: the next tile's scores are formed in the same stretch of code, without branches, as this tile's weights and
 // products, so that matrix and vector instructions of one wavefront overlap; tiles that every query sees whole take no mask; the
 // maximum is raised only where it has to be. 1.4B-like layer (8 rows of 4096, 32 heads on 8 key heads of 128, bf16, causal):
-// 1.42 ms; one row of 16384, 16 heads of 128: 1.35 ms: three products of 0.55 TFLOP for two, 1.16 and 1.22 PFLOP/s of matrix
-// instructions, where a library product of 8192³ runs at 1.18 to 1.20: they bound it. Weights in one part take 1.11 and 1.03 ms.
+// 1.42 to 1.51 ms from card to card; one row of 16384, 16 heads of 128: 1.34 to 1.43 ms: three products of 0.55 TFLOP for two, 1.09 to
+// 1.16 and 1.15 to 1.23 PFLOP/s of matrix instructions, where library products of 8192³ and 16384³ run at 1.14 to 1.33: the matrix
+// units are busy 63 and 68 % of the time at the 1.7 GHz that the card holds then. Weights in one part take 1.11 and 1.03 ms.
 // Steps measured on the way with one part (1.4B-like, ms): tiles through registers 5.59; straight into LDS without bank
 // conflicts 1.46; key heads kept to an XCD 1.43; scores ahead 1.29; no masks and no path for NaN in the loop over whole
 // tiles 1.10.

@@ -9,7 +9,7 @@
 // piece; the four are joined in LDS, and the pieces of a row, where there are several, by a second launch. The next tile's
 // keys and page numbers are on their way while a tile is computed, and so are its own values: 64 KB a workgroup of D 128.
 // 512 rows of 1 to 4096 tokens, 32 heads on 8 key heads of 128, bf16, pages of 64 (4.24 GB): 0.82 ms, 5.2 TB/s, what a copy
-// reaches. One row of 131072 tokens on 2 key heads: 27 us for its 256 pieces (5.0 TB/s) and 8 to join them (38 a call).
+// reaches. One row of 131072 tokens on 2 key heads: 27 us for its 256 pieces (5.1 TB/s) and 9 to join them (39 a call).
 #include "softmax_common.h"
 
 namespace ssm {
