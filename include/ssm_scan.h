@@ -406,16 +406,17 @@ SSM_API ssm_status_t ssm_layernorm_bwd(const void *x, const float *w, const void
  *   workspace         as for ssm_linattn_fwd, of the bytes the call's _workspace function gives (may be 0)
  * Products are exact bf16 products summed in fp32 (bf16) or fp32 products (f32); the softmax' statistics and all sums are
  * fp32. With bf16, weights enter the product with v in two bf16 parts, 2^-16 of each, so that o is its own rounding off; in
- * gradients weights and ds, those of the scores, enter theirs so as well. Results are deterministic. A NaN or Inf reaches the queries that see its key and no others (an Inf in v may come out as NaN); in
- * gradients it may also reach queries and keys of the same sequence less than 160 from it, a query standing at its last key. A query all of whose scores are
- * −Inf counts as one that sees no key.
+ * gradients weights and ds, those of the scores, enter theirs so as well. Results are deterministic. A NaN or Inf reaches the
+ * queries that see its key and no others (an Inf in v may come out as NaN); in gradients it may also reach queries and keys of
+ * the same sequence less than 160 from it, a query standing at its last key. A query all of whose scores are −Inf counts as one
+ * that sees no key.
  * b, H, G, D >= 1; G divides H; D <= SSM_ATTN_MAX_D and scale finite (SSM_ERR_UNSUPPORTED otherwise); Lq, Lk <= 2^30; H·D and
  * strides between tokens at most 2^24; a launch takes fewer than 2^32 threads: SSM_ERR_SHAPE where b·H·⌈Lq/128⌉ or
  * b·G·⌈Lk/128⌉ (b·G rounded up to a multiple of 8, and ⌈./128⌉ to one of ⌈8/G⌉) reaches 2^23. Packed sequences count as
  * ⌊tokens/128⌋ + b blocks in place of b·⌈L/128⌉ (rounded up to a multiple of 8) where that is less and b·⌈L/128⌉ times the heads
- * passes 2^16. No output may overlap an
- * input, the workspace or another output. Where few blocks of 128 queries (keys, in the gradient for k and v) leave the device idle,
- * the keys (queries) are summed in up to 16 pieces: then fp32 sums, and so the last bits, depend on b, H, G, the lengths' bounds and tokens.
+ * passes 2^16. No output may overlap an input, the workspace or another output. Where few blocks of 128 queries (keys, in the
+ * gradient for k and v) leave the device idle, the keys (queries) are summed in up to 16 pieces: then fp32 sums, and so the last
+ * bits, depend on b, H, G, the lengths' bounds and tokens.
  */
 #define SSM_ATTN_MAX_D 128
 typedef ssm_linattn_strides_t ssm_attn_strides_t;
